@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) single-precision matrix multiply, C = A x B.
+"""GB300 (sm_103a) single-precision matrix multiply, C = A x B, and products
+grouped by expert and on 4-bit microscaled operands (``experts.py``).
 
 Thin Python binding over the C ABI in ``include/sgemm.h``: it checks tensor
 types, reads sizes and strides, passes raw device pointers and the current
@@ -13,6 +14,14 @@ import torch
 
 from . import _lib
 from ._lib import Options, SgemmError
+from .experts import (
+    sgemm_grouped,
+    sgemm_grouped_wgrad,
+    sgemm_mxfp4,
+    sgemm_mxfp4_dequantize,
+    sgemm_mxfp4_grouped,
+    sgemm_mxfp4_quantize,
+)
 
 __all__ = [
     "sgemm_f32",
@@ -22,6 +31,12 @@ __all__ = [
     "sgemm_3xtf32",
     "sgemm_3xtf32_ex",
     "sgemm_f32_host",
+    "sgemm_grouped",
+    "sgemm_grouped_wgrad",
+    "sgemm_mxfp4_quantize",
+    "sgemm_mxfp4_dequantize",
+    "sgemm_mxfp4",
+    "sgemm_mxfp4_grouped",
     "check_status",
     "describe",
     "Options",

@@ -1,4 +1,5 @@
-"""ctypes view of the C ABI declared in include/sgemm.h and include/sgemm_bench.h.
+"""ctypes view of the C ABI declared in include/sgemm.h, include/sgemm_experts.h
+and include/sgemm_bench.h.
 
 Loading never falls back to anything: if the shared library is missing it is
 built (nvcc), and if that fails the import error propagates.
@@ -22,10 +23,14 @@ ERR_CUDA = 3
 ERR_TIMEOUT = 4
 ERR_NOT_IMPLEMENTED = 5
 
+# Element types (include/sgemm_experts.h).
+TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
+
 PRODUCER_AUTO, PRODUCER_TMA, PRODUCER_CPASYNC, PRODUCER_TMA_WG, PRODUCER_FUSED, PRODUCER_TMA_X, PRODUCER_SMALL = 0, 1, 2, 3, 4, 5, 6
 
 # Every symbol the headers declare, with its ctypes signature.
 _i, _p, _u64, _d = ctypes.c_int, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_double
+_i64 = ctypes.c_int64
 
 
 class Options(ctypes.Structure):
@@ -63,6 +68,12 @@ SIGNATURES = {
     "sgemm_check_status": (_i, [_p]),
     "sgemm_status_string": (ctypes.c_char_p, [_i]),
     "sgemm_describe": (ctypes.c_char_p, [_i, _i, _i, _p, _i, _p, _i, _p, _i]),
+    "sgemm_grouped": (_i, [_i, _i, _i, _i, _i, _i, _p, _i64, _p, _i64, _i64, _p, _p, _i64, _p]),
+    "sgemm_grouped_wgrad": (_i, [_i, _i, _i, _i, _i, _i, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _p]),
+    "sgemm_mxfp4_quantize": (_i, [_i, _i, _i, _i, _p, _i64, _i64, _i, _p, _p, _p, _p]),
+    "sgemm_mxfp4_dequantize": (_i, [_i, _i, _i, _i, _p, _p, _i, _p, _p, _i64, _i64, _p]),
+    "sgemm_mxfp4": (_i, [_i, _i, _i, _i, _p, _p, _p, _p, _p, _i64, _p]),
+    "sgemm_mxfp4_grouped": (_i, [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _i64, _p]),
     "sgemm_bench_fma_peak": (_i, [_i, _i, _i, _p, _p, ctypes.POINTER(_d)]),
     "sgemm_bench_copy": (_i, [_p, _p, ctypes.c_longlong, _i, _p]),
 }

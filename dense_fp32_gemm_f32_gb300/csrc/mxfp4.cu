@@ -1,0 +1,222 @@
+// MXFP4 quantisation and its inverse.
+//
+// A block of 32 columns shares the scale 2^s, s = floor(log2 m) - 2 for its
+// largest magnitude m: m 2^-s lies in [4, 8), next to the largest 4-bit value
+// 6 = 1.5 * 2^2.  The exponent field of m's bits gives s without a logarithm,
+// and m is taken over the bits as integers, in which a NaN counts as larger
+// than any number.
+//
+// Both kernels move bytes and compute next to nothing.  A warp takes one row
+// and up to 1024 of its columns, 8 columns a lane and step: 16-byte loads (two
+// for float32), the block's maximum by two shuffles among 4 lanes, 4 bytes of
+// codes a lane (128 contiguous bytes a warp) and the 4 scales of 128 columns
+// as one 4-byte word.  All of a warp's loads are issued before the first use.
+#include "../../include/sgemm_experts.h"
+#include "experts.h"
+#include "experts_groups.cuh"
+
+namespace gb300 {
+namespace {
+
+constexpr int kSteps = 4;               // steps of 256 columns a warp takes
+constexpr int kCols = 256 * kSteps;     // columns a warp takes
+constexpr int kWarps = 4;               // warps a CTA
+
+// Eight float32 to eight codes, the first in the low bits: to nearest, ties to
+// the even code, magnitudes beyond 6 to 6.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Eight codes to eight float32 (exact).
+__device__ __forceinline__ void from_e2m1x8(uint32_t c, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 x = *reinterpret_cast<const __half2*>(&h[i]);
+        v[2 * i] = __low2float(x);
+        v[2 * i + 1] = __high2float(x);
+    }
+}
+
+// Columns c .. c + 7 of a row of K, zeros past its end.  `vec`: the row is
+// 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int K, bool vec, float (&v)[8]) {
+    if (vec && c + 8 <= K) {
+        constexpr int n = 16 / sizeof(T);
+#pragma unroll
+        for (int h = 0; h < 8 / n; ++h) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + c + h * n));
+            const T* t = reinterpret_cast<const T*>(&w);
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[h * n + i] = to_f32(t[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < K ? to_f32(row[c + i]) : 0.f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int c, int K, bool vec, const float (&v)[8]) {
+    if (vec && c + 8 <= K) {
+        constexpr int n = 16 / sizeof(T);
+#pragma unroll
+        for (int h = 0; h < 8 / n; ++h) {
+            uint4 w;
+            T* t = reinterpret_cast<T*>(&w);
+#pragma unroll
+            for (int i = 0; i < n; ++i) t[i] = from_f32<T>(v[h * n + i]);
+            *reinterpret_cast<uint4*>(row + c + h * n) = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < K) row[c + i] = from_f32<T>(v[i]);
+    }
+}
+
+// What a warp works on: a matrix, a row, the row's place among the scale
+// blocks' rows (< 0: a row of no expert) and its first column.
+struct Work {
+    int matrix, row, col;
+    long long scale_row;
+};
+
+__device__ __forceinline__ bool find_work(const QuantParams& p, Work& w) {
+    const int chunks = (p.K + kCols - 1) / kCols;
+    const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const long long r = id / chunks;
+    if (r >= static_cast<long long>(p.batch) * p.rows) return false;
+    w.col = static_cast<int>(id % chunks) * kCols;
+    w.matrix = static_cast<int>(r / p.rows);
+    w.row = static_cast<int>(r % p.rows);
+    w.scale_row = w.row;
+    if (p.offsets) {
+        GroupCursor c = group_begin(p.offsets, p.rows);
+        GroupHit h;
+        const bool ok = w.row >= c.start &&
+                        group_find(p.offsets, p.E, p.rows, w.row - c.start, c, [](int n) { return n; }, h);
+        w.scale_row = ok ? 128ll * h.block0 + h.local : -1;
+    }
+    return true;
+}
+
+// Word of the 4 scales of columns 128 q .. of a scale row.
+__device__ __forceinline__ long long scale_word(long long scale_row, int q, int kq) {
+    return ((scale_row >> 7) * kq + q) * 128 + (scale_row & 31) * 4 + ((scale_row & 127) >> 5);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) quantize_kernel(const QuantParams p) {
+    Work w;
+    if (!find_work(p, w)) return;
+    const int lane = threadIdx.x & 31;
+    const int kb = (p.K + 31) / 32, kq = (kb + 3) / 4;
+    const T* row = static_cast<const T*>(p.X) + w.matrix * p.sx + w.row * p.ldx;
+    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
+    uint8_t* codes = p.codes + (static_cast<long long>(w.matrix) * p.rows + w.row) * 16 * kb;
+    const long long nb = (p.rows + 127) / 128;
+    uint32_t* scales = reinterpret_cast<uint32_t*>(p.scales) + w.matrix * nb * kq * 128;
+    float v[kSteps][8];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) load8(row, w.col + 256 * s + 8 * lane, p.K, vec, v[s]);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int c = w.col + 256 * s + 8 * lane;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[s][i]) & 0x7fffffffu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t field = m >> 23;  // exponent of the largest: floor(log2 m) + 127
+        const uint32_t byte = field == 255 ? 255 : field > 2 ? field - 2 : 0;
+        // 2^-s = 2^(127 - byte); a block that stands for NaN holds codes 0
+        const float f = byte == 255 ? 0.f : __uint_as_float((254u - byte) << 23);
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = byte == 255 ? 0.f : v[s][i] * f;
+        if (c < 32 * kb) *reinterpret_cast<uint32_t*>(codes + (c >> 1)) = to_e2m1x8(u);
+        uint32_t word = byte << (8 * ((lane >> 2) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        if ((lane & 15) == 0 && c < p.K && w.scale_row >= 0) scales[scale_word(w.scale_row, c >> 7, kq)] = word;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(const QuantParams p) {
+    Work w;
+    if (!find_work(p, w)) return;
+    const int lane = threadIdx.x & 31;
+    const int kb = (p.K + 31) / 32, kq = (kb + 3) / 4;
+    T* row = static_cast<T*>(p.Y) + w.matrix * p.sy + w.row * p.ldy;
+    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
+    const uint8_t* codes = p.codes_in + (static_cast<long long>(w.matrix) * p.rows + w.row) * 16 * kb;
+    const long long nb = (p.rows + 127) / 128;
+    const uint32_t* scales = reinterpret_cast<const uint32_t*>(p.scales_in) + w.matrix * nb * kq * 128;
+    uint32_t code[kSteps], word[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int c = w.col + 256 * s + 8 * lane;
+        const bool in = c < p.K && w.scale_row >= 0;
+        code[s] = in ? __ldg(reinterpret_cast<const uint32_t*>(codes + (c >> 1))) : 0;
+        word[s] = in ? __ldg(scales + scale_word(w.scale_row, c >> 7, kq)) : 0;
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int c = w.col + 256 * s + 8 * lane;
+        if (c >= p.K) continue;
+        const uint32_t byte = (word[s] >> (8 * ((lane >> 2) & 3))) & 255;
+        const float f = __uint_as_float(byte == 255 ? 0x7fffffffu : byte == 0 ? 0x00400000u : byte << 23);
+        float v[8];
+        from_e2m1x8(code[s], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= f;
+        store8(row, c, p.K, vec, v);
+    }
+}
+
+template <typename K>
+int launch(K kernel, const QuantParams& p, cudaStream_t s) {
+    const long long warps = static_cast<long long>(p.batch) * p.rows * ((p.K + kCols - 1) / kCols);
+    const long long ctas = (warps + kWarps - 1) / kWarps;
+    if (ctas == 0) return SGEMM_OK;
+    if (ctas > 0x7fffffffll) return SGEMM_ERR_INVALID_ARG;
+    kernel<<<static_cast<unsigned>(ctas), 32 * kWarps, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
+}
+
+}  // namespace
+
+int mxfp4_quantize(const QuantParams& p, int type, cudaStream_t s) {
+    return type == SGEMM_TYPE_F32    ? launch(quantize_kernel<float>, p, s)
+           : type == SGEMM_TYPE_BF16 ? launch(quantize_kernel<__nv_bfloat16>, p, s)
+                                     : launch(quantize_kernel<__half>, p, s);
+}
+
+int mxfp4_dequantize(const QuantParams& p, int type, cudaStream_t s) {
+    return type == SGEMM_TYPE_F32    ? launch(dequantize_kernel<float>, p, s)
+           : type == SGEMM_TYPE_BF16 ? launch(dequantize_kernel<__nv_bfloat16>, p, s)
+                                     : launch(dequantize_kernel<__half>, p, s);
+}
+
+}  // namespace gb300

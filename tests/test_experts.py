@@ -1,0 +1,399 @@
+"""Products grouped by expert: forward and both gradients, against plain products in 64 bits.
+
+Acceptance, per element: |y - exact| <= TOL * b + u * (|exact| + TOL * b) + tiny, with b = sum_k |a_k||b_k| the bound that
+every entry of the library keeps in float32 (TOL = 5e-5), u the output type's unit roundoff (half its spacing at 1: 2^-8 for
+bf16, 2^-11 for f16; float32's own rounding is inside TOL * b) and tiny half its smallest subnormal.  A value past the
+type's largest rounds to the infinity of its sign.
+"""
+import pytest
+import torch
+
+import dense_fp32_gemm_f32_gb300 as g
+from parity import TOL
+
+U = {torch.float32: 0.0, torch.bfloat16: torch.finfo(torch.bfloat16).eps / 2, torch.float16: torch.finfo(torch.float16).eps / 2}
+TINY = {torch.float32: 2.0 ** -149, torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+NAMES = {torch.float32: "f32", torch.bfloat16: "bf16", torch.float16: "f16"}
+
+
+def typed(params):
+    return pytest.mark.parametrize("dtype", params, ids=[NAMES[t] for t in params])
+
+
+def check(y, exact, bound, what=""):
+    assert y.shape == exact.shape, what
+    lim = TOL * bound + U[y.dtype] * (exact.abs() + TOL * bound) + TINY[y.dtype]
+    err = (y.double() - exact).abs()
+    most = torch.finfo(y.dtype).max
+    over = y.isinf() & (y.sign() == exact.sign()) & (exact.abs() * (1 + U[y.dtype]) + TOL * bound >= most)
+    bad = ~(err <= lim) & ~over
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} outside, first at {bad.nonzero()[0].tolist()}: "
+                           f"{y[bad][0].item()} vs {exact[bad][0].item()}, allowed {lim[bad][0].item()}")
+
+
+def padded(x, pad=0, shift=0):
+    """x in a buffer whose rows are `pad` elements wider (NaN), begun `shift` elements in."""
+    lead, cols = x.shape[:-1], x.shape[-1]
+    n = x.numel() // max(cols, 1)
+    store = torch.full((n * (cols + pad) + shift,), float("nan"), dtype=x.dtype, device=x.device)
+    v = store[shift:].view(lead + (cols + pad,))[..., :cols]
+    v.copy_(x)
+    return v
+
+
+def bounds_of(offsets, T):
+    """The boundaries as the operators take them: clamped to [0, T], running maximum."""
+    o, out = 0, []
+    for i, v in enumerate(offsets):
+        v = min(max(v, 0), T)
+        o = v if i == 0 else max(o, v)
+        out.append(o)
+    return out
+
+
+def operands(T, E, K, N, dtype, seed=0, transw=False):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    X = torch.randn((T, K), generator=gen, device="cuda").to(dtype)
+    W = torch.randn((E, N, K) if transw else (E, K, N), generator=gen, device="cuda").to(dtype)
+    return X, W
+
+
+def forward64(X, W, offsets, transw=False):
+    o = bounds_of(offsets, X.shape[0])
+    N = W.shape[1 if transw else 2]
+    Y = torch.zeros((X.shape[0], N), dtype=torch.float64, device=X.device)
+    B = Y.clone()
+    for e in range(W.shape[0]):
+        w = W[e].double().T if transw else W[e].double()
+        x = X[o[e]: o[e + 1]].double()
+        Y[o[e]: o[e + 1]] = x @ w
+        B[o[e]: o[e + 1]] = x.abs() @ w.abs()
+    return Y, B
+
+
+def wgrad64(X, dY, offsets, E):
+    o = bounds_of(offsets, X.shape[0])
+    out = torch.zeros((E, X.shape[1], dY.shape[1]), dtype=torch.float64, device=X.device)
+    B = out.clone()
+    for e in range(E):
+        x, d = X[o[e]: o[e + 1]].double(), dY[o[e]: o[e + 1]].double()
+        out[e], B[e] = x.T @ d, x.abs().T @ d.abs()
+    return out, B
+
+
+def dev(offsets):
+    return torch.tensor(offsets, dtype=torch.int32, device="cuda")
+
+
+# (T, E, K, N, offsets): one token to many, groups of none, one group, widths off every tile and every vector
+SHAPES = [
+    (1, 1, 1, 1, [0, 1]),
+    (1, 8, 64, 128, [0, 0, 0, 1, 1, 1, 1, 1, 1]),
+    (3, 2, 31, 17, [0, 1, 3]),
+    (5, 4, 128, 136, [0, 0, 5, 5, 5]),
+    (40, 3, 72, 264, [0, 7, 23, 40]),
+    (130, 4, 200, 72, [0, 129, 129, 130, 130]),
+    (257, 2, 65, 129, [0, 256, 257]),
+    (600, 5, 328, 520, [0, 1, 17, 300, 300, 600]),
+    (777, 3, 1025, 255, [0, 256, 512, 777]),
+    (1500, 3, 256, 640, [0, 700, 701, 1500]),
+    (64, 70, 96, 80, [min(i, 64) for i in range(71)]),
+    (300, 40, 136, 256, [0] * 5 + [13 * i for i in range(23)] + [300] * 13),
+]
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("transw", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s[:4])))
+def test_forward(shape, transw, dtype):
+    T, E, K, N, offsets = shape
+    X, W = operands(T, E, K, N, dtype, 1, transw)
+    exact, bound = forward64(X, W, offsets, transw)
+    check(g.sgemm_grouped(X, W, dev(offsets), transw=transw), exact, bound)
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("pad,shift", [(8, 0), (0, 8), (3, 0), (1, 5)])
+@pytest.mark.parametrize("transw", [False, True])
+def test_forward_strides_and_alignment(pad, shift, transw, dtype):
+    T, E, K, N, offsets = 333, 3, 136, 200, [0, 100, 101, 333]
+    X, W = operands(T, E, K, N, dtype, 2, transw)
+    exact, bound = forward64(X, W, offsets, transw)
+    out = padded(torch.zeros((T, N), dtype=dtype, device="cuda"), pad, shift)
+    whole = out.untyped_storage()
+    y = g.sgemm_grouped(padded(X, pad, shift), padded(W, pad, shift), dev(offsets), out, transw=transw)
+    assert y is out
+    check(y, exact, bound)
+    store = torch.empty(0, dtype=dtype, device="cuda").set_(whole, 0, (whole.nbytes() // out.element_size(),), (1,))
+    assert int(store.isnan().sum()) == shift + T * pad, "padding was written"
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+def test_forward_tensor_exact_on_integers(dtype):
+    """Integers in -8..8 (int64 sums below 2^11 in f16's exact range by a short K): exact in every type but for the output's rounding."""
+    T, E, K, N, offsets = 200, 3, 24, 136, [0, 3, 150, 200]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randint(-2, 3, (T, K), generator=gen, device="cuda").to(dtype)
+    W = torch.randint(-2, 3, (E, K, N), generator=gen, device="cuda").to(dtype)
+    exact, _ = forward64(X, W, offsets)
+    assert torch.equal(g.sgemm_grouped(X, W, dev(offsets)).double(), exact)
+
+
+OFFSETS = [
+    [5, 50, 60, 90],          # rows of no expert at both ends
+    [0, 0, 0, 0],             # no rows at all
+    [100, 100, 100, 100],     # none, all before the first
+    [0, 70, 30, 100],         # a decreasing entry: an empty group
+    [-7, 40, 2000000000, 5],  # out of range at both ends
+    [2000000000, -5, 3, 7],   # first boundary past the end
+]
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("offsets", OFFSETS, ids=str)
+def test_rows_of_no_expert_and_boundaries_out_of_order(offsets, dtype):
+    T, E, K, N = 100, 3, 136, 264
+    X, W = operands(T, E, K, N, dtype, 4)
+    out = torch.full((T, N), float("nan"), dtype=dtype, device="cuda")
+    exact, bound = forward64(X, W, offsets)
+    check(g.sgemm_grouped(X, W, dev(offsets), out), exact, bound)
+    dY = torch.randn((T, N), device="cuda").to(dtype)
+    exact, bound = wgrad64(X, dY, offsets, E)
+    check(g.sgemm_grouped_wgrad(X, dY, dev(offsets)), exact, bound)
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_values_stay_in_their_own_rows(bad, dtype):
+    """Non-finite rows of a neighbouring group, of no group, and weights of another expert reach nothing else."""
+    T, E, K, N, offsets = 300, 4, 72, 136, [2, 100, 101, 290, 290]
+    X, W = operands(T, E, K, N, dtype, 5)
+    dY = torch.randn((T, N), device="cuda").to(dtype)
+    exact, bound = forward64(X, W, offsets)
+    dexact, dbound = wgrad64(X, dY, offsets, E)
+    X, W, dY = X.clone(), W.clone(), dY.clone()
+    for t in (0, 1, 100, 295, 299):  # rows of no group, and the whole of group 1
+        X[t], dY[t] = bad, bad
+    W[3] = bad  # an expert without rows
+    y = g.sgemm_grouped(X, W, dev(offsets))
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[100] = False
+    check(y[keep], exact[keep], bound[keep])
+    assert not y[100].isfinite().any()
+    dw = g.sgemm_grouped_wgrad(X, dY, dev(offsets))
+    for e in (0, 2, 3):
+        check(dw[e], dexact[e], dbound[e], f"expert {e}")
+    assert not dw[1].isfinite().any()
+    # one bad element: its own row of the output only
+    X, W = operands(T, E, K, N, dtype, 5)
+    X[50, 7] = bad
+    y = g.sgemm_grouped(X, W, dev(offsets))
+    keep[100], keep[50] = True, False
+    check(y[keep], exact[keep], bound[keep])
+    assert not y[50].isfinite().any()
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("out32", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s[:4])))
+def test_wgrad(shape, out32, dtype):
+    T, E, K, N, offsets = shape
+    X, _ = operands(T, E, K, N, dtype, 6)
+    dY = torch.randn((T, N), generator=torch.Generator(device="cuda").manual_seed(7), device="cuda").to(dtype)
+    exact, bound = wgrad64(X, dY, offsets, E)
+    dw = g.sgemm_grouped_wgrad(X, dY, dev(offsets), dtype=torch.float32 if out32 else None)
+    assert dw.dtype == (torch.float32 if out32 else dtype)
+    check(dw, exact, bound)
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (1, 5)])
+def test_wgrad_strides_and_alignment(pad, shift, dtype):
+    T, E, K, N, offsets = 333, 3, 136, 200, [0, 100, 101, 333]
+    X, _ = operands(T, E, K, N, dtype, 8)
+    dY = torch.randn((T, N), device="cuda").to(dtype)
+    exact, bound = wgrad64(X, dY, offsets, E)
+    out = padded(torch.zeros((E, K, N), dtype=dtype, device="cuda"), pad, shift)
+    check(g.sgemm_grouped_wgrad(padded(X, pad, shift), padded(dY, pad, shift), dev(offsets), out), exact, bound)
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+def test_gradients_against_differences(dtype):
+    """The product is linear in each operand: a central difference of L = sum(Y * R) along one element, computed by the
+    forward operator itself, is the gradient up to rounding.  Step 1 on operands of a few bits, so that in every type
+    each product and sum is exact and the two must be equal."""
+    T, E, K, N, offsets = 60, 3, 40, 48, [0, 20, 21, 60]
+    gen = torch.Generator(device="cuda").manual_seed(9)
+
+    def ints(*shape):
+        return torch.randint(-2, 3, shape, generator=gen, device="cuda").to(dtype)
+
+    X, W, R = ints(T, K), ints(E, K, N), ints(T, N)
+    o = dev(offsets)
+    dX = g.sgemm_grouped(R, W, o, transw=True)
+    dW = g.sgemm_grouped_wgrad(X, R, o)
+
+    def loss(x, w):
+        return (g.sgemm_grouped(x, w, o).double() * R.double()).sum()
+
+    for t, k in ((0, 0), (19, 39), (20, 3), (59, 17)):
+        hi, lo = X.clone(), X.clone()
+        hi[t, k] += 1
+        lo[t, k] -= 1
+        assert ((loss(hi, W) - loss(lo, W)) / 2).item() == dX[t, k].item()
+    for e, k, n in ((0, 0, 0), (1, 39, 47), (2, 5, 31)):
+        hi, lo = W.clone(), W.clone()
+        hi[e, k, n] += 1
+        lo[e, k, n] -= 1
+        assert ((loss(X, hi) - loss(X, lo)) / 2).item() == dW[e, k, n].item()
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+def test_transposed_weights_gradient(dtype):
+    """Weights stored (E, N, K): swapping X and dY gives their gradient."""
+    T, E, K, N, offsets = 90, 2, 40, 72, [0, 33, 90]
+    X, _ = operands(T, E, K, N, dtype, 10)
+    dY = torch.randn((T, N), device="cuda").to(dtype)
+    exact, bound = wgrad64(X, dY, offsets, E)
+    check(g.sgemm_grouped_wgrad(dY, X, dev(offsets)), exact.mT, bound.mT)
+
+
+@pytest.mark.gpu
+def test_other_streams_and_graphs():
+    T, E, K, N, offsets = 200, 4, 256, 384, [0, 10, 10, 150, 200]
+    X, W = operands(T, E, K, N, torch.bfloat16, 11)
+    exact, bound = forward64(X, W, offsets)
+    o = dev(offsets)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = g.sgemm_grouped(X, W, o, stream=s)
+    s.synchronize()
+    check(y, exact, bound)
+    # recorded once, replayed on other rows and other groups
+    out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    dw = torch.empty((E, K, N), dtype=torch.float32, device="cuda")
+    dY = torch.randn((T, N), device="cuda").to(torch.bfloat16)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.sgemm_grouped(X, W, o, out)
+        g.sgemm_grouped_wgrad(X, dY, o, dw)
+    for seed, new in ((12, [0, 0, 199, 200, 200]), (13, [0, 50, 100, 150, 200])):
+        X.copy_(operands(T, E, K, N, torch.bfloat16, seed)[0])
+        o.copy_(dev(new))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, *forward64(X, W, new))
+        check(dw, *wgrad64(X, dY, new, E))
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+def test_results_do_not_depend_on_timing(dtype):
+    T, E, K, N = 500, 6, 1032, 264
+    offsets = [0, 1, 2, 100, 360, 360, 500]
+    X, W = operands(T, E, K, N, dtype, 14)
+    dY = torch.randn((T, N), device="cuda").to(dtype)
+    o = dev(offsets)
+    y, dw = g.sgemm_grouped(X, W, o), g.sgemm_grouped_wgrad(X, dY, o)
+    for _ in range(5):
+        assert torch.equal(g.sgemm_grouped(X, W, o), y)
+        assert torch.equal(g.sgemm_grouped_wgrad(X, dY, o), dw)
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+def test_empty_sizes(dtype):
+    X, W = operands(4, 2, 8, 16, dtype)
+    o = dev([0, 2, 4])
+    assert g.sgemm_grouped(X[:0], W, dev([0, 0, 0])).shape == (0, 16)
+    assert g.sgemm_grouped(X, W[:, :, :0], o).shape == (4, 0)
+    assert torch.equal(g.sgemm_grouped(X[:, :0], W[:, :0], o), torch.zeros((4, 16), dtype=dtype, device="cuda"))
+    assert torch.equal(g.sgemm_grouped(X, W[:0], dev([0])), torch.zeros((4, 16), dtype=dtype, device="cuda"))
+    assert torch.equal(g.sgemm_grouped_wgrad(X[:0], W[0, :0], dev([0, 0, 0])),
+                       torch.zeros((2, 8, 16), dtype=dtype, device="cuda"))
+    assert g.sgemm_grouped_wgrad(X, X, dev([0])).shape == (0, 8, 8)
+
+
+@pytest.mark.gpu
+def test_binding_refuses():
+    X, W = operands(4, 2, 8, 16, torch.bfloat16)
+    o = dev([0, 2, 4])
+    with pytest.raises(TypeError):
+        g.sgemm_grouped(X.cpu(), W, o)
+    with pytest.raises(TypeError):
+        g.sgemm_grouped(X, W.float(), o)
+    with pytest.raises(TypeError):
+        g.sgemm_grouped(X.double(), W.double(), o)
+    with pytest.raises(TypeError):
+        g.sgemm_grouped(X, W, o.long())
+    with pytest.raises(ValueError):
+        g.sgemm_grouped(X, W, o[:2])
+    with pytest.raises(ValueError):
+        g.sgemm_grouped(X, W, o, transw=True)
+    with pytest.raises(ValueError):
+        g.sgemm_grouped(X, W[0], o)
+    with pytest.raises(ValueError):
+        g.sgemm_grouped(X.T.contiguous().T, W, o)
+    with pytest.raises(ValueError):
+        g.sgemm_grouped(X[:1].expand(4, 8), W, o)
+    with pytest.raises(ValueError):
+        g.sgemm_grouped(X, W, o, torch.empty((4, 16), device="cuda"))
+    with pytest.raises(g.SgemmError):
+        g.sgemm_grouped(X, W, o, W[0, :4])  # the output in the weights
+    with pytest.raises(ValueError):
+        g.sgemm_grouped_wgrad(X, X[:3], o)
+    with pytest.raises(TypeError):
+        g.sgemm_grouped_wgrad(X, X, o, dtype=torch.float16)
+
+
+FAKE_X, FAKE_W, FAKE_O, FAKE_Y = 0x10000000, 0x20000000, 0x30000000, 0x40000000  # never dereferenced
+
+
+@pytest.mark.parametrize("change", [
+    {"type": 3}, {"type": -1}, {"transw": 2}, {"T": -1}, {"E": -1}, {"N": -1}, {"K": -1}, {"X": 0}, {"W": 0}, {"o": 0},
+    {"Y": 0}, {"ldx": 7}, {"ldw": 15}, {"sw": 127}, {"ldy": 15}, {"X": FAKE_X + 1}, {"W": FAKE_W + 1}, {"o": FAKE_O + 2},
+    {"Y": FAKE_Y + 1}, {"Y": FAKE_X + 16}, {"Y": FAKE_W + 16}, {"ldx": 1 << 60}, {"sw": 1 << 61}, {"T": (1 << 30) + 1},
+], ids=str)
+def test_invalid_arguments_rejected_on_host(change):
+    from dense_fp32_gemm_f32_gb300 import _lib
+
+    a = {"type": 1, "transw": 0, "T": 4, "E": 2, "N": 16, "K": 8, "X": FAKE_X, "ldx": 8, "W": FAKE_W, "ldw": 16, "sw": 128,
+         "o": FAKE_O, "Y": FAKE_Y, "ldy": 16} | change
+    lib = _lib.load()
+    assert lib.sgemm_grouped(*a.values(), None) == _lib.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    {"type": 3}, {"out": 2}, {"out": 5}, {"T": -1}, {"E": -1}, {"K": -1}, {"N": -1}, {"X": 0}, {"dY": 0}, {"o": 0}, {"dW": 0},
+    {"ldx": 7}, {"lddy": 15}, {"lddw": 15}, {"sdw": 127}, {"dW": FAKE_X}, {"dW": FAKE_W}, {"dW": FAKE_Y + 1},
+], ids=str)
+def test_invalid_gradient_arguments_rejected_on_host(change):
+    from dense_fp32_gemm_f32_gb300 import _lib
+
+    a = {"type": 1, "out": 1, "T": 4, "E": 2, "K": 8, "N": 16, "X": FAKE_X, "ldx": 8, "dY": FAKE_W, "lddy": 16, "o": FAKE_O,
+         "dW": FAKE_Y, "lddw": 16, "sdw": 128} | change
+    lib = _lib.load()
+    assert lib.sgemm_grouped_wgrad(*a.values(), None) == _lib.ERR_INVALID_ARG
+
+
+def test_header_states_which_entry_points_allocate():
+    import os
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "sgemm_experts.h")).read()
+    listed = [re.search(r"^\s*\*\s*" + tag + r":\s*([\w ]+)$", text, flags=re.M).group(1).split()
+              for tag in ("EXPERTS-ALLOCATING", "EXPERTS-NON-ALLOCATING")]
+    code = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    declared = re.findall(r"^\s*int\s+(sgemm_\w+)\s*\(", code, flags=re.M)
+    assert sorted(listed[0] + listed[1]) == sorted(declared)
