@@ -51,11 +51,6 @@ View scales_view(const uint8_t* p, int64_t count, int64_t row_blocks, int64_t K)
 // Row blocks of T rows grouped by E experts, at most.
 int64_t grouped_blocks(int64_t T, int64_t E) { return (T + 127 * std::min(T, E)) / 128; }
 
-int device(DeviceState** st) {
-    int dev = 0;
-    return current_device(&dev, st);
-}
-
 Mxfp4Operand mxfp4_operand(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K) {
     const int64_t pitch = 16 * blocks32(K), kq = blocks128(K);
     return {codes, scales, rows * pitch, blocks128(rows) * kq * 512, static_cast<int>(pitch), static_cast<int>(kq)};
@@ -91,18 +86,21 @@ int sgemm_grouped(int type, int transw, int T, int E, int N, int K, const void* 
     if (!x.ok(size) || !w.ok(size) || !y.ok(size) || !offsets_ok(offsets) || overlap(y, x) || overlap(y, w))
         return SGEMM_ERR_INVALID_ARG;
     if (y.empty()) return SGEMM_OK;
+    int dev = 0;
     DeviceState* st = nullptr;
-    const int rc = device(&st);
+    const int rc = current_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (E == 0 || K == 0) return zero_rows(Y, 1, T, N, ldy, 0, size, s);
-    SimpleParams p = {};
-    p.A = {X, 0, ldx, 1};
-    p.B = transw ? StridedOperand{W, stride_w, ldw, 1} : StridedOperand{W, stride_w, 1, ldw};
-    p.offsets = offsets;
-    p.T = T, p.E = E, p.N = N, p.K = K;
-    p.out = Y, p.ldo = ldy;
-    return simple_forward(p, type, s);
+    GroupedCall c = {};
+    c.a = {W, E, transw ? N : K, transw ? K : N, ldw, stride_w};
+    c.b = {X, 1, T, K, ldx, 0};
+    c.a_mn = !transw;
+    c.type = c.out_type = type;
+    c.T = T, c.E = E, c.F = N, c.K = K;
+    c.offsets = offsets;
+    c.out = Y, c.ldo = ldy;
+    return grouped_tc(c, dev, *st, s);
 }
 
 int sgemm_grouped_wgrad(int type, int out_type, int T, int E, int K, int N, const void* X, int64_t ldx,
@@ -117,17 +115,21 @@ int sgemm_grouped_wgrad(int type, int out_type, int T, int E, int K, int N, cons
     if (!x.ok(size) || !dy.ok(size) || !dw.ok(osize) || !offsets_ok(offsets) || overlap(dw, x) || overlap(dw, dy))
         return SGEMM_ERR_INVALID_ARG;
     if (dw.empty()) return SGEMM_OK;
+    int dev = 0;
     DeviceState* st = nullptr;
-    const int rc = device(&st);
+    const int rc = current_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    SimpleParams p = {};
-    p.A = {X, 0, 1, ldx};
-    p.B = {dY, 0, 1, lddy};
-    p.offsets = offsets;
-    p.T = T, p.E = E, p.R = K, p.N = N;
-    p.out = dW, p.ldo = lddw, p.so = stride_dw;
-    return simple_wgrad(p, type, out_type, s);
+    if (T == 0) return zero_rows(dW, E, K, N, lddw, stride_dw, osize, s);
+    GroupedCall c = {};
+    c.a = {dY, 1, T, N, lddy, 0};
+    c.b = {X, 1, T, K, ldx, 0};
+    c.wgrad = c.a_mn = true;
+    c.type = type, c.out_type = out_type;
+    c.T = T, c.E = E, c.F = N, c.C = K;
+    c.offsets = offsets;
+    c.out = dW, c.ldo = lddw, c.so = stride_dw;
+    return grouped_tc(c, dev, *st, s);
 }
 
 static int quant_check(int type, int batch, int rows, int K, const View& x, int E, const int* offsets,
@@ -148,8 +150,9 @@ int sgemm_mxfp4_quantize(int type, int batch, int rows, int K, const void* X, in
     const View x{X, batch, rows, K, ldx, stride_x, type_bytes(type)};
     int rc = quant_check(type, batch, rows, K, x, E, offsets, codes, scales);
     if (rc != SGEMM_OK || x.empty()) return rc;
+    int dev = 0;
     DeviceState* st = nullptr;
-    rc = device(&st);
+    rc = current_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     QuantParams p = {};
     p.X = X, p.ldx = ldx, p.sx = stride_x;
@@ -163,8 +166,9 @@ int sgemm_mxfp4_dequantize(int type, int batch, int rows, int K, const uint8_t* 
     const View y{Y, batch, rows, K, ldy, stride_y, type_bytes(type)};
     int rc = quant_check(type, batch, rows, K, y, E, offsets, codes, scales);
     if (rc != SGEMM_OK || y.empty()) return rc;
+    int dev = 0;
     DeviceState* st = nullptr;
-    rc = device(&st);
+    rc = current_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     QuantParams p = {};
     p.Y = Y, p.ldy = ldy, p.sy = stride_y;
@@ -185,8 +189,9 @@ static int mxfp4_product(int out_type, int T, int E, int N, int K, const uint8_t
     if (!x.ok(16) || !w.ok(16) || !xs.ok(16) || !ws.ok(16) || !y.ok(size)) return SGEMM_ERR_INVALID_ARG;
     if (overlap(y, x) || overlap(y, xs) || overlap(y, w) || overlap(y, ws)) return SGEMM_ERR_INVALID_ARG;
     if (y.empty()) return SGEMM_OK;
+    int dev = 0;
     DeviceState* st = nullptr;
-    const int rc = device(&st);
+    const int rc = current_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (E == 0 || K == 0) return zero_rows(Y, 1, T, N, ldy, 0, size, s);

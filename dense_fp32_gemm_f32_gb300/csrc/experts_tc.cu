@@ -1,0 +1,159 @@
+// Launches of the tensor-core grouped products (experts_tc.cuh): operand
+// copies where needed, tensor maps, tile shape and grid.
+#include "../../include/sgemm_experts.h"
+#include "experts_tc.cuh"
+
+#include "api_internal.h"
+#include "experts.h"
+
+namespace gb300 {
+namespace detail {
+namespace {
+
+// An operand as the tensor maps read it: 16-bit elements, third dimension the
+// matrices (and planes of parts).
+struct TcOperand {
+    const void* p;
+    long long inner, rows, third, ld, stride;  // elements
+};
+
+int encode_3d(CUtensorMap* map, const TcOperand& o, bool f16, int box_inner, int box_rows) {
+    if (!g_encode) return SGEMM_ERR_CUDA;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.inner), static_cast<cuuint64_t>(o.rows),
+                                static_cast<cuuint64_t>(o.third)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2, static_cast<cuuint64_t>(o.stride) * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r =
+        g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                 const_cast<void*>(o.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
+}
+
+// 16-bit matrices that a tensor map reads as they are.
+bool tma_readable(const MatrixArg& m) {
+    return (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 && m.ld % 8 == 0 && (m.count == 1 || m.se % 8 == 0);
+}
+
+template <bool AMN, bool BMN, int TN, int CG>
+int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p, long long tiles, int sms,
+           cudaStream_t s) {
+    using S = GroupedShape<TN, CG>;
+    const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, sms / CG) * CG));
+    cfg.blockDim = dim3(kGrThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, a, b, p) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_CUDA;
+    }
+    return SGEMM_OK;
+}
+
+template <bool AMN, bool BMN, int TN, int CG>
+int set_up() {
+    return cudaFuncSetAttribute(grouped_tc_kernel<AMN, BMN, TN, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                GroupedShape<TN, CG>::kSmem) == cudaSuccess
+               ? SGEMM_OK
+               : SGEMM_ERR_CUDA;
+}
+
+// Operands of one product copied into the library's pool for the length of
+// the call.
+struct Packs {
+    void* ws = nullptr;
+    cudaStream_t s = nullptr;
+    ~Packs() {
+        if (ws) (void)cudaFreeAsync(ws, s);
+    }
+};
+
+}  // namespace
+
+int experts_tc_set_up() {
+    if (set_up<true, false, 32, 1>() || set_up<false, false, 32, 1>() || set_up<true, false, 256, kWideCG>() ||
+        set_up<false, false, 256, kWideCG>() || set_up<true, true, 256, kWideCG>()) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_CUDA;
+    }
+    return SGEMM_OK;
+}
+
+int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
+    const bool f32 = c.type == SGEMM_TYPE_F32, f16 = c.type == SGEMM_TYPE_F16;
+    // The first dimension of every operand as stored: A (W, or dY) and B (X).
+    const MatrixArg m[2] = {c.a, c.b};
+    TcOperand o[2];
+    PackJob job[2] = {};
+    size_t bytes[2] = {0, 0};
+    for (int i = 0; i < 2; ++i) {
+        const bool copy = f32 || !tma_readable(m[i]);
+        const long long dld = (m[i].cols + 7) / 8 * 8;
+        if (copy) {
+            job[i] = {m[i].p, m[i].count, m[i].rows, m[i].ld, m[i].se, static_cast<int>(m[i].cols), nullptr, dld};
+            bytes[i] = (static_cast<size_t>(f32 ? 3 : 1) * m[i].count * m[i].rows * dld * 2 + 255) & ~size_t{255};
+            o[i] = {nullptr, m[i].cols, m[i].rows, (f32 ? 3 : 1) * m[i].count, dld, m[i].rows * dld};
+        } else {
+            // (a dimension of one matrix has no stride of its own: any that the encoder takes)
+            o[i] = {m[i].p, m[i].cols, m[i].rows, m[i].count, m[i].ld, m[i].count > 1 ? m[i].se : m[i].rows * m[i].ld};
+        }
+    }
+    Packs packs;
+    packs.s = s;
+    if (bytes[0] + bytes[1]) {
+        cudaMemPool_t pool = workspace_pool(dev, st);
+        if (!pool || cudaMallocFromPoolAsync(&packs.ws, bytes[0] + bytes[1], pool, s) != cudaSuccess) {
+            (void)cudaGetLastError();
+            packs.ws = nullptr;
+            return SGEMM_ERR_CUDA;
+        }
+        if (bytes[0]) o[0].p = job[0].dst = packs.ws;
+        if (bytes[1]) o[1].p = job[1].dst = static_cast<char*>(packs.ws) + bytes[0];
+        const int rc = experts_pack(job[0], job[1], f32, s);
+        if (rc != SGEMM_OK) return rc;
+    }
+
+    const bool narrow = !c.wgrad && c.T <= 32ll * std::min(c.T, c.E);
+    const int tn = narrow ? 32 : 256, cg = narrow ? 1 : kWideCG;
+    GroupedTcParams p = {};
+    p.offsets = c.offsets;
+    p.T = c.T, p.E = c.E;
+    p.wgrad = c.wgrad;
+    p.F = c.F, p.C = c.C, p.K = c.K;
+    p.ftiles = static_cast<int>(ceil_div(c.F, 128 * cg));
+    p.ctiles = c.wgrad ? static_cast<int>(ceil_div(c.C, tn)) : 0;
+    p.nseg = f32 ? 6 : 1;
+    p.a_planes = c.wgrad ? 1 : c.E;
+    p.out = c.out, p.ldo = c.ldo, p.so = c.so, p.out_type = c.out_type;
+    p.timeout_ns = kDefaultTimeoutNs;
+    p.status = st.status_word;
+    const uint32_t fmt = f16 ? 0 : 1;
+    p.idesc = 1u << 4 | fmt << 7 | fmt << 10 | (c.a_mn ? 1u << 15 : 0) | (c.wgrad ? 1u << 16 : 0) |
+              static_cast<uint32_t>(128 * cg / 16) << 24;
+    const long long tiles = c.wgrad ? static_cast<long long>(c.E) * p.ftiles * p.ctiles
+                                    : (c.T / tn + std::min(c.T, c.E)) * static_cast<long long>(p.ftiles);
+    if (tiles > 0x7fffffffll - 65536) return SGEMM_ERR_INVALID_ARG;
+    alignas(64) CUtensorMap ma, mb;
+    int rc = encode_3d(&ma, o[0], f16, 64, c.a_mn ? 64 : 128);
+    if (rc == SGEMM_OK) rc = encode_3d(&mb, o[1], f16, 64, c.wgrad ? 64 : 32);
+    if (rc != SGEMM_OK) return rc;
+    if (c.wgrad) return launch<true, true, 256, kWideCG>(ma, mb, p, tiles, st.sm_count, s);
+    if (c.a_mn)
+        return narrow ? launch<true, false, 32, 1>(ma, mb, p, tiles, st.sm_count, s)
+                      : launch<true, false, 256, kWideCG>(ma, mb, p, tiles, st.sm_count, s);
+    return narrow ? launch<false, false, 32, 1>(ma, mb, p, tiles, st.sm_count, s)
+                  : launch<false, false, 256, kWideCG>(ma, mb, p, tiles, st.sm_count, s);
+}
+
+}  // namespace detail
+}  // namespace gb300
