@@ -54,6 +54,7 @@ struct DeviceState {
     int status = SGEMM_ERR_CUDA;  // result of the one-time set-up
     int sm_count = 0;
     int max_clusters_split[9] = {0};
+    int max_pairs = 0;            // co-resident CTA pairs of the grouped products' wide kernels
     bool regsplit_ok = false;     // the register-split kernels were built at kRegsLaunch registers
     int fused_per_sm[7] = {0};    // co-resident fused-producer CTAs per SM, by stage count
     unsigned int* status_word = nullptr;  // device address of g_sgemm_status

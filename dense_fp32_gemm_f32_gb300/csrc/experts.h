@@ -89,8 +89,8 @@ struct GroupedCall {
 };
 
 struct DeviceState;
-constexpr int kWideCG = 1;  // CTAs a wide tile's MMAs span
-int experts_tc_set_up();
+constexpr int kWideCG = 2;  // CTAs a wide tile's MMAs span
+int experts_tc_set_up(DeviceState& st);
 int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s);
 
 }  // namespace detail

@@ -37,12 +37,12 @@ bool tma_readable(const MatrixArg& m) {
 }
 
 template <bool AMN, bool BMN, int TN, int CG>
-int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p, long long tiles, int sms,
-           cudaStream_t s) {
+int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p, long long tiles,
+           const DeviceState& st, cudaStream_t s) {
     using S = GroupedShape<TN, CG>;
     const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, sms / CG) * CG));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, CG == 2 ? st.max_pairs : st.sm_count) * CG));
     cfg.blockDim = dim3(kGrThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -80,9 +80,26 @@ struct Packs {
 
 }  // namespace
 
-int experts_tc_set_up() {
+int experts_tc_set_up(DeviceState& st) {
     if (set_up<true, false, 32, 1>() || set_up<false, false, 32, 1>() || set_up<true, false, 256, kWideCG>() ||
         set_up<false, false, 256, kWideCG>() || set_up<true, true, 256, kWideCG>()) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_CUDA;
+    }
+    // Pairs that fit the GPU at once: persistent kernels launch no more.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * st.sm_count);
+    cfg.blockDim = dim3(kGrThreads);
+    cfg.dynamicSmemBytes = GroupedShape<256, 2>::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&st.max_pairs, grouped_tc_kernel<true, false, 256, kWideCG>, &cfg) !=
+            cudaSuccess ||
+        st.max_pairs < 1) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -147,12 +164,12 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     int rc = encode_3d(&ma, o[0], f16, 64, c.a_mn ? 64 : 128);
     if (rc == SGEMM_OK) rc = encode_3d(&mb, o[1], f16, 64, c.wgrad ? 64 : 32);
     if (rc != SGEMM_OK) return rc;
-    if (c.wgrad) return launch<true, true, 256, kWideCG>(ma, mb, p, tiles, st.sm_count, s);
+    if (c.wgrad) return launch<true, true, 256, kWideCG>(ma, mb, p, tiles, st, s);
     if (c.a_mn)
-        return narrow ? launch<true, false, 32, 1>(ma, mb, p, tiles, st.sm_count, s)
-                      : launch<true, false, 256, kWideCG>(ma, mb, p, tiles, st.sm_count, s);
-    return narrow ? launch<false, false, 32, 1>(ma, mb, p, tiles, st.sm_count, s)
-                  : launch<false, false, 256, kWideCG>(ma, mb, p, tiles, st.sm_count, s);
+        return narrow ? launch<true, false, 32, 1>(ma, mb, p, tiles, st, s)
+                      : launch<true, false, 256, kWideCG>(ma, mb, p, tiles, st, s);
+    return narrow ? launch<false, false, 32, 1>(ma, mb, p, tiles, st, s)
+                  : launch<false, false, 256, kWideCG>(ma, mb, p, tiles, st, s);
 }
 
 }  // namespace detail

@@ -28,10 +28,10 @@
 // warp finds from the boundary array by itself (group_find), so the host
 // never needs the group sizes.  Warps:
 //   warp 0      loads: tensor-map copies of 64 k of A and B into a ring;
-//   warp 1      MMAs (the pair's first CTA; in the second the warp relays its
-//               own ring's arrivals to the first).  For a weight gradient it
-//               first zeroes the rows past the group's end in the slice that
-//               holds them: they are the next group's, and may hold anything;
+//   warp 1      MMAs (the pair's first CTA).  For a weight gradient the warp
+//               first zeroes, in either CTA's shared memory, the rows past the
+//               group's end in the slice that holds them: they are the next
+//               group's, and may hold anything;
 //   warps 2..5  epilogue: tensor memory -> registers -> HBM, while the MMAs of
 //               the next tile fill the other accumulator.
 //
@@ -117,6 +117,10 @@ __device__ __forceinline__ bool grouped_tile(const GroupedTcParams& p, int i, Gr
     t.e = h.e;
     return true;
 }
+
+// A weight gradient's slice with `left` rows from its first to the group's end
+// whose last instruction takes rows past that end.
+__device__ __forceinline__ bool grouped_tail(int left) { return left < kGrBK && (left & 15) != 0; }
 
 template <typename T>
 __device__ __forceinline__ void grouped_store(void* out, long long at, long long ld, const uint32_t (&v)[32], int n,
@@ -210,26 +214,35 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                     const int pb = p.nseg > 1 ? seg_b(seg) : 0;
                     for (int kt = 0; kt < nk; ++kt, ++it) {
                         const int s = it % S::kStages, round = it / S::kStages;
-                        if (round > 0) {
-                            if (!mbar_wait_bounded_cluster(empty(s), (round - 1) & 1, tmo)) {
-                                timed_out = true;
-                                break;
-                            }
-                            if (CG == 2 && rank == 0) mbar_arrive_cluster(map_shared_rank(empty(s), 1));
+                        if (round > 0 && !mbar_wait_spin<CG == 2>(empty(s), (round - 1) & 1, tmo)) {
+                            timed_out = true;
+                            break;
                         }
                         const int k = t.k0 + kt * kGrBK;
-                        mbar_arrive_expect_tx(full(s), S::kABytes + boxes * kBox);
+                        // The pair's loads all arrive on the first CTA's
+                        // barrier, but for a slice whose rows past the end
+                        // the second CTA has to zero first.
+                        const bool own = CG == 1 || (BMN && grouped_tail(t.klen - kt * kGrBK));
+                        const uint32_t bar = own || rank == 0 ? full(s) : map_shared_rank(full(s), 0);
+                        const uint32_t bytes = S::kABytes + boxes * kBox;
+                        if (own || rank == 0) mbar_arrive_expect_tx(full(s), own ? bytes : 2 * bytes);
+                        auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                            if constexpr (CG == 2)
+                                tma_load_3d_pair(dst, map, bar, x, y, z);
+                            else
+                                tma_load_3d(dst, map, bar, x, y, z);
+                        };
                         if constexpr (AMN) {
-                            tma_load_3d(sA(s), &tmA, full(s), f0, k, pa);
-                            tma_load_3d(sA(s) + 64 * 128, &tmA, full(s), f0 + 64, k, pa);
+                            load(sA(s), &tmA, f0, k, pa);
+                            load(sA(s) + 64 * 128, &tmA, f0 + 64, k, pa);
                         } else {
-                            tma_load_3d(sA(s), &tmA, full(s), k, f0, pa);
+                            load(sA(s), &tmA, k, f0, pa);
                         }
                         for (int b = 0; b < boxes; ++b) {
                             if constexpr (BMN)
-                                tma_load_3d(sB(s) + b * kBox, &tmB, full(s), c0 + 64 * b, k, pb);
+                                load(sB(s) + b * kBox, &tmB, c0 + 64 * b, k, pb);
                             else
-                                tma_load_3d(sB(s) + b * kBox, &tmB, full(s), k, c0 + 32 * b, pb);
+                                load(sB(s) + b * kBox, &tmB, k, c0 + 32 * b, pb);
                         }
                     }
                 }
@@ -237,13 +250,16 @@ __global__ void __launch_bounds__(kGrThreads, 1)
             it = __shfl_sync(0xffffffffu, it, 0);
             timed_out = __shfl_sync(0xffffffffu, timed_out ? 1 : 0, 0) != 0;
         }
-        if (lane == 0) {  // every copy has landed before the CTA ends
+        // (every copy lands before its CTA ends: the MMAs wait for it, and the
+        // epilogue for them; after a timeout, the wait below, in the first CTA
+        // for the pair)
+        if (timed_out && rank == 0 && lane == 0)
             for (int j = max(0, it - S::kStages); j < it; ++j)
-                if (!mbar_wait_bounded(full(j % S::kStages), (j / S::kStages) & 1, tmo)) timed_out = true;
-        }
+                (void)mbar_wait_spin<CG == 2>(full(j % S::kStages), (j / S::kStages) & 1, tmo);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         int it = 0, tile = 0;
+        int tails = 0;  // bit s: parity of such slices so far in stage s
         for (int i = cluster; !timed_out && grouped_tile<TN, FT>(p, i, cur, t); i += clusters, ++tile) {
             const int nk = (t.klen + kGrBK - 1) / kGrBK;
             const int cols = (t.cols + 15) & ~15;
@@ -251,7 +267,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
             const uint32_t acc = tmem + static_cast<uint32_t>(buf * S::kAccCols);
             const uint32_t idesc = p.idesc | static_cast<uint32_t>(cols >> 3) << 17;
             if (rank == 0 && tile >= 2) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(acc_empty(buf), ((tile >> 1) - 1) & 1, tmo))) {
+                if (!__all_sync(0xffffffffu, mbar_wait_spin<CG == 2>(acc_empty(buf), ((tile >> 1) - 1) & 1, tmo))) {
                     timed_out = true;
                     break;
                 }
@@ -260,16 +276,20 @@ __global__ void __launch_bounds__(kGrThreads, 1)
             for (int n = 0; n < p.nseg * nk && !timed_out; ++n, ++it) {
                 const int kt = n % nk;
                 const int s = it % S::kStages, phase = (it / S::kStages) & 1;
-                if (!mbar_wait_bounded_warp(full(s), phase, tmo)) {
+                const int left = t.klen - kt * kGrBK;  // of the contraction, from this slice on
+                const bool tail = BMN && grouped_tail(left);
+                if (rank != 0 && !tail) continue;  // (the first CTA waits for this one's loads)
+                // (the second CTA's barriers see such slices' loads only)
+                const int full_phase = rank != 0 ? tails >> s & 1 : phase;
+                if (!__all_sync(0xffffffffu, mbar_wait_spin<CG == 2>(full(s), full_phase, tmo))) {
                     timed_out = true;
                     break;
                 }
-                const int left = t.klen - kt * kGrBK;  // of the contraction, from this slice on
                 if constexpr (BMN) {
                     // Rows left .. of the last instruction's 16 belong to
                     // others: zeros (rows of 128 bytes in blocks of 64 rows).
-                    const int past = min(kGrBK, (left + 15) & ~15);
-                    if (left < past) {
+                    if (tail) {
+                        const int past = (left + 15) & ~15;
                         const int blocks = 2 + S::kBBytes / (64 * 128);  // A's and B's
                         for (int j = lane; j < blocks * (past - left) * 8; j += 32) {
                             const int q = j & 7, row = left + (j >> 3) % (past - left), b = (j >> 3) / (past - left);
@@ -278,16 +298,19 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
+                        if constexpr (CG == 2) {
+                            const int tail_phase = tails >> s & 1;
+                            tails ^= 1 << s;
+                            if (rank != 0) {
+                                if (lane == 0) mbar_arrive_cluster(map_shared_rank(peer_full(s), 0));
+                                continue;
+                            }
+                            if (!__all_sync(0xffffffffu, mbar_wait_spin<true>(peer_full(s), tail_phase, tmo))) {
+                                timed_out = true;
+                                break;
+                            }
+                        }
                     }
-                }
-                if (CG == 2 && rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(map_shared_rank(peer_full(s), 0));
-                    continue;
-                }
-                if (CG == 2 &&
-                    !__all_sync(0xffffffffu, mbar_wait_bounded_cluster(peer_full(s), phase, tmo))) {
-                    timed_out = true;
-                    break;
                 }
                 tc_fence_after_sync();
                 if (lane == 0) {
@@ -299,15 +322,19 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                     for (int kk = 0; kk < kGrBK / 16; ++kk)
                         if (kk * 16 < left) umma_f16<CG>(acc, da + kk * ka, db + kk * kb, idesc, n > 0 || kk > 0);
                     umma_commit_cg<CG>(empty(s));
+                    if constexpr (CG == 2) umma_commit_cg<CG>(map_shared_rank(empty(s), 1));
                 }
                 __syncwarp();
             }
-            if (rank == 0 && !timed_out && lane == 0) umma_commit_cg<CG>(acc_full(buf));
+            if (rank == 0 && !timed_out && lane == 0) {
+                umma_commit_cg<CG>(acc_full(buf));
+                if constexpr (CG == 2) umma_commit_cg<CG>(map_shared_rank(acc_full(buf), 1));
+            }
             __syncwarp();
         }
         if (timed_out && rank == 0 && lane == 0) {  // the MMAs in flight end before tensor memory is freed
             umma_commit_cg<CG>(acc_full(tile & 1));
-            (void)mbar_wait_bounded(acc_full(tile & 1), (tile >> 1) & 1, tmo);
+            (void)mbar_wait_spin<CG == 2>(acc_full(tile & 1), (tile >> 1) & 1, tmo);
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -322,13 +349,10 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         int tile = 0;
         for (int i = cluster; grouped_tile<TN, FT>(p, i, cur, t); i += clusters, ++tile) {
             const int buf = tile & 1;
-            const bool ok = rank == 0 ? mbar_wait_bounded(acc_full(buf), (tile >> 1) & 1, tmo)
-                                      : mbar_wait_bounded_cluster(acc_full(buf), (tile >> 1) & 1, tmo);
-            if (!__all_sync(0xffffffffu, ok)) {
+            if (!__all_sync(0xffffffffu, mbar_wait_spin<CG == 2>(acc_full(buf), (tile >> 1) & 1, tmo))) {
                 timed_out = true;
                 break;
             }
-            if (CG == 2 && rank == 0 && warp == 2 && lane == 0) mbar_arrive_cluster(map_shared_rank(acc_full(buf), 1));
             tc_fence_after_sync();
             const uint32_t acc =
                 tmem + static_cast<uint32_t>(buf * S::kAccCols) + (static_cast<uint32_t>(32 * q) << 16);

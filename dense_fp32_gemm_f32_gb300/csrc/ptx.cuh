@@ -84,12 +84,20 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
     return ok != 0;
 }
 
-__device__ __forceinline__ bool mbar_wait_bounded_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+// Bounded wait that reads the global timer (slow next to a try_wait) only
+// once in 64 polls.  CLUSTER: phases that another CTA of the cluster completes.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
     while (true) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (global_timer_ns() - t0 > limit_ns) return false;
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0)
+            t0 = t;
+        else if (t - t0 > limit_ns)
+            return false;
     }
 }
 
@@ -120,6 +128,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint3
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// The same from a CTA of a pair, signalling the barrier at shared::cluster
+// address `bar` of either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
