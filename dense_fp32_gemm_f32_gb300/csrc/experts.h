@@ -89,7 +89,6 @@ struct GroupedCall {
 };
 
 struct DeviceState;
-constexpr int kWideCG = 2;  // CTAs a wide tile's MMAs span
 int experts_tc_set_up(DeviceState& st);
 int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s);
 

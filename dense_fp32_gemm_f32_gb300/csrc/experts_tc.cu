@@ -36,11 +36,11 @@ bool tma_readable(const MatrixArg& m) {
     return (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 && m.ld % 8 == 0 && (m.count == 1 || m.se % 8 == 0);
 }
 
-template <bool AMN, bool BMN, int TN, int CG>
+template <bool AMN, bool BMN, int TN, int CG, int PARTS>
 int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p, long long tiles,
            const DeviceState& st, cudaStream_t s) {
-    using S = GroupedShape<TN, CG>;
-    const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG>;
+    using S = GroupedShape<TN, CG, PARTS>;
+    const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG, PARTS>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, CG == 2 ? st.max_pairs : st.sm_count) * CG));
     cfg.blockDim = dim3(kGrThreads);
@@ -60,10 +60,10 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
     return SGEMM_OK;
 }
 
-template <bool AMN, bool BMN, int TN, int CG>
+template <bool AMN, bool BMN, int TN, int CG, int PARTS>
 int set_up() {
-    return cudaFuncSetAttribute(grouped_tc_kernel<AMN, BMN, TN, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                GroupedShape<TN, CG>::kSmem) == cudaSuccess
+    return cudaFuncSetAttribute(grouped_tc_kernel<AMN, BMN, TN, CG, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                GroupedShape<TN, CG, PARTS>::kSmem) == cudaSuccess
                ? SGEMM_OK
                : SGEMM_ERR_CUDA;
 }
@@ -81,8 +81,10 @@ struct Packs {
 }  // namespace
 
 int experts_tc_set_up(DeviceState& st) {
-    if (set_up<true, false, 32, 1>() || set_up<false, false, 32, 1>() || set_up<true, false, 256, kWideCG>() ||
-        set_up<false, false, 256, kWideCG>() || set_up<true, true, 256, kWideCG>()) {
+    if (set_up<true, false, 32, 1, 1>() || set_up<false, false, 32, 1, 1>() || set_up<true, false, 256, 2, 1>() ||
+        set_up<false, false, 256, 2, 1>() || set_up<true, true, 256, 2, 1>() || set_up<true, false, 32, 1, 3>() ||
+        set_up<false, false, 32, 1, 3>() || set_up<true, false, 128, 2, 3>() || set_up<false, false, 128, 2, 3>() ||
+        set_up<true, true, 128, 2, 3>()) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -90,14 +92,14 @@ int experts_tc_set_up(DeviceState& st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * st.sm_count);
     cfg.blockDim = dim3(kGrThreads);
-    cfg.dynamicSmemBytes = GroupedShape<256, 2>::kSmem;
+    cfg.dynamicSmemBytes = GroupedShape<256, 2, 1>::kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&st.max_pairs, grouped_tc_kernel<true, false, 256, kWideCG>, &cfg) !=
+    if (cudaOccupancyMaxActiveClusters(&st.max_pairs, grouped_tc_kernel<true, false, 256, 2, 1>, &cfg) !=
             cudaSuccess ||
         st.max_pairs < 1) {
         (void)cudaGetLastError();
@@ -141,15 +143,13 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     }
 
     const bool narrow = !c.wgrad && c.T <= 32ll * std::min(c.T, c.E);
-    const int tn = narrow ? 32 : 256, cg = narrow ? 1 : kWideCG;
+    const int tn = narrow ? 32 : f32 ? 128 : 256, cg = narrow ? 1 : 2;
     GroupedTcParams p = {};
     p.offsets = c.offsets;
     p.T = c.T, p.E = c.E;
-    p.wgrad = c.wgrad;
     p.F = c.F, p.C = c.C, p.K = c.K;
     p.ftiles = static_cast<int>(ceil_div(c.F, 128 * cg));
     p.ctiles = c.wgrad ? static_cast<int>(ceil_div(c.C, tn)) : 0;
-    p.nseg = f32 ? 6 : 1;
     p.a_planes = c.wgrad ? 1 : c.E;
     p.out = c.out, p.ldo = c.ldo, p.so = c.so, p.out_type = c.out_type;
     p.timeout_ns = kDefaultTimeoutNs;
@@ -162,14 +162,20 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     if (tiles > 0x7fffffffll - 65536) return SGEMM_ERR_INVALID_ARG;
     alignas(64) CUtensorMap ma, mb;
     int rc = encode_3d(&ma, o[0], f16, 64, c.a_mn ? 64 : 128);
-    if (rc == SGEMM_OK) rc = encode_3d(&mb, o[1], f16, 64, c.wgrad ? 64 : 32);
+    if (rc == SGEMM_OK) rc = encode_3d(&mb, o[1], f16, 64, narrow ? 32 : 64);
     if (rc != SGEMM_OK) return rc;
-    if (c.wgrad) return launch<true, true, 256, kWideCG>(ma, mb, p, tiles, st, s);
+    if (c.wgrad)
+        return f32 ? launch<true, true, 128, 2, 3>(ma, mb, p, tiles, st, s)
+                   : launch<true, true, 256, 2, 1>(ma, mb, p, tiles, st, s);
     if (c.a_mn)
-        return narrow ? launch<true, false, 32, 1>(ma, mb, p, tiles, st, s)
-                      : launch<true, false, 256, kWideCG>(ma, mb, p, tiles, st, s);
-    return narrow ? launch<false, false, 32, 1>(ma, mb, p, tiles, st, s)
-                  : launch<false, false, 256, kWideCG>(ma, mb, p, tiles, st, s);
+        return f32 ? narrow ? launch<true, false, 32, 1, 3>(ma, mb, p, tiles, st, s)
+                            : launch<true, false, 128, 2, 3>(ma, mb, p, tiles, st, s)
+               : narrow ? launch<true, false, 32, 1, 1>(ma, mb, p, tiles, st, s)
+                        : launch<true, false, 256, 2, 1>(ma, mb, p, tiles, st, s);
+    return f32 ? narrow ? launch<false, false, 32, 1, 3>(ma, mb, p, tiles, st, s)
+                        : launch<false, false, 128, 2, 3>(ma, mb, p, tiles, st, s)
+           : narrow ? launch<false, false, 32, 1, 1>(ma, mb, p, tiles, st, s)
+                    : launch<false, false, 256, 2, 1>(ma, mb, p, tiles, st, s);
 }
 
 }  // namespace detail

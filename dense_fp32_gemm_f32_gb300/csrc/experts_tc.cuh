@@ -18,8 +18,13 @@
 //
 // float32 operands come as three bf16 parts each, x = x0 + x1 + x2 (8 bits
 // each, rounded to nearest: what is left is below 2^-25 |x|), and the sum runs
-// over the six products of parts whose error a float32 product would show,
-// smallest first; the three dropped ones are below 2^-24 |a||b| together.
+// over the six products of parts that a float32 product would show; the three
+// dropped ones are below 2^-24 |a||b| together.  The tensor core adds into
+// its accumulator by cutting, not rounding, so errors of one sign pile up with
+// the number of additions: x0 y0 has an accumulator of its own, the five small
+// products another (256 times smaller), and every kGrChunk of the contraction
+// both go to float32 registers, which round to nearest.  Measured against 64
+// bits with one accumulator over a contraction of 2048: 2.1e-6, so: below 5e-7.
 //
 // Persistent CTAs (CG = 1) or CTA pairs (CG = 2: one instruction of the pair's
 // first CTA multiplies 256 features by up to 256 columns, each CTA holding
@@ -53,39 +58,39 @@ constexpr int kGrBK = 64;                // contraction per ring stage (128 byte
 constexpr int kGrThreads = 192;          // producer warp, MMA warp, 4 epilogue warps
 constexpr unsigned int kGrStatusTimeout = 4u;  // the library's timeout bit
 
+// Contraction after which float32's accumulators go to registers.
+constexpr int kGrChunk = 512;
+
 struct GroupedTcParams {
     const int* offsets;
     int T, E;
-    int wgrad;          // 0: the group's rows are columns c; 1: they are the contraction
-    int F, C, K;        // features; wgrad: columns; forward: contraction length
-    int ftiles, ctiles; // feature tiles; wgrad: column tiles
-    int nseg;           // products of parts summed: 1, or 6 for float32
-    int a_planes;       // third coordinate of A's part p, expert e: p * a_planes + (wgrad ? 0 : e)
+    int F, C, K;        // features; weight gradient: columns; forward: contraction length
+    int ftiles, ctiles; // feature tiles; weight gradient: column tiles
+    int a_planes;       // third coordinate of A's part p, expert e: p * a_planes + (weight gradient ? 0 : e)
     void* out;
-    long long ldo, so;  // elements between rows; wgrad: between experts
+    long long ldo, so;  // elements between rows; weight gradient: between experts
     int out_type;
     uint32_t idesc;     // instruction descriptor without the column count
     unsigned long long timeout_ns;
     unsigned int* status;
 };
 
-// Parts of A and B in each of float32's six products.
-__device__ __forceinline__ int seg_a(int seg) { return (0x210100 >> (4 * (5 - seg))) & 15; }
-__device__ __forceinline__ int seg_b(int seg) { return (0x012010 >> (4 * (5 - seg))) & 15; }
-
-template <int TN_, int CG_>
+template <int TN_, int CG_, int PARTS_>
 struct GroupedShape {
-    static constexpr int TN = TN_, CG = CG_;
-    static constexpr int kABytes = 128 * 128;        // 128 features x 64 k
-    static constexpr int kBBytes = TN / CG * 128;    // this CTA's columns x 64 k
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = (200 * 1024) / kStageBytes;
-    static constexpr int kAccCols = TN < 32 ? 32 : TN;
+    static constexpr int TN = TN_, CG = CG_, PARTS = PARTS_;
+    static constexpr int kCols = TN / CG;            // columns this CTA loads
+    static constexpr int kABytes = 128 * 128;        // a part: 128 features x 64 k
+    static constexpr int kBBytes = kCols * 128;      // a part: the columns x 64 k
+    static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
+    static constexpr int kStages = (218 * 1024) / kStageBytes < 10 ? (218 * 1024) / kStageBytes : 10;
+    static constexpr int kBoxCols = kCols < 64 ? kCols : 64;  // columns of a tensor-map box of B
+    static constexpr int kAccCols = PARTS > 1 ? 2 * TN : TN;  // tensor-memory columns of one accumulator (pair)
     static constexpr int kTmemCols = 2 * kAccCols;
     static constexpr int kBars = 3 * kStages + 4;    // full, empty, peer_full; acc_full, acc_empty x 2
     static constexpr int kSmem = kStages * kStageBytes + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
+    static_assert(kStages >= 2 && kBBytes % 1024 == 0, "ring");
+    static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
 };
 
 struct GroupedTile {
@@ -93,10 +98,10 @@ struct GroupedTile {
 };
 
 // Tile number `i`, from the same cursor in increasing order.
-template <int TN, int FT>
+template <bool WGRAD, int TN, int FT>
 __device__ __forceinline__ bool grouped_tile(const GroupedTcParams& p, int i, GroupCursor& cur, GroupedTile& t) {
     GroupHit h;
-    if (p.wgrad) {
+    if constexpr (WGRAD) {
         const int per = p.ftiles * p.ctiles;
         if (!group_find(p.offsets, p.E, p.T, i, cur, [&](int) { return per; }, h)) return false;
         t.f0 = h.local / p.ctiles * FT;
@@ -122,15 +127,30 @@ __device__ __forceinline__ bool grouped_tile(const GroupedTcParams& p, int i, Gr
 // whose last instruction takes rows past that end.
 __device__ __forceinline__ bool grouped_tail(int left) { return left < kGrBK && (left & 15) != 0; }
 
-template <typename T>
-__device__ __forceinline__ void grouped_store(void* out, long long at, long long ld, const uint32_t (&v)[32], int n,
-                                              bool zero) {
+// 32 columns of one feature to their rows of the output.
+template <typename T, typename V>
+__device__ __forceinline__ void grouped_store(void* out, long long at, long long ld, const V* v, int n) {
     T* o = static_cast<T*>(out) + at;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-        if (j < n) *o = from_f32<T>(zero ? 0.f : __uint_as_float(v[j]));
+        if (j < n) {
+            if constexpr (sizeof(V) == 4 && !__is_same(V, float))
+                *o = from_f32<T>(__uint_as_float(v[j]));
+            else
+                *o = from_f32<T>(v[j]);
+        }
         o += ld;
     }
+}
+
+template <typename V>
+__device__ __forceinline__ void grouped_store_typed(const GroupedTcParams& p, long long at, const V* v, int n) {
+    if (p.out_type == 0)
+        grouped_store<float>(p.out, at, p.ldo, v, n);
+    else if (p.out_type == 1)
+        grouped_store<__nv_bfloat16>(p.out, at, p.ldo, v, n);
+    else
+        grouped_store<__half>(p.out, at, p.ldo, v, n);
 }
 
 // Rows of no expert: zeros, spread over the CTAs' epilogue warps.
@@ -148,39 +168,39 @@ __device__ void grouped_zero_rows(const GroupedTcParams& p, int worker, int work
     }
 }
 
-// AMN, BMN: the operand is MN-major in HBM and shared memory (else K-major).
-template <bool AMN, bool BMN, int TN, int CG>
+// AMN, BMN: the operand is MN-major in HBM and shared memory (else K-major);
+// both: a weight gradient.
+template <bool AMN, bool BMN, int TN, int CG, int PARTS>
 __global__ void __launch_bounds__(kGrThreads, 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const GroupedTcParams p) {
-    using S = GroupedShape<TN, CG>;
+    using S = GroupedShape<TN, CG, PARTS>;
+    constexpr bool WGRAD = AMN && BMN;
+    static_assert(!BMN || (AMN && S::kCols % 64 == 0), "the weight gradient's columns come in blocks of 64");
     constexpr int FT = 128 * CG;
+    constexpr bool PAIR = CG == 2;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    auto sA = [&](int s) { return base + static_cast<uint32_t>(s * S::kStageBytes); };
-    auto sB = [&](int s) { return sA(s) + S::kABytes; };
+    const uint32_t baseB = base + PARTS * S::kABytes;  // B's parts follow A's in a stage
     const uint32_t bars = base + S::kStages * S::kStageBytes;
-    auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (S::kStages + s); };
-    auto peer_full = [&](int s) { return bars + 8u * (2 * S::kStages + s); };
-    auto acc_full = [&](int b) { return bars + 8u * (3 * S::kStages + b); };
-    auto acc_empty = [&](int b) { return bars + 8u * (3 * S::kStages + 2 + b); };
+    const uint32_t full0 = bars, empty0 = bars + 8 * S::kStages, peer0 = bars + 16 * S::kStages;
+    const uint32_t acc_full0 = bars + 24 * S::kStages, acc_empty0 = acc_full0 + 16;
     const uint32_t tmem_slot = bars + 8u * S::kBars;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
+    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
     const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
     const unsigned long long tmo = p.timeout_ns;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
-            mbar_init(peer_full(s), 1);
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+            mbar_init(peer0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), 4 * CG);
+            mbar_init(acc_full0 + 8 * b, 1);
+            mbar_init(acc_empty0 + 8 * b, 4 * CG);
         }
         fence_mbarrier_init();
         prefetch_tensormap(&tmA);
@@ -189,195 +209,279 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, S::kTmemCols);
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync_all();  // the peer's barriers are ready
+    if constexpr (PAIR) cluster_sync_all();  // the peer's barriers are ready
     tc_fence_after_sync();
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
 
+    // The loops below keep their ring position by counting, their addresses by
+    // adding, and run in one lane: a division or a vote in them costs as much as
+    // a twentieth of a stage's MMAs (measured: the index arithmetic of n / nk
+    // alone 150 of a stage's 970 cycles).
     bool timed_out = false;
     GroupCursor cur = group_begin(p.offsets, p.T);
     GroupedTile t;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        int it = 0;  // ring position, over all tiles
-        for (int i = cluster; !timed_out && grouped_tile<TN, FT>(p, i, cur, t); i += clusters) {
-            const int nk = (t.klen + kGrBK - 1) / kGrBK;
-            const int cols = (t.cols + 15) & ~15;            // columns of the instruction,
-            const int mine = CG == 2 ? cols / 2 : cols;      // this CTA's part of them
-            const int c0 = t.c0 + static_cast<int>(rank) * mine;
-            const int f0 = t.f0 + static_cast<int>(rank) * 128;
-            const int boxes = BMN ? (mine + 63) / 64 : (mine + 31) / 32;
-            constexpr int kBox = BMN ? 64 * 128 : 32 * 128;
+        const uint32_t bar0 = PAIR && rank != 0 ? map_shared_rank(full0, 0) : full0;
+        uint32_t s = 0, phase = 1;  // (the first round finds every stage empty)
+        int issued = 0;
+        for (int i = cluster; !timed_out && grouped_tile<WGRAD, TN, FT>(p, i, cur, t); i += clusters) {
+            const int cols = (t.cols + 15) & ~15;    // columns of the instruction,
+            const int mine = cols / CG;              // this CTA's part of them
+            const int c0 = t.c0 + rank * mine, f0 = t.f0 + rank * 128;
+            const int boxes = (mine + S::kBoxCols - 1) / S::kBoxCols;
+            constexpr uint32_t kBox = S::kBoxCols * 128;
+            const uint32_t bytes = PARTS * (S::kABytes + boxes * kBox);
+            const int pa = WGRAD ? 0 : t.e;
             if (lane == 0) {
-                for (int seg = 0; seg < p.nseg && !timed_out; ++seg) {
-                    const int pa = (p.nseg > 1 ? seg_a(seg) : 0) * p.a_planes + (p.wgrad ? 0 : t.e);
-                    const int pb = p.nseg > 1 ? seg_b(seg) : 0;
-                    for (int kt = 0; kt < nk; ++kt, ++it) {
-                        const int s = it % S::kStages, round = it / S::kStages;
-                        if (round > 0 && !mbar_wait_spin<CG == 2>(empty(s), (round - 1) & 1, tmo)) {
-                            timed_out = true;
-                            break;
-                        }
-                        const int k = t.k0 + kt * kGrBK;
-                        // The pair's loads all arrive on the first CTA's
-                        // barrier, but for a slice whose rows past the end
-                        // the second CTA has to zero first.
-                        const bool own = CG == 1 || (BMN && grouped_tail(t.klen - kt * kGrBK));
-                        const uint32_t bar = own || rank == 0 ? full(s) : map_shared_rank(full(s), 0);
-                        const uint32_t bytes = S::kABytes + boxes * kBox;
-                        if (own || rank == 0) mbar_arrive_expect_tx(full(s), own ? bytes : 2 * bytes);
-                        auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
-                            if constexpr (CG == 2)
-                                tma_load_3d_pair(dst, map, bar, x, y, z);
-                            else
-                                tma_load_3d(dst, map, bar, x, y, z);
-                        };
+                for (int k = 0; k < t.klen; k += kGrBK) {
+                    if (!mbar_wait_spin<false>(empty0 + 8 * s, phase, tmo)) {
+                        timed_out = true;
+                        break;
+                    }
+                    // A pair's loads all arrive on the first CTA's barrier,
+                    // but for a slice with rows past the group's end that the
+                    // second CTA has to zero first.
+                    const bool own = !PAIR || (WGRAD && grouped_tail(t.klen - k));
+                    const uint32_t bar = (own ? full0 : bar0) + 8 * s;
+                    if (own || rank == 0) mbar_arrive_expect_tx(bar, own ? bytes : 2 * bytes);
+                    auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                        if constexpr (PAIR)
+                            tma_load_3d_pair(dst, map, bar, x, y, z);
+                        else
+                            tma_load_3d(dst, map, bar, x, y, z);
+                    };
+                    const uint32_t a = base + s * S::kStageBytes, b = baseB + s * S::kStageBytes;
+                    const int kc = t.k0 + k;
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
                         if constexpr (AMN) {
-                            load(sA(s), &tmA, f0, k, pa);
-                            load(sA(s) + 64 * 128, &tmA, f0 + 64, k, pa);
+                            load(a + part * S::kABytes, &tmA, f0, kc, part * p.a_planes + pa);
+                            load(a + part * S::kABytes + 64 * 128, &tmA, f0 + 64, kc, part * p.a_planes + pa);
                         } else {
-                            load(sA(s), &tmA, k, f0, pa);
+                            load(a + part * S::kABytes, &tmA, kc, f0, part * p.a_planes + pa);
                         }
-                        for (int b = 0; b < boxes; ++b) {
+#pragma unroll 1
+                        for (int j = 0; j < boxes; ++j) {
                             if constexpr (BMN)
-                                load(sB(s) + b * kBox, &tmB, c0 + 64 * b, k, pb);
+                                load(b + part * S::kBBytes + j * kBox, &tmB, c0 + S::kBoxCols * j, kc, part);
                             else
-                                load(sB(s) + b * kBox, &tmB, k, c0 + 32 * b, pb);
+                                load(b + part * S::kBBytes + j * kBox, &tmB, kc, c0 + S::kBoxCols * j, part);
                         }
+                    }
+                    ++issued;
+                    if (++s == S::kStages) {
+                        s = 0;
+                        phase ^= 1;
                     }
                 }
             }
-            it = __shfl_sync(0xffffffffu, it, 0);
-            timed_out = __shfl_sync(0xffffffffu, timed_out ? 1 : 0, 0) != 0;
+            timed_out = __any_sync(0xffffffffu, timed_out);
         }
         // (every copy lands before its CTA ends: the MMAs wait for it, and the
         // epilogue for them; after a timeout, the wait below, in the first CTA
         // for the pair)
         if (timed_out && rank == 0 && lane == 0)
-            for (int j = max(0, it - S::kStages); j < it; ++j)
-                (void)mbar_wait_spin<CG == 2>(full(j % S::kStages), (j / S::kStages) & 1, tmo);
+            for (int j = max(0, issued - S::kStages); j < issued; ++j)
+                (void)mbar_wait_spin<false>(full0 + 8 * (j % S::kStages), (j / S::kStages) & 1, tmo);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
-        int it = 0, tile = 0;
-        int tails = 0;  // bit s: parity of such slices so far in stage s
-        for (int i = cluster; !timed_out && grouped_tile<TN, FT>(p, i, cur, t); i += clusters, ++tile) {
-            const int nk = (t.klen + kGrBK - 1) / kGrBK;
-            const int cols = (t.cols + 15) & ~15;
-            const int buf = tile & 1;
-            const uint32_t acc = tmem + static_cast<uint32_t>(buf * S::kAccCols);
-            const uint32_t idesc = p.idesc | static_cast<uint32_t>(cols >> 3) << 17;
-            if (rank == 0 && tile >= 2) {
-                if (!__all_sync(0xffffffffu, mbar_wait_spin<CG == 2>(acc_empty(buf), ((tile >> 1) - 1) & 1, tmo))) {
-                    timed_out = true;
-                    break;
+        const uint64_t descA = AMN ? umma_desc_mnmajor_sw128(base, 64 * 128) : umma_desc_kmajor_sw128(base);
+        const uint64_t descB = BMN ? umma_desc_mnmajor_sw128(baseB, 64 * 128) : umma_desc_kmajor_sw128(baseB);
+        // 16 k: 32 bytes of each row (K-major), 16 rows of 128 bytes (MN-major); addresses in units of 16
+        constexpr uint32_t ka = AMN ? 128 : 2, kb = BMN ? 128 : 2;
+        constexpr uint32_t pa = S::kABytes / 16, pb = S::kBBytes / 16;
+        const uint32_t peer_empty0 = PAIR ? map_shared_rank(empty0, 1) : 0;
+        const uint32_t peer_acc_full0 = PAIR ? map_shared_rank(acc_full0, 1) : 0;
+        const uint32_t lead_peer0 = PAIR ? map_shared_rank(peer0, 0) : 0;
+        uint32_t s = 0, phase = 0;
+        uint32_t tails = 0;  // bit s: parity of the slices with rows to zero so far in stage s
+        int unit = 0;        // accumulators filled
+        for (int i = cluster; !timed_out && grouped_tile<WGRAD, TN, FT>(p, i, cur, t); i += clusters) {
+            const uint32_t idesc = p.idesc | static_cast<uint32_t>((t.cols + 15) >> 4) << 18;
+            const bool tail = WGRAD && grouped_tail(t.klen % kGrBK ? t.klen % kGrBK : kGrBK);
+            const int chunk = PARTS > 1 ? kGrChunk : t.klen;
+            int k = 0;
+            do {
+                const int buf = unit & 1;
+                const uint32_t acc = tmem + static_cast<uint32_t>(buf * S::kAccCols);
+                const int end = min(t.klen, k + chunk);
+                const int plain = tail && end == t.klen ? end / kGrBK * kGrBK : end;  // slices up to here: as they are
+                bool more = false;  // the accumulators hold something
+                auto slice = [&](int left) {
+                    const uint32_t off = s * (S::kStageBytes / 16);
+                    const uint64_t a = descA + off, b = descB + off;
+#pragma unroll
+                    for (int kk = 0; kk < kGrBK / 16; ++kk) {
+                        if (left > kk * 16) {
+                            if constexpr (PARTS == 1) {
+                                umma_f16<CG>(acc, a + kk * ka, b + kk * kb, idesc, more);
+                            } else {
+                                auto mma = [&](uint32_t d, int i, int j, bool add) {
+                                    umma_f16<CG>(d, a + i * pa + kk * ka, b + j * pb + kk * kb, idesc, add);
+                                };
+                                mma(acc + TN, 2, 0, more);
+                                mma(acc + TN, 1, 1, true);
+                                mma(acc + TN, 0, 2, true);
+                                mma(acc + TN, 1, 0, true);
+                                mma(acc + TN, 0, 1, true);
+                                mma(acc, 0, 0, more);
+                            }
+                            more = true;
+                        }
+                    }
+                    umma_commit_cg<CG>(empty0 + 8 * s);
+                    if constexpr (PAIR) umma_commit_cg<CG>(peer_empty0 + 8 * s);
+                };
+                auto next = [&] {
+                    if (++s == S::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                };
+                if (rank == 0 && lane == 0) {
+                    if (unit >= 2 && !mbar_wait_spin<PAIR>(acc_empty0 + 8 * buf, ((unit >> 1) - 1) & 1, tmo))
+                        timed_out = true;
+                    tc_fence_after_sync();
+                    for (int q = k; q < plain && !timed_out; q += kGrBK) {
+                        if (!mbar_wait_spin<false>(full0 + 8 * s, phase, tmo)) {
+                            timed_out = true;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        slice(end - q);
+                        next();
+                    }
                 }
-                tc_fence_after_sync();
-            }
-            for (int n = 0; n < p.nseg * nk && !timed_out; ++n, ++it) {
-                const int kt = n % nk;
-                const int s = it % S::kStages, phase = (it / S::kStages) & 1;
-                const int left = t.klen - kt * kGrBK;  // of the contraction, from this slice on
-                const bool tail = BMN && grouped_tail(left);
-                if (rank != 0 && !tail) continue;  // (the first CTA waits for this one's loads)
-                // (the second CTA's barriers see such slices' loads only)
-                const int full_phase = rank != 0 ? tails >> s & 1 : phase;
-                if (!__all_sync(0xffffffffu, mbar_wait_spin<CG == 2>(full(s), full_phase, tmo))) {
-                    timed_out = true;
-                    break;
-                }
-                if constexpr (BMN) {
-                    // Rows left .. of the last instruction's 16 belong to
-                    // others: zeros (rows of 128 bytes in blocks of 64 rows).
-                    if (tail) {
-                        const int past = (left + 15) & ~15;
-                        const int blocks = 2 + S::kBBytes / (64 * 128);  // A's and B's
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if constexpr (WGRAD) {
+                    if (rank != 0 || lane != 0)
+                        for (int q = k; q < plain; q += kGrBK) next();
+                    if (plain < end && !timed_out) {
+                        // The last slice: rows left .. of its last instruction's
+                        // 16 belong to others.  Zeros (rows of 128 bytes in
+                        // blocks of 64 rows, A's and B's).
+                        const int left = end - plain, past = (left + 15) & ~15;
+                        const uint32_t full_phase = rank != 0 ? tails >> s & 1 : phase;
+                        if (!mbar_wait_spin<false>(full0 + 8 * s, full_phase, tmo)) timed_out = true;
+                        constexpr int blocks = S::kStageBytes / (64 * 128);
                         for (int j = lane; j < blocks * (past - left) * 8; j += 32) {
-                            const int q = j & 7, row = left + (j >> 3) % (past - left), b = (j >> 3) / (past - left);
-                            sts128(sA(s) + static_cast<uint32_t>(b * 64 * 128 + row * 128 + q * 16),
+                            const int row = left + (j >> 3) % (past - left), b = (j >> 3) / (past - left);
+                            sts128(base + s * S::kStageBytes + static_cast<uint32_t>(b * 64 * 128 + row * 128 + (j & 7) * 16),
                                    make_float4(0.f, 0.f, 0.f, 0.f));
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if constexpr (CG == 2) {
-                            const int tail_phase = tails >> s & 1;
-                            tails ^= 1 << s;
+                        if (lane == 0 && !timed_out) {
                             if (rank != 0) {
-                                if (lane == 0) mbar_arrive_cluster(map_shared_rank(peer_full(s), 0));
-                                continue;
-                            }
-                            if (!__all_sync(0xffffffffu, mbar_wait_spin<true>(peer_full(s), tail_phase, tmo))) {
-                                timed_out = true;
-                                break;
+                                mbar_arrive_cluster(lead_peer0 + 8 * s);
+                            } else {
+                                if (PAIR && !mbar_wait_spin<true>(peer0 + 8 * s, tails >> s & 1, tmo)) timed_out = true;
+                                tc_fence_after_sync();
+                                if (!timed_out) slice(left);
                             }
                         }
+                        tails ^= 1u << s;
+                        next();
+                        timed_out = __any_sync(0xffffffffu, timed_out);
                     }
                 }
-                tc_fence_after_sync();
-                if (lane == 0) {
-                    const uint64_t da = AMN ? umma_desc_mnmajor_sw128(sA(s), 64 * 128) : umma_desc_kmajor_sw128(sA(s));
-                    const uint64_t db = BMN ? umma_desc_mnmajor_sw128(sB(s), 64 * 128) : umma_desc_kmajor_sw128(sB(s));
-                    // 16 k: 32 bytes of each row (K-major), 16 rows of 128 bytes (MN-major); addresses in units of 16
-                    constexpr uint64_t ka = AMN ? 128 : 2, kb = BMN ? 128 : 2;
-#pragma unroll
-                    for (int kk = 0; kk < kGrBK / 16; ++kk)
-                        if (kk * 16 < left) umma_f16<CG>(acc, da + kk * ka, db + kk * kb, idesc, n > 0 || kk > 0);
-                    umma_commit_cg<CG>(empty(s));
-                    if constexpr (CG == 2) umma_commit_cg<CG>(map_shared_rank(empty(s), 1));
+                if (rank == 0 && lane == 0 && !timed_out) {
+                    umma_commit_cg<CG>(acc_full0 + 8 * buf);
+                    if constexpr (PAIR) umma_commit_cg<CG>(peer_acc_full0 + 8 * buf);
                 }
                 __syncwarp();
-            }
-            if (rank == 0 && !timed_out && lane == 0) {
-                umma_commit_cg<CG>(acc_full(buf));
-                if constexpr (CG == 2) umma_commit_cg<CG>(map_shared_rank(acc_full(buf), 1));
-            }
-            __syncwarp();
+                if (timed_out) break;
+                ++unit;
+                k = end;
+            } while (k < t.klen);
         }
         if (timed_out && rank == 0 && lane == 0) {  // the MMAs in flight end before tensor memory is freed
-            umma_commit_cg<CG>(acc_full(tile & 1));
-            (void)mbar_wait_spin<CG == 2>(acc_full(tile & 1), (tile >> 1) & 1, tmo);
+            umma_commit_cg<CG>(acc_full0 + 8 * (unit & 1));
+            (void)mbar_wait_spin<false>(acc_full0 + 8 * (unit & 1), (unit >> 1) & 1, tmo);
         }
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
-        if (!p.wgrad) {
+        const uint32_t acc_empty_lead = PAIR && rank != 0 ? map_shared_rank(acc_empty0, 0) : acc_empty0;
+        if (!WGRAD) {
             const int worker = static_cast<int>(blockIdx.x) * 4 + q, workers = static_cast<int>(gridDim.x) * 4;
             if (p.out_type == 0)
                 grouped_zero_rows<float>(p, worker, workers);
             else  // (bf16 and f16 zeros are the same bits)
                 grouped_zero_rows<__half>(p, worker, workers);
         }
-        int tile = 0;
-        for (int i = cluster; grouped_tile<TN, FT>(p, i, cur, t); i += clusters, ++tile) {
-            const int buf = tile & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_spin<CG == 2>(acc_full(buf), (tile >> 1) & 1, tmo))) {
-                timed_out = true;
-                break;
-            }
-            tc_fence_after_sync();
-            const uint32_t acc =
-                tmem + static_cast<uint32_t>(buf * S::kAccCols) + (static_cast<uint32_t>(32 * q) << 16);
-            const int f = t.f0 + static_cast<int>(rank) * 128 + 32 * q + lane;
-            const bool zero = t.klen == 0;  // no MMA wrote the accumulator
-            for (int c = 0; c < t.cols; c += 32) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
-                tmem_wait_ld();
-                const long long at = (p.wgrad ? t.e * p.so : 0ll) + (t.c0 + c) * p.ldo + f;
-                const int n = f < p.F ? t.cols - c : 0;
-                if (p.out_type == 0)
-                    grouped_store<float>(p.out, at, p.ldo, v, n, zero);
-                else if (p.out_type == 1)
-                    grouped_store<__nv_bfloat16>(p.out, at, p.ldo, v, n, zero);
-                else
-                    grouped_store<__half>(p.out, at, p.ldo, v, n, zero);
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 1 || rank == 0)
-                    mbar_arrive(acc_empty(buf));
-                else
-                    mbar_arrive_cluster(map_shared_rank(acc_empty(buf), 0));
+        int unit = 0;
+        for (int i = cluster; !timed_out && grouped_tile<WGRAD, TN, FT>(p, i, cur, t); i += clusters) {
+            const int f = t.f0 + rank * 128 + 32 * q + lane;
+            const int cols = f < p.F ? t.cols : 0;
+            const long long out0 = (WGRAD ? t.e * p.so : 0ll) + t.c0 * p.ldo + f;
+            auto wait = [&](uint32_t& acc) {
+                const int buf = unit & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait_spin<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, tmo)))
+                    return false;
+                tc_fence_after_sync();
+                acc = tmem + static_cast<uint32_t>(buf * S::kAccCols) + (static_cast<uint32_t>(32 * q) << 16);
+                return true;
+            };
+            auto release = [&] {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (!PAIR || rank == 0)
+                        mbar_arrive(acc_empty0 + 8 * (unit & 1));
+                    else
+                        mbar_arrive_cluster(acc_empty_lead + 8 * (unit & 1));
+                }
+                ++unit;
+            };
+            uint32_t acc;
+            if constexpr (PARTS == 1) {
+                if (!wait(acc)) {
+                    timed_out = true;
+                    break;
+                }
+                for (int c = 0; c < t.cols; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
+                    tmem_wait_ld();
+                    if (WGRAD && t.klen == 0) {  // no MMA wrote the accumulator
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0;
+                    }
+                    grouped_store_typed(p, out0 + c * p.ldo, v, cols - c);
+                }
+                release();
+            } else {
+                float sum[TN];
+#pragma unroll
+                for (int j = 0; j < TN; ++j) sum[j] = 0.f;
+                for (int k = 0; k < t.klen || k == 0; k += kGrChunk) {
+                    if (!wait(acc)) {
+                        timed_out = true;
+                        break;
+                    }
+                    if (t.klen > 0) {
+#pragma unroll
+                        for (int c = 0; c < TN; c += 32) {
+                            if (c < t.cols) {
+                                uint32_t v[32], w[32];
+                                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(TN + c), w);
+                                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    sum[c + j] += __uint_as_float(v[j]) + __uint_as_float(w[j]);
+                            }
+                        }
+                    }
+                    release();
+                }
+                if (timed_out) break;
+#pragma unroll
+                for (int c = 0; c < TN; c += 32)
+                    if (c < t.cols) grouped_store_typed(p, out0 + c * p.ldo, sum + c, cols - c);
             }
         }
     }
@@ -385,7 +489,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     if (timed_out) atomicOr(p.status, kGrStatusTimeout);
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync_all();  // nothing of the peer's is under way in this CTA's memory
+    if constexpr (PAIR) cluster_sync_all();  // nothing of the peer's is under way in this CTA's memory
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_cg<CG>(tmem, S::kTmemCols);
