@@ -51,11 +51,6 @@ View scales_view(const uint8_t* p, int64_t count, int64_t row_blocks, int64_t K)
 // Row blocks of T rows grouped by E experts, at most.
 int64_t grouped_blocks(int64_t T, int64_t E) { return (T + 127 * std::min(T, E)) / 128; }
 
-Mxfp4Operand mxfp4_operand(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K) {
-    const int64_t pitch = 16 * blocks32(K), kq = blocks128(K);
-    return {codes, scales, rows * pitch, blocks128(rows) * kq * 512, static_cast<int>(pitch), static_cast<int>(kq)};
-}
-
 int zero_rows(void* p, int64_t count, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int size,
               cudaStream_t s) {
     for (int64_t e = 0; e < count; ++e)
@@ -195,13 +190,8 @@ static int mxfp4_product(int out_type, int T, int E, int N, int K, const uint8_t
     if (rc != SGEMM_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (E == 0 || K == 0) return zero_rows(Y, 1, T, N, ldy, 0, size, s);
-    SimpleParams p = {};
-    p.qA = mxfp4_operand(X, x_scales, T, K);
-    p.qB = mxfp4_operand(W, w_scales, N, K);
-    p.offsets = offsets;
-    p.T = T, p.E = E, p.N = N, p.K = K;
-    p.out = Y, p.ldo = ldy;
-    return simple_mxfp4(p, out_type, s);
+    Mxfp4Call c = {X, x_scales, W, w_scales, xs.rows, out_type, T, E, N, K, offsets, Y, ldy};
+    return mxfp4_tc(c, *st, s);
 }
 
 int sgemm_mxfp4(int out_type, int M, int N, int K, const uint8_t* A, const uint8_t* a_scales, const uint8_t* B,

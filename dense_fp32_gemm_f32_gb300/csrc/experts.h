@@ -8,36 +8,6 @@
 
 namespace gb300 {
 
-// One operand of a product in HBM, element (row, k) of matrix e.
-struct StridedOperand {
-    const void* p;
-    long long se, sr, sk;  // strides in elements: matrix, row, contraction
-};
-
-// MXFP4 operand: codes (rows of `pitch` bytes) and scale blocks.
-struct Mxfp4Operand {
-    const uint8_t* codes;
-    const uint8_t* scales;
-    long long codes_e, scales_e;  // bytes between matrices
-    int pitch;                    // bytes per row of codes
-    int kq;                       // scale blocks per row of blocks
-};
-
-// The simple kernels' launch (experts_simple.cu).  mode: rows of the first
-// operand grouped (forward), or the contraction grouped (weight gradient).
-struct SimpleParams {
-    StridedOperand A, B;    // A: (rows or the output's rows) x k, B: (columns) x k
-    Mxfp4Operand qA, qB;
-    const int* offsets;     // null: one group of all T rows
-    int T, E;
-    int R, N, K;            // weight gradient: output rows R; forward: R unused
-    void* out;
-    long long ldo, so;      // output row pitch; matrix stride (weight gradient)
-};
-int simple_forward(const SimpleParams& p, int type, cudaStream_t s);
-int simple_wgrad(const SimpleParams& p, int type, int out_type, cudaStream_t s);
-int simple_mxfp4(const SimpleParams& p, int out_type, cudaStream_t s);
-
 // One operand copied for the tensor maps (experts_pack.cu): `count` matrices
 // of rows x cols at src (`ld` elements a row, `se` a matrix) to dst, rows of
 // dld elements (a multiple of 8) one after the other; float32 to three bf16
@@ -88,7 +58,20 @@ struct GroupedCall {
     long long ldo, so;
 };
 
+// An MXFP4 product as mxfp4_tc.cuh takes it: rows X (T x K), weights W (E
+// matrices N x K); offsets null: one matrix.
+struct Mxfp4Call {
+    const uint8_t *X, *x_scales, *W, *w_scales;
+    long long x_blocks;  // row blocks of X's scales
+    int out_type, T, E, N, K;
+    const int* offsets;
+    void* out;
+    long long ldo;
+};
+
 struct DeviceState;
+int mxfp4_tc_set_up();
+int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s);
 int experts_tc_set_up(DeviceState& st);
 int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s);
 
