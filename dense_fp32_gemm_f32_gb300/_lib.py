@@ -86,6 +86,8 @@ def library_path() -> str:
 def load() -> ctypes.CDLL:
     """Load (building first if needed) the CUDA library and bind its symbols."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()

@@ -152,6 +152,8 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     p.ctiles = c.wgrad ? static_cast<int>(ceil_div(c.C, tn)) : 0;
     p.a_planes = c.wgrad ? 1 : c.E;
     p.out = c.out, p.ldo = c.ldo, p.so = c.so, p.out_type = c.out_type;
+    p.vec_store = c.out_type != SGEMM_TYPE_F32 && (reinterpret_cast<uintptr_t>(c.out) & 15) == 0 && c.ldo % 8 == 0 &&
+                  c.so % 8 == 0;
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
     const uint32_t fmt = f16 ? 0 : 1;

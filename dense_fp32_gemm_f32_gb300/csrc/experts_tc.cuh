@@ -29,16 +29,23 @@
 // Persistent CTAs (CG = 1) or CTA pairs (CG = 2: one instruction of the pair's
 // first CTA multiplies 256 features by up to 256 columns, each CTA holding
 // half of either operand, which halves the shared-memory fill per flop).
-// Tile i goes to cluster i mod clusters; which expert's rows it falls on every
-// warp finds from the boundary array by itself (group_find), so the host
-// never needs the group sizes.  Warps:
+// Tile i goes to cluster i mod clusters.  Warps:
 //   warp 0      loads: tensor-map copies of 64 k of A and B into a ring;
 //   warp 1      MMAs (the pair's first CTA).  For a weight gradient the warp
 //               first zeroes, in either CTA's shared memory, the rows past the
 //               group's end in the slice that holds them: they are the next
 //               group's, and may hold anything;
-//   warps 2..5  epilogue: tensor memory -> registers -> HBM, while the MMAs of
+//   warp 2      schedule: which expert's rows a tile falls on, from the
+//               boundary array alone (group_find: the host never needs the
+//               group sizes), handed to the other warps through shared memory
+//               a few tiles ahead;
+//   warps 3..6  epilogue: tensor memory -> registers -> HBM, while the MMAs of
 //               the next tile fill the other accumulator.
+//
+// The load and MMA warps' loops are uniform over the warp, with one elected
+// lane issuing: the operands of the instructions then live in uniform
+// registers.  (In a loop of one lane they do not, and moving them cost more
+// than the MMAs: 775 cycles a stage of the wide tile, whose MMAs take 512.)
 //
 // Every wait is bounded by `timeout_ns`; on expiry the thread records the
 // timeout in the status word and goes to the final barrier.
@@ -55,7 +62,7 @@
 namespace gb300 {
 
 constexpr int kGrBK = 64;                // contraction per ring stage (128 bytes of 16-bit values)
-constexpr int kGrThreads = 192;          // producer warp, MMA warp, 4 epilogue warps
+constexpr int kGrThreads = 224;          // load, MMA and schedule warps, 4 epilogue warps
 constexpr unsigned int kGrStatusTimeout = 4u;  // the library's timeout bit
 
 // Contraction after which float32's accumulators go to registers.
@@ -70,10 +77,24 @@ struct GroupedTcParams {
     void* out;
     long long ldo, so;  // elements between rows; weight gradient: between experts
     int out_type;
+    int vec_store;      // 16-bit output with rows on the 16-byte grid
     uint32_t idesc;     // instruction descriptor without the column count
     unsigned long long timeout_ns;
     unsigned int* status;
 };
+
+constexpr int kGrPatchPitch = 80;  // an epilogue warp's patch: 32 rows of 64 bytes (grouped_store)
+constexpr int kGrPatchBytes = 32 * kGrPatchPitch;
+
+constexpr int kSchedSlots = 4;  // tiles that the schedule warp is ahead
+constexpr int kSchedBytes = 32 * kSchedSlots, kSchedBars = 2 * kSchedSlots;
+
+// Ring stages that fit beside `other` bytes and the barriers; 10 cover the
+// latency of the narrow tiles' stages too.
+constexpr int kRing(int stage, int other) {
+    const int n = (227 * 1024 - 1024 - 512 - other) / stage;
+    return n < 10 ? n : 10;
+}
 
 template <int TN_, int CG_, int PARTS_>
 struct GroupedShape {
@@ -82,22 +103,25 @@ struct GroupedShape {
     static constexpr int kABytes = 128 * 128;        // a part: 128 features x 64 k
     static constexpr int kBBytes = kCols * 128;      // a part: the columns x 64 k
     static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
-    static constexpr int kStages = (218 * 1024) / kStageBytes < 10 ? (218 * 1024) / kStageBytes : 10;
+    static constexpr int kPatches = PARTS > 1 ? 0 : 4 * kGrPatchBytes;  // the epilogue warps' (float32 output: none)
+    static constexpr int kStages = kRing(PARTS * (kABytes + kBBytes), kPatches);
     static constexpr int kBoxCols = kCols < 64 ? kCols : 64;  // columns of a tensor-map box of B
     static constexpr int kAccCols = PARTS > 1 ? 2 * TN : TN;  // tensor-memory columns of one accumulator (pair)
     static constexpr int kTmemCols = 2 * kAccCols;
-    static constexpr int kBars = 3 * kStages + 4;    // full, empty, peer_full; acc_full, acc_empty x 2
-    static constexpr int kSmem = kStages * kStageBytes + 8 * kBars + 16 + 1024;
+    static constexpr int kBars = 3 * kStages + 4 + kSchedBars;  // full, empty, peer_full; acc_full, acc_empty x 2
+    static constexpr int kSmem = kStages * kStageBytes + kPatches + kSchedBytes + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kStages >= 2 && kBBytes % 1024 == 0, "ring");
     static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
 };
 
 struct GroupedTile {
-    int e, f0, c0, cols, k0, klen;  // c0: row t (forward) or column of X; k0: first row of the contraction (wgrad)
+    int valid, e, f0, c0, cols;  // c0: row t, or column of X (weight gradient)
+    int k0, klen;                // weight gradient: the contraction's first row and length
+    int srow;                    // MXFP4: the first column's place among the scale blocks' rows
 };
 
-// Tile number `i`, from the same cursor in increasing order.
+// Tile number `i`, from the same cursor in increasing order (whole warp).
 template <bool WGRAD, int TN, int FT>
 __device__ __forceinline__ bool grouped_tile(const GroupedTcParams& p, int i, GroupCursor& cur, GroupedTile& t) {
     GroupHit h;
@@ -120,37 +144,118 @@ __device__ __forceinline__ bool grouped_tile(const GroupedTcParams& p, int i, Gr
         t.klen = p.K;
     }
     t.e = h.e;
+    t.srow = 0;
     return true;
 }
+
+// The schedule warp: tiles first, first + step, ... into the slots at `slots`
+// (barriers: a full and an empty one a slot), then one that is not valid.
+// Whole warp; false on a timeout.
+template <typename Find>
+__device__ __forceinline__ bool sched_run(uint32_t slots, uint32_t bars, int first, int step, uint64_t tmo, Find find) {
+    int n = 0;
+    for (int i = first;; i += step, ++n) {
+        GroupedTile t;
+        t.valid = find(i, t) ? 1 : 0;
+        const int slot = n % kSchedSlots, round = n / kSchedSlots;
+        if (round > 0 && !mbar_wait_warp<false>(bars + 8 * (kSchedSlots + slot), (round - 1) & 1, tmo)) return false;
+        if (elect_one()) {
+            sts128i(slots + 32 * slot, make_int4(t.valid, t.e, t.f0, t.c0));
+            sts128i(slots + 32 * slot + 16, make_int4(t.cols, t.k0, t.klen, t.srow));
+            mbar_arrive(bars + 8 * slot);
+        }
+        __syncwarp();
+        if (!t.valid) return true;
+    }
+}
+
+// A consumer warp's next tile; false at the end, or (timed_out set) on a timeout.
+struct SchedReader {
+    uint32_t slots, bars;
+    int n = 0;
+    __device__ __forceinline__ bool next(GroupedTile& t, uint64_t tmo, bool& timed_out) {
+        const int slot = n % kSchedSlots, round = n / kSchedSlots;
+        if (!mbar_wait_warp<false>(bars + 8 * slot, round & 1, tmo)) {
+            timed_out = true;
+            return false;
+        }
+        const int4 a = lds128i(slots + 32 * slot), b = lds128i(slots + 32 * slot + 16);
+        t.valid = warp_uniform(a.x), t.e = warp_uniform(a.y), t.f0 = warp_uniform(a.z), t.c0 = warp_uniform(a.w);
+        t.cols = warp_uniform(b.x), t.k0 = warp_uniform(b.y), t.klen = warp_uniform(b.z), t.srow = warp_uniform(b.w);
+        if (elect_one()) mbar_arrive(bars + 8 * (kSchedSlots + slot));
+        __syncwarp();
+        ++n;
+        return t.valid != 0;
+    }
+};
 
 // A weight gradient's slice with `left` rows from its first to the group's end
 // whose last instruction takes rows past that end.
 __device__ __forceinline__ bool grouped_tail(int left) { return left < kGrBK && (left & 15) != 0; }
 
-// 32 columns of one feature to their rows of the output.
+// A warp's 32 features x 32 columns, a feature a lane, to the output's rows
+// (columns 0 .. n - 1; features below `features`).  Elements of 2 bytes stored
+// as they lie would be 64 bytes an instruction; so they pass through the
+// warp's own patch of shared memory (a column a row, 80 bytes apart so that
+// the 16-byte reads of neighbouring rows fall on other banks) and go out as
+// 16-byte stores, 8 rows an instruction.  Measured on 16 groups of 1024 rows,
+// 4096 x 4096 weight gradients (a tile every 16 ring stages): 533 us with 2-byte
+// stores.  Rows off the 16-byte grid, the last features of a width that is no
+// multiple of 8, and float32 (128 bytes an instruction already) go directly.
 template <typename T, typename V>
-__device__ __forceinline__ void grouped_store(void* out, long long at, long long ld, const V* v, int n) {
-    T* o = static_cast<T*>(out) + at;
+__device__ __forceinline__ void grouped_store(uint32_t patch, void* out, long long at, long long ld, const V* v, int n,
+                                              int features, bool vec) {
+    const int lane = threadIdx.x & 31;
+    auto value = [&](int j) {
+        if constexpr (__is_same(V, float))
+            return v[j];
+        else
+            return __uint_as_float(v[j]);
+    };
+    if constexpr (sizeof(T) == 2) {
+        if (vec) {  // (warp-uniform)
+            T* o = static_cast<T*>(out) + at;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const T x = from_f32<T>(value(j));
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(patch + j * kGrPatchPitch + lane * 2),
+                             "h"(*reinterpret_cast<const unsigned short*>(&x))
+                             : "memory");
+            }
+            __syncwarp();
+            const int f = (lane & 3) * 8;
+            if (f < features) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    const int c = j + (lane >> 2);
+                    if (c < n)
+                        *reinterpret_cast<float4*>(o + c * ld + f) = lds128(patch + c * kGrPatchPitch + f * 2);
+                }
+            }
+            __syncwarp();
+            return;
+        }
+    }
+    T* o = static_cast<T*>(out) + at + lane;
+    if (lane >= features) n = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-        if (j < n) {
-            if constexpr (sizeof(V) == 4 && !__is_same(V, float))
-                *o = from_f32<T>(__uint_as_float(v[j]));
-            else
-                *o = from_f32<T>(v[j]);
-        }
+        if (j < n) *o = from_f32<T>(value(j));
         o += ld;
     }
 }
 
-template <typename V>
-__device__ __forceinline__ void grouped_store_typed(const GroupedTcParams& p, long long at, const V* v, int n) {
+// `at`: the element of the first feature and column.
+template <typename P, typename V>
+__device__ __forceinline__ void grouped_store_typed(const P& p, uint32_t patch, long long at, const V* v, int n,
+                                                    int features) {
+    const bool vec = p.vec_store && (features >= 32 || features % 8 == 0);
     if (p.out_type == 0)
-        grouped_store<float>(p.out, at, p.ldo, v, n);
+        grouped_store<float>(patch, p.out, at, p.ldo, v, n, features, false);
     else if (p.out_type == 1)
-        grouped_store<__nv_bfloat16>(p.out, at, p.ldo, v, n);
+        grouped_store<__nv_bfloat16>(patch, p.out, at, p.ldo, v, n, features, vec);
     else
-        grouped_store<__half>(p.out, at, p.ldo, v, n);
+        grouped_store<__half>(patch, p.out, at, p.ldo, v, n, features, vec);
 }
 
 // Rows of no expert: zeros, spread over the CTAs' epilogue warps.
@@ -182,13 +287,15 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t baseB = base + PARTS * S::kABytes;  // B's parts follow A's in a stage
-    const uint32_t bars = base + S::kStages * S::kStageBytes;
+    const uint32_t patches = base + S::kStages * S::kStageBytes;
+    const uint32_t slots = patches + S::kPatches;
+    const uint32_t bars = slots + kSchedBytes;
     const uint32_t full0 = bars, empty0 = bars + 8 * S::kStages, peer0 = bars + 16 * S::kStages;
-    const uint32_t acc_full0 = bars + 24 * S::kStages, acc_empty0 = acc_full0 + 16;
+    const uint32_t acc_full0 = bars + 24 * S::kStages, acc_empty0 = acc_full0 + 16, sched0 = acc_empty0 + 16;
     const uint32_t tmem_slot = bars + 8u * S::kBars;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int rank = PAIR ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
     const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
     const unsigned long long tmo = p.timeout_ns;
 
@@ -202,10 +309,15 @@ __global__ void __launch_bounds__(kGrThreads, 1)
             mbar_init(acc_full0 + 8 * b, 1);
             mbar_init(acc_empty0 + 8 * b, 4 * CG);
         }
+        for (int j = 0; j < kSchedSlots; ++j) {
+            mbar_init(sched0 + 8 * j, 1);
+            mbar_init(sched0 + 8 * (kSchedSlots + j), 6);  // load, MMA and epilogue warps
+        }
         fence_mbarrier_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
     }
+    __syncwarp();
     if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, S::kTmemCols);
     tc_fence_before_sync();
     __syncthreads();
@@ -213,20 +325,18 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     tc_fence_after_sync();
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+    tmem = warp_uniform(tmem);
 
-    // The loops below keep their ring position by counting, their addresses by
-    // adding, and run in one lane: a division or a vote in them costs as much as
-    // a twentieth of a stage's MMAs (measured: the index arithmetic of n / nk
-    // alone 150 of a stage's 970 cycles).
     bool timed_out = false;
-    GroupCursor cur = group_begin(p.offsets, p.T);
     GroupedTile t;
+    SchedReader tiles{slots, sched0};
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        const uint32_t bar0 = PAIR && rank != 0 ? map_shared_rank(full0, 0) : full0;
+        const uint32_t bar0 = PAIR ? warp_uniform(map_shared_rank(full0, 0)) : full0;
+        const bool issuer = elect_one();
         uint32_t s = 0, phase = 1;  // (the first round finds every stage empty)
         int issued = 0;
-        for (int i = cluster; !timed_out && grouped_tile<WGRAD, TN, FT>(p, i, cur, t); i += clusters) {
+        while (!timed_out && tiles.next(t, tmo, timed_out)) {
             const int cols = (t.cols + 15) & ~15;    // columns of the instruction,
             const int mine = cols / CG;              // this CTA's part of them
             const int c0 = t.c0 + rank * mine, f0 = t.f0 + rank * 128;
@@ -234,26 +344,29 @@ __global__ void __launch_bounds__(kGrThreads, 1)
             constexpr uint32_t kBox = S::kBoxCols * 128;
             const uint32_t bytes = PARTS * (S::kABytes + boxes * kBox);
             const int pa = WGRAD ? 0 : t.e;
-            if (lane == 0) {
-                for (int k = 0; k < t.klen; k += kGrBK) {
-                    if (!mbar_wait_spin<false>(empty0 + 8 * s, phase, tmo)) {
-                        timed_out = true;
-                        break;
-                    }
-                    // A pair's loads all arrive on the first CTA's barrier,
-                    // but for a slice with rows past the group's end that the
-                    // second CTA has to zero first.
-                    const bool own = !PAIR || (WGRAD && grouped_tail(t.klen - k));
-                    const uint32_t bar = (own ? full0 : bar0) + 8 * s;
-                    if (own || rank == 0) mbar_arrive_expect_tx(bar, own ? bytes : 2 * bytes);
+            for (int k = 0; k < t.klen; k += kGrBK) {
+                if (!mbar_wait_warp<false>(empty0 + 8 * s, phase, tmo)) {
+                    timed_out = true;
+                    break;
+                }
+                // A pair's loads all arrive on the first CTA's barrier, but
+                // for a slice with rows past the group's end that the second
+                // CTA has to zero first.
+                const bool own = !PAIR || (WGRAD && grouped_tail(t.klen - k));
+                const uint32_t bar = (own ? full0 : bar0) + 8 * s;
+                const uint32_t a = base + s * S::kStageBytes, b = baseB + s * S::kStageBytes;
+                const int kc = t.k0 + k;
+                if (issuer) {
+                    if (own)
+                        mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+                    else if (rank == 0)
+                        mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
                     auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
                         if constexpr (PAIR)
                             tma_load_3d_pair(dst, map, bar, x, y, z);
                         else
                             tma_load_3d(dst, map, bar, x, y, z);
                     };
-                    const uint32_t a = base + s * S::kStageBytes, b = baseB + s * S::kStageBytes;
-                    const int kc = t.k0 + k;
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         if constexpr (AMN) {
@@ -262,29 +375,31 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                         } else {
                             load(a + part * S::kABytes, &tmA, kc, f0, part * p.a_planes + pa);
                         }
-#pragma unroll 1
-                        for (int j = 0; j < boxes; ++j) {
-                            if constexpr (BMN)
-                                load(b + part * S::kBBytes + j * kBox, &tmB, c0 + S::kBoxCols * j, kc, part);
-                            else
-                                load(b + part * S::kBBytes + j * kBox, &tmB, kc, c0 + S::kBoxCols * j, part);
+#pragma unroll
+                        for (int j = 0; j < S::kCols / S::kBoxCols; ++j) {
+                            if (j < boxes) {
+                                if constexpr (BMN)
+                                    load(b + part * S::kBBytes + j * kBox, &tmB, c0 + S::kBoxCols * j, kc, part);
+                                else
+                                    load(b + part * S::kBBytes + j * kBox, &tmB, kc, c0 + S::kBoxCols * j, part);
+                            }
                         }
                     }
-                    ++issued;
-                    if (++s == S::kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++s == S::kStages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
-            timed_out = __any_sync(0xffffffffu, timed_out);
         }
         // (every copy lands before its CTA ends: the MMAs wait for it, and the
         // epilogue for them; after a timeout, the wait below, in the first CTA
         // for the pair)
-        if (timed_out && rank == 0 && lane == 0)
+        if (timed_out && rank == 0)
             for (int j = max(0, issued - S::kStages); j < issued; ++j)
-                (void)mbar_wait_spin<false>(full0 + 8 * (j % S::kStages), (j / S::kStages) & 1, tmo);
+                (void)mbar_wait_warp<false>(full0 + 8 * (j % S::kStages), (j / S::kStages) & 1, tmo);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         const uint64_t descA = AMN ? umma_desc_mnmajor_sw128(base, 64 * 128) : umma_desc_kmajor_sw128(base);
@@ -292,13 +407,21 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         // 16 k: 32 bytes of each row (K-major), 16 rows of 128 bytes (MN-major); addresses in units of 16
         constexpr uint32_t ka = AMN ? 128 : 2, kb = BMN ? 128 : 2;
         constexpr uint32_t pa = S::kABytes / 16, pb = S::kBBytes / 16;
-        const uint32_t peer_empty0 = PAIR ? map_shared_rank(empty0, 1) : 0;
-        const uint32_t peer_acc_full0 = PAIR ? map_shared_rank(acc_full0, 1) : 0;
-        const uint32_t lead_peer0 = PAIR ? map_shared_rank(peer0, 0) : 0;
+        const uint32_t peer_empty0 = PAIR ? warp_uniform(map_shared_rank(empty0, 1)) : 0;
+        const uint32_t peer_acc_full0 = PAIR ? warp_uniform(map_shared_rank(acc_full0, 1)) : 0;
+        const uint32_t lead_peer0 = PAIR ? warp_uniform(map_shared_rank(peer0, 0)) : 0;
+        const bool issuer = elect_one();
         uint32_t s = 0, phase = 0;
         uint32_t tails = 0;  // bit s: parity of the slices with rows to zero so far in stage s
         int unit = 0;        // accumulators filled
-        for (int i = cluster; !timed_out && grouped_tile<WGRAD, TN, FT>(p, i, cur, t); i += clusters) {
+        auto next = [&] {
+            if (++s == S::kStages) {
+                s = 0;
+                phase ^= 1;
+            }
+        };
+        while (!timed_out && tiles.next(t, tmo, timed_out)) {
+            if (rank != 0 && !WGRAD) continue;  // (the first CTA issues for both)
             const uint32_t idesc = p.idesc | static_cast<uint32_t>((t.cols + 15) >> 4) << 18;
             const bool tail = WGRAD && grouped_tail(t.klen % kGrBK ? t.klen % kGrBK : kGrBK);
             const int chunk = PARTS > 1 ? kGrChunk : t.klen;
@@ -312,40 +435,38 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                 auto slice = [&](int left) {
                     const uint32_t off = s * (S::kStageBytes / 16);
                     const uint64_t a = descA + off, b = descB + off;
+                    if (issuer) {
 #pragma unroll
-                    for (int kk = 0; kk < kGrBK / 16; ++kk) {
-                        if (left > kk * 16) {
-                            if constexpr (PARTS == 1) {
-                                umma_f16<CG>(acc, a + kk * ka, b + kk * kb, idesc, more);
-                            } else {
-                                auto mma = [&](uint32_t d, int i, int j, bool add) {
-                                    umma_f16<CG>(d, a + i * pa + kk * ka, b + j * pb + kk * kb, idesc, add);
-                                };
-                                mma(acc + TN, 2, 0, more);
-                                mma(acc + TN, 1, 1, true);
-                                mma(acc + TN, 0, 2, true);
-                                mma(acc + TN, 1, 0, true);
-                                mma(acc + TN, 0, 1, true);
-                                mma(acc, 0, 0, more);
+                        for (int kk = 0; kk < kGrBK / 16; ++kk) {
+                            if (left > kk * 16) {
+                                const bool add = more || kk > 0;
+                                if constexpr (PARTS == 1) {
+                                    umma_f16<CG>(acc, a + kk * ka, b + kk * kb, idesc, add);
+                                } else {
+                                    auto mma = [&](uint32_t d, int i, int j, bool sum) {
+                                        umma_f16<CG>(d, a + i * pa + kk * ka, b + j * pb + kk * kb, idesc, sum);
+                                    };
+                                    mma(acc + TN, 2, 0, add);
+                                    mma(acc + TN, 1, 1, true);
+                                    mma(acc + TN, 0, 2, true);
+                                    mma(acc + TN, 1, 0, true);
+                                    mma(acc + TN, 0, 1, true);
+                                    mma(acc, 0, 0, add);
+                                }
                             }
-                            more = true;
                         }
+                        umma_commit_cg<CG>(empty0 + 8 * s);
+                        if constexpr (PAIR) umma_commit_cg<CG>(peer_empty0 + 8 * s);
                     }
-                    umma_commit_cg<CG>(empty0 + 8 * s);
-                    if constexpr (PAIR) umma_commit_cg<CG>(peer_empty0 + 8 * s);
+                    __syncwarp();
+                    more = true;
                 };
-                auto next = [&] {
-                    if (++s == S::kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                };
-                if (rank == 0 && lane == 0) {
-                    if (unit >= 2 && !mbar_wait_spin<PAIR>(acc_empty0 + 8 * buf, ((unit >> 1) - 1) & 1, tmo))
+                if (rank == 0) {
+                    if (unit >= 2 && !mbar_wait_warp<PAIR>(acc_empty0 + 8 * buf, ((unit >> 1) - 1) & 1, tmo))
                         timed_out = true;
                     tc_fence_after_sync();
                     for (int q = k; q < plain && !timed_out; q += kGrBK) {
-                        if (!mbar_wait_spin<false>(full0 + 8 * s, phase, tmo)) {
+                        if (!mbar_wait_warp<false>(full0 + 8 * s, phase, tmo)) {
                             timed_out = true;
                             break;
                         }
@@ -353,18 +474,17 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                         slice(end - q);
                         next();
                     }
+                } else {
+                    for (int q = k; q < plain; q += kGrBK) next();
                 }
-                timed_out = __any_sync(0xffffffffu, timed_out);
                 if constexpr (WGRAD) {
-                    if (rank != 0 || lane != 0)
-                        for (int q = k; q < plain; q += kGrBK) next();
                     if (plain < end && !timed_out) {
                         // The last slice: rows left .. of its last instruction's
                         // 16 belong to others.  Zeros (rows of 128 bytes in
                         // blocks of 64 rows, A's and B's).
                         const int left = end - plain, past = (left + 15) & ~15;
                         const uint32_t full_phase = rank != 0 ? tails >> s & 1 : phase;
-                        if (!mbar_wait_spin<false>(full0 + 8 * s, full_phase, tmo)) timed_out = true;
+                        if (!mbar_wait_warp<false>(full0 + 8 * s, full_phase, tmo)) timed_out = true;
                         constexpr int blocks = S::kStageBytes / (64 * 128);
                         for (int j = lane; j < blocks * (past - left) * 8; j += 32) {
                             const int row = left + (j >> 3) % (past - left), b = (j >> 3) / (past - left);
@@ -373,38 +493,45 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && !timed_out) {
+                        if (!timed_out) {
                             if (rank != 0) {
-                                mbar_arrive_cluster(lead_peer0 + 8 * s);
+                                if (issuer) mbar_arrive_cluster(lead_peer0 + 8 * s);
+                                __syncwarp();
                             } else {
-                                if (PAIR && !mbar_wait_spin<true>(peer0 + 8 * s, tails >> s & 1, tmo)) timed_out = true;
+                                if (PAIR && !mbar_wait_warp<true>(peer0 + 8 * s, tails >> s & 1, tmo)) timed_out = true;
                                 tc_fence_after_sync();
                                 if (!timed_out) slice(left);
                             }
                         }
                         tails ^= 1u << s;
                         next();
-                        timed_out = __any_sync(0xffffffffu, timed_out);
                     }
                 }
-                if (rank == 0 && lane == 0 && !timed_out) {
+                if (timed_out) break;
+                if (rank == 0 && issuer) {
                     umma_commit_cg<CG>(acc_full0 + 8 * buf);
                     if constexpr (PAIR) umma_commit_cg<CG>(peer_acc_full0 + 8 * buf);
                 }
                 __syncwarp();
-                if (timed_out) break;
                 ++unit;
                 k = end;
             } while (k < t.klen);
         }
-        if (timed_out && rank == 0 && lane == 0) {  // the MMAs in flight end before tensor memory is freed
-            umma_commit_cg<CG>(acc_full0 + 8 * (unit & 1));
-            (void)mbar_wait_spin<false>(acc_full0 + 8 * (unit & 1), (unit >> 1) & 1, tmo);
+        if (timed_out && rank == 0) {  // the MMAs in flight end before tensor memory is freed
+            if (issuer) umma_commit_cg<CG>(acc_full0 + 8 * (unit & 1));
+            __syncwarp();
+            (void)mbar_wait_warp<false>(acc_full0 + 8 * (unit & 1), (unit >> 1) & 1, tmo);
         }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ schedule
+        GroupCursor cur = group_begin(p.offsets, p.T);
+        if (!sched_run(slots, sched0, cluster, clusters, tmo,
+                       [&](int i, GroupedTile& u) { return grouped_tile<WGRAD, TN, FT>(p, i, cur, u); }))
+            timed_out = true;
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
-        const uint32_t acc_empty_lead = PAIR && rank != 0 ? map_shared_rank(acc_empty0, 0) : acc_empty0;
+        const uint32_t acc_empty_lead = PAIR ? warp_uniform(map_shared_rank(acc_empty0, 0)) : acc_empty0;
         if (!WGRAD) {
             const int worker = static_cast<int>(blockIdx.x) * 4 + q, workers = static_cast<int>(gridDim.x) * 4;
             if (p.out_type == 0)
@@ -413,14 +540,13 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                 grouped_zero_rows<__half>(p, worker, workers);
         }
         int unit = 0;
-        for (int i = cluster; !timed_out && grouped_tile<WGRAD, TN, FT>(p, i, cur, t); i += clusters) {
-            const int f = t.f0 + rank * 128 + 32 * q + lane;
-            const int cols = f < p.F ? t.cols : 0;
+        while (!timed_out && tiles.next(t, tmo, timed_out)) {
+            const int f = t.f0 + rank * 128 + 32 * q;  // the warp's first feature
+            const uint32_t patch = patches + q * kGrPatchBytes;
             const long long out0 = (WGRAD ? t.e * p.so : 0ll) + t.c0 * p.ldo + f;
             auto wait = [&](uint32_t& acc) {
                 const int buf = unit & 1;
-                if (!__all_sync(0xffffffffu, mbar_wait_spin<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, tmo)))
-                    return false;
+                if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, tmo)) return false;
                 tc_fence_after_sync();
                 acc = tmem + static_cast<uint32_t>(buf * S::kAccCols) + (static_cast<uint32_t>(32 * q) << 16);
                 return true;
@@ -432,8 +558,9 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                     if (!PAIR || rank == 0)
                         mbar_arrive(acc_empty0 + 8 * (unit & 1));
                     else
-                        mbar_arrive_cluster(acc_empty_lead + 8 * (unit & 1));
+                        mbar_arrive_cluster_relaxed(acc_empty_lead + 8 * (unit & 1));
                 }
+                __syncwarp();
                 ++unit;
             };
             uint32_t acc;
@@ -444,13 +571,14 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                 }
                 for (int c = 0; c < t.cols; c += 32) {
                     uint32_t v[32];
+                    __syncwarp();
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
                     tmem_wait_ld();
                     if (WGRAD && t.klen == 0) {  // no MMA wrote the accumulator
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0;
                     }
-                    grouped_store_typed(p, out0 + c * p.ldo, v, cols - c);
+                    grouped_store_typed(p, patch, out0 + c * p.ldo, v, t.cols - c, p.F - f);
                 }
                 release();
             } else {
@@ -481,15 +609,18 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                 if (timed_out) break;
 #pragma unroll
                 for (int c = 0; c < TN; c += 32)
-                    if (c < t.cols) grouped_store_typed(p, out0 + c * p.ldo, sum + c, cols - c);
+                    if (c < t.cols) grouped_store_typed(p, patch, out0 + c * p.ldo, sum + c, t.cols - c, p.F - f);
+                __syncwarp();
             }
         }
     }
 
     if (timed_out) atomicOr(p.status, kGrStatusTimeout);
+    __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();  // nothing of the peer's is under way in this CTA's memory
+    __syncwarp();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_cg<CG>(tmem, S::kTmemCols);

@@ -35,6 +35,7 @@ struct Mxfp4TcParams {
     void* out;
     long long ldo;
     int out_type;
+    int vec_store;
     unsigned long long timeout_ns;
     unsigned int* status;
 };
@@ -48,28 +49,25 @@ struct Mxfp4Shape {
     static constexpr int kSbBlocks = (TN + 127) / 128;         // scale row blocks of the columns
     static constexpr int kSaBytes = 1024, kSbBytes = 1024 * kSbBlocks;
     static constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
-    static constexpr int kStages = (218 * 1024) / kStageBytes < 10 ? (218 * 1024) / kStageBytes : 10;
     static constexpr int kBoxCols = kCols < 64 ? kCols : 64;
     static constexpr int kAccs = TN > 128 ? 1 : 2;              // accumulators
     static constexpr int kScaleCol = kAccs * TN;                // tensor-memory column of the scales
-    static constexpr int kTmemUsed = kScaleCol + 2 * (4 + 4 * kSbBlocks);
+    static constexpr int kScaleCols = 2 * (4 + 4 * kSbBlocks);  // of a stage; two stages take turns
+    static constexpr int kTmemUsed = kScaleCol + 2 * kScaleCols;
     static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
     static constexpr int kEpilogueWarps = TN > 128 ? 8 : 4;
-    static constexpr int kThreads = 64 + 32 * kEpilogueWarps;
-    static constexpr int kBars = 2 * kStages + 4;               // full, empty; acc_full, acc_empty x 2
-    static constexpr int kSmem = kStages * kStageBytes + 8 * kBars + 16 + 1024;
+    static constexpr int kThreads = 96 + 32 * kEpilogueWarps;
+    static constexpr int kPatches = kEpilogueWarps * kGrPatchBytes;
+    static constexpr int kStages = kRing(kStageBytes, kPatches);
+    static constexpr int kBars = 2 * kStages + 4 + kSchedBars;  // full, empty; acc_full, acc_empty x 2
+    static constexpr int kSmem = kStages * kStageBytes + kPatches + kSchedBytes + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kStageBytes % 1024 == 0, "operand tiles start on the swizzle's 1024 bytes");
     static_assert(kTmemUsed <= 512, "tensor memory columns");
 };
 
-struct Mxfp4Tile {
-    int e, f0, c0, cols;
-    int srow;  // the first column's place among the scale blocks' rows
-};
-
 template <int TN, int FT>
-__device__ __forceinline__ bool mxfp4_tile(const Mxfp4TcParams& p, int i, GroupCursor& cur, Mxfp4Tile& t) {
+__device__ __forceinline__ bool mxfp4_tile(const Mxfp4TcParams& p, int i, GroupCursor& cur, GroupedTile& t) {
     int start = 0, end = p.T, local = i, block0 = 0, e = 0;
     if (p.offsets) {
         GroupHit h;
@@ -85,6 +83,8 @@ __device__ __forceinline__ bool mxfp4_tile(const Mxfp4TcParams& p, int i, GroupC
     t.f0 = local / n * FT;
     t.c0 = start + off;
     t.cols = min(TN, end - t.c0);
+    t.k0 = 0;
+    t.klen = p.K;
     t.srow = 128 * block0 + off;
     return true;
 }
@@ -100,13 +100,15 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t baseB = base + S::kABytes, baseSa = baseB + S::kBBytes, baseSb = baseSa + S::kSaBytes;
-    const uint32_t bars = base + S::kStages * S::kStageBytes;
+    const uint32_t patches = base + S::kStages * S::kStageBytes;
+    const uint32_t slots = patches + S::kPatches;
+    const uint32_t bars = slots + kSchedBytes;
     const uint32_t full0 = bars, empty0 = bars + 8 * S::kStages;
-    const uint32_t acc_full0 = bars + 16 * S::kStages, acc_empty0 = acc_full0 + 16;
+    const uint32_t acc_full0 = bars + 16 * S::kStages, acc_empty0 = acc_full0 + 16, sched0 = acc_empty0 + 16;
     const uint32_t tmem_slot = bars + 8u * S::kBars;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int rank = PAIR ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
     const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
     const unsigned long long tmo = p.timeout_ns;
 
@@ -119,10 +121,17 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
             mbar_init(acc_full0 + 8 * b, 1);
             mbar_init(acc_empty0 + 8 * b, S::kEpilogueWarps * CG);
         }
+        for (int j = 0; j < kSchedSlots; ++j) {
+            mbar_init(sched0 + 8 * j, 1);
+            mbar_init(sched0 + 8 * (kSchedSlots + j), 2 + S::kEpilogueWarps);
+        }
         fence_mbarrier_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmSa);
+        prefetch_tensormap(&tmSb);
     }
+    __syncwarp();
     if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, S::kTmemCols);
     tc_fence_before_sync();
     __syncthreads();
@@ -130,83 +139,90 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     tc_fence_after_sync();
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+    tmem = warp_uniform(tmem);
 
     bool timed_out = false;
-    GroupCursor cur = p.offsets ? group_begin(p.offsets, p.T) : GroupCursor();
-    Mxfp4Tile t;
+    GroupedTile t;
+    SchedReader tiles{slots, sched0};
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        const uint32_t bar0 = PAIR && rank != 0 ? map_shared_rank(full0, 0) : full0;
+        const uint32_t bar0 = PAIR ? warp_uniform(map_shared_rank(full0, 0)) : full0;
+        const bool issuer = elect_one();
         uint32_t s = 0, phase = 1;
         int issued = 0;
-        for (int i = cluster; !timed_out && mxfp4_tile<TN, FT>(p, i, cur, t); i += clusters) {
+        while (!timed_out && tiles.next(t, tmo, timed_out)) {
             const int mine = ((t.cols + 15) & ~15) / CG;
             const int c0 = t.c0 + rank * mine, f0 = t.f0 + rank * 128;
             const int boxes = (mine + S::kBoxCols - 1) / S::kBoxCols;
             constexpr uint32_t kBox = S::kBoxCols * 128;
             const uint32_t bytes = S::kABytes + boxes * kBox + S::kSaBytes + S::kSbBytes;
-            if (lane == 0) {
-                for (int k = 0; k < p.K; k += kMxBK) {
-                    if (!mbar_wait_spin<false>(empty0 + 8 * s, phase, tmo)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint32_t bar = bar0 + 8 * s;
-                    const uint32_t st = s * S::kStageBytes;
+            for (int k = 0; k < p.K; k += kMxBK) {
+                if (!mbar_wait_warp<false>(empty0 + 8 * s, phase, tmo)) {
+                    timed_out = true;
+                    break;
+                }
+                const uint32_t bar = bar0 + 8 * s;
+                const uint32_t st = s * S::kStageBytes;
+                if (issuer) {
                     auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
                         if constexpr (PAIR)
                             tma_load_3d_pair(dst, map, bar, x, y, z);
                         else
                             tma_load_3d(dst, map, bar, x, y, z);
                     };
-                    if (rank == 0) mbar_arrive_expect_tx(bar, CG * bytes);
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, CG * bytes);
                     load(base + st, &tmA, k >> 1, f0, t.e);
-#pragma unroll 1
-                    for (int j = 0; j < boxes; ++j)
-                        load(baseB + st + j * kBox, &tmB, k >> 1, c0 + S::kBoxCols * j, 0);
+#pragma unroll
+                    for (int j = 0; j < S::kCols / S::kBoxCols; ++j)
+                        if (j < boxes) load(baseB + st + j * kBox, &tmB, k >> 1, c0 + S::kBoxCols * j, 0);
                     // (words; the 8 scales of 256 k are 1024 bytes of 128 rows)
                     load(baseSa + st, &tmSa, k, f0 >> 7, t.e);
                     load(baseSb + st, &tmSb, k, t.srow >> 7, 0);
-                    ++issued;
-                    if (++s == S::kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++s == S::kStages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
-            timed_out = __any_sync(0xffffffffu, timed_out);
         }
-        if (timed_out && rank == 0 && lane == 0)
+        if (timed_out && rank == 0)  // (as in grouped_tc_kernel)
             for (int j = max(0, issued - S::kStages); j < issued; ++j)
-                (void)mbar_wait_spin<false>(full0 + 8 * (j % S::kStages), (j / S::kStages) & 1, tmo);
+                (void)mbar_wait_warp<false>(full0 + 8 * (j % S::kStages), (j / S::kStages) & 1, tmo);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         const uint64_t descA = umma_desc_kmajor_sw128(base), descB = umma_desc_kmajor_sw128(baseB);
         const uint64_t descSa = umma_desc_rows16(baseSa), descSb = umma_desc_rows16(baseSb);
-        const uint32_t sfa = tmem + S::kScaleCol, sfb = sfa + 8;
-        const uint32_t peer_empty0 = PAIR ? map_shared_rank(empty0, 1) : 0;
-        const uint32_t peer_acc_full0 = PAIR ? map_shared_rank(acc_full0, 1) : 0;
+        const uint32_t peer_empty0 = PAIR ? warp_uniform(map_shared_rank(empty0, 1)) : 0;
+        const uint32_t peer_acc_full0 = PAIR ? warp_uniform(map_shared_rank(acc_full0, 1)) : 0;
         // float32 accumulator, e2m1 x e2m1, e8m0 scales, M
         constexpr uint32_t kIdesc = 1u << 7 | 1u << 10 | 1u << 23 | static_cast<uint32_t>(FT / 16) << 24;
-        uint32_t s = 0, phase = 0;
+        const bool issuer = elect_one();
+        uint32_t s = 0, phase = 0, turn = 0;  // turn: the scale columns' half
         int unit = 0;
-        for (int i = cluster; !timed_out && mxfp4_tile<TN, FT>(p, i, cur, t); i += clusters, ++unit) {
+        while (!timed_out && tiles.next(t, tmo, timed_out)) {
+            if (rank != 0) continue;
             const int buf = unit % S::kAccs, round = unit / S::kAccs;
             const uint32_t acc = tmem + static_cast<uint32_t>(buf * TN);
             const uint32_t idesc = kIdesc | static_cast<uint32_t>((t.cols + 15) >> 4) << 18;
-            const uint32_t sb_col = sfb + ((t.srow & 127) >> 5);  // (32 rows of scales a column)
-            if (rank == 0 && lane == 0) {
-                if (round > 0 && !mbar_wait_spin<PAIR>(acc_empty0 + 8 * buf, (round - 1) & 1, tmo)) timed_out = true;
+            const uint32_t sb_shift = static_cast<uint32_t>((t.srow & 127) >> 5);  // (32 rows of scales a column)
+            if (round > 0 && !mbar_wait_warp<PAIR>(acc_empty0 + 8 * buf, (round - 1) & 1, tmo)) {
+                timed_out = true;
+                break;
+            }
+            tc_fence_after_sync();
+            for (int k = 0; k < p.K; k += kMxBK) {
+                if (!mbar_wait_warp<false>(full0 + 8 * s, phase, tmo)) {
+                    timed_out = true;
+                    break;
+                }
                 tc_fence_after_sync();
-                for (int k = 0; k < p.K && !timed_out; k += kMxBK) {
-                    if (!mbar_wait_spin<false>(full0 + 8 * s, phase, tmo)) {
-                        timed_out = true;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t off = s * (S::kStageBytes / 16);
-                    const uint64_t a = descA + off, b = descB + off, ca = descSa + off, cb = descSb + off;
-                    const int left = p.K - k;
+                const uint32_t off = s * (S::kStageBytes / 16);
+                const uint64_t a = descA + off, b = descB + off, ca = descSa + off, cb = descSb + off;
+                const uint32_t sfa = tmem + S::kScaleCol + turn * S::kScaleCols, sfb = sfa + 8;
+                const int left = p.K - k;
+                if (issuer) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 128 k: one scale block of each row block
                         if (left > 128 * h) {
@@ -214,44 +230,55 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
 #pragma unroll
                             for (int j = 0; j < S::kSbBlocks; ++j)
                                 tmem_cp_32x128b_x4<CG>(sfb + 4 * (S::kSbBlocks * h + j), cb + 64 * j + 32 * h);
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)  // 64 k: scales 0, 1 or 2, 3 of the block
-                                if (left > 128 * h + 64 * kk)
-                                    umma_mxf4<CG>(acc, a + 4 * h + 2 * kk, b + 4 * h + 2 * kk,
-                                                  idesc | (kk ? 2u << 4 | 2u << 29 : 0u), sfa + 4 * h,
-                                                  sb_col + 4 * S::kSbBlocks * h, k > 0 || h > 0 || kk > 0);
                         }
                     }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // 64 k: scales 0, 1 or 2, 3 of a block
+                        if (left > 64 * kk)
+                            umma_mxf4<CG>(acc, a + 2 * kk, b + 2 * kk, idesc | (kk & 1 ? 2u << 4 | 2u << 29 : 0u),
+                                          sfa + 4 * (kk >> 1), sfb + sb_shift + 4 * S::kSbBlocks * (kk >> 1),
+                                          k > 0 || kk > 0);
                     umma_commit_cg<CG>(empty0 + 8 * s);
                     if constexpr (PAIR) umma_commit_cg<CG>(peer_empty0 + 8 * s);
-                    if (++s == S::kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
                 }
-                if (!timed_out) {
-                    umma_commit_cg<CG>(acc_full0 + 8 * buf);
-                    if constexpr (PAIR) umma_commit_cg<CG>(peer_acc_full0 + 8 * buf);
+                __syncwarp();
+                turn ^= 1;
+                if (++s == S::kStages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
-            timed_out = __any_sync(0xffffffffu, timed_out);
             if (timed_out) break;
+            if (issuer) {
+                umma_commit_cg<CG>(acc_full0 + 8 * buf);
+                if constexpr (PAIR) umma_commit_cg<CG>(peer_acc_full0 + 8 * buf);
+            }
+            __syncwarp();
+            ++unit;
         }
-        if (timed_out && rank == 0 && lane == 0) {
+        if (timed_out && rank == 0) {
             const int buf = unit % S::kAccs, round = unit / S::kAccs;
-            umma_commit_cg<CG>(acc_full0 + 8 * buf);
-            (void)mbar_wait_spin<false>(acc_full0 + 8 * buf, round & 1, tmo);
+            if (issuer) umma_commit_cg<CG>(acc_full0 + 8 * buf);
+            __syncwarp();
+            (void)mbar_wait_warp<false>(acc_full0 + 8 * buf, round & 1, tmo);
         }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ schedule
+        GroupCursor cur = p.offsets ? group_begin(p.offsets, p.T) : GroupCursor();
+        if (!sched_run(slots, sched0, cluster, clusters, tmo,
+                       [&](int i, GroupedTile& u) { return mxfp4_tile<TN, FT>(p, i, cur, u); }))
+            timed_out = true;
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
         constexpr int kMine = TN / (S::kEpilogueWarps / 4);  // columns of this warp
-        const int mine0 = (warp - 2) / 4 * kMine;
-        const uint32_t acc_empty_lead = PAIR && rank != 0 ? map_shared_rank(acc_empty0, 0) : acc_empty0;
+        const int mine0 = (warp - 3) / 4 * kMine;
+        const uint32_t patch = patches + (warp - 3) * kGrPatchBytes;
+        const uint32_t acc_empty_lead = PAIR ? warp_uniform(map_shared_rank(acc_empty0, 0)) : acc_empty0;
         if (p.offsets) {
             GroupedTcParams z;  // (the fields that the zeroing reads)
             z.offsets = p.offsets, z.T = p.T, z.E = p.E, z.F = p.F, z.out = p.out, z.ldo = p.ldo;
-            const int worker = static_cast<int>(blockIdx.x) * S::kEpilogueWarps + warp - 2;
+            const int worker = static_cast<int>(blockIdx.x) * S::kEpilogueWarps + warp - 3;
             const int workers = static_cast<int>(gridDim.x) * S::kEpilogueWarps;
             if (p.out_type == 0)
                 grouped_zero_rows<float>(z, worker, workers);
@@ -259,12 +286,13 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
                 grouped_zero_rows<__half>(z, worker, workers);
         }
         int unit = 0;
-        for (int i = cluster; mxfp4_tile<TN, FT>(p, i, cur, t); i += clusters, ++unit) {
+        while (tiles.next(t, tmo, timed_out)) {
             const int buf = unit % S::kAccs, round = unit / S::kAccs;
-            if (!__all_sync(0xffffffffu, mbar_wait_spin<false>(acc_full0 + 8 * buf, round & 1, tmo))) {
+            if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, round & 1, tmo)) {
                 timed_out = true;
                 break;
             }
+            ++unit;
             tc_fence_after_sync();
             const uint32_t acc = tmem + static_cast<uint32_t>(buf * TN + mine0) + (static_cast<uint32_t>(32 * q) << 16);
             uint32_t v[kMine / 32][32];
@@ -278,31 +306,25 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
                 if (!PAIR || rank == 0)
                     mbar_arrive(acc_empty0 + 8 * buf);
                 else
-                    mbar_arrive_cluster(acc_empty_lead + 8 * buf);
+                    mbar_arrive_cluster_relaxed(acc_empty_lead + 8 * buf);
             }
-            const int f = t.f0 + rank * 128 + 32 * q + lane;
-            const int cols = (f < p.F ? t.cols : 0) - mine0;
-            void* const out = p.out;
+            __syncwarp();
+            const int f = t.f0 + rank * 128 + 32 * q;
             const long long at = static_cast<long long>(t.c0 + mine0) * p.ldo + f;
 #pragma unroll
-            for (int c = 0; c < kMine / 32; ++c) {
-                if (mine0 + 32 * c < t.cols) {
-                    const long long o = at + 32 * c * p.ldo;
-                    if (p.out_type == 0)
-                        grouped_store<float>(out, o, p.ldo, v[c], cols - 32 * c);
-                    else if (p.out_type == 1)
-                        grouped_store<__nv_bfloat16>(out, o, p.ldo, v[c], cols - 32 * c);
-                    else
-                        grouped_store<__half>(out, o, p.ldo, v[c], cols - 32 * c);
-                }
-            }
+            for (int c = 0; c < kMine / 32; ++c)
+                if (mine0 + 32 * c < t.cols)
+                    grouped_store_typed(p, patch, at + 32 * c * p.ldo, v[c], t.cols - mine0 - 32 * c, p.F - f);
+            __syncwarp();
         }
     }
 
     if (timed_out) atomicOr(p.status, kGrStatusTimeout);
+    __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();
+    __syncwarp();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_cg<CG>(tmem, S::kTmemCols);

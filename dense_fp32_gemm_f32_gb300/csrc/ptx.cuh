@@ -84,27 +84,55 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
     return ok != 0;
 }
 
-// Bounded wait that reads the global timer (slow next to a try_wait) only
-// once in 64 polls.  CLUSTER: phases that another CTA of the cluster completes.
+// Warp-uniform bounded wait: the whole converged warp polls and votes, so that
+// the code after it stays uniform (its values in uniform registers), and
+// reads the global timer (slow next to a try_wait) only once in 64 polls.
+// CLUSTER: phases that another CTA of the cluster completes by an arrival.
 template <bool CLUSTER>
-__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    auto ready = [&] {
+        return __all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) != 0;
+    };
+    if (ready()) return true;
     uint64_t t0 = 0;
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+            if (ready()) return true;
         const uint64_t t = global_timer_ns();
         if (t0 == 0)
             t0 = t;
-        else if (t - t0 > limit_ns)
+        else if (__any_sync(0xffffffffu, t - t0 > limit_ns))
             return false;
     }
 }
+
+// True in one lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// Lane 0's value, known to the compiler as the same in every lane.
+__device__ __forceinline__ int warp_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Arrival on the barrier at shared::cluster address `bar` (from
 // map_shared_rank), ordered after this thread's earlier accesses.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same without that order: for a thread whose earlier accesses the arrival
+// says nothing about (it has read tensor memory into registers), and which may
+// have global stores under way that a release would wait for.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ---------------------------------------------------------------- TMA
@@ -261,6 +289,18 @@ __device__ __forceinline__ float4 lds128(uint32_t addr) {
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(addr));
     return v;
+}
+
+__device__ __forceinline__ int4 lds128i(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts128i(uint32_t addr, int4 v) {
+    asm volatile("st.shared.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, float4 v) {

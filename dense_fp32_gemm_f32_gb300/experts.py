@@ -6,8 +6,6 @@ it is never read on the host, so no call here waits for the GPU.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib
@@ -22,57 +20,80 @@ def _type(dtype, name: str) -> int:
     return t
 
 
-def _cuda(X, name: str, dims, dtype=None) -> None:
+def _cuda(X, name: str, dim: int, dtype=None) -> int:
+    """Checks that X is a CUDA tensor of `dim` dimensions (and `dtype`); returns its device's number."""
     if not isinstance(X, torch.Tensor) or not X.is_cuda or (dtype is not None and X.dtype != dtype):
-        raise TypeError(f"{name} must be a CUDA {dtype or ''} tensor".replace("  ", " "))
-    if X.dim() not in dims:
-        raise ValueError(f"{name} must be {' or '.join(map(str, dims))}-D, got shape {tuple(X.shape)}")
+        raise TypeError(f"{name} must be a CUDA tensor" + (f" of {dtype}" if dtype is not None else ""))
+    if X.dim() != dim:
+        raise ValueError(f"{name} must be {dim}-D, got shape {tuple(X.shape)}")
+    return X.get_device()
 
 
-def _strides(X, name: str):
+def _strides(X, shape, name: str):
     """(row stride, matrix stride) of a 2-D or 3-D tensor with unit column stride."""
-    shape, st = X.shape, X.stride()
-    if shape[-1] > 1 and st[-1] != 1:
+    st = X.stride()
+    cols, rows = shape[-1], shape[-2]
+    if cols > 1 and st[-1] != 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = st[-2] if shape[-2] > 1 else shape[-1]
-    if ld < shape[-1]:
+    ld = st[-2] if rows > 1 else cols
+    if ld < cols:
         raise ValueError(f"{name} has overlapping rows")
-    se = st[0] if X.dim() == 3 and shape[0] > 1 else ld * shape[-2]
-    return ld, se
+    return ld, st[0] if len(shape) == 3 and shape[0] > 1 else ld * rows
 
 
-def _offsets(offsets, device, name="offsets") -> int:
-    _cuda(offsets, name, (1,), torch.int32)
-    if offsets.device != device:
+def _offsets(offsets, dev: int) -> int:
+    """Checks the boundaries; returns the number of experts."""
+    if _cuda(offsets, "offsets", 1, torch.int32) != dev:
+        raise ValueError("offsets is on another device")
+    n = offsets.shape[0]
+    if n < 1 or (n > 1 and offsets.stride(0) != 1):
+        raise ValueError("offsets must hold E + 1 contiguous boundaries")
+    return n - 1
+
+
+def _same_device(dev: int, X, name: str) -> None:
+    if X.get_device() != dev:
         raise ValueError(f"{name} is on another device")
-    if offsets.numel() < 1 or (offsets.numel() > 1 and offsets.stride(0) != 1):
-        raise ValueError(f"{name} must hold E + 1 contiguous boundaries")
-    return offsets.numel() - 1
 
 
-def _same_device(device, **tensors):
-    for name, X in tensors.items():
-        if X.device != device:
-            raise ValueError(f"{name} is on another device")
+# The current stream's handle without a Stream object around it, where this torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Makes ``device`` current, and ``stream`` too if given: outputs that a call
-    allocates belong to the stream that its kernels run on."""
-    if stream is not None:
-        with torch.cuda.device(device), torch.cuda.stream(stream):
-            yield int(stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            yield int(torch.cuda.current_stream().cuda_stream)
+class _On:
+    """Makes a call's device current, and its stream if one is given: outputs that the call allocates belong to the stream
+    that its kernels run on.  The value is the stream's handle.  Nothing is switched in the usual case, the current device
+    and stream (a switch costs as much as a launch)."""
+
+    __slots__ = ("dev", "stream", "undo")
+
+    def __init__(self, dev: int, stream):
+        self.dev, self.stream, self.undo = dev, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            self.undo = torch.cuda.stream(self.stream)  # (its device too)
+            self.undo.__enter__()
+            if torch.cuda.current_device() != self.dev:
+                self.__exit__(None, None, None)
+                raise ValueError("stream is on another device than the operands")
+            return int(self.stream.cuda_stream)
+        if torch.cuda.current_device() != self.dev:
+            self.undo = torch.cuda.device(self.dev)
+            self.undo.__enter__()
+        return _raw_stream(self.dev)
+
+    def __exit__(self, *exc):
+        if self.undo is not None:
+            self.undo.__exit__(*exc)
 
 
-def _out(out, shape, dtype, device, name="out"):
+def _out(out, like, shape, dtype, name="out"):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.device != device or tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+        return like.new_empty(shape, dtype=dtype)
+    if (not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != like.get_device()
+            or tuple(out.shape) != shape):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {like.device}")
     return out
 
 
@@ -83,23 +104,26 @@ def sgemm_grouped(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, out: 
     ``X`` is (T, K), sorted by expert; ``W`` is (E, K, N), or (E, N, K) with ``transw``; all of one type (float32,
     bfloat16, float16).  The gradient of the rows is the same call on the output's gradient with ``transw`` inverted.
     """
-    _cuda(X, "X", (2,))
-    _cuda(W, "W", (3,), X.dtype)
-    t = _type(X.dtype, "X")
-    T, K = X.shape
-    E, N = W.shape[0], W.shape[1 if transw else 2]
-    if W.shape[2 if transw else 1] != K:
-        raise ValueError(f"shapes do not multiply: {(T, K)} x op(W) of {tuple(W.shape)}, transw={bool(transw)}")
-    _same_device(X.device, W=W)
-    if _offsets(offsets, X.device) != E:
+    dev = _cuda(X, "X", 2)
+    dtype = X.dtype
+    _cuda(W, "W", 3, dtype)
+    t = _type(dtype, "X")
+    xs, ws = X.shape, W.shape
+    T, K = xs
+    E, N, KW = (ws[0], ws[1], ws[2]) if transw else (ws[0], ws[2], ws[1])
+    if KW != K:
+        raise ValueError(f"shapes do not multiply: {(T, K)} x op(W) of {tuple(ws)}, transw={bool(transw)}")
+    _same_device(dev, W, "W")
+    if _offsets(offsets, dev) != E:
         raise ValueError(f"offsets must hold {E + 1} boundaries, got {offsets.numel()}")
-    ldx, _ = _strides(X, "X")
-    ldw, sw = _strides(W, "W")
+    ldx = _strides(X, xs, "X")[0]
+    ldw, sw = _strides(W, ws, "W")
     lib = _lib.load()
-    with _on(X.device, stream) as s:
-        out = _out(out, (T, N), X.dtype, X.device)
-        rc = lib.sgemm_grouped(t, int(bool(transw)), T, E, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, sw,
-                               offsets.data_ptr(), out.data_ptr(), _strides(out, "out")[0], s)
+    with _On(dev, stream) as s:
+        shape = (T, N)
+        out = _out(out, X, shape, dtype)
+        rc = lib.sgemm_grouped(t, 1 if transw else 0, T, E, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, sw,
+                               offsets.data_ptr(), out.data_ptr(), _strides(out, shape, "out")[0], s)
     _lib.check(rc, "sgemm_grouped")
     return out
 
@@ -111,29 +135,35 @@ def sgemm_grouped_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor
     ``X`` is (T, K) and ``dY`` (T, N), of one type; ``dtype`` is that type (default) or float32.  For weights stored
     (E, N, K) swap ``X`` and ``dY``.
     """
-    _cuda(X, "X", (2,))
-    _cuda(dY, "dY", (2,), X.dtype)
+    dev = _cuda(X, "X", 2)
+    _cuda(dY, "dY", 2, X.dtype)
     t = _type(X.dtype, "X")
     dtype = dtype if dtype is not None else out.dtype if out is not None else X.dtype
     if dtype not in (X.dtype, torch.float32):
         raise TypeError(f"the gradient's type must be {X.dtype} or float32, got {dtype}")
-    (T, K), N = X.shape, dY.shape[1]
-    if dY.shape[0] != T:
-        raise ValueError(f"X has {T} rows, dY {dY.shape[0]}")
-    _same_device(X.device, dY=dY)
-    E = _offsets(offsets, X.device)
+    xs, ys = X.shape, dY.shape
+    (T, K), N = xs, ys[1]
+    if ys[0] != T:
+        raise ValueError(f"X has {T} rows, dY {ys[0]}")
+    _same_device(dev, dY, "dY")
+    E = _offsets(offsets, dev)
     lib = _lib.load()
-    with _on(X.device, stream) as s:
-        out = _out(out, (E, K, N), dtype, X.device)
-        ldo, so = _strides(out, "out")
-        rc = lib.sgemm_grouped_wgrad(t, _TYPES[dtype], T, E, K, N, X.data_ptr(), _strides(X, "X")[0], dY.data_ptr(),
-                                     _strides(dY, "dY")[0], offsets.data_ptr(), out.data_ptr(), ldo, so, s)
+    with _On(dev, stream) as s:
+        shape = (E, K, N)
+        out = _out(out, X, shape, dtype)
+        ldo, so = _strides(out, shape, "out")
+        rc = lib.sgemm_grouped_wgrad(t, _TYPES[dtype], T, E, K, N, X.data_ptr(), _strides(X, xs, "X")[0], dY.data_ptr(),
+                                     _strides(dY, ys, "dY")[0], offsets.data_ptr(), out.data_ptr(), ldo, so, s)
     _lib.check(rc, "sgemm_grouped_wgrad")
     return out
 
 
 def _blocks(rows: int) -> int:
     return (rows + 127) // 128
+
+
+def _grouped_blocks(rows: int, E: int) -> int:
+    return (rows + 127 * min(rows, E)) // 128
 
 
 def sgemm_mxfp4_quantize(X: torch.Tensor, offsets: torch.Tensor | None = None, *, codes: torch.Tensor | None = None,
@@ -144,51 +174,51 @@ def sgemm_mxfp4_quantize(X: torch.Tensor, offsets: torch.Tensor | None = None, *
     dimensions and 16 * ceil(K / 32) bytes a row; ``scales`` is uint8 (..., row blocks, ceil(K / 128), 32, 4, 4).
     With ``offsets`` the rows are grouped by expert, and every expert's rows begin a scale block.
     """
-    _cuda(X, "X", (2, 3))
+    dim = X.dim() if isinstance(X, torch.Tensor) and X.dim() == 3 else 2
+    dev = _cuda(X, "X", dim)
     t = _type(X.dtype, "X")
-    if offsets is not None and X.dim() != 2:
-        raise ValueError("rows grouped by expert must be 2-D")
-    lead, (rows, K) = tuple(X.shape[:-2]), X.shape[-2:]
-    batch = lead[0] if lead else 1
-    E = _offsets(offsets, X.device) if offsets is not None else 0
-    nb = (rows + 127 * min(rows, E)) // 128 if offsets is not None else _blocks(rows)
-    ldx, sx = _strides(X, "X")
+    shape = tuple(X.shape)
+    lead, (rows, K) = shape[:-2], shape[-2:]
+    E, nb = 0, _blocks(rows)
+    if offsets is not None:
+        if dim != 2:
+            raise ValueError("rows grouped by expert must be 2-D")
+        E = _offsets(offsets, dev)
+        nb = _grouped_blocks(rows, E)
+    ldx, sx = _strides(X, shape, "X")
     lib = _lib.load()
-    with _on(X.device, stream) as s:
-        codes = _out(codes, lead + (rows, 16 * ((K + 31) // 32)), torch.uint8, X.device, "codes")
-        scales = _out(scales, lead + (nb, _blocks(K), 32, 4, 4), torch.uint8, X.device, "scales")
-        _contiguous(codes=codes, scales=scales)
-        rc = lib.sgemm_mxfp4_quantize(t, batch, rows, K, X.data_ptr(), ldx, sx, E,
-                                      offsets.data_ptr() if offsets is not None else None, codes.data_ptr(),
+    with _On(dev, stream) as s:
+        codes = _out(codes, X, lead + (rows, 16 * ((K + 31) // 32)), torch.uint8, "codes")
+        scales = _out(scales, X, lead + (nb, _blocks(K), 32, 4, 4), torch.uint8, "scales")
+        _contiguous(codes, "codes")
+        _contiguous(scales, "scales")
+        rc = lib.sgemm_mxfp4_quantize(t, lead[0] if lead else 1, rows, K, X.data_ptr(), ldx, sx, E,
+                                      None if offsets is None else offsets.data_ptr(), codes.data_ptr(),
                                       scales.data_ptr(), s)
     _lib.check(rc, "sgemm_mxfp4_quantize")
     return codes, scales
 
 
-def _contiguous(**tensors):
-    for name, X in tensors.items():
-        if not X.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _contiguous(X, name: str) -> None:
+    if not X.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _mxfp4(codes, scales, name: str, dims, cols=None, E: int | None = None):
-    """Checks an MXFP4 operand; returns its (rows, 32 * blocks or ``cols``)."""
-    _cuda(codes, name, dims, torch.uint8)
-    _cuda(scales, f"{name}'s scales", (codes.dim() + 3,), torch.uint8)
-    _same_device(codes.device, **{f"{name}'s scales": scales})
-    _contiguous(**{name: codes, f"{name}'s scales": scales})
-    rows, K = codes.shape[-2], 2 * codes.shape[-1]
+def _mxfp4(codes, scales, name: str, dim: int, E: int | None = None):
+    """Checks an MXFP4 operand (rows grouped by E experts if E is given); returns (device, rows, 32 * blocks)."""
+    dev = _cuda(codes, name, dim, torch.uint8)
+    if _cuda(scales, f"{name}'s scales", dim + 3, torch.uint8) != dev:
+        raise ValueError(f"{name}'s scales are on another device")
+    _contiguous(codes, name)
+    _contiguous(scales, f"{name}'s scales")
+    shape = tuple(codes.shape)
+    rows, K = shape[-2], 2 * shape[-1]
     if K % 32:
-        raise ValueError(f"{name} must have 16 bytes for each block of 32 columns, got rows of {codes.shape[-1]} bytes")
-    nb = _blocks(rows) if E is None else (rows + 127 * min(rows, E)) // 128
-    shape = tuple(codes.shape[:-2]) + (nb, _blocks(K), 32, 4, 4)
-    if tuple(scales.shape) != shape:
-        raise ValueError(f"{name}'s scales must have shape {shape}, got {tuple(scales.shape)}")
-    if cols is not None:
-        if not 0 <= K - cols < 32:
-            raise ValueError(f"{name} holds {K - 31 if K else 0} to {K} columns, not {cols}")
-        K = cols
-    return rows, K
+        raise ValueError(f"{name} must have 16 bytes for each block of 32 columns, got rows of {shape[-1]} bytes")
+    want = shape[:-2] + (_blocks(rows) if E is None else _grouped_blocks(rows, E), _blocks(K), 32, 4, 4)
+    if tuple(scales.shape) != want:
+        raise ValueError(f"{name}'s scales must have shape {want}, got {tuple(scales.shape)}")
+    return dev, rows, K
 
 
 def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor | None = None, *,
@@ -199,16 +229,22 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
     if out is not None:
         dtype = out.dtype
     t = _type(dtype, "dtype")
-    _cuda(codes, "codes", (2, 3), torch.uint8)
-    E = _offsets(offsets, codes.device) if offsets is not None else 0
-    rows, K = _mxfp4(codes, scales, "codes", (2,) if offsets is not None else (2, 3), cols, E if offsets is not None else None)
-    batch = codes.shape[0] if codes.dim() == 3 else 1
+    dim = codes.dim() if isinstance(codes, torch.Tensor) and codes.dim() == 3 and offsets is None else 2
+    dev = _cuda(codes, "codes", dim, torch.uint8)
+    E = None if offsets is None else _offsets(offsets, dev)
+    _, rows, K = _mxfp4(codes, scales, "codes", dim, E)
+    if cols is not None:
+        if not 0 <= K - cols < 32:
+            raise ValueError(f"codes hold {max(K - 31, 0)} to {K} columns, not {cols}")
+        K = cols
+    shape = tuple(codes.shape[:-1]) + (K,)
     lib = _lib.load()
-    with _on(codes.device, stream) as s:
-        out = _out(out, tuple(codes.shape[:-1]) + (K,), dtype, codes.device)
-        ldy, sy = _strides(out, "out")
-        rc = lib.sgemm_mxfp4_dequantize(t, batch, rows, K, codes.data_ptr(), scales.data_ptr(), E,
-                                        offsets.data_ptr() if offsets is not None else None, out.data_ptr(), ldy, sy, s)
+    with _On(dev, stream) as s:
+        out = _out(out, codes, shape, dtype)
+        ldy, sy = _strides(out, shape, "out")
+        rc = lib.sgemm_mxfp4_dequantize(t, shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(), scales.data_ptr(),
+                                        E or 0, None if offsets is None else offsets.data_ptr(), out.data_ptr(), ldy,
+                                        sy, s)
     _lib.check(rc, "sgemm_mxfp4_dequantize")
     return out
 
@@ -216,18 +252,19 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
 def sgemm_mxfp4(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor,
                 out: torch.Tensor | None = None, *, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """``A @ B.T`` (M, N) of two MXFP4 matrices, A (M, K) and B (N, K), both quantised along K, as ``dtype``."""
-    M, K = _mxfp4(A, a_scales, "A", (2,))
-    N, KB = _mxfp4(B, b_scales, "B", (2,))
+    dev, M, K = _mxfp4(A, a_scales, "A", 2)
+    _, N, KB = _mxfp4(B, b_scales, "B", 2)
     if K != KB:
         raise ValueError(f"A's rows hold {K} columns, B's {KB}")
-    _same_device(A.device, B=B)
+    _same_device(dev, B, "B")
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
     lib = _lib.load()
-    with _on(A.device, stream) as s:
-        out = _out(out, (M, N), dtype, A.device)
+    with _On(dev, stream) as s:
+        shape = (M, N)
+        out = _out(out, A, shape, dtype)
         rc = lib.sgemm_mxfp4(t, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
-                             out.data_ptr(), _strides(out, "out")[0], s)
+                             out.data_ptr(), _strides(out, shape, "out")[0], s)
     _lib.check(rc, "sgemm_mxfp4")
     return out
 
@@ -237,20 +274,21 @@ def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor
                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """``out[t] = X[t] @ W[e].T`` for the rows of each expert, zeros for rows of none: X (T, K) quantised with the
     same ``offsets``, W (E, N, K) quantised along K."""
-    _cuda(X, "X", (2,), torch.uint8)
-    E = _offsets(offsets, X.device)
-    T, K = _mxfp4(X, x_scales, "X", (2,), E=E)
-    N, KW = _mxfp4(W, w_scales, "W", (3,))
+    dev = _cuda(X, "X", 2, torch.uint8)
+    E = _offsets(offsets, dev)
+    _, T, K = _mxfp4(X, x_scales, "X", 2, E)
+    _, N, KW = _mxfp4(W, w_scales, "W", 3)
     if K != KW or W.shape[0] != E:
         raise ValueError(f"X (columns {K}, {E} experts) and W ({tuple(W.shape)} bytes) do not match")
-    _same_device(X.device, W=W)
+    _same_device(dev, W, "W")
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
     lib = _lib.load()
-    with _on(X.device, stream) as s:
-        out = _out(out, (T, N), dtype, X.device)
+    with _On(dev, stream) as s:
+        shape = (T, N)
+        out = _out(out, X, shape, dtype)
         rc = lib.sgemm_mxfp4_grouped(t, T, E, N, K, X.data_ptr(), x_scales.data_ptr(), W.data_ptr(),
                                      w_scales.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                                     _strides(out, "out")[0], s)
+                                     _strides(out, shape, "out")[0], s)
     _lib.check(rc, "sgemm_mxfp4_grouped")
     return out
