@@ -90,7 +90,7 @@ class _On:
 
 def _out(out, like, shape, dtype, name="out"):
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)  # (like.new_empty takes 3 us longer)
     if (not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != like.get_device()
             or tuple(out.shape) != shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {like.device}")
