@@ -69,6 +69,12 @@ struct Mxfp4Call {
     long long ldo;
 };
 
+// Bytes (2 .. 16) that the rows of a 2-byte output are aligned to.
+inline int row_alignment(const void* out, long long ld, long long stride) {
+    const unsigned long long bits = reinterpret_cast<uintptr_t>(out) | 2ull * ld | 2ull * stride | 16;
+    return static_cast<int>(bits & (~bits + 1));
+}
+
 struct DeviceState;
 int mxfp4_tc_set_up();
 int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s);

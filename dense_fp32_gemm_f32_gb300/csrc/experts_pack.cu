@@ -16,6 +16,7 @@
 #include "../../include/sgemm_experts.h"
 #include "experts.h"
 #include "experts_groups.cuh"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace {
@@ -100,6 +101,7 @@ __device__ __forceinline__ void pack8(const PackJob& j, uint32_t id) {
 
 template <bool F32>
 __global__ void __launch_bounds__(256) pack_kernel(const PackJob a, const PackJob b, uint32_t na, uint32_t nb) {
+    grid_dependency_launch();
     const uint32_t id = blockIdx.x * 256 + threadIdx.x;
     if (id < na)
         pack8<F32>(a, id);

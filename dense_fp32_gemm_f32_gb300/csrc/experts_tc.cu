@@ -46,13 +46,17 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
     cfg.blockDim = dim3(kGrThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    // The kernel's set-up may run beside the end of the kernel before it (the
+    // quantiser, the operand copies): it reads global memory only after it has
+    // waited for that one.
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a, b, p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
@@ -152,8 +156,7 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     p.ctiles = c.wgrad ? static_cast<int>(ceil_div(c.C, tn)) : 0;
     p.a_planes = c.wgrad ? 1 : c.E;
     p.out = c.out, p.ldo = c.ldo, p.so = c.so, p.out_type = c.out_type;
-    p.vec_store = c.out_type != SGEMM_TYPE_F32 && (reinterpret_cast<uintptr_t>(c.out) & 15) == 0 && c.ldo % 8 == 0 &&
-                  c.so % 8 == 0;
+    p.align = row_alignment(c.out, c.ldo, c.so);
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
     const uint32_t fmt = f16 ? 0 : 1;

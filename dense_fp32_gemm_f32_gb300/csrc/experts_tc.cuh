@@ -77,7 +77,7 @@ struct GroupedTcParams {
     void* out;
     long long ldo, so;  // elements between rows; weight gradient: between experts
     int out_type;
-    int vec_store;      // 16-bit output with rows on the 16-byte grid
+    int align;          // 2-byte output: bytes that its rows are aligned to (2 .. 16)
     uint32_t idesc;     // instruction descriptor without the column count
     unsigned long long timeout_ns;
     unsigned int* status;
@@ -197,14 +197,13 @@ __device__ __forceinline__ bool grouped_tail(int left) { return left < kGrBK && 
 // (columns 0 .. n - 1; features below `features`).  Elements of 2 bytes stored
 // as they lie would be 64 bytes an instruction; so they pass through the
 // warp's own patch of shared memory (a column a row, 80 bytes apart so that
-// the 16-byte reads of neighbouring rows fall on other banks) and go out as
-// 16-byte stores, 8 rows an instruction.  Measured on 16 groups of 1024 rows,
-// 4096 x 4096 weight gradients (a tile every 16 ring stages): 533 us with 2-byte
-// stores.  Rows off the 16-byte grid, the last features of a width that is no
-// multiple of 8, and float32 (128 bytes an instruction already) go directly.
-template <typename T, typename V>
+// the reads of neighbouring rows fall on other banks) and go out in the
+// widest stores that the rows' alignment and the number of features allow, G
+// bytes a lane (16: 8 rows an instruction).  float32, 128 bytes an
+// instruction already, and odd rows of 2-byte elements go directly.
+template <int G, typename T, typename V>
 __device__ __forceinline__ void grouped_store(uint32_t patch, void* out, long long at, long long ld, const V* v, int n,
-                                              int features, bool vec) {
+                                              int features) {
     const int lane = threadIdx.x & 31;
     auto value = [&](int j) {
         if constexpr (__is_same(V, float))
@@ -212,36 +211,48 @@ __device__ __forceinline__ void grouped_store(uint32_t patch, void* out, long lo
         else
             return __uint_as_float(v[j]);
     };
-    if constexpr (sizeof(T) == 2) {
-        if (vec) {  // (warp-uniform)
-            T* o = static_cast<T*>(out) + at;
+    T* const o = static_cast<T*>(out) + at;
+    if constexpr (G > static_cast<int>(sizeof(T))) {
+        static_assert(sizeof(T) == 2, "2-byte elements");
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const T x = from_f32<T>(value(j));
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(patch + j * kGrPatchPitch + lane * 2),
-                             "h"(*reinterpret_cast<const unsigned short*>(&x))
-                             : "memory");
-            }
-            __syncwarp();
-            const int f = (lane & 3) * 8;
-            if (f < features) {
+        for (int j = 0; j < 32; ++j) {
+            const T x = from_f32<T>(value(j));
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(patch + j * kGrPatchPitch + lane * 2),
+                         "h"(*reinterpret_cast<const unsigned short*>(&x))
+                         : "memory");
+        }
+        __syncwarp();
+        constexpr int kLanes = 64 / G, kRows = 32 / kLanes;  // lanes a row, rows an instruction
+        const int f = lane % kLanes * (G / 2);
+        if (f < features) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    const int c = j + (lane >> 2);
-                    if (c < n)
-                        *reinterpret_cast<float4*>(o + c * ld + f) = lds128(patch + c * kGrPatchPitch + f * 2);
+            for (int j = 0; j < 32; j += kRows) {
+                const int c = j + lane / kLanes;
+                const uint32_t from = patch + c * kGrPatchPitch + f * 2;
+                if (c < n) {
+                    if constexpr (G == 16) {
+                        *reinterpret_cast<float4*>(o + c * ld + f) = lds128(from);
+                    } else if constexpr (G == 8) {
+                        uint2 w;
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(from) : "memory");
+                        *reinterpret_cast<uint2*>(o + c * ld + f) = w;
+                    } else {
+                        uint32_t w;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(from) : "memory");
+                        *reinterpret_cast<uint32_t*>(o + c * ld + f) = w;
+                    }
                 }
             }
-            __syncwarp();
-            return;
         }
-    }
-    T* o = static_cast<T*>(out) + at + lane;
-    if (lane >= features) n = 0;
+        __syncwarp();
+    } else {
+        T* d = o + lane;
+        if (lane >= features) n = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        if (j < n) *o = from_f32<T>(value(j));
-        o += ld;
+        for (int j = 0; j < 32; ++j) {
+            if (j < n) *d = from_f32<T>(value(j));
+            d += ld;
+        }
     }
 }
 
@@ -249,13 +260,25 @@ __device__ __forceinline__ void grouped_store(uint32_t patch, void* out, long lo
 template <typename P, typename V>
 __device__ __forceinline__ void grouped_store_typed(const P& p, uint32_t patch, long long at, const V* v, int n,
                                                     int features) {
-    const bool vec = p.vec_store && (features >= 32 || features % 8 == 0);
+    // p.align: bytes that every row of a 2-byte output is aligned to (2 .. 16)
+    auto half = [&](auto zero) {
+        using T = decltype(zero);
+        const int odd = features >= 32 ? 0 : features;  // (features past a store's width: narrower stores)
+        if (p.align == 16 && odd % 8 == 0)
+            grouped_store<16, T>(patch, p.out, at, p.ldo, v, n, features);
+        else if (p.align >= 8 && odd % 4 == 0)
+            grouped_store<8, T>(patch, p.out, at, p.ldo, v, n, features);
+        else if (p.align >= 4 && odd % 2 == 0)
+            grouped_store<4, T>(patch, p.out, at, p.ldo, v, n, features);
+        else
+            grouped_store<2, T>(patch, p.out, at, p.ldo, v, n, features);
+    };
     if (p.out_type == 0)
-        grouped_store<float>(patch, p.out, at, p.ldo, v, n, features, false);
+        grouped_store<4, float>(patch, p.out, at, p.ldo, v, n, features);
     else if (p.out_type == 1)
-        grouped_store<__nv_bfloat16>(patch, p.out, at, p.ldo, v, n, features, vec);
+        half(__nv_bfloat16());
     else
-        grouped_store<__half>(patch, p.out, at, p.ldo, v, n, features, vec);
+        half(__half());
 }
 
 // Rows of no expert: zeros, spread over the CTAs' epilogue warps.
@@ -326,6 +349,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
     tmem = warp_uniform(tmem);
+    grid_dependency_wait();  // the set-up above ran beside the end of the kernel before
 
     bool timed_out = false;
     GroupedTile t;

@@ -14,6 +14,7 @@
 #include "../../include/sgemm_experts.h"
 #include "experts.h"
 #include "experts_groups.cuh"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace {
@@ -197,6 +198,7 @@ __device__ __forceinline__ void quantize_row(const QuantParams& p, const Work& w
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) quantize_kernel(const QuantParams p) {
+    grid_dependency_launch();
     Work w;
     if (!find_work(p, w)) return;
     const T* row = static_cast<const T*>(p.X) + w.matrix * p.sx + w.row * p.ldx;

@@ -32,12 +32,17 @@ int launch(const CUtensorMap (&m)[4], const Mxfp4TcParams& p, long long tiles, c
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // The kernel's set-up may run beside the end of the kernel before it (the
+    // quantiser, the operand copies): it reads global memory only after it has
+    // waited for that one.
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, mxfp4_tc_kernel<TN, CG>, m[0], m[1], m[2], m[3], p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
@@ -56,7 +61,7 @@ int set_up() {
 }  // namespace
 
 int mxfp4_tc_set_up() {
-    if (set_up<32, 1>() || set_up<256, 2>()) {
+    if (set_up<64, 1>() || set_up<192, 2>()) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -64,34 +69,34 @@ int mxfp4_tc_set_up() {
 }
 
 int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s) {
-    const bool narrow = c.T <= 32ll * std::min(c.T, c.E);
-    const int tn = narrow ? 32 : 256, cg = narrow ? 1 : 2;
+    const bool narrow = c.T <= 64ll * std::min(c.T, c.E);
+    const int tn = narrow ? 64 : 192, cg = narrow ? 1 : 2;
     const long long kb = ceil_div(c.K, 32), kq = ceil_div(c.K, 128);
     Mxfp4TcParams p = {};
     p.offsets = c.offsets;
     p.T = c.T, p.E = c.E, p.F = c.N, p.K = static_cast<int>(32 * kb);
     p.ftiles = static_cast<int>(ceil_div(c.N, 128 * cg));
     p.out = c.out, p.ldo = c.ldo, p.out_type = c.out_type;
-    p.vec_store = c.out_type != SGEMM_TYPE_F32 && (reinterpret_cast<uintptr_t>(c.out) & 15) == 0 && c.ldo % 8 == 0;
+    p.align = row_alignment(c.out, c.ldo, 0);
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
     const long long tiles = (c.T / tn + std::min(c.T, c.E)) * static_cast<long long>(p.ftiles);
     if (tiles > 0x7fffffffll - 65536) return SGEMM_ERR_INVALID_ARG;
-    const int box = narrow ? 32 : 64;
     alignas(64) CUtensorMap m[4];
     int rc = encode_bytes(&m[0], c.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 16 * kb, c.N, c.E, 128, 128,
                           CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc == SGEMM_OK)
-        rc = encode_bytes(&m[1], c.X, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 16 * kb, c.T, 1, 128, box,
+        rc = encode_bytes(&m[1], c.X, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 16 * kb, c.T, 1, 128,
+                          narrow ? Mxfp4Shape<64, 1>::kBoxCols : Mxfp4Shape<192, 2>::kBoxCols,
                           CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc == SGEMM_OK)
         rc = encode_bytes(&m[2], c.w_scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, 128 * kq, ceil_div(c.N, 128), c.E, 256,
                           1, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc == SGEMM_OK)
         rc = encode_bytes(&m[3], c.x_scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, 128 * kq, c.x_blocks, 1, 256,
-                          narrow ? 1 : 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+                          narrow ? Mxfp4Shape<64, 1>::kSbBlocks : Mxfp4Shape<192, 2>::kSbBlocks, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc != SGEMM_OK) return rc;
-    return narrow ? launch<32, 1>(m, p, tiles, st, s) : launch<256, 2>(m, p, tiles, st, s);
+    return narrow ? launch<64, 1>(m, p, tiles, st, s) : launch<192, 2>(m, p, tiles, st, s);
 }
 
 }  // namespace detail

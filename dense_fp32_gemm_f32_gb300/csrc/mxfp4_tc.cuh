@@ -14,11 +14,12 @@
 // without a thread touching them.  An instruction takes 64 k and, through its descriptor, one half of the
 // 4 bytes.
 //
-// The wide tile (256 features x 256 columns a CTA pair) fills half of tensor
-// memory and the scales need some of the rest, so it has one accumulator; its 8
-// epilogue warps take it whole into registers before they store, and the next
-// tile's MMAs start after the reading (about 1/20 of the MMAs of K = 4096)
-// and not after the stores.
+// The wide tile has 192 columns and not 256: two accumulators of 256 would fill
+// tensor memory and leave the scales no room, and with one accumulator the
+// MMAs wait for the epilogue to empty it (1.5 us a tile: of 16384 rows, 8
+// experts of 8192 x 4096, 155 us; with 192 columns and two, @x).  Tiles are
+// multiples of 64 columns, so that a tile's scales begin 0 or 2 tensor-memory
+// columns into their block: B's scales have to begin at an even column.
 #pragma once
 
 #include "experts_tc.cuh"
@@ -35,7 +36,7 @@ struct Mxfp4TcParams {
     void* out;
     long long ldo;
     int out_type;
-    int vec_store;
+    int align;
     unsigned long long timeout_ns;
     unsigned int* status;
 };
@@ -46,24 +47,25 @@ struct Mxfp4Shape {
     static constexpr int kCols = TN / CG;
     static constexpr int kABytes = 128 * 128;
     static constexpr int kBBytes = kCols * 128;
-    static constexpr int kSbBlocks = (TN + 127) / 128;         // scale row blocks of the columns
+    static constexpr int kBoxCols = kCols / 2;                  // columns of a tensor-map box of B
+    // Scale row blocks of a tile's columns, which begin 0 or 64 rows into one.
+    static constexpr int kSbBlocks = (TN + 64 + 127) / 128;
     static constexpr int kSaBytes = 1024, kSbBytes = 1024 * kSbBlocks;
     static constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
-    static constexpr int kBoxCols = kCols < 64 ? kCols : 64;
-    static constexpr int kAccs = TN > 128 ? 1 : 2;              // accumulators
-    static constexpr int kScaleCol = kAccs * TN;                // tensor-memory column of the scales
-    static constexpr int kScaleCols = 2 * (4 + 4 * kSbBlocks);  // of a stage; two stages take turns
+    static constexpr int kScaleCol = 2 * TN;                       // tensor-memory column of the scales
+    static constexpr int kScaleCols = 2 * (4 + 4 * kSbBlocks);     // of a stage; two stages take turns
     static constexpr int kTmemUsed = kScaleCol + 2 * kScaleCols;
     static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-    static constexpr int kEpilogueWarps = TN > 128 ? 8 : 4;
-    static constexpr int kThreads = 96 + 32 * kEpilogueWarps;
-    static constexpr int kPatches = kEpilogueWarps * kGrPatchBytes;
+    static constexpr int kThreads = kGrThreads;
+    static constexpr int kPatches = 4 * kGrPatchBytes;
     static constexpr int kStages = kRing(kStageBytes, kPatches);
     static constexpr int kBars = 2 * kStages + 4 + kSchedBars;  // full, empty; acc_full, acc_empty x 2
     static constexpr int kSmem = kStages * kStageBytes + kPatches + kSchedBytes + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(kStageBytes % 1024 == 0, "operand tiles start on the swizzle's 1024 bytes");
+    static_assert(TN % 128 == 64 && kCols % 8 == 0 && kBoxCols % 8 == 0 && kCols % kBoxCols == 0, "tile");
+    static_assert(kStageBytes % 1024 == 0 && kBBytes % 1024 == 0, "operand tiles start on the swizzle's 1024 bytes");
     static_assert(kTmemUsed <= 512, "tensor memory columns");
+    static_assert(kBoxCols * 128 % 1024 == 0, "boxes start on the swizzle's 1024 bytes");
 };
 
 template <int TN, int FT>
@@ -117,13 +119,13 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
-        for (int b = 0; b < S::kAccs; ++b) {
+        for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, S::kEpilogueWarps * CG);
+            mbar_init(acc_empty0 + 8 * b, 4 * CG);
         }
         for (int j = 0; j < kSchedSlots; ++j) {
             mbar_init(sched0 + 8 * j, 1);
-            mbar_init(sched0 + 8 * (kSchedSlots + j), 2 + S::kEpilogueWarps);
+            mbar_init(sched0 + 8 * (kSchedSlots + j), 6);
         }
         fence_mbarrier_init();
         prefetch_tensormap(&tmA);
@@ -140,6 +142,7 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
     tmem = warp_uniform(tmem);
+    grid_dependency_wait();  // the set-up above ran beside the end of the kernel before
 
     bool timed_out = false;
     GroupedTile t;
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
         int unit = 0;
         while (!timed_out && tiles.next(t, tmo, timed_out)) {
             if (rank != 0) continue;
-            const int buf = unit % S::kAccs, round = unit / S::kAccs;
+            const int buf = unit & 1, round = unit >> 1;
             const uint32_t acc = tmem + static_cast<uint32_t>(buf * TN);
             const uint32_t idesc = kIdesc | static_cast<uint32_t>((t.cols + 15) >> 4) << 18;
             const uint32_t sb_shift = static_cast<uint32_t>((t.srow & 127) >> 5);  // (32 rows of scales a column)
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
             ++unit;
         }
         if (timed_out && rank == 0) {
-            const int buf = unit % S::kAccs, round = unit / S::kAccs;
+            const int buf = unit & 1, round = unit >> 1;
             if (issuer) umma_commit_cg<CG>(acc_full0 + 8 * buf);
             __syncwarp();
             (void)mbar_wait_warp<false>(acc_full0 + 8 * buf, round & 1, tmo);
@@ -271,15 +274,12 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
-        constexpr int kMine = TN / (S::kEpilogueWarps / 4);  // columns of this warp
-        const int mine0 = (warp - 3) / 4 * kMine;
-        const uint32_t patch = patches + (warp - 3) * kGrPatchBytes;
+        const uint32_t patch = patches + q * kGrPatchBytes;
         const uint32_t acc_empty_lead = PAIR ? warp_uniform(map_shared_rank(acc_empty0, 0)) : acc_empty0;
         if (p.offsets) {
             GroupedTcParams z;  // (the fields that the zeroing reads)
             z.offsets = p.offsets, z.T = p.T, z.E = p.E, z.F = p.F, z.out = p.out, z.ldo = p.ldo;
-            const int worker = static_cast<int>(blockIdx.x) * S::kEpilogueWarps + warp - 3;
-            const int workers = static_cast<int>(gridDim.x) * S::kEpilogueWarps;
+            const int worker = static_cast<int>(blockIdx.x) * 4 + q, workers = static_cast<int>(gridDim.x) * 4;
             if (p.out_type == 0)
                 grouped_zero_rows<float>(z, worker, workers);
             else
@@ -287,19 +287,23 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
         }
         int unit = 0;
         while (tiles.next(t, tmo, timed_out)) {
-            const int buf = unit % S::kAccs, round = unit / S::kAccs;
+            const int buf = unit & 1, round = unit >> 1;
             if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, round & 1, tmo)) {
                 timed_out = true;
                 break;
             }
             ++unit;
             tc_fence_after_sync();
-            const uint32_t acc = tmem + static_cast<uint32_t>(buf * TN + mine0) + (static_cast<uint32_t>(32 * q) << 16);
-            uint32_t v[kMine / 32][32];
-#pragma unroll
-            for (int c = 0; c < kMine / 32; ++c)
-                if (mine0 + 32 * c < t.cols) tmem_ld_32x32b_x32(acc + 32 * c, v[c]);
-            tmem_wait_ld();
+            const uint32_t acc = tmem + static_cast<uint32_t>(buf * TN) + (static_cast<uint32_t>(32 * q) << 16);
+            const int f = t.f0 + rank * 128 + 32 * q;
+            const long long at = static_cast<long long>(t.c0) * p.ldo + f;
+            for (int c = 0; c < t.cols; c += 32) {
+                uint32_t v[32];
+                __syncwarp();
+                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
+                tmem_wait_ld();
+                grouped_store_typed(p, patch, at + c * p.ldo, v, t.cols - c, p.F - f);
+            }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -308,13 +312,6 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
                 else
                     mbar_arrive_cluster_relaxed(acc_empty_lead + 8 * buf);
             }
-            __syncwarp();
-            const int f = t.f0 + rank * 128 + 32 * q;
-            const long long at = static_cast<long long>(t.c0 + mine0) * p.ldo + f;
-#pragma unroll
-            for (int c = 0; c < kMine / 32; ++c)
-                if (mine0 + 32 * c < t.cols)
-                    grouped_store_typed(p, patch, at + 32 * c * p.ldo, v[c], t.cols - mine0 - 32 * c, p.F - f);
             __syncwarp();
         }
     }

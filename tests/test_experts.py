@@ -99,6 +99,7 @@ SHAPES = [
     (777, 3, 1025, 255, [0, 256, 512, 777]),
     (1500, 3, 256, 640, [0, 700, 701, 1500]),
     (64, 70, 96, 80, [min(i, 64) for i in range(71)]),
+    (150, 8, 136, 288, [0, 0, 131, 132, 132, 140, 150, 150, 150]),
     (300, 40, 136, 256, [0] * 5 + [13 * i for i in range(23)] + [300] * 13),
 ]
 

@@ -168,7 +168,8 @@ def random_mxfp4(shape, seed, spread=6):
 
 
 PRODUCTS = [(1, 1, 1), (1, 128, 64), (5, 200, 96), (16, 136, 1056), (128, 128, 128), (129, 257, 65), (300, 520, 1000),
-            (256, 256, 4096), (700, 384, 544)]
+            (256, 256, 4096), (700, 384, 544),
+            (33, 130, 160), (64, 136, 288), (65, 128, 96), (193, 264, 352), (385, 72, 192)]
 
 
 @pytest.mark.gpu
@@ -217,7 +218,8 @@ def test_product_non_finite_rows_and_unused_scales():
 
 EXPERTS = [(1, 4, 128, 96, [0, 0, 1, 1, 1]), (20, 3, 200, 1024, [0, 3, 3, 20]), (300, 5, 264, 416, [0, 1, 1, 130, 259, 300]),
            (70, 3, 136, 65, [5, 10, 40, 60]), (200, 3, 128, 256, [0, 150, 20, 900]), (100, 2, 128, 64, [0, 0, 0]),
-           (800, 2, 640, 1152, [0, 300, 800]), (80, 40, 72, 160, [2 * i for i in range(41)])]
+           (800, 2, 640, 1152, [0, 300, 800]),
+           (150, 8, 136, 288, [0, 0, 131, 132, 132, 140, 150, 150, 150]), (500, 3, 200, 96, [0, 65, 258, 500]), (80, 40, 72, 160, [2 * i for i in range(41)])]
 
 
 @pytest.mark.gpu
