@@ -20,13 +20,20 @@ def _type(dtype, name: str) -> int:
     return t
 
 
-def _cuda(X, name: str, dim: int, dtype=None) -> int:
+# The checks below run before every launch, and a call's host time is what a
+# small product costs: they ask each tensor as little as they can.
+
+
+def _operand(X, name: str, dim: int, dtype=None) -> int:
     """Checks that X is a CUDA tensor of `dim` dimensions (and `dtype`); returns its device's number."""
-    if not isinstance(X, torch.Tensor) or not X.is_cuda or (dtype is not None and X.dtype != dtype):
+    if not isinstance(X, torch.Tensor) or (dtype is not None and X.dtype is not dtype):
         raise TypeError(f"{name} must be a CUDA tensor" + (f" of {dtype}" if dtype is not None else ""))
+    dev = X.get_device()
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor, got one on {X.device}")
     if X.dim() != dim:
         raise ValueError(f"{name} must be {dim}-D, got shape {tuple(X.shape)}")
-    return X.get_device()
+    return dev
 
 
 def _strides(X, shape, name: str):
@@ -43,7 +50,7 @@ def _strides(X, shape, name: str):
 
 def _offsets(offsets, dev: int) -> int:
     """Checks the boundaries; returns the number of experts."""
-    if _cuda(offsets, "offsets", 1, torch.int32) != dev:
+    if _operand(offsets, "offsets", 1, torch.int32) != dev:
         raise ValueError("offsets is on another device")
     n = offsets.shape[0]
     if n < 1 or (n > 1 and offsets.stride(0) != 1):
@@ -51,8 +58,8 @@ def _offsets(offsets, dev: int) -> int:
     return n - 1
 
 
-def _same_device(dev: int, X, name: str) -> None:
-    if X.get_device() != dev:
+def _same_device(dev: int, other: int, name: str) -> None:
+    if other != dev:
         raise ValueError(f"{name} is on another device")
 
 
@@ -60,41 +67,29 @@ def _same_device(dev: int, X, name: str) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-class _On:
-    """Makes a call's device current, and its stream if one is given: outputs that the call allocates belong to the stream
-    that its kernels run on.  The value is the stream's handle.  Nothing is switched in the usual case, the current device
-    and stream (a switch costs as much as a launch)."""
-
-    __slots__ = ("dev", "stream", "undo")
-
-    def __init__(self, dev: int, stream):
-        self.dev, self.stream, self.undo = dev, stream, None
-
-    def __enter__(self) -> int:
-        if self.stream is not None:
-            self.undo = torch.cuda.stream(self.stream)  # (its device too)
-            self.undo.__enter__()
-            if torch.cuda.current_device() != self.dev:
-                self.__exit__(None, None, None)
-                raise ValueError("stream is on another device than the operands")
-            return int(self.stream.cuda_stream)
-        if torch.cuda.current_device() != self.dev:
-            self.undo = torch.cuda.device(self.dev)
-            self.undo.__enter__()
-        return _raw_stream(self.dev)
-
-    def __exit__(self, *exc):
-        if self.undo is not None:
-            self.undo.__exit__(*exc)
+def _launch(dev: int, stream, call):
+    """``call(handle)`` with the operands' device current, and ``stream`` too if one is given: outputs that the call
+    allocates then belong to the stream that its kernels run on.  Nothing is switched in the usual case, the current
+    device and stream (a switch costs as much as a launch)."""
+    if stream is None:
+        if torch.cuda.current_device() == dev:
+            return call(_raw_stream(dev))
+        with torch.cuda.device(dev):
+            return call(_raw_stream(dev))
+    with torch.cuda.stream(stream):  # (its device too)
+        if torch.cuda.current_device() != dev:
+            raise ValueError("stream is on another device than the operands")
+        return call(int(stream.cuda_stream))
 
 
 def _out(out, like, shape, dtype, name="out"):
+    """(the output, its row stride): allocated beside `like`, or checked."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)  # (like.new_empty takes 3 us longer)
+        return torch.empty(shape, dtype=dtype, device=like.device), shape[-1]  # (like.new_empty takes 3 us longer)
     if (not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != like.get_device()
             or tuple(out.shape) != shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {like.device}")
-    return out
+    return out, _strides(out, shape, name)[0]
 
 
 def sgemm_grouped(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None, *,
@@ -104,28 +99,27 @@ def sgemm_grouped(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, out: 
     ``X`` is (T, K), sorted by expert; ``W`` is (E, K, N), or (E, N, K) with ``transw``; all of one type (float32,
     bfloat16, float16).  The gradient of the rows is the same call on the output's gradient with ``transw`` inverted.
     """
-    dev = _cuda(X, "X", 2)
+    dev = _operand(X, "X", 2)
     dtype = X.dtype
-    _cuda(W, "W", 3, dtype)
     t = _type(dtype, "X")
+    _same_device(dev, _operand(W, "W", 3, dtype), "W")
     xs, ws = X.shape, W.shape
     T, K = xs
     E, N, KW = (ws[0], ws[1], ws[2]) if transw else (ws[0], ws[2], ws[1])
     if KW != K:
         raise ValueError(f"shapes do not multiply: {(T, K)} x op(W) of {tuple(ws)}, transw={bool(transw)}")
-    _same_device(dev, W, "W")
     if _offsets(offsets, dev) != E:
         raise ValueError(f"offsets must hold {E + 1} boundaries, got {offsets.numel()}")
     ldx = _strides(X, xs, "X")[0]
     ldw, sw = _strides(W, ws, "W")
-    lib = _lib.load()
-    with _On(dev, stream) as s:
-        shape = (T, N)
-        out = _out(out, X, shape, dtype)
-        rc = lib.sgemm_grouped(t, 1 if transw else 0, T, E, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, sw,
-                               offsets.data_ptr(), out.data_ptr(), _strides(out, shape, "out")[0], s)
-    _lib.check(rc, "sgemm_grouped")
-    return out
+
+    def call(s):
+        y, ldy = _out(out, X, (T, N), dtype)
+        _lib.check(_lib.load().sgemm_grouped(t, 1 if transw else 0, T, E, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw,
+                                             sw, offsets.data_ptr(), y.data_ptr(), ldy, s), "sgemm_grouped")
+        return y
+
+    return _launch(dev, stream, call)
 
 
 def sgemm_grouped_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None, *,
@@ -135,8 +129,8 @@ def sgemm_grouped_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor
     ``X`` is (T, K) and ``dY`` (T, N), of one type; ``dtype`` is that type (default) or float32.  For weights stored
     (E, N, K) swap ``X`` and ``dY``.
     """
-    dev = _cuda(X, "X", 2)
-    _cuda(dY, "dY", 2, X.dtype)
+    dev = _operand(X, "X", 2)
+    _same_device(dev, _operand(dY, "dY", 2, X.dtype), "dY")
     t = _type(X.dtype, "X")
     dtype = dtype if dtype is not None else out.dtype if out is not None else X.dtype
     if dtype not in (X.dtype, torch.float32):
@@ -145,17 +139,18 @@ def sgemm_grouped_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor
     (T, K), N = xs, ys[1]
     if ys[0] != T:
         raise ValueError(f"X has {T} rows, dY {ys[0]}")
-    _same_device(dev, dY, "dY")
     E = _offsets(offsets, dev)
-    lib = _lib.load()
-    with _On(dev, stream) as s:
-        shape = (E, K, N)
-        out = _out(out, X, shape, dtype)
-        ldo, so = _strides(out, shape, "out")
-        rc = lib.sgemm_grouped_wgrad(t, _TYPES[dtype], T, E, K, N, X.data_ptr(), _strides(X, xs, "X")[0], dY.data_ptr(),
-                                     _strides(dY, ys, "dY")[0], offsets.data_ptr(), out.data_ptr(), ldo, so, s)
-    _lib.check(rc, "sgemm_grouped_wgrad")
-    return out
+    ldx, ldy = _strides(X, xs, "X")[0], _strides(dY, ys, "dY")[0]
+
+    def call(s):
+        dW, ldo = _out(out, X, (E, K, N), dtype)
+        so = _strides(dW, (E, K, N), "out")[1] if out is not None else K * N
+        _lib.check(_lib.load().sgemm_grouped_wgrad(t, _TYPES[dtype], T, E, K, N, X.data_ptr(), ldx, dY.data_ptr(), ldy,
+                                                   offsets.data_ptr(), dW.data_ptr(), ldo, so, s),
+                   "sgemm_grouped_wgrad")
+        return dW
+
+    return _launch(dev, stream, call)
 
 
 def _blocks(rows: int) -> int:
@@ -174,8 +169,8 @@ def sgemm_mxfp4_quantize(X: torch.Tensor, offsets: torch.Tensor | None = None, *
     dimensions and 16 * ceil(K / 32) bytes a row; ``scales`` is uint8 (..., row blocks, ceil(K / 128), 32, 4, 4).
     With ``offsets`` the rows are grouped by expert, and every expert's rows begin a scale block.
     """
-    dim = X.dim() if isinstance(X, torch.Tensor) and X.dim() == 3 else 2
-    dev = _cuda(X, "X", dim)
+    dim = 3 if isinstance(X, torch.Tensor) and X.dim() == 3 else 2
+    dev = _operand(X, "X", dim)
     t = _type(X.dtype, "X")
     shape = tuple(X.shape)
     lead, (rows, K) = shape[:-2], shape[-2:]
@@ -186,17 +181,20 @@ def sgemm_mxfp4_quantize(X: torch.Tensor, offsets: torch.Tensor | None = None, *
         E = _offsets(offsets, dev)
         nb = _grouped_blocks(rows, E)
     ldx, sx = _strides(X, shape, "X")
-    lib = _lib.load()
-    with _On(dev, stream) as s:
-        codes = _out(codes, X, lead + (rows, 16 * ((K + 31) // 32)), torch.uint8, "codes")
-        scales = _out(scales, X, lead + (nb, _blocks(K), 32, 4, 4), torch.uint8, "scales")
-        _contiguous(codes, "codes")
-        _contiguous(scales, "scales")
-        rc = lib.sgemm_mxfp4_quantize(t, lead[0] if lead else 1, rows, K, X.data_ptr(), ldx, sx, E,
-                                      None if offsets is None else offsets.data_ptr(), codes.data_ptr(),
-                                      scales.data_ptr(), s)
-    _lib.check(rc, "sgemm_mxfp4_quantize")
-    return codes, scales
+
+    def call(s):
+        c, _ = _out(codes, X, lead + (rows, 16 * ((K + 31) // 32)), torch.uint8, "codes")
+        f, _ = _out(scales, X, lead + (nb, _blocks(K), 32, 4, 4), torch.uint8, "scales")
+        if codes is not None:
+            _contiguous(c, "codes")
+        if scales is not None:
+            _contiguous(f, "scales")
+        _lib.check(_lib.load().sgemm_mxfp4_quantize(t, lead[0] if lead else 1, rows, K, X.data_ptr(), ldx, sx, E,
+                                                    None if offsets is None else offsets.data_ptr(), c.data_ptr(),
+                                                    f.data_ptr(), s), "sgemm_mxfp4_quantize")
+        return c, f
+
+    return _launch(dev, stream, call)
 
 
 def _contiguous(X, name: str) -> None:
@@ -206,11 +204,10 @@ def _contiguous(X, name: str) -> None:
 
 def _mxfp4(codes, scales, name: str, dim: int, E: int | None = None):
     """Checks an MXFP4 operand (rows grouped by E experts if E is given); returns (device, rows, 32 * blocks)."""
-    dev = _cuda(codes, name, dim, torch.uint8)
-    if _cuda(scales, f"{name}'s scales", dim + 3, torch.uint8) != dev:
-        raise ValueError(f"{name}'s scales are on another device")
+    dev = _operand(codes, name, dim, torch.uint8)
+    _same_device(dev, _operand(scales, "scales", dim + 3, torch.uint8), "scales")
     _contiguous(codes, name)
-    _contiguous(scales, f"{name}'s scales")
+    _contiguous(scales, "scales")
     shape = tuple(codes.shape)
     rows, K = shape[-2], 2 * shape[-1]
     if K % 32:
@@ -229,8 +226,8 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
     if out is not None:
         dtype = out.dtype
     t = _type(dtype, "dtype")
-    dim = codes.dim() if isinstance(codes, torch.Tensor) and codes.dim() == 3 and offsets is None else 2
-    dev = _cuda(codes, "codes", dim, torch.uint8)
+    dim = 3 if isinstance(codes, torch.Tensor) and codes.dim() == 3 and offsets is None else 2
+    dev = _operand(codes, "codes", dim, torch.uint8)
     E = None if offsets is None else _offsets(offsets, dev)
     _, rows, K = _mxfp4(codes, scales, "codes", dim, E)
     if cols is not None:
@@ -238,35 +235,37 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
             raise ValueError(f"codes hold {max(K - 31, 0)} to {K} columns, not {cols}")
         K = cols
     shape = tuple(codes.shape[:-1]) + (K,)
-    lib = _lib.load()
-    with _On(dev, stream) as s:
-        out = _out(out, codes, shape, dtype)
-        ldy, sy = _strides(out, shape, "out")
-        rc = lib.sgemm_mxfp4_dequantize(t, shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(), scales.data_ptr(),
-                                        E or 0, None if offsets is None else offsets.data_ptr(), out.data_ptr(), ldy,
-                                        sy, s)
-    _lib.check(rc, "sgemm_mxfp4_dequantize")
-    return out
+
+    def call(s):
+        y, ldy = _out(out, codes, shape, dtype)
+        sy = ldy * rows if out is None else _strides(y, shape, "out")[1]
+        _lib.check(_lib.load().sgemm_mxfp4_dequantize(t, shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(),
+                                                      scales.data_ptr(), E or 0,
+                                                      None if offsets is None else offsets.data_ptr(), y.data_ptr(),
+                                                      ldy, sy, s), "sgemm_mxfp4_dequantize")
+        return y
+
+    return _launch(dev, stream, call)
 
 
 def sgemm_mxfp4(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor,
                 out: torch.Tensor | None = None, *, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """``A @ B.T`` (M, N) of two MXFP4 matrices, A (M, K) and B (N, K), both quantised along K, as ``dtype``."""
     dev, M, K = _mxfp4(A, a_scales, "A", 2)
-    _, N, KB = _mxfp4(B, b_scales, "B", 2)
+    other, N, KB = _mxfp4(B, b_scales, "B", 2)
+    _same_device(dev, other, "B")
     if K != KB:
         raise ValueError(f"A's rows hold {K} columns, B's {KB}")
-    _same_device(dev, B, "B")
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
-    lib = _lib.load()
-    with _On(dev, stream) as s:
-        shape = (M, N)
-        out = _out(out, A, shape, dtype)
-        rc = lib.sgemm_mxfp4(t, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
-                             out.data_ptr(), _strides(out, shape, "out")[0], s)
-    _lib.check(rc, "sgemm_mxfp4")
-    return out
+
+    def call(s):
+        C, ldc = _out(out, A, (M, N), dtype)
+        _lib.check(_lib.load().sgemm_mxfp4(t, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
+                                           b_scales.data_ptr(), C.data_ptr(), ldc, s), "sgemm_mxfp4")
+        return C
+
+    return _launch(dev, stream, call)
 
 
 def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
@@ -274,21 +273,21 @@ def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor
                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """``out[t] = X[t] @ W[e].T`` for the rows of each expert, zeros for rows of none: X (T, K) quantised with the
     same ``offsets``, W (E, N, K) quantised along K."""
-    dev = _cuda(X, "X", 2, torch.uint8)
+    dev = _operand(X, "X", 2, torch.uint8)
     E = _offsets(offsets, dev)
     _, T, K = _mxfp4(X, x_scales, "X", 2, E)
-    _, N, KW = _mxfp4(W, w_scales, "W", 3)
+    other, N, KW = _mxfp4(W, w_scales, "W", 3)
+    _same_device(dev, other, "W")
     if K != KW or W.shape[0] != E:
         raise ValueError(f"X (columns {K}, {E} experts) and W ({tuple(W.shape)} bytes) do not match")
-    _same_device(dev, W, "W")
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
-    lib = _lib.load()
-    with _On(dev, stream) as s:
-        shape = (T, N)
-        out = _out(out, X, shape, dtype)
-        rc = lib.sgemm_mxfp4_grouped(t, T, E, N, K, X.data_ptr(), x_scales.data_ptr(), W.data_ptr(),
-                                     w_scales.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                                     _strides(out, shape, "out")[0], s)
-    _lib.check(rc, "sgemm_mxfp4_grouped")
-    return out
+
+    def call(s):
+        y, ldy = _out(out, X, (T, N), dtype)
+        _lib.check(_lib.load().sgemm_mxfp4_grouped(t, T, E, N, K, X.data_ptr(), x_scales.data_ptr(), W.data_ptr(),
+                                                   w_scales.data_ptr(), offsets.data_ptr(), y.data_ptr(), ldy, s),
+                   "sgemm_mxfp4_grouped")
+        return y
+
+    return _launch(dev, stream, call)
