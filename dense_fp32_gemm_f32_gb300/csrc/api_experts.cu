@@ -117,11 +117,11 @@ int sgemm_grouped_wgrad(int type, int out_type, int T, int E, int K, int N, cons
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return zero_rows(dW, E, K, N, lddw, stride_dw, osize, s);
     GroupedCall c = {};
-    c.a = {dY, 1, T, N, lddy, 0};
-    c.b = {X, 1, T, K, ldx, 0};
+    c.a = {X, 1, T, K, ldx, 0};
+    c.b = {dY, 1, T, N, lddy, 0};
     c.wgrad = c.a_mn = true;
     c.type = type, c.out_type = out_type;
-    c.T = T, c.E = E, c.F = N, c.C = K;
+    c.T = T, c.E = E, c.F = K, c.C = N;
     c.offsets = offsets;
     c.out = dW, c.ldo = lddw, c.so = stride_dw;
     return grouped_tc(c, dev, *st, s);

@@ -47,7 +47,7 @@ struct MatrixArg {
 
 // A grouped product as the tensor-core kernels take it (experts_tc.cuh):
 // forward: a = the weights (F the output's columns, K the contraction), b = X;
-// weight gradient: a = dY (F its columns), b = X (C its columns).
+// weight gradient: a = X (F its columns), b = dY (C its columns).
 struct GroupedCall {
     MatrixArg a, b;
     bool wgrad, a_mn;  // a_mn: the weights' contiguous dimension is F
@@ -69,9 +69,10 @@ struct Mxfp4Call {
     long long ldo;
 };
 
-// Bytes (2 .. 16) that the rows of a 2-byte output are aligned to.
-inline int row_alignment(const void* out, long long ld, long long stride) {
-    const unsigned long long bits = reinterpret_cast<uintptr_t>(out) | 2ull * ld | 2ull * stride | 16;
+// Bytes (2 .. 16) that the rows of an output of `size`-byte elements are
+// aligned to.
+inline int row_alignment(const void* out, int size, long long ld, long long stride) {
+    const unsigned long long bits = reinterpret_cast<uintptr_t>(out) | size * ld | size * stride | 16;
     return static_cast<int>(bits & (~bits + 1));
 }
 

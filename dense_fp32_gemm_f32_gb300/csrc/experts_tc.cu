@@ -43,7 +43,7 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
     const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG, PARTS>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, CG == 2 ? st.max_pairs : st.sm_count) * CG));
-    cfg.blockDim = dim3(kGrThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
     // The kernel's set-up may run beside the end of the kernel before it (the
@@ -95,7 +95,7 @@ int experts_tc_set_up(DeviceState& st) {
     // Pairs that fit the GPU at once: persistent kernels launch no more.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * st.sm_count);
-    cfg.blockDim = dim3(kGrThreads);
+    cfg.blockDim = dim3(GroupedShape<256, 2, 1>::kThreads);
     cfg.dynamicSmemBytes = GroupedShape<256, 2, 1>::kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -114,7 +114,7 @@ int experts_tc_set_up(DeviceState& st) {
 
 int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     const bool f32 = c.type == SGEMM_TYPE_F32, f16 = c.type == SGEMM_TYPE_F16;
-    // The first dimension of every operand as stored: A (W, or dY) and B (X).
+    // The first dimension of every operand as stored: A (W, or X) and B (X, or dY).
     const MatrixArg m[2] = {c.a, c.b};
     TcOperand o[2];
     PackJob job[2] = {};
@@ -156,7 +156,7 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     p.ctiles = c.wgrad ? static_cast<int>(ceil_div(c.C, tn)) : 0;
     p.a_planes = c.wgrad ? 1 : c.E;
     p.out = c.out, p.ldo = c.ldo, p.so = c.so, p.out_type = c.out_type;
-    p.align = row_alignment(c.out, c.ldo, c.so);
+    p.align = row_alignment(c.out, c.out_type == SGEMM_TYPE_F32 ? 4 : 2, c.ldo, c.so);
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
     const uint32_t fmt = f16 ? 0 : 1;

@@ -13,8 +13,12 @@
 //   forward     f = output column n, c = row t of the group, k: A = W_e
 //               (f innermost in HBM: MN-major), B = X (k innermost: K-major)
 //   transposed  the same with A = W_e stored N x K (K-major)
-//   gradient of the weights: f = n, c = k of X, contraction over the group's
-//               rows t: A = dY, B = X, both MN-major, read as stored
+//   gradient of the weights: f = row k of dW, c = its column n, contraction
+//               over the group's rows t: A = X, B = dY, both MN-major, read as
+//               stored.  (Nothing is ragged in f and c here, and a lane that
+//               holds a row's neighbouring elements packs them by itself: 164
+//               us the other way round, @w so, for 32 groups of 2 rows, 2048 x
+//               4096, bound by the epilogue.)
 //
 // float32 operands come as three bf16 parts each, x = x0 + x1 + x2 (8 bits
 // each, rounded to nearest: what is left is below 2^-25 |x|), and the sum runs
@@ -39,7 +43,7 @@
 //               boundary array alone (group_find: the host never needs the
 //               group sizes), handed to the other warps through shared memory
 //               a few tiles ahead;
-//   warps 3..6  epilogue: tensor memory -> registers -> HBM, while the MMAs of
+//   the others  epilogue: tensor memory -> registers -> HBM, while the MMAs of
 //               the next tile fill the other accumulator.
 //
 // The load and MMA warps' loops are uniform over the warp, with one elected
@@ -62,7 +66,6 @@
 namespace gb300 {
 
 constexpr int kGrBK = 64;                // contraction per ring stage (128 bytes of 16-bit values)
-constexpr int kGrThreads = 224;          // load, MMA and schedule warps, 4 epilogue warps
 constexpr unsigned int kGrStatusTimeout = 4u;  // the library's timeout bit
 
 // Contraction after which float32's accumulators go to registers.
@@ -71,20 +74,19 @@ constexpr int kGrChunk = 512;
 struct GroupedTcParams {
     const int* offsets;
     int T, E;
-    int F, C, K;        // features; weight gradient: columns; forward: contraction length
+    int F, C, K;        // features (weight gradient: rows of dW); its columns; forward: contraction length
     int ftiles, ctiles; // feature tiles; weight gradient: column tiles
     int a_planes;       // third coordinate of A's part p, expert e: p * a_planes + (weight gradient ? 0 : e)
     void* out;
     long long ldo, so;  // elements between rows; weight gradient: between experts
     int out_type;
-    int align;          // 2-byte output: bytes that its rows are aligned to (2 .. 16)
+    int align;          // bytes that the output's rows are aligned to (2 .. 16)
     uint32_t idesc;     // instruction descriptor without the column count
     unsigned long long timeout_ns;
     unsigned int* status;
 };
 
-constexpr int kGrPatchPitch = 80;  // an epilogue warp's patch: 32 rows of 64 bytes (grouped_store)
-constexpr int kGrPatchBytes = 32 * kGrPatchPitch;
+constexpr int kGrPatchBytes = 32 * 64;  // an epilogue warp's patch: 32 rows of 64 bytes
 
 constexpr int kSchedSlots = 4;  // tiles that the schedule warp is ahead
 constexpr int kSchedBytes = 32 * kSchedSlots, kSchedBars = 2 * kSchedSlots;
@@ -103,7 +105,11 @@ struct GroupedShape {
     static constexpr int kABytes = 128 * 128;        // a part: 128 features x 64 k
     static constexpr int kBBytes = kCols * 128;      // a part: the columns x 64 k
     static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
-    static constexpr int kPatches = PARTS > 1 ? 0 : 4 * kGrPatchBytes;  // the epilogue warps' (float32 output: none)
+    // Epilogue warps: two a quarter of the lanes for wide tiles, which short
+    // contractions (weight gradients of few rows) leave to the epilogue's speed.
+    static constexpr int kEpiWarps = PARTS == 1 && TN > 64 ? 8 : 4;
+    static constexpr int kThreads = 32 * (3 + kEpiWarps);
+    static constexpr int kPatches = kEpiWarps * kGrPatchBytes;
     static constexpr int kStages = kRing(PARTS * (kABytes + kBBytes), kPatches);
     static constexpr int kBoxCols = kCols < 64 ? kCols : 64;  // columns of a tensor-map box of B
     static constexpr int kAccCols = PARTS > 1 ? 2 * TN : TN;  // tensor-memory columns of one accumulator (pair)
@@ -193,92 +199,155 @@ struct SchedReader {
 // whose last instruction takes rows past that end.
 __device__ __forceinline__ bool grouped_tail(int left) { return left < kGrBK && (left & 15) != 0; }
 
-// A warp's 32 features x 32 columns, a feature a lane, to the output's rows
-// (columns 0 .. n - 1; features below `features`).  Elements of 2 bytes stored
-// as they lie would be 64 bytes an instruction; so they pass through the
-// warp's own patch of shared memory (a column a row, 80 bytes apart so that
-// the reads of neighbouring rows fall on other banks) and go out in the
-// widest stores that the rows' alignment and the number of features allow, G
-// bytes a lane (16: 8 rows an instruction).  float32, 128 bytes an
-// instruction already, and odd rows of 2-byte elements go directly.
-template <int G, typename T, typename V>
-__device__ __forceinline__ void grouped_store(uint32_t patch, void* out, long long at, long long ld, const V* v, int n,
-                                              int features) {
+// Byte `byte` of row `row` of a warp's patch.  The 16-byte pieces of a row trade
+// places by the row's number, so that 8 lanes a row apart and 8 lanes two rows
+// of 4 fall on all banks alike.
+__device__ __forceinline__ uint32_t patch_at(uint32_t patch, int row, int byte) {
+    return patch + static_cast<uint32_t>(row * 64 + ((((byte >> 4) ^ (row >> 1)) & 3) << 4) + (byte & 15));
+}
+
+// The patch's rows to the output's, G bytes a lane: rows 0 .. rows - 1 of `ld`
+// elements, columns below `cols`.
+template <int G, typename T>
+__device__ __forceinline__ void patch_store(uint32_t patch, T* o, long long ld, int rows, int cols) {
     const int lane = threadIdx.x & 31;
-    auto value = [&](int j) {
-        if constexpr (__is_same(V, float))
-            return v[j];
-        else
-            return __uint_as_float(v[j]);
-    };
-    T* const o = static_cast<T*>(out) + at;
-    if constexpr (G > static_cast<int>(sizeof(T))) {
-        static_assert(sizeof(T) == 2, "2-byte elements");
+    constexpr int kLanes = 64 / G, kRows = 32 / kLanes;  // lanes a row, rows an instruction
+    const int byte = lane % kLanes * G, col = byte / static_cast<int>(sizeof(T));
+    if (col < cols) {
+        T* d = o + (lane / kLanes) * ld + col;
+#pragma unroll
+        for (int j = 0; j < 32; j += kRows) {
+            const int r = j + lane / kLanes;
+            const uint32_t from = patch_at(patch, r, byte);
+            if (r < rows) {
+                if constexpr (G == 16) {
+                    *reinterpret_cast<float4*>(d) = lds128(from);
+                } else if constexpr (G == 8) {
+                    uint2 w;
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(from) : "memory");
+                    *reinterpret_cast<uint2*>(d) = w;
+                } else if constexpr (G == 4) {
+                    uint32_t w;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(from) : "memory");
+                    *reinterpret_cast<uint32_t*>(d) = w;
+                } else {
+                    unsigned short w;
+                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(from) : "memory");
+                    *reinterpret_cast<unsigned short*>(d) = w;
+                }
+            }
+            d += kRows * ld;
+        }
+    }
+}
+
+// The widest stores that the rows' alignment (`align` bytes, 2 .. 16) and the
+// number of columns allow.
+template <typename T>
+__device__ __forceinline__ void patch_store_any(uint32_t patch, int align, T* o, long long ld, int rows, int cols) {
+    constexpr int kAll = 64 / sizeof(T);
+    const int odd = (cols >= kAll ? 0 : cols) * static_cast<int>(sizeof(T));  // bytes of a row's last columns
+    if (align == 16 && odd % 16 == 0)
+        patch_store<16>(patch, o, ld, rows, cols);
+    else if (align >= 8 && odd % 8 == 0)
+        patch_store<8>(patch, o, ld, rows, cols);
+    else if (sizeof(T) == 4 || (align >= 4 && odd % 4 == 0))
+        patch_store<4>(patch, o, ld, rows, cols);
+    else
+        patch_store<2>(patch, o, ld, rows, cols);
+}
+
+template <typename V>
+__device__ __forceinline__ float as_f32(V v) {
+    if constexpr (__is_same(V, float))
+        return v;
+    else
+        return __uint_as_float(v);
+}
+
+// A warp's 32 features x 32 columns, a feature a lane, to the output's rows,
+// of which each column is one (columns 0 .. n - 1; features below `features`).
+// float32 goes out directly, 128 bytes an instruction; 2-byte elements would
+// be 64, so they pass through the patch.
+template <typename T, typename V>
+__device__ __forceinline__ void store_features(uint32_t patch, int align, T* o, long long ld, const V* v, int n,
+                                               int features) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            const T x = from_f32<T>(value(j));
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(patch + j * kGrPatchPitch + lane * 2),
+            const T x = from_f32<T>(as_f32(v[j]));
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(patch_at(patch, j, lane * 2)),
                          "h"(*reinterpret_cast<const unsigned short*>(&x))
                          : "memory");
         }
         __syncwarp();
-        constexpr int kLanes = 64 / G, kRows = 32 / kLanes;  // lanes a row, rows an instruction
-        const int f = lane % kLanes * (G / 2);
-        if (f < features) {
-#pragma unroll
-            for (int j = 0; j < 32; j += kRows) {
-                const int c = j + lane / kLanes;
-                const uint32_t from = patch + c * kGrPatchPitch + f * 2;
-                if (c < n) {
-                    if constexpr (G == 16) {
-                        *reinterpret_cast<float4*>(o + c * ld + f) = lds128(from);
-                    } else if constexpr (G == 8) {
-                        uint2 w;
-                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(from) : "memory");
-                        *reinterpret_cast<uint2*>(o + c * ld + f) = w;
-                    } else {
-                        uint32_t w;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(from) : "memory");
-                        *reinterpret_cast<uint32_t*>(o + c * ld + f) = w;
-                    }
-                }
-            }
-        }
+        patch_store_any(patch, align, o, ld, n, features);
         __syncwarp();
     } else {
         T* d = o + lane;
         if (lane >= features) n = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            if (j < n) *d = from_f32<T>(value(j));
+            if (j < n) *d = as_f32(v[j]);
             d += ld;
         }
     }
 }
 
-// `at`: the element of the first feature and column.
-template <typename P, typename V>
-__device__ __forceinline__ void grouped_store_typed(const P& p, uint32_t patch, long long at, const V* v, int n,
-                                                    int features) {
-    // p.align: bytes that every row of a 2-byte output is aligned to (2 .. 16)
-    auto half = [&](auto zero) {
+// A warp's 32 rows x 32 columns, a row a lane, to the output (rows 0 .. rows -
+// 1, columns below `cols`): through the patch, 64 bytes of each row at a time.
+template <typename T, typename V>
+__device__ __forceinline__ void store_rows(uint32_t patch, int align, T* o, long long ld, const V* v, int rows,
+                                           int cols) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kStep = 64 / sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 32; c += kStep) {
+        if (c < cols) {  // (warp-uniform)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 4) {
+                        w[j] = __float_as_uint(as_f32(v[c + 4 * i + j]));
+                    } else {
+                        const T lo = from_f32<T>(as_f32(v[8 * i + 2 * j])), hi = from_f32<T>(as_f32(v[8 * i + 2 * j + 1]));
+                        w[j] = *reinterpret_cast<const unsigned short*>(&lo) |
+                               static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(&hi)) << 16;
+                    }
+                }
+                sts128i(patch_at(patch, lane, 16 * i), make_int4(w[0], w[1], w[2], w[3]));
+            }
+            __syncwarp();
+            patch_store_any(patch, align, o + c, ld, rows, cols - c);
+            __syncwarp();
+        }
+    }
+}
+
+// `at`: the element of the first row and column.  ONLY_F32: the output is
+// (float32 operands).  ROWS: a lane holds a row of
+// the output (else a feature); n rows, `cols` columns are there.
+template <bool ROWS, bool ONLY_F32 = false, typename P, typename V>
+__device__ __forceinline__ void grouped_store(const P& p, uint32_t patch, long long at, const V* v, int n, int cols) {
+    auto typed = [&](auto zero) {
         using T = decltype(zero);
-        const int odd = features >= 32 ? 0 : features;  // (features past a store's width: narrower stores)
-        if (p.align == 16 && odd % 8 == 0)
-            grouped_store<16, T>(patch, p.out, at, p.ldo, v, n, features);
-        else if (p.align >= 8 && odd % 4 == 0)
-            grouped_store<8, T>(patch, p.out, at, p.ldo, v, n, features);
-        else if (p.align >= 4 && odd % 2 == 0)
-            grouped_store<4, T>(patch, p.out, at, p.ldo, v, n, features);
+        T* const o = static_cast<T*>(p.out) + at;
+        if constexpr (ROWS)
+            store_rows(patch, p.align, o, p.ldo, v, n, cols);
         else
-            grouped_store<2, T>(patch, p.out, at, p.ldo, v, n, features);
+            store_features(patch, p.align, o, p.ldo, v, n, cols);
     };
-    if (p.out_type == 0)
-        grouped_store<4, float>(patch, p.out, at, p.ldo, v, n, features);
-    else if (p.out_type == 1)
-        half(__nv_bfloat16());
-    else
-        half(__half());
+    if (ONLY_F32 || p.out_type == 0)
+        typed(0.f);
+    else if constexpr (!ONLY_F32) {
+        if (p.out_type == 1)
+            typed(__nv_bfloat16());
+        else
+            typed(__half());
+    }
 }
 
 // Rows of no expert: zeros, spread over the CTAs' epilogue warps.
@@ -299,7 +368,7 @@ __device__ void grouped_zero_rows(const GroupedTcParams& p, int worker, int work
 // AMN, BMN: the operand is MN-major in HBM and shared memory (else K-major);
 // both: a weight gradient.
 template <bool AMN, bool BMN, int TN, int CG, int PARTS>
-__global__ void __launch_bounds__(kGrThreads, 1)
+__global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const GroupedTcParams p) {
     using S = GroupedShape<TN, CG, PARTS>;
@@ -330,11 +399,11 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, 4 * CG);
+            mbar_init(acc_empty0 + 8 * b, S::kEpiWarps * CG);
         }
         for (int j = 0; j < kSchedSlots; ++j) {
             mbar_init(sched0 + 8 * j, 1);
-            mbar_init(sched0 + 8 * (kSchedSlots + j), 6);  // load, MMA and epilogue warps
+            mbar_init(sched0 + 8 * (kSchedSlots + j), 2 + S::kEpiWarps);  // load, MMA and epilogue warps
         }
         fence_mbarrier_init();
         prefetch_tensormap(&tmA);
@@ -510,11 +579,11 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                         const uint32_t full_phase = rank != 0 ? tails >> s & 1 : phase;
                         if (!mbar_wait_warp<false>(full0 + 8 * s, full_phase, tmo)) timed_out = true;
                         constexpr int blocks = S::kStageBytes / (64 * 128);
-                        for (int j = lane; j < blocks * (past - left) * 8; j += 32) {
-                            const int row = left + (j >> 3) % (past - left), b = (j >> 3) / (past - left);
-                            sts128(base + s * S::kStageBytes + static_cast<uint32_t>(b * 64 * 128 + row * 128 + (j & 7) * 16),
-                                   make_float4(0.f, 0.f, 0.f, 0.f));
-                        }
+                        for (int row = left + (lane >> 3); row < past; row += 4)
+#pragma unroll
+                            for (int b = 0; b < blocks; ++b)
+                                sts128(base + s * S::kStageBytes + static_cast<uint32_t>(b * 64 * 128 + row * 128 + (lane & 7) * 16),
+                                       make_float4(0.f, 0.f, 0.f, 0.f));
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (!timed_out) {
@@ -556,8 +625,10 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
         const uint32_t acc_empty_lead = PAIR ? warp_uniform(map_shared_rank(acc_empty0, 0)) : acc_empty0;
+        const int half = (warp - 3) >> 2;  // of the chunks of 32 columns, every second one each
         if (!WGRAD) {
-            const int worker = static_cast<int>(blockIdx.x) * 4 + q, workers = static_cast<int>(gridDim.x) * 4;
+            const int worker = static_cast<int>(blockIdx.x) * S::kEpiWarps + warp - 3;
+            const int workers = static_cast<int>(gridDim.x) * S::kEpiWarps;
             if (p.out_type == 0)
                 grouped_zero_rows<float>(p, worker, workers);
             else  // (bf16 and f16 zeros are the same bits)
@@ -565,9 +636,14 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         }
         int unit = 0;
         while (!timed_out && tiles.next(t, tmo, timed_out)) {
-            const int f = t.f0 + rank * 128 + 32 * q;  // the warp's first feature
-            const uint32_t patch = patches + q * kGrPatchBytes;
-            const long long out0 = (WGRAD ? t.e * p.so : 0ll) + t.c0 * p.ldo + f;
+            const int f = t.f0 + rank * 128 + 32 * q;  // the warp's first feature (weight gradient: row)
+            const uint32_t patch = patches + (warp - 3) * kGrPatchBytes;
+            auto store = [&](int c, const auto* v) {
+                if constexpr (WGRAD)
+                    grouped_store<true, (PARTS > 1)>(p, patch, t.e * p.so + f * p.ldo + t.c0 + c, v, p.F - f, t.cols - c);
+                else
+                    grouped_store<false, (PARTS > 1)>(p, patch, (t.c0 + c) * p.ldo + f, v, t.cols - c, p.F - f);
+            };
             auto wait = [&](uint32_t& acc) {
                 const int buf = unit & 1;
                 if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, tmo)) return false;
@@ -593,7 +669,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                     timed_out = true;
                     break;
                 }
-                for (int c = 0; c < t.cols; c += 32) {
+                for (int c = 32 * half; c < t.cols; c += 8 * S::kEpiWarps) {
                     uint32_t v[32];
                     __syncwarp();
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
@@ -602,7 +678,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0;
                     }
-                    grouped_store_typed(p, patch, out0 + c * p.ldo, v, t.cols - c, p.F - f);
+                    store(c, v);
                 }
                 release();
             } else {
@@ -633,7 +709,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                 if (timed_out) break;
 #pragma unroll
                 for (int c = 0; c < TN; c += 32)
-                    if (c < t.cols) grouped_store_typed(p, patch, out0 + c * p.ldo, sum + c, t.cols - c, p.F - f);
+                    if (c < t.cols) store(c, sum + c);
                 __syncwarp();
             }
         }

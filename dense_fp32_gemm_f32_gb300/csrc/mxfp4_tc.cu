@@ -77,7 +77,7 @@ int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s) {
     p.T = c.T, p.E = c.E, p.F = c.N, p.K = static_cast<int>(32 * kb);
     p.ftiles = static_cast<int>(ceil_div(c.N, 128 * cg));
     p.out = c.out, p.ldo = c.ldo, p.out_type = c.out_type;
-    p.align = row_alignment(c.out, c.ldo, 0);
+    p.align = row_alignment(c.out, c.out_type == SGEMM_TYPE_F32 ? 4 : 2, c.ldo, 0);
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
     const long long tiles = (c.T / tn + std::min(c.T, c.E)) * static_cast<long long>(p.ftiles);
