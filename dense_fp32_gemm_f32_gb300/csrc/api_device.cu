@@ -133,7 +133,7 @@ int init_device(int dev, DeviceState& st) {
         set_smem_attr(tf32x3_wide_kernel()) != SGEMM_OK || set_smem_attr(tf32x3_wide_pb_kernel()) != SGEMM_OK ||
         set_smem_attr(tf32x3_res_kernel()) != SGEMM_OK)
         return SGEMM_ERR_CUDA;
-    if (experts_tc_set_up(st) != SGEMM_OK || mxfp4_tc_set_up() != SGEMM_OK) return SGEMM_ERR_CUDA;
+    if (experts_tc_set_up(st) != SGEMM_OK || experts_few_set_up() != SGEMM_OK || mxfp4_tc_set_up() != SGEMM_OK) return SGEMM_ERR_CUDA;
     const KernelEntry ref = ffma_kernel_tma(4, kMathFfma2);
     st.max_clusters_split[1] = st.sm_count;
     for (int s = 2; s <= 8; ++s) st.max_clusters_split[s] = max_active_clusters(ref, 1, s);

@@ -81,6 +81,9 @@ int mxfp4_tc_set_up();
 int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s);
 int experts_tc_set_up(DeviceState& st);
 int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s);
+// Forward products of float32 operands with few rows a group (experts_few.cu).
+int experts_few_set_up();
+int grouped_few(const GroupedCall& c, const DeviceState& st, cudaStream_t s);
 
 }  // namespace detail
 }  // namespace gb300

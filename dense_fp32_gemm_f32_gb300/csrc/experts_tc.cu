@@ -10,6 +10,11 @@ namespace gb300 {
 namespace detail {
 namespace {
 
+// Rows an expert on average up to which float32 products run on the CUDA cores
+// (experts_few.cu).  Measured for 8 experts of 1024 x 2048, us there / by parts:
+// 4 12 / 48, 8 17 / 48, 16 32 / 48, 24 50 / 48 (transposed 15, 22, 41, 63).
+constexpr long long kFewRows = 18;
+
 // An operand as the tensor maps read it: 16-bit elements, third dimension the
 // matrices (and planes of parts).
 struct TcOperand {
@@ -64,12 +69,49 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
     return SGEMM_OK;
 }
 
+struct Tile {
+    int tn, cg;  // columns; CTAs that share a tile
+};
+
+// Tile of a product.  Measured on GB300, bf16, us for 128 columns a CTA / 128 a
+// pair / 256 a pair, by rows an expert on average (16 experts of 2048 x 2048):
+// 16 23.6 / 24.5 / 24.6, 64 24.2 / 25.3 / 26.3, 96 25.3 / 26.2 / 26.8, 128 29.4 /
+// 29.0 / 27.3, 256 40.1 / 37.6 / 35.1, 512 57.5 / 52.6 / 53.5; 8 experts of 4096
+// x 1024: 96 15.5 / 14.3 / 20.0, 256 26.8 / 26.8 / 24.5, 512 31.2 / 29.3 / 43.4.
+// So: single CTAs up to 96 rows an expert (the weights' bytes count, and more,
+// smaller tiles spread them more evenly), else pairs, with the width whose
+// rounds of tiles over the GPU come to fewer columns; half the width moves A
+// twice as often and has to save a quarter (16 experts of 4096 x 4096 and 16384
+// rows: 320 us for a pair's 128 columns, 293 for 256).  float32, whose stages
+// hold three parts of either operand, has 128 (64: 45 us instead of 39 for 2047
+// rows, 8 experts of 1025 x 1023, although that is two rounds of tiles).
+Tile choose_tile(const GroupedCall& c, const DeviceState& st) {
+    if (c.type == SGEMM_TYPE_F32) return {128, 2};
+    const long long groups = std::min(c.T, c.E);
+    if (!c.wgrad && c.T <= 96 * groups) return {128, 1};
+    const long long ft = ceil_div(c.F, 256);
+    auto columns = [&](int tn) {  // of one pair, over its rounds
+        const long long t = c.wgrad ? c.E * ceil_div(c.C, tn) : ceil_div(c.T, tn) + groups / 2;
+        return ceil_div(t * ft, st.max_pairs) * tn;
+    };
+    return {columns(128) * 13 < columns(256) * 10 ? 128 : 256, 2};
+}
+
 template <bool AMN, bool BMN, int TN, int CG, int PARTS>
 int set_up() {
     return cudaFuncSetAttribute(grouped_tc_kernel<AMN, BMN, TN, CG, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 GroupedShape<TN, CG, PARTS>::kSmem) == cudaSuccess
                ? SGEMM_OK
                : SGEMM_ERR_CUDA;
+}
+
+template <bool AMN>
+int launch_forward(const Tile& tile, bool f32, const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
+                   long long tiles, const DeviceState& st, cudaStream_t s) {
+    if (f32) return launch<AMN, false, 128, 2, 3>(a, b, p, tiles, st, s);
+    if (tile.cg == 1) return launch<AMN, false, 128, 1, 1>(a, b, p, tiles, st, s);
+    return tile.tn == 128 ? launch<AMN, false, 128, 2, 1>(a, b, p, tiles, st, s)
+                          : launch<AMN, false, 256, 2, 1>(a, b, p, tiles, st, s);
 }
 
 // Operands of one product copied into the library's pool for the length of
@@ -85,10 +127,10 @@ struct Packs {
 }  // namespace
 
 int experts_tc_set_up(DeviceState& st) {
-    if (set_up<true, false, 32, 1, 1>() || set_up<false, false, 32, 1, 1>() || set_up<true, false, 256, 2, 1>() ||
-        set_up<false, false, 256, 2, 1>() || set_up<true, true, 256, 2, 1>() || set_up<true, false, 32, 1, 3>() ||
-        set_up<false, false, 32, 1, 3>() || set_up<true, false, 128, 2, 3>() || set_up<false, false, 128, 2, 3>() ||
-        set_up<true, true, 128, 2, 3>()) {
+    if (set_up<true, false, 128, 1, 1>() || set_up<true, false, 128, 2, 1>() || set_up<true, false, 256, 2, 1>() ||
+        set_up<false, false, 128, 1, 1>() || set_up<false, false, 128, 2, 1>() || set_up<false, false, 256, 2, 1>() ||
+        set_up<true, true, 128, 2, 1>() || set_up<true, true, 256, 2, 1>() || set_up<true, false, 128, 2, 3>() ||
+        set_up<false, false, 128, 2, 3>() || set_up<true, true, 128, 2, 3>()) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -113,6 +155,11 @@ int experts_tc_set_up(DeviceState& st) {
 }
 
 int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
+    // (float32 with few rows an expert; where its grid would be too large, the parts)
+    if (c.type == SGEMM_TYPE_F32 && !c.wgrad && c.T <= kFewRows * std::min(c.T, c.E)) {
+        const int rc = grouped_few(c, st, s);
+        if (rc != SGEMM_ERR_UNSUPPORTED) return rc;
+    }
     const bool f32 = c.type == SGEMM_TYPE_F32, f16 = c.type == SGEMM_TYPE_F16;
     // The first dimension of every operand as stored: A (W, or X) and B (X, or dY).
     const MatrixArg m[2] = {c.a, c.b};
@@ -146,8 +193,8 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
         if (rc != SGEMM_OK) return rc;
     }
 
-    const bool narrow = !c.wgrad && c.T <= 32ll * std::min(c.T, c.E);
-    const int tn = narrow ? 32 : f32 ? 128 : 256, cg = narrow ? 1 : 2;
+    const Tile tile = choose_tile(c, st);
+    const int tn = tile.tn, cg = tile.cg;
     GroupedTcParams p = {};
     p.offsets = c.offsets;
     p.T = c.T, p.E = c.E;
@@ -167,20 +214,14 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     if (tiles > 0x7fffffffll - 65536) return SGEMM_ERR_INVALID_ARG;
     alignas(64) CUtensorMap ma, mb;
     int rc = encode_3d(&ma, o[0], f16, 64, c.a_mn ? 64 : 128);
-    if (rc == SGEMM_OK) rc = encode_3d(&mb, o[1], f16, 64, narrow ? 32 : 64);
+    if (rc == SGEMM_OK) rc = encode_3d(&mb, o[1], f16, 64, std::min(64, tn / cg));
     if (rc != SGEMM_OK) return rc;
     if (c.wgrad)
-        return f32 ? launch<true, true, 128, 2, 3>(ma, mb, p, tiles, st, s)
-                   : launch<true, true, 256, 2, 1>(ma, mb, p, tiles, st, s);
-    if (c.a_mn)
-        return f32 ? narrow ? launch<true, false, 32, 1, 3>(ma, mb, p, tiles, st, s)
-                            : launch<true, false, 128, 2, 3>(ma, mb, p, tiles, st, s)
-               : narrow ? launch<true, false, 32, 1, 1>(ma, mb, p, tiles, st, s)
-                        : launch<true, false, 256, 2, 1>(ma, mb, p, tiles, st, s);
-    return f32 ? narrow ? launch<false, false, 32, 1, 3>(ma, mb, p, tiles, st, s)
-                        : launch<false, false, 128, 2, 3>(ma, mb, p, tiles, st, s)
-           : narrow ? launch<false, false, 32, 1, 1>(ma, mb, p, tiles, st, s)
-                    : launch<false, false, 256, 2, 1>(ma, mb, p, tiles, st, s);
+        return f32         ? launch<true, true, 128, 2, 3>(ma, mb, p, tiles, st, s)
+               : tn == 128 ? launch<true, true, 128, 2, 1>(ma, mb, p, tiles, st, s)
+                           : launch<true, true, 256, 2, 1>(ma, mb, p, tiles, st, s);
+    return c.a_mn ? launch_forward<true>(tile, f32, ma, mb, p, tiles, st, s)
+                  : launch_forward<false>(tile, f32, ma, mb, p, tiles, st, s);
 }
 
 }  // namespace detail

@@ -293,6 +293,12 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- shared memory
 
 __device__ __forceinline__ float4 lds128(uint32_t addr) {
