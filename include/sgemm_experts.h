@@ -21,8 +21,11 @@
  * Entry points that may allocate device memory from the library's
  * stream-ordered pool (see sgemm.h), freed in stream order at the end of the
  * call, and those that never do:
- *   EXPERTS-ALLOCATING: sgemm_grouped sgemm_grouped_wgrad sgemm_mxfp4 sgemm_mxfp4_grouped
- *   EXPERTS-NON-ALLOCATING: sgemm_mxfp4_quantize sgemm_mxfp4_dequantize
+ *   EXPERTS-ALLOCATING: sgemm_grouped sgemm_grouped_wgrad
+ *   EXPERTS-NON-ALLOCATING: sgemm_mxfp4_quantize sgemm_mxfp4_dequantize sgemm_mxfp4 sgemm_mxfp4_grouped
+ * (16-bit operands whose base or rows are off the 16-byte grid are copied into
+ * pitched rows, float32 operands into three bf16 parts, 6 bytes an element,
+ * but for forward products of few rows an expert.)
  */
 #ifndef GB300_SGEMM_EXPERTS_H
 #define GB300_SGEMM_EXPERTS_H
@@ -100,8 +103,9 @@ int sgemm_grouped_wgrad(int type, int out_type, int T, int E, int K, int N,
  * ceil(R / 128) x ceil(K / 128) blocks is byte
  *     ((r / 128) * ceil(K / 128) + b / 4) * 512 + (r % 32) * 16
  *         + (r % 128 / 32) * 4 + b % 4.
- * 16-byte aligned.  Scales of rows and columns beyond the matrix are present
- * and ignored where their codes are (the quantiser writes zeros there).
+ * 16-byte aligned.  Scales of rows beyond the matrix are present and may hold
+ * anything; those of columns beyond it, anything but 255 (the quantiser writes
+ * zeros).
  * Rows grouped by expert: every expert's rows begin a new block of 128 (the
  * experts' blocks follow one another, none for an expert without rows), so
  * that T rows take at most (T + 127 min(T, E)) / 128 row blocks.
@@ -113,7 +117,8 @@ int sgemm_grouped_wgrad(int type, int out_type, int T, int E, int K, int N,
  * For each block, m = its largest magnitude, s = max(floor(log2 m) - 2, -127):
  * scale byte s + 127 (0 for a block of zeros), codes x * 2^-s rounded to
  * nearest, ties to the even code, magnitudes beyond 6 to 6.  A block with an
- * infinity or a NaN gets the scale byte 255, which stands for NaN.
+ * infinity or a NaN gets the scale byte 255, with which all its values stand
+ * for NaN, whatever their codes.
  *   type       of X
  *   batch, rows, K   X is `batch` matrices of rows x K, stride_x apart
  *   E, offsets NULL: each matrix has scale blocks of its own.  Otherwise

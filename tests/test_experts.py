@@ -398,3 +398,86 @@ def test_header_states_which_entry_points_allocate():
     code = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     declared = re.findall(r"^\s*int\s+(sgemm_\w+)\s*\(", code, flags=re.M)
     assert sorted(listed[0] + listed[1]) == sorted(declared)
+
+
+@pytest.fixture(autouse=True)
+def no_wait_gave_up(request):
+    """After every GPU test: no kernel abandoned a bounded wait."""
+    yield
+    if request.node.get_closest_marker("gpu"):
+        assert g.check_status() == 0
+
+
+# Sizes at which the rule on tiles takes each of them: many tiles of 256 columns, few of 128, single CTAs; float32
+# with few rows an expert, its contraction split over CTAs.
+TILES = [
+    (3000, 4, 136, 1024, [0, 700, 1500, 2999, 3000]),
+    (800, 4, 264, 520, [0, 200, 401, 600, 800]),
+    (200, 3, 1200, 392, [0, 60, 61, 200]),
+    (5, 1, 2100, 300, [0, 5]),
+    (12, 2, 4100, 136, [0, 3, 12]),
+    (100, 4, 2052, 520, [0, 0, 9, 60, 100]),
+]
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("transw", [False, True])
+@pytest.mark.parametrize("shape", TILES, ids=lambda s: "x".join(map(str, s[:4])))
+def test_forward_every_tile(shape, transw, dtype):
+    T, E, K, N, offsets = shape
+    X, W = operands(T, E, K, N, dtype, 21, transw)
+    exact, bound = forward64(X, W, offsets, transw)
+    check(g.sgemm_grouped(X, W, dev(offsets), transw=transw), exact, bound)
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("shape", [(300, 4, 520, 1100, [0, 64, 128, 299, 300]), (2000, 2, 256, 384, [0, 1990, 2000])],
+                         ids=lambda s: "x".join(map(str, s[:4])))
+def test_wgrad_every_tile(shape, dtype):
+    T, E, K, N, offsets = shape
+    X, _ = operands(T, E, K, N, dtype, 22)
+    dY = torch.randn((T, N), device="cuda").to(dtype)
+    check(g.sgemm_grouped_wgrad(X, dY, dev(offsets)), *wgrad64(X, dY, offsets, E))
+
+
+@pytest.mark.gpu
+@typed([torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad", [1, 2, 4, 8])
+def test_output_rows_of_every_alignment(pad, dtype):
+    """Outputs whose rows are aligned to 2, 4, 8 and 16 bytes, and whose widths end at every part of a store; nothing past
+    a row's end is written."""
+    T, E, K, offsets = 150, 2, 72, [0, 70, 150]
+    for N in (33, 34, 36, 40, 64, 129):
+        X, W = operands(T, E, K, N, dtype, 23)
+        out = padded(torch.zeros((T, N), dtype=dtype, device="cuda"), pad)
+        check(g.sgemm_grouped(X, W, dev(offsets), out), *forward64(X, W, offsets))
+        dY = torch.randn((T, N), device="cuda").to(dtype)
+        dw = padded(torch.zeros((E, K, N), dtype=dtype, device="cuda"), pad)
+        check(g.sgemm_grouped_wgrad(X, dY, dev(offsets), dw), *wgrad64(X, dY, offsets, E))
+        for v in (out, dw):
+            store = torch.empty(0, dtype=dtype, device="cuda").set_(v.untyped_storage(), 0, (v.untyped_storage().nbytes() // v.element_size(),), (1,))
+            assert int(store.isnan().sum()) == v.numel() // N * pad, N
+
+
+@pytest.mark.gpu
+def test_outputs_past_2_to_the_31_elements():
+    T, N, K, offsets = 70000, 40000, 16, [0, 69000, 70000]
+    X, W = operands(T, 2, K, N, torch.bfloat16, 24)
+    y = g.sgemm_grouped(X, W, dev(offsets))
+    assert y.numel() > 2 ** 31
+    for r in (slice(0, 3), slice(53686, 53690), slice(68998, 69003), slice(69990, 70000)):
+        at = [min(max(o - r.start, 0), r.stop - r.start) for o in offsets]
+        check(y[r], *forward64(X[r], W, at))
+    del y, W
+    torch.cuda.empty_cache()
+    T, K, N = 20, 30000, 30000
+    X = torch.randn((T, K), device="cuda").to(torch.bfloat16)
+    dY = torch.randn((T, N), device="cuda").to(torch.bfloat16)
+    dw = g.sgemm_grouped_wgrad(X, dY, dev([0, 5, 5, 20]))
+    assert dw.numel() > 2 ** 31
+    for rows in (slice(0, 2), slice(29990, 30000)):
+        check(dw[:, rows], *wgrad64(X[:, rows], dY, [0, 5, 5, 20], 3))
+    del dw
+    torch.cuda.empty_cache()

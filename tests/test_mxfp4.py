@@ -334,3 +334,44 @@ def test_invalid_quantize_arguments_rejected_on_host(change):
          "codes": 0x30000000, "scales": 0x40000000} | change
     lib = _lib.load()
     assert lib.sgemm_mxfp4_quantize(*a.values(), None) == _lib.ERR_INVALID_ARG
+
+
+@pytest.fixture(autouse=True)
+def no_wait_gave_up(request):
+    """After every GPU test: no kernel abandoned a bounded wait."""
+    yield
+    if request.node.get_closest_marker("gpu"):
+        assert g.check_status() == 0
+
+
+@pytest.mark.gpu
+def test_arrays_past_2_to_the_31_elements():
+    x = torch.randn((40, 60000), device="cuda").to(torch.bfloat16).repeat(1000, 1)
+    assert x.numel() > 2 ** 31
+    codes, scales = g.sgemm_mxfp4_quantize(x)
+    few, fs = g.sgemm_mxfp4_quantize(x[:128].contiguous())
+    assert torch.equal(codes[-40:], few[:40])
+    y = g.sgemm_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16)
+    assert torch.equal(y[-40:], g.sgemm_mxfp4_dequantize(few, fs, dtype=torch.bfloat16)[:40])
+    del x, y, codes, scales
+    torch.cuda.empty_cache()
+    a, sa, va = random_mxfp4((60000, 64), 5)
+    b, sb, vb = random_mxfp4((40000, 64), 6)
+    c = g.sgemm_mxfp4(a, sa, b, sb)
+    assert c.numel() > 2 ** 31
+    for r in (slice(0, 2), slice(53680, 53690), slice(59995, 60000)):
+        check(c[r], va[r] @ vb.T, va[r].abs() @ vb.abs().T)
+    del c
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [1, 2, 4, 8])
+def test_product_output_rows_of_every_alignment(pad):
+    for N in (33, 34, 36, 40, 193):
+        a, sa, va = random_mxfp4((70, 96), 7)
+        b, sb, vb = random_mxfp4((N, 96), 8)
+        out = padded(torch.zeros((70, N), dtype=torch.float16, device="cuda"), pad)
+        check(g.sgemm_mxfp4(a, sa, b, sb, out), va @ vb.T, va.abs() @ vb.abs().T)
+        store = torch.empty(0, dtype=torch.float16, device="cuda").set_(out.untyped_storage(), 0, (out.untyped_storage().nbytes() // 2,), (1,))
+        assert int(store.isnan().sum()) == 70 * pad
