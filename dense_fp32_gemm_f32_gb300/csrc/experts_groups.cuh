@@ -89,6 +89,28 @@ __device__ __forceinline__ bool group_find(const int* offsets, int E, int T, int
     return false;
 }
 
+// Whole warp.  Items of all groups.
+template <typename Units>
+__device__ __forceinline__ int group_total(const int* offsets, int E, int T, Units units) {
+    const int lane = threadIdx.x & 31;
+    int from = group_bound(offsets, 0, T), total = 0;
+    for (int base = 0; base < E; base += 32) {
+        const int i = base + lane;
+        int end = i < E ? group_bound(offsets, i + 1, T) : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d) end = max(end, v);
+        }
+        end = max(end, from);
+        int start = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) start = from;
+        total += __reduce_add_sync(0xffffffffu, i < E ? units(end - start) : 0);
+        from = __shfl_sync(0xffffffffu, end, 31);
+    }
+    return total;
+}
+
 // Element types as sgemm_experts.h numbers them.
 template <int TYPE>
 struct ElemOf;

@@ -47,7 +47,9 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
     using S = GroupedShape<TN, CG, PARTS>;
     const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG, PARTS>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, CG == 2 ? st.max_pairs : st.sm_count) * CG));
+    // (a pair's tiles may be split into columns of 64: LastRound)
+    cfg.gridDim = dim3(static_cast<unsigned>(CG == 2 ? 2 * std::min<long long>(tiles * (TN / 64), st.max_pairs)
+                                                     : std::min<long long>(tiles, st.sm_count)));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;

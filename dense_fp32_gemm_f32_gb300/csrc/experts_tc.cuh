@@ -42,7 +42,8 @@
 //   warp 2      schedule: which expert's rows a tile falls on, from the
 //               boundary array alone (group_find: the host never needs the
 //               group sizes), handed to the other warps through shared memory
-//               a few tiles ahead;
+//               a few tiles ahead.  The tiles of a last round that would leave
+//               half of the pairs idle are split by columns among them;
 //   the others  epilogue: tensor memory -> registers -> HBM, while the MMAs of
 //               the next tile fill the other accumulator.
 //
@@ -136,22 +137,31 @@ struct GroupedTile {
     int srow;                    // MXFP4: the first column's place among the scale blocks' rows
 };
 
-// Tile number `i`, from the same cursor in increasing order (whole warp).
+// Tiles of the whole product.
+template <bool WGRAD, int TN>
+__device__ __forceinline__ int grouped_tiles(const GroupedTcParams& p) {
+    if constexpr (WGRAD)
+        return p.E * p.ftiles * p.ctiles;
+    else
+        return group_total(p.offsets, p.E, p.T, [&](int n) { return (n + TN - 1) / TN * p.ftiles; });
+}
+
+// Tile number `i` (there is one), from the same cursor in increasing order
+// (whole warp).
 template <bool WGRAD, int TN, int FT>
-__device__ __forceinline__ bool grouped_tile(const GroupedTcParams& p, int i, GroupCursor& cur, GroupedTile& t) {
-    GroupHit h;
+__device__ __forceinline__ void grouped_tile(const GroupedTcParams& p, int i, GroupCursor& cur, GroupedTile& t) {
+    GroupHit h = {};
     if constexpr (WGRAD) {
         const int per = p.ftiles * p.ctiles;
-        if (!group_find(p.offsets, p.E, p.T, i, cur, [&](int) { return per; }, h)) return false;
+        (void)group_find(p.offsets, p.E, p.T, i, cur, [&](int) { return per; }, h);
         t.f0 = h.local / p.ctiles * FT;
         t.c0 = h.local % p.ctiles * TN;
         t.cols = min(TN, p.C - t.c0);
         t.k0 = h.start;
         t.klen = h.end - h.start;
     } else {
-        if (!group_find(p.offsets, p.E, p.T, i, cur, [&](int n) { return (n + TN - 1) / TN * p.ftiles; }, h))
-            return false;
-        const int n = (h.end - h.start + TN - 1) / TN;
+        (void)group_find(p.offsets, p.E, p.T, i, cur, [&](int n) { return (n + TN - 1) / TN * p.ftiles; }, h);
+        const int n = max(1, (h.end - h.start + TN - 1) / TN);
         t.f0 = h.local / n * FT;
         t.c0 = h.start + h.local % n * TN;
         t.cols = min(TN, h.end - t.c0);
@@ -160,19 +170,52 @@ __device__ __forceinline__ bool grouped_tile(const GroupedTcParams& p, int i, Gr
     }
     t.e = h.e;
     t.srow = 0;
-    return true;
 }
 
-// The schedule warp: tiles first, first + step, ... into the slots at `slots`
+// Tiles of the last, partial round over the clusters, split by columns when
+// that round has at most half as many as there are clusters: item i of a
+// cluster's sequence is tile i while i < full, then part (i - full) % parts of
+// tile full + (i - full) / parts.
+struct LastRound {
+    int total, full, parts;
+    // PARTS: the most parts, a divisor of the tile's columns into multiples of 64.
+    template <int PARTS>
+    __device__ __forceinline__ void set(int tiles, int clusters) {
+        total = tiles;
+        full = tiles / clusters * clusters;
+        const int fit = total > full ? clusters / (total - full) : 1;
+        parts = fit >= PARTS ? PARTS : PARTS == 4 && fit >= 2 ? 2 : 1;
+    }
+};
+
+// The schedule warp: items first, first + step, ... into the slots at `slots`
 // (barriers: a full and an empty one a slot), then one that is not valid.
-// Whole warp; false on a timeout.
-template <typename Find>
-__device__ __forceinline__ bool sched_run(uint32_t slots, uint32_t bars, int first, int step, uint64_t tmo, Find find) {
+// find(tile, t) fills in a tile; TN: its columns.  Whole warp; false on a
+// timeout.
+template <int TN, typename Find>
+__device__ __forceinline__ bool sched_run(uint32_t slots, uint32_t bars, int first, int step, const LastRound& last,
+                                          uint64_t tmo, Find find) {
     int n = 0;
-    for (int i = first;; i += step, ++n) {
-        GroupedTile t;
-        t.valid = find(i, t) ? 1 : 0;
+    for (int i = first;; i += step) {
+        GroupedTile t = {};
+        int tile = i, part = 0;
+        if (i >= last.full && last.parts > 1) {
+            tile = last.full + (i - last.full) / last.parts;
+            part = (i - last.full) % last.parts;
+        }
+        if (tile < last.total) {
+            find(tile, t);
+            t.valid = 1;
+            if (last.parts > 1 && i >= last.full) {
+                const int width = TN / last.parts, off = part * width;
+                t.cols = min(width, t.cols - off);
+                t.c0 += off;
+                t.srow += off;
+                if (t.cols <= 0) continue;
+            }
+        }
         const int slot = n % kSchedSlots, round = n / kSchedSlots;
+        ++n;
         if (round > 0 && !mbar_wait_warp<false>(bars + 8 * (kSchedSlots + slot), (round - 1) & 1, tmo)) return false;
         if (elect_one()) {
             sts128i(slots + 32 * slot, make_int4(t.valid, t.e, t.f0, t.c0));
@@ -627,8 +670,10 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------ schedule
         GroupCursor cur = group_begin(p.offsets, p.T);
-        if (!sched_run(slots, sched0, cluster, clusters, tmo,
-                       [&](int i, GroupedTile& u) { return grouped_tile<WGRAD, TN, FT>(p, i, cur, u); }))
+        LastRound last;
+        last.set<(PAIR ? TN / 64 : 1)>(grouped_tiles<WGRAD, TN>(p), clusters);
+        if (!sched_run<TN>(slots, sched0, cluster, clusters, last, tmo,
+                           [&](int i, GroupedTile& u) { grouped_tile<WGRAD, TN, FT>(p, i, cur, u); }))
             timed_out = true;
     } else {
         // ------------------------------------------------------------ epilogue

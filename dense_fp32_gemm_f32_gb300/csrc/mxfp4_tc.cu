@@ -28,7 +28,9 @@ int launch(const CUtensorMap (&m)[4], const Mxfp4TcParams& p, long long tiles, c
            cudaStream_t s) {
     using S = Mxfp4Shape<TN, CG>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, CG == 2 ? st.max_pairs : st.sm_count) * CG));
+    // (a pair's tiles may be split into columns of 64: LastRound)
+    cfg.gridDim = dim3(static_cast<unsigned>(CG == 2 ? 2 * std::min<long long>(tiles * (TN / 64), st.max_pairs)
+                                                     : std::min<long long>(tiles, st.sm_count)));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;

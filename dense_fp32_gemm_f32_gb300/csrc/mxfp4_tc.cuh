@@ -72,27 +72,26 @@ struct Mxfp4Shape {
     static_assert(kBoxCols * 128 % 1024 == 0, "boxes start on the swizzle's 1024 bytes");
 };
 
+template <int TN>
+__device__ __forceinline__ int mxfp4_tiles(const Mxfp4TcParams& p) {
+    auto units = [&](int n) { return (n + TN - 1) / TN * p.ftiles; };
+    return p.offsets ? group_total(p.offsets, p.E, p.T, units) : units(p.T);
+}
+
 template <int TN, int FT>
-__device__ __forceinline__ bool mxfp4_tile(const Mxfp4TcParams& p, int i, GroupCursor& cur, GroupedTile& t) {
-    int start = 0, end = p.T, local = i, block0 = 0, e = 0;
-    if (p.offsets) {
-        GroupHit h;
-        if (!group_find(p.offsets, p.E, p.T, i, cur, [&](int n) { return (n + TN - 1) / TN * p.ftiles; }, h))
-            return false;
-        start = h.start, end = h.end, local = h.local, block0 = h.block0, e = h.e;
-    } else if (i >= (p.T + TN - 1) / TN * p.ftiles) {
-        return false;
-    }
-    const int n = (end - start + TN - 1) / TN;
-    const int off = local % n * TN;
-    t.e = e;
-    t.f0 = local / n * FT;
-    t.c0 = start + off;
-    t.cols = min(TN, end - t.c0);
+__device__ __forceinline__ void mxfp4_tile(const Mxfp4TcParams& p, int i, GroupCursor& cur, GroupedTile& t) {
+    GroupHit h = {0, 0, p.T, i, 0};
+    if (p.offsets)
+        (void)group_find(p.offsets, p.E, p.T, i, cur, [&](int n) { return (n + TN - 1) / TN * p.ftiles; }, h);
+    const int n = max(1, (h.end - h.start + TN - 1) / TN);
+    const int off = h.local % n * TN;
+    t.e = h.e;
+    t.f0 = h.local / n * FT;
+    t.c0 = h.start + off;
+    t.cols = min(TN, h.end - t.c0);
     t.k0 = 0;
     t.klen = p.K;
-    t.srow = 128 * block0 + off;
-    return true;
+    t.srow = 128 * h.block0 + off;
 }
 
 template <int TN, int CG>
@@ -272,8 +271,10 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------ schedule
         GroupCursor cur = p.offsets ? group_begin(p.offsets, p.T) : GroupCursor();
-        if (!sched_run(slots, sched0, cluster, clusters, tmo,
-                       [&](int i, GroupedTile& u) { return mxfp4_tile<TN, FT>(p, i, cur, u); }))
+        LastRound last;
+        last.set<(PAIR ? TN / 64 : 1)>(mxfp4_tiles<TN>(p), clusters);
+        if (!sched_run<TN>(slots, sched0, cluster, clusters, last, tmo,
+                           [&](int i, GroupedTile& u) { mxfp4_tile<TN, FT>(p, i, cur, u); }))
             timed_out = true;
     } else {
         // ------------------------------------------------------------ epilogue
