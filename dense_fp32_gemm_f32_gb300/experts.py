@@ -24,16 +24,16 @@ def _type(dtype, name: str) -> int:
 # small product costs: they ask each tensor as little as they can.
 
 
-def _operand(X, name: str, dim: int, dtype=None) -> int:
-    """Checks that X is a CUDA tensor of `dim` dimensions (and `dtype`); returns its device's number."""
+def _operand(X, name: str, dim: int, dtype=None):
+    """Checks that X is a CUDA tensor of `dim` dimensions (and `dtype`); returns its device's number and its shape."""
     if not isinstance(X, torch.Tensor) or (dtype is not None and X.dtype is not dtype):
         raise TypeError(f"{name} must be a CUDA tensor" + (f" of {dtype}" if dtype is not None else ""))
-    dev = X.get_device()
+    dev, shape = X.get_device(), X.shape
     if dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor, got one on {X.device}")
-    if X.dim() != dim:
-        raise ValueError(f"{name} must be {dim}-D, got shape {tuple(X.shape)}")
-    return dev
+    if len(shape) != dim:
+        raise ValueError(f"{name} must be {dim}-D, got shape {tuple(shape)}")
+    return dev, shape
 
 
 def _strides(X, shape, name: str):
@@ -50,9 +50,9 @@ def _strides(X, shape, name: str):
 
 def _offsets(offsets, dev: int) -> int:
     """Checks the boundaries; returns the number of experts."""
-    if _operand(offsets, "offsets", 1, torch.int32) != dev:
-        raise ValueError("offsets is on another device")
-    n = offsets.shape[0]
+    other, shape = _operand(offsets, "offsets", 1, torch.int32)
+    _same_device(dev, other, "offsets")
+    n = shape[0]
     if n < 1 or (n > 1 and offsets.stride(0) != 1):
         raise ValueError("offsets must hold E + 1 contiguous boundaries")
     return n - 1
@@ -67,19 +67,27 @@ def _same_device(dev: int, other: int, name: str) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _launch(dev: int, stream, call):
-    """``call(handle)`` with the operands' device current, and ``stream`` too if one is given: outputs that the call
-    allocates then belong to the stream that its kernels run on.  Nothing is switched in the usual case, the current
-    device and stream (a switch costs as much as a launch)."""
-    if stream is None:
-        if torch.cuda.current_device() == dev:
-            return call(_raw_stream(dev))
-        with torch.cuda.device(dev):
-            return call(_raw_stream(dev))
-    with torch.cuda.stream(stream):  # (its device too)
+class _Switch:
+    """The operands' device made current, and ``stream`` too if one is given: outputs that a call allocates then belong to
+    the stream that its kernels run on.  Undone by close()."""
+
+    def __init__(self, dev: int, stream):
+        self.context = torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)  # (its device too)
+        self.context.__enter__()
         if torch.cuda.current_device() != dev:
+            self.close()
             raise ValueError("stream is on another device than the operands")
-        return call(int(stream.cuda_stream))
+
+    def close(self):
+        self.context.__exit__(None, None, None)
+
+
+def _enter(dev: int, stream):
+    """(stream handle, what to close after the call or None).  Nothing is switched in the usual case, the current device
+    and stream: a switch costs as much as a launch."""
+    if stream is None:
+        return _raw_stream(dev), (None if torch.cuda.current_device() == dev else _Switch(dev, None))
+    return int(stream.cuda_stream), _Switch(dev, stream)
 
 
 def _out(out, like, shape, dtype, name="out"):
@@ -99,27 +107,28 @@ def sgemm_grouped(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, out: 
     ``X`` is (T, K), sorted by expert; ``W`` is (E, K, N), or (E, N, K) with ``transw``; all of one type (float32,
     bfloat16, float16).  The gradient of the rows is the same call on the output's gradient with ``transw`` inverted.
     """
-    dev = _operand(X, "X", 2)
+    dev, (T, K) = _operand(X, "X", 2)
     dtype = X.dtype
     t = _type(dtype, "X")
-    _same_device(dev, _operand(W, "W", 3, dtype), "W")
-    xs, ws = X.shape, W.shape
-    T, K = xs
+    other, ws = _operand(W, "W", 3, dtype)
+    _same_device(dev, other, "W")
     E, N, KW = (ws[0], ws[1], ws[2]) if transw else (ws[0], ws[2], ws[1])
     if KW != K:
         raise ValueError(f"shapes do not multiply: {(T, K)} x op(W) of {tuple(ws)}, transw={bool(transw)}")
     if _offsets(offsets, dev) != E:
         raise ValueError(f"offsets must hold {E + 1} boundaries, got {offsets.numel()}")
-    ldx = _strides(X, xs, "X")[0]
+    ldx = _strides(X, (T, K), "X")[0]
     ldw, sw = _strides(W, ws, "W")
-
-    def call(s):
-        y, ldy = _out(out, X, (T, N), dtype)
-        _lib.check(_lib.load().sgemm_grouped(t, 1 if transw else 0, T, E, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw,
-                                             sw, offsets.data_ptr(), y.data_ptr(), ldy, s), "sgemm_grouped")
-        return y
-
-    return _launch(dev, stream, call)
+    s, switch = _enter(dev, stream)
+    try:
+        out, ldy = _out(out, X, (T, N), dtype)
+        rc = _lib.load().sgemm_grouped(t, 1 if transw else 0, T, E, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, sw,
+                                       offsets.data_ptr(), out.data_ptr(), ldy, s)
+    finally:
+        if switch is not None:
+            switch.close()
+    _lib.check(rc, "sgemm_grouped")
+    return out
 
 
 def sgemm_grouped_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None, *,
@@ -129,32 +138,30 @@ def sgemm_grouped_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor
     ``X`` is (T, K) and ``dY`` (T, N), of one type; ``dtype`` is that type (default) or float32.  For weights stored
     (E, N, K) swap ``X`` and ``dY``.
     """
-    dev = _operand(X, "X", 2)
-    _same_device(dev, _operand(dY, "dY", 2, X.dtype), "dY")
+    dev, (T, K) = _operand(X, "X", 2)
+    other, (rows, N) = _operand(dY, "dY", 2, X.dtype)
+    _same_device(dev, other, "dY")
     t = _type(X.dtype, "X")
     dtype = dtype if dtype is not None else out.dtype if out is not None else X.dtype
     if dtype not in (X.dtype, torch.float32):
         raise TypeError(f"the gradient's type must be {X.dtype} or float32, got {dtype}")
-    xs, ys = X.shape, dY.shape
-    (T, K), N = xs, ys[1]
-    if ys[0] != T:
-        raise ValueError(f"X has {T} rows, dY {ys[0]}")
+    if rows != T:
+        raise ValueError(f"X has {T} rows, dY {rows}")
     E = _offsets(offsets, dev)
-    ldx, ldy = _strides(X, xs, "X")[0], _strides(dY, ys, "dY")[0]
-
-    def call(s):
-        dW, ldo = _out(out, X, (E, K, N), dtype)
-        so = _strides(dW, (E, K, N), "out")[1] if out is not None else K * N
-        _lib.check(_lib.load().sgemm_grouped_wgrad(t, _TYPES[dtype], T, E, K, N, X.data_ptr(), ldx, dY.data_ptr(), ldy,
-                                                   offsets.data_ptr(), dW.data_ptr(), ldo, so, s),
-                   "sgemm_grouped_wgrad")
-        return dW
-
-    return _launch(dev, stream, call)
-
-
-def _blocks(rows: int) -> int:
-    return (rows + 127) // 128
+    ldx, ldy = _strides(X, (T, K), "X")[0], _strides(dY, (T, N), "dY")[0]
+    s, switch = _enter(dev, stream)
+    try:
+        so = K * N if out is None else None
+        out, ldo = _out(out, X, (E, K, N), dtype)
+        if so is None:
+            so = _strides(out, (E, K, N), "out")[1]
+        rc = _lib.load().sgemm_grouped_wgrad(t, _TYPES[dtype], T, E, K, N, X.data_ptr(), ldx, dY.data_ptr(), ldy,
+                                             offsets.data_ptr(), out.data_ptr(), ldo, so, s)
+    finally:
+        if switch is not None:
+            switch.close()
+    _lib.check(rc, "sgemm_grouped_wgrad")
+    return out
 
 
 def _grouped_blocks(rows: int, E: int) -> int:
@@ -170,31 +177,33 @@ def sgemm_mxfp4_quantize(X: torch.Tensor, offsets: torch.Tensor | None = None, *
     With ``offsets`` the rows are grouped by expert, and every expert's rows begin a scale block.
     """
     dim = 3 if isinstance(X, torch.Tensor) and X.dim() == 3 else 2
-    dev = _operand(X, "X", dim)
+    dev, shape = _operand(X, "X", dim)
     t = _type(X.dtype, "X")
-    shape = tuple(X.shape)
-    lead, (rows, K) = shape[:-2], shape[-2:]
-    E, nb = 0, _blocks(rows)
+    rows, K = shape[-2:]
+    lead = () if dim == 2 else (shape[0],)
+    E, nb = 0, (rows + 127) // 128
     if offsets is not None:
         if dim != 2:
             raise ValueError("rows grouped by expert must be 2-D")
         E = _offsets(offsets, dev)
         nb = _grouped_blocks(rows, E)
     ldx, sx = _strides(X, shape, "X")
-
-    def call(s):
-        c, _ = _out(codes, X, lead + (rows, 16 * ((K + 31) // 32)), torch.uint8, "codes")
-        f, _ = _out(scales, X, lead + (nb, _blocks(K), 32, 4, 4), torch.uint8, "scales")
-        if codes is not None:
-            _contiguous(c, "codes")
-        if scales is not None:
-            _contiguous(f, "scales")
-        _lib.check(_lib.load().sgemm_mxfp4_quantize(t, lead[0] if lead else 1, rows, K, X.data_ptr(), ldx, sx, E,
-                                                    None if offsets is None else offsets.data_ptr(), c.data_ptr(),
-                                                    f.data_ptr(), s), "sgemm_mxfp4_quantize")
-        return c, f
-
-    return _launch(dev, stream, call)
+    s, switch = _enter(dev, stream)
+    try:
+        given = codes is not None or scales is not None
+        codes, _ = _out(codes, X, lead + (rows, 16 * ((K + 31) // 32)), torch.uint8, "codes")
+        scales, _ = _out(scales, X, lead + (nb, (K + 127) // 128, 32, 4, 4), torch.uint8, "scales")
+        if given:
+            _contiguous(codes, "codes")
+            _contiguous(scales, "scales")
+        rc = _lib.load().sgemm_mxfp4_quantize(t, shape[0] if dim == 3 else 1, rows, K, X.data_ptr(), ldx, sx, E,
+                                              None if offsets is None else offsets.data_ptr(), codes.data_ptr(),
+                                              scales.data_ptr(), s)
+    finally:
+        if switch is not None:
+            switch.close()
+    _lib.check(rc, "sgemm_mxfp4_quantize")
+    return codes, scales
 
 
 def _contiguous(X, name: str) -> None:
@@ -204,17 +213,17 @@ def _contiguous(X, name: str) -> None:
 
 def _mxfp4(codes, scales, name: str, dim: int, E: int | None = None):
     """Checks an MXFP4 operand (rows grouped by E experts if E is given); returns (device, rows, 32 * blocks)."""
-    dev = _operand(codes, name, dim, torch.uint8)
-    _same_device(dev, _operand(scales, "scales", dim + 3, torch.uint8), "scales")
+    dev, shape = _operand(codes, name, dim, torch.uint8)
+    other, got = _operand(scales, "scales", dim + 3, torch.uint8)
+    _same_device(dev, other, "scales")
     _contiguous(codes, name)
     _contiguous(scales, "scales")
-    shape = tuple(codes.shape)
     rows, K = shape[-2], 2 * shape[-1]
     if K % 32:
         raise ValueError(f"{name} must have 16 bytes for each block of 32 columns, got rows of {shape[-1]} bytes")
-    want = shape[:-2] + (_blocks(rows) if E is None else _grouped_blocks(rows, E), _blocks(K), 32, 4, 4)
-    if tuple(scales.shape) != want:
-        raise ValueError(f"{name}'s scales must have shape {want}, got {tuple(scales.shape)}")
+    want = ((rows + 127) // 128 if E is None else _grouped_blocks(rows, E), (K + 127) // 128, 32, 4, 4)
+    if got[-5:] != want or got[:-5] != shape[:-2]:
+        raise ValueError(f"{name}'s scales must have shape {tuple(shape[:-2]) + want}, got {tuple(got)}")
     return dev, rows, K
 
 
@@ -227,25 +236,28 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
         dtype = out.dtype
     t = _type(dtype, "dtype")
     dim = 3 if isinstance(codes, torch.Tensor) and codes.dim() == 3 and offsets is None else 2
-    dev = _operand(codes, "codes", dim, torch.uint8)
-    E = None if offsets is None else _offsets(offsets, dev)
-    _, rows, K = _mxfp4(codes, scales, "codes", dim, E)
+    E = None if offsets is None else _offsets(offsets, _operand(codes, "codes", 2, torch.uint8)[0])
+    dev, rows, K = _mxfp4(codes, scales, "codes", dim, E)
     if cols is not None:
         if not 0 <= K - cols < 32:
             raise ValueError(f"codes hold {max(K - 31, 0)} to {K} columns, not {cols}")
         K = cols
     shape = tuple(codes.shape[:-1]) + (K,)
 
-    def call(s):
-        y, ldy = _out(out, codes, shape, dtype)
-        sy = ldy * rows if out is None else _strides(y, shape, "out")[1]
-        _lib.check(_lib.load().sgemm_mxfp4_dequantize(t, shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(),
-                                                      scales.data_ptr(), E or 0,
-                                                      None if offsets is None else offsets.data_ptr(), y.data_ptr(),
-                                                      ldy, sy, s), "sgemm_mxfp4_dequantize")
-        return y
-
-    return _launch(dev, stream, call)
+    s, switch = _enter(dev, stream)
+    try:
+        sy = rows * K if out is None else None
+        out, ldy = _out(out, codes, shape, dtype)
+        if sy is None:
+            sy = _strides(out, shape, "out")[1]
+        rc = _lib.load().sgemm_mxfp4_dequantize(t, shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(), scales.data_ptr(),
+                                                E or 0, None if offsets is None else offsets.data_ptr(),
+                                                out.data_ptr(), ldy, sy, s)
+    finally:
+        if switch is not None:
+            switch.close()
+    _lib.check(rc, "sgemm_mxfp4_dequantize")
+    return out
 
 
 def sgemm_mxfp4(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor,
@@ -259,13 +271,16 @@ def sgemm_mxfp4(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scal
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
 
-    def call(s):
-        C, ldc = _out(out, A, (M, N), dtype)
-        _lib.check(_lib.load().sgemm_mxfp4(t, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(),
-                                           b_scales.data_ptr(), C.data_ptr(), ldc, s), "sgemm_mxfp4")
-        return C
-
-    return _launch(dev, stream, call)
+    s, switch = _enter(dev, stream)
+    try:
+        out, ldc = _out(out, A, (M, N), dtype)
+        rc = _lib.load().sgemm_mxfp4(t, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
+                                     out.data_ptr(), ldc, s)
+    finally:
+        if switch is not None:
+            switch.close()
+    _lib.check(rc, "sgemm_mxfp4")
+    return out
 
 
 def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
@@ -273,9 +288,8 @@ def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor
                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """``out[t] = X[t] @ W[e].T`` for the rows of each expert, zeros for rows of none: X (T, K) quantised with the
     same ``offsets``, W (E, N, K) quantised along K."""
-    dev = _operand(X, "X", 2, torch.uint8)
-    E = _offsets(offsets, dev)
-    _, T, K = _mxfp4(X, x_scales, "X", 2, E)
+    E = _offsets(offsets, _operand(X, "X", 2, torch.uint8)[0])
+    dev, T, K = _mxfp4(X, x_scales, "X", 2, E)
     other, N, KW = _mxfp4(W, w_scales, "W", 3)
     _same_device(dev, other, "W")
     if K != KW or W.shape[0] != E:
@@ -283,11 +297,13 @@ def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
 
-    def call(s):
-        y, ldy = _out(out, X, (T, N), dtype)
-        _lib.check(_lib.load().sgemm_mxfp4_grouped(t, T, E, N, K, X.data_ptr(), x_scales.data_ptr(), W.data_ptr(),
-                                                   w_scales.data_ptr(), offsets.data_ptr(), y.data_ptr(), ldy, s),
-                   "sgemm_mxfp4_grouped")
-        return y
-
-    return _launch(dev, stream, call)
+    s, switch = _enter(dev, stream)
+    try:
+        out, ldy = _out(out, X, (T, N), dtype)
+        rc = _lib.load().sgemm_mxfp4_grouped(t, T, E, N, K, X.data_ptr(), x_scales.data_ptr(), W.data_ptr(),
+                                             w_scales.data_ptr(), offsets.data_ptr(), out.data_ptr(), ldy, s)
+    finally:
+        if switch is not None:
+            switch.close()
+    _lib.check(rc, "sgemm_mxfp4_grouped")
+    return out
