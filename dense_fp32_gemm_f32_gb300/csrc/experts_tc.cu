@@ -38,7 +38,8 @@ int encode_3d(CUtensorMap* map, const TcOperand& o, bool f16, int box_inner, int
 
 // 16-bit matrices that a tensor map reads as they are.
 bool tma_readable(const MatrixArg& m) {
-    return (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 && m.ld % 8 == 0 && (m.count == 1 || m.se % 8 == 0);
+    return (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 && (m.rows == 1 || m.ld % 8 == 0) &&
+           (m.count == 1 || m.se % 8 == 0);
 }
 
 template <bool AMN, bool BMN, int TN, int CG, int PARTS>
@@ -176,8 +177,9 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
             bytes[i] = (static_cast<size_t>(f32 ? 3 : 1) * m[i].count * m[i].rows * dld * 2 + 255) & ~size_t{255};
             o[i] = {nullptr, m[i].cols, m[i].rows, (f32 ? 3 : 1) * m[i].count, dld, m[i].rows * dld};
         } else {
-            // (a dimension of one matrix has no stride of its own: any that the encoder takes)
-            o[i] = {m[i].p, m[i].cols, m[i].rows, m[i].count, m[i].ld, m[i].count > 1 ? m[i].se : m[i].rows * m[i].ld};
+            // (a dimension of one row or matrix has no stride of its own: any that the encoder takes)
+            const long long ld = m[i].rows > 1 ? m[i].ld : dld;
+            o[i] = {m[i].p, m[i].cols, m[i].rows, m[i].count, ld, m[i].count > 1 ? m[i].se : m[i].rows * ld};
         }
     }
     Packs packs;
