@@ -76,6 +76,15 @@ inline int row_alignment(const void* out, int size, long long ld, long long stri
     return static_cast<int>(bits & (~bits + 1));
 }
 
+// CTAs that share a tile's contraction where `tiles` (at most) leave half of the
+// SMs idle: as many as keep every cluster on one tile, with parts of `least`
+// or more.
+inline int split_parts(long long tiles, int K, int least, int sms) {
+    int ks = 1;
+    while (ks < 8 && 2 * ks * tiles <= sms && K >= 2 * ks * least) ks *= 2;
+    return ks;
+}
+
 struct DeviceState;
 int mxfp4_tc_set_up();
 int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s);

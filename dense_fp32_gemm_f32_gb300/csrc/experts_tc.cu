@@ -42,15 +42,16 @@ bool tma_readable(const MatrixArg& m) {
            (m.count == 1 || m.se % 8 == 0);
 }
 
-template <bool AMN, bool BMN, int TN, int CG, int PARTS>
+template <bool AMN, bool BMN, int TN, int CG, int PARTS, bool SPLIT = false>
 int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p, long long tiles,
            const DeviceState& st, cudaStream_t s) {
     using S = GroupedShape<TN, CG, PARTS>;
-    const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG, PARTS>;
+    const auto kernel = grouped_tc_kernel<AMN, BMN, TN, CG, PARTS, SPLIT>;
+    const int share = SPLIT ? p.ks : CG;  // CTAs of a cluster
     cudaLaunchConfig_t cfg = {};
     // (a pair's tiles may be split into columns of 64: LastRound)
     cfg.gridDim = dim3(static_cast<unsigned>(CG == 2 ? 2 * std::min<long long>(tiles * (TN / 64), st.max_pairs)
-                                                     : std::min<long long>(tiles, st.sm_count)));
+                                                     : SPLIT ? tiles * p.ks : std::min<long long>(tiles, st.sm_count)));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -61,10 +62,10 @@ int launch(const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(share);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 2 : 1;
+    cfg.numAttrs = share > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a, b, p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
@@ -100,9 +101,9 @@ Tile choose_tile(const GroupedCall& c, const DeviceState& st) {
     return {columns(128) * 13 < columns(256) * 10 ? 128 : 256, 2};
 }
 
-template <bool AMN, bool BMN, int TN, int CG, int PARTS>
+template <bool AMN, bool BMN, int TN, int CG, int PARTS, bool SPLIT = false>
 int set_up() {
-    return cudaFuncSetAttribute(grouped_tc_kernel<AMN, BMN, TN, CG, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(grouped_tc_kernel<AMN, BMN, TN, CG, PARTS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 GroupedShape<TN, CG, PARTS>::kSmem) == cudaSuccess
                ? SGEMM_OK
                : SGEMM_ERR_CUDA;
@@ -112,7 +113,9 @@ template <bool AMN>
 int launch_forward(const Tile& tile, bool f32, const CUtensorMap& a, const CUtensorMap& b, const GroupedTcParams& p,
                    long long tiles, const DeviceState& st, cudaStream_t s) {
     if (f32) return launch<AMN, false, 128, 2, 3>(a, b, p, tiles, st, s);
-    if (tile.cg == 1) return launch<AMN, false, 128, 1, 1>(a, b, p, tiles, st, s);
+    if (tile.cg == 1)
+        return p.ks > 1 ? launch<AMN, false, 128, 1, 1, true>(a, b, p, tiles, st, s)
+                        : launch<AMN, false, 128, 1, 1>(a, b, p, tiles, st, s);
     return tile.tn == 128 ? launch<AMN, false, 128, 2, 1>(a, b, p, tiles, st, s)
                           : launch<AMN, false, 256, 2, 1>(a, b, p, tiles, st, s);
 }
@@ -130,7 +133,8 @@ struct Packs {
 }  // namespace
 
 int experts_tc_set_up(DeviceState& st) {
-    if (set_up<true, false, 128, 1, 1>() || set_up<true, false, 128, 2, 1>() || set_up<true, false, 256, 2, 1>() ||
+    if (set_up<true, false, 128, 1, 1, true>() || set_up<false, false, 128, 1, 1, true>() ||
+        set_up<true, false, 128, 1, 1>() || set_up<true, false, 128, 2, 1>() || set_up<true, false, 256, 2, 1>() ||
         set_up<false, false, 128, 1, 1>() || set_up<false, false, 128, 2, 1>() || set_up<false, false, 256, 2, 1>() ||
         set_up<true, true, 128, 2, 1>() || set_up<true, true, 256, 2, 1>() || set_up<true, false, 128, 2, 3>() ||
         set_up<false, false, 128, 2, 3>() || set_up<true, true, 128, 2, 3>()) {
@@ -216,6 +220,7 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
     const long long tiles = c.wgrad ? static_cast<long long>(c.E) * p.ftiles * p.ctiles
                                     : (c.T / tn + std::min(c.T, c.E)) * static_cast<long long>(p.ftiles);
     if (tiles > 0x7fffffffll - 65536) return SGEMM_ERR_INVALID_ARG;
+    p.ks = cg == 1 ? split_parts(tiles, c.K, 256, st.sm_count) : 1;
     alignas(64) CUtensorMap ma, mb;
     int rc = encode_3d(&ma, o[0], f16, 64, c.a_mn ? 64 : 128);
     if (rc == SGEMM_OK) rc = encode_3d(&mb, o[1], f16, 64, std::min(64, tn / cg));

@@ -47,6 +47,12 @@
 //   the others  epilogue: tensor memory -> registers -> HBM, while the MMAs of
 //               the next tile fill the other accumulator.
 //
+// Where the tiles are too few for the GPU (a token or a few, one projection), a
+// cluster of 2 to 8 CTAs shares one (SPLIT): each takes a part of the
+// contraction, leaves its sums in its shared memory, and adds up the columns
+// that are its own from all parts, in their order.  (4 rows, 40 experts of 6690 x
+// 480: 21 us on 16 SMs, 14 so.)
+//
 // The load and MMA warps' loops are uniform over the warp, with one elected
 // lane issuing: the operands of the instructions then live in uniform
 // registers.  (In a loop of one lane they do not, and moving them cost more
@@ -90,6 +96,7 @@ struct GroupedTcParams {
     void* out;
     long long ldo, so;  // elements between rows; weight gradient: between experts
     int out_type;
+    int ks;             // SPLIT: CTAs of a cluster
     int align;          // bytes that the output's rows are aligned to (2 .. 16)
     uint32_t idesc;     // instruction descriptor without the column count
     unsigned long long timeout_ns;
@@ -402,6 +409,45 @@ __device__ __forceinline__ void grouped_store(const P& p, uint32_t patch, long l
     }
 }
 
+// The split form: this CTA's part of a tile's contraction, in whole stages.
+__device__ __forceinline__ void split_contraction(GroupedTile& t, int part, int parts, int stage) {
+    const int per = ((t.klen + stage - 1) / stage + parts - 1) / parts * stage;
+    const int from = min(t.klen, part * per);
+    t.k0 = from;
+    t.klen = min(t.klen, from + per) - from;
+}
+
+// Its sums, columns c .. c + 31 of feature f, to the (idle) ring: a column a
+// row of 128.
+__device__ __forceinline__ void leave_part(uint32_t ring, int c, int f, const uint32_t (&v)[32], bool zero) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ring + static_cast<uint32_t>(((c + j) * 128 + f) * 4)),
+                     "r"(zero ? 0u : v[j])
+                     : "memory");
+}
+
+// The columns that are this CTA's, part p of `parts` every `parts`-th, from
+// all CTAs of the cluster.
+template <typename P>
+__device__ __forceinline__ void add_parts(const P& p, uint32_t ring, const GroupedTile& t, int part, int parts,
+                                          int thread, int threads) {
+    const int f = thread & 127;
+    if (t.f0 + f >= p.F) return;
+    for (int c = part + parts * (thread >> 7); c < t.cols; c += parts * (threads >> 7)) {
+        const uint32_t at = ring + static_cast<uint32_t>((c * 128 + f) * 4);
+        float s = 0.f;
+        for (int q = 0; q < parts; ++q) s += ld_shared_cluster_f32(map_shared_rank(at, q));
+        const long long o = (t.c0 + c) * p.ldo + t.f0 + f;
+        if (p.out_type == 0)
+            static_cast<float*>(p.out)[o] = s;
+        else if (p.out_type == 1)
+            static_cast<__nv_bfloat16*>(p.out)[o] = from_f32<__nv_bfloat16>(s);
+        else
+            static_cast<__half*>(p.out)[o] = from_f32<__half>(s);
+    }
+}
+
 // Rows of no expert: zeros, spread over the CTAs' epilogue warps.
 template <typename T>
 __device__ void grouped_zero_rows(const GroupedTcParams& p, int worker, int workers) {
@@ -419,13 +465,14 @@ __device__ void grouped_zero_rows(const GroupedTcParams& p, int worker, int work
 
 // AMN, BMN: the operand is MN-major in HBM and shared memory (else K-major);
 // both: a weight gradient.
-template <bool AMN, bool BMN, int TN, int CG, int PARTS>
+template <bool AMN, bool BMN, int TN, int CG, int PARTS, bool SPLIT = false>
 __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const GroupedTcParams p) {
     using S = GroupedShape<TN, CG, PARTS>;
     constexpr bool WGRAD = AMN && BMN;
     static_assert(!BMN || (AMN && S::kCols % 64 == 0), "the weight gradient's columns come in blocks of 64");
+    static_assert(!SPLIT || (CG == 1 && PARTS == 1 && !BMN && S::kStages * S::kStageBytes >= TN * 128 * 4), "split form");
     constexpr int FT = 128 * CG;
     constexpr bool PAIR = CG == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -440,7 +487,9 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
 
     const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = PAIR ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
-    const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
+    const int share = SPLIT ? p.ks : CG;  // CTAs of a tile
+    const int part = SPLIT ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
+    const int cluster = static_cast<int>(blockIdx.x) / share, clusters = static_cast<int>(gridDim.x) / share;
     const unsigned long long tmo = p.timeout_ns;
 
     if (threadIdx.x == 0) {
@@ -473,7 +522,7 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
     grid_dependency_wait();  // the set-up above ran beside the end of the kernel before
 
     bool timed_out = false;
-    GroupedTile t;
+    GroupedTile t, split = {};  // split: the tile whose parts this cluster has to add up
     SchedReader tiles{slots, sched0};
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -673,7 +722,10 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
         LastRound last;
         last.set<(PAIR ? TN / 64 : 1)>(grouped_tiles<WGRAD, TN>(p), clusters);
         if (!sched_run<TN>(slots, sched0, cluster, clusters, last, tmo,
-                           [&](int i, GroupedTile& u) { grouped_tile<WGRAD, TN, FT>(p, i, cur, u); }))
+                           [&](int i, GroupedTile& u) {
+                               grouped_tile<WGRAD, TN, FT>(p, i, cur, u);
+                               if constexpr (SPLIT) split_contraction(u, part, p.ks, kGrBK);
+                           }))
             timed_out = true;
     } else {
         // ------------------------------------------------------------ epilogue
@@ -718,7 +770,21 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
                 ++unit;
             };
             uint32_t acc;
-            if constexpr (PARTS == 1) {
+            if constexpr (SPLIT) {
+                if (!wait(acc)) {
+                    timed_out = true;
+                    break;
+                }
+                for (int c = 32 * half; c < t.cols; c += 8 * S::kEpiWarps) {
+                    uint32_t v[32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
+                    tmem_wait_ld();
+                    leave_part(base, c, 32 * q + lane, v, t.klen == 0);
+                }
+                split = t;
+                release();
+            } else if constexpr (PARTS == 1) {
                 if (!wait(acc)) {
                     timed_out = true;
                     break;
@@ -774,6 +840,12 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();  // nothing of the peer's is under way in this CTA's memory
+    if constexpr (SPLIT) {
+        cluster_sync_all();  // every part is there
+        if (warp >= 3 && split.valid && !timed_out)
+            add_parts(p, base, split, part, p.ks, (warp - 3) * 32 + lane, 32 * S::kEpiWarps);
+        cluster_sync_all();  // and has been read
+    }
     __syncwarp();
     if (warp == 1) {
         tc_fence_after_sync();

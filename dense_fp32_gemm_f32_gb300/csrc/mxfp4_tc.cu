@@ -23,14 +23,15 @@ int encode_bytes(CUtensorMap* map, const void* p, CUtensorMapDataType type, int 
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
 
-template <int TN, int CG>
+template <int TN, int CG, bool SPLIT = false>
 int launch(const CUtensorMap (&m)[4], const Mxfp4TcParams& p, long long tiles, const DeviceState& st,
            cudaStream_t s) {
     using S = Mxfp4Shape<TN, CG>;
+    const int share = SPLIT ? p.ks : CG;  // CTAs of a cluster
     cudaLaunchConfig_t cfg = {};
     // (a pair's tiles may be split into columns of 64: LastRound)
     cfg.gridDim = dim3(static_cast<unsigned>(CG == 2 ? 2 * std::min<long long>(tiles * (TN / 64), st.max_pairs)
-                                                     : std::min<long long>(tiles, st.sm_count)));
+                                                     : SPLIT ? tiles * p.ks : std::min<long long>(tiles, st.sm_count)));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -41,20 +42,20 @@ int launch(const CUtensorMap (&m)[4], const Mxfp4TcParams& p, long long tiles, c
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(share);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, mxfp4_tc_kernel<TN, CG>, m[0], m[1], m[2], m[3], p) != cudaSuccess) {
+    cfg.numAttrs = share > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, mxfp4_tc_kernel<TN, CG, SPLIT>, m[0], m[1], m[2], m[3], p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
     return SGEMM_OK;
 }
 
-template <int TN, int CG>
+template <int TN, int CG, bool SPLIT = false>
 int set_up() {
-    return cudaFuncSetAttribute(mxfp4_tc_kernel<TN, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(mxfp4_tc_kernel<TN, CG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 Mxfp4Shape<TN, CG>::kSmem) == cudaSuccess
                ? SGEMM_OK
                : SGEMM_ERR_CUDA;
@@ -63,7 +64,7 @@ int set_up() {
 }  // namespace
 
 int mxfp4_tc_set_up() {
-    if (set_up<64, 1>() || set_up<192, 2>()) {
+    if (set_up<64, 1, true>() || set_up<64, 1>() || set_up<192, 2>()) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -98,6 +99,8 @@ int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s) {
         rc = encode_bytes(&m[3], c.x_scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, 128 * kq, c.x_blocks, 1, 256,
                           narrow ? Mxfp4Shape<64, 1>::kSbBlocks : Mxfp4Shape<192, 2>::kSbBlocks, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc != SGEMM_OK) return rc;
+    p.ks = narrow ? split_parts(tiles, p.K, 1024, st.sm_count) : 1;
+    if (p.ks > 1) return launch<64, 1, true>(m, p, tiles, st, s);
     return narrow ? launch<64, 1>(m, p, tiles, st, s) : launch<192, 2>(m, p, tiles, st, s);
 }
 

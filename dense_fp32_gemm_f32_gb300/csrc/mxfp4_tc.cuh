@@ -40,6 +40,7 @@ struct Mxfp4TcParams {
     long long ldo;
     int out_type;
     int align;
+    int ks;  // SPLIT: CTAs of a cluster
     unsigned long long timeout_ns;
     unsigned int* status;
 };
@@ -94,7 +95,8 @@ __device__ __forceinline__ void mxfp4_tile(const Mxfp4TcParams& p, int i, GroupC
     t.srow = 128 * h.block0 + off;
 }
 
-template <int TN, int CG>
+// SPLIT: as in grouped_tc_kernel.
+template <int TN, int CG, bool SPLIT = false>
 __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     mxfp4_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
@@ -114,7 +116,10 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
 
     const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = PAIR ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
-    const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
+    static_assert(!SPLIT || (CG == 1 && S::kStages * S::kStageBytes >= TN * 128 * 4), "split form");
+    const int share = SPLIT ? p.ks : CG;
+    const int part = SPLIT ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
+    const int cluster = static_cast<int>(blockIdx.x) / share, clusters = static_cast<int>(gridDim.x) / share;
     const unsigned long long tmo = p.timeout_ns;
 
     if (threadIdx.x == 0) {
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     grid_dependency_wait();  // the set-up above ran beside the end of the kernel before
 
     bool timed_out = false;
-    GroupedTile t;
+    GroupedTile t, split = {};
     SchedReader tiles{slots, sched0};
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
             const int boxes = (mine + S::kBoxCols - 1) / S::kBoxCols;
             constexpr uint32_t kBox = S::kBoxCols * 128;
             const uint32_t bytes = S::kABytes + boxes * kBox + S::kSaBytes + S::kSbBytes;
-            for (int k = 0; k < p.K; k += kMxBK) {
+            for (int k = t.k0; k < t.k0 + t.klen; k += kMxBK) {
                 if (!mbar_wait_warp<false>(empty0 + 8 * s, phase, tmo)) {
                     timed_out = true;
                     break;
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
                 break;
             }
             tc_fence_after_sync();
-            for (int k = 0; k < p.K; k += kMxBK) {
+            for (int k = 0; k < t.klen; k += kMxBK) {
                 if (!mbar_wait_warp<false>(full0 + 8 * s, phase, tmo)) {
                     timed_out = true;
                     break;
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
                 const uint32_t off = s * (S::kStageBytes / 16);
                 const uint64_t a = descA + off, b = descB + off, ca = descSa + off, cb = descSb + off;
                 const uint32_t sfa = tmem + S::kScaleCol + turn * S::kScaleCols, sfb = sfa + 8;
-                const int left = p.K - k;
+                const int left = t.klen - k;
                 if (issuer) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 128 k: one scale block of each row block
@@ -274,7 +279,10 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
         LastRound last;
         last.set<(PAIR ? TN / 64 : 1)>(mxfp4_tiles<TN>(p), clusters);
         if (!sched_run<TN>(slots, sched0, cluster, clusters, last, tmo,
-                           [&](int i, GroupedTile& u) { mxfp4_tile<TN, FT>(p, i, cur, u); }))
+                           [&](int i, GroupedTile& u) {
+                               mxfp4_tile<TN, FT>(p, i, cur, u);
+                               if constexpr (SPLIT) split_contraction(u, part, p.ks, kMxBK);
+                           }))
             timed_out = true;
     } else {
         // ------------------------------------------------------------ epilogue
@@ -309,8 +317,12 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
                 __syncwarp();
                 tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
                 tmem_wait_ld();
-                grouped_store<false>(p, patch, at + c * p.ldo, v, t.cols - c, p.F - f);
+                if constexpr (SPLIT)
+                    leave_part(base, c, 32 * q + lane, v, t.klen == 0);
+                else
+                    grouped_store<false>(p, patch, at + c * p.ldo, v, t.cols - c, p.F - f);
             }
+            if constexpr (SPLIT) split = t;
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -328,6 +340,12 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();
+    if constexpr (SPLIT) {
+        cluster_sync_all();
+        if (warp >= 3 && split.valid && !timed_out)
+            add_parts(p, base, split, part, p.ks, (warp - 3) * 32 + lane, 32 * S::kEpiWarps);
+        cluster_sync_all();
+    }
     __syncwarp();
     if (warp == 1) {
         tc_fence_after_sync();

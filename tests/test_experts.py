@@ -481,3 +481,18 @@ def test_outputs_past_2_to_the_31_elements():
         check(dw[:, rows], *wgrad64(X[:, rows], dY, [0, 5, 5, 20], 3))
     del dw
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("transw", [False, True])
+@pytest.mark.parametrize("shape", [(1, 1, 600, 130, [0, 1]), (9, 6, 3000, 136, [0, 0, 2, 2, 9, 9, 9]), (90, 1, 5000, 264, [0, 88]),
+                                   (4, 40, 2090, 72, [0, 1, 1, 2, 4] + [4] * 36)], ids=lambda s: "x".join(map(str, s[:4])))
+def test_contraction_split_over_ctas(shape, transw, dtype):
+    """Few tiles and a long contraction: a cluster of CTAs adds up its parts."""
+    T, E, K, N, offsets = shape
+    X, W = operands(T, E, K, N, dtype, 25, transw)
+    exact, bound = forward64(X, W, offsets, transw)
+    y = g.sgemm_grouped(X, W, dev(offsets), transw=transw)
+    check(y, exact, bound)
+    assert torch.equal(y, g.sgemm_grouped(X, W, dev(offsets), transw=transw))

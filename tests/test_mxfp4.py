@@ -375,3 +375,28 @@ def test_product_output_rows_of_every_alignment(pad):
         check(g.sgemm_mxfp4(a, sa, b, sb, out), va @ vb.T, va.abs() @ vb.abs().T)
         store = torch.empty(0, dtype=torch.float16, device="cuda").set_(out.untyped_storage(), 0, (out.untyped_storage().nbytes() // 2,), (1,))
         assert int(store.isnan().sum()) == 70 * pad
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("T,E,N,K,offsets", [(3, 1, 200, 5000, [0, 3]), (40, 1, 130, 2080, [0, 40]), (64, 2, 392, 9000, [0, 1, 64]),
+                                             (9, 6, 136, 4128, [0, 0, 2, 2, 9, 9, 9]), (70, 2, 128, 8192, [3, 68, 68])], ids=str)
+def test_contraction_split_over_ctas(T, E, N, K, offsets, dtype):
+    """Few tiles and a long contraction: a cluster of CTAs adds up its parts."""
+    w, sw, vw = random_mxfp4((E, N, K), 9)
+    x = torch.randn((T, K), device="cuda")
+    o = dev(offsets)
+    a, sa = g.sgemm_mxfp4_quantize(x, o)
+    va = g.sgemm_mxfp4_dequantize(a, sa, o, cols=K).double()
+    b = bounds_of(offsets, T)
+    exact = torch.zeros((T, N), dtype=torch.float64, device="cuda")
+    bound = exact.clone()
+    for e in range(E):
+        exact[b[e]: b[e + 1]] = va[b[e]: b[e + 1]] @ vw[e].T
+        bound[b[e]: b[e + 1]] = va[b[e]: b[e + 1]].abs() @ vw[e].abs().T
+    y = g.sgemm_mxfp4_grouped(a, sa, w, sw, o, dtype=dtype)
+    check(y, exact, bound)
+    assert torch.equal(y, g.sgemm_mxfp4_grouped(a, sa, w, sw, o, dtype=dtype))
+    if E == 1:
+        a, sa = g.sgemm_mxfp4_quantize(x)
+        assert torch.equal(y, g.sgemm_mxfp4(a, sa, w[0], sw[0], dtype=dtype))
