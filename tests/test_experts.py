@@ -496,3 +496,45 @@ def test_contraction_split_over_ctas(shape, transw, dtype):
     y = g.sgemm_grouped(X, W, dev(offsets), transw=transw)
     check(y, exact, bound)
     assert torch.equal(y, g.sgemm_grouped(X, W, dev(offsets), transw=transw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,K,N", [(torch.float32, 256, 384), (torch.float32, 255, 130), (torch.float16, 131, 130)], ids=str)
+def test_graphs_with_operand_copies(dtype, K, N):
+    """Calls that take a copy of their operands from the pool, recorded and replayed on other rows and groups."""
+    T, E = 200, 3
+    X, W = operands(T, E, K, N, dtype, 26)
+    dY = torch.randn((T, N), device="cuda").to(dtype)
+    o = dev([0, 60, 61, 200])
+    g.sgemm_grouped(X, W, o)  # (the library's first call on a device is made outside a capture)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = g.sgemm_grouped(X, W, o)
+        dw = g.sgemm_grouped_wgrad(X, dY, o)
+    for seed, new in ((27, [0, 0, 150, 200]), (28, [7, 100, 199, 199])):
+        X.copy_(operands(T, E, K, N, dtype, seed)[0])
+        o.copy_(dev(new))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(y, *forward64(X, W, new))
+        check(dw, *wgrad64(X, dY, new, E))
+
+
+@pytest.mark.gpu
+def test_concurrent_streams():
+    """Calls of every kind in flight on four streams at once."""
+    T, E, K, N, offsets = 700, 4, 264, 520, [0, 100, 350, 351, 700]
+    o = dev(offsets)
+    sets = []
+    for i, dtype in enumerate((torch.float32, torch.bfloat16, torch.float16, torch.float32)):
+        X, W = operands(T, E, K, N, dtype, 30 + i)
+        sets.append((X, W, torch.randn((T, N), device="cuda").to(dtype), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    results = []
+    for _ in range(3):
+        for X, W, dY, s in sets:
+            results.append((X, W, dY, g.sgemm_grouped(X, W, o, stream=s), g.sgemm_grouped_wgrad(X, dY, o, stream=s)))
+    torch.cuda.synchronize()
+    for X, W, dY, y, dw in results:
+        check(y, *forward64(X, W, offsets))
+        check(dw, *wgrad64(X, dY, offsets, E))
