@@ -538,3 +538,20 @@ def test_concurrent_streams():
     for X, W, dY, y, dw in results:
         check(y, *forward64(X, W, offsets))
         check(dw, *wgrad64(X, dY, offsets, E))
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+def test_many_tiles_of_ragged_groups(dtype):
+    """Many rounds of tiles over the GPU, of unequal groups."""
+    T, E, K, N = 5000, 8, 72, 5000
+    offsets = [0, 3, 1500, 1500, 2100, 2101, 3000, 4900, 4990]
+    X, W = operands(T, E, K, N, dtype, 40)
+    check(g.sgemm_grouped(X, W, dev(offsets)), *forward64(X, W, offsets))
+    dY = torch.randn((T, 1300), device="cuda").to(dtype)
+    X = torch.randn((T, 1500), device="cuda").to(dtype)
+    dw = g.sgemm_grouped_wgrad(X, dY, dev(offsets * 2)[: E + 1])
+    check(dw, *wgrad64(X, dY, offsets, E))
+    o = sorted(offsets * 3)[: 25]
+    dw = g.sgemm_grouped_wgrad(X, dY, dev(o))
+    check(dw, *wgrad64(X, dY, o, 24))

@@ -400,3 +400,20 @@ def test_contraction_split_over_ctas(T, E, N, K, offsets, dtype):
     if E == 1:
         a, sa = g.sgemm_mxfp4_quantize(x)
         assert torch.equal(y, g.sgemm_mxfp4(a, sa, w[0], sw[0], dtype=dtype))
+
+
+@pytest.mark.gpu
+def test_many_tiles_of_ragged_groups():
+    """Many rounds of tiles over the GPU, of unequal groups."""
+    T, E, N, K, offsets = 5000, 6, 5000, 160, [0, 3, 1500, 2100, 2101, 4000, 4990]
+    w, sw, vw = random_mxfp4((E, N, K), 10)
+    x = torch.randn((T, K), device="cuda")
+    o = dev(offsets)
+    a, sa = g.sgemm_mxfp4_quantize(x, o)
+    va = g.sgemm_mxfp4_dequantize(a, sa, o, cols=K).double()
+    exact = torch.zeros((T, N), dtype=torch.float64, device="cuda")
+    bound = exact.clone()
+    for e in range(E):
+        r = slice(offsets[e], offsets[e + 1])
+        exact[r], bound[r] = va[r] @ vw[e].T, va[r].abs() @ vw[e].abs().T
+    check(g.sgemm_mxfp4_grouped(a, sa, w, sw, o), exact, bound)
