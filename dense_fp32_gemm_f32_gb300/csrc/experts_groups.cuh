@@ -111,22 +111,6 @@ __device__ __forceinline__ int group_total(const int* offsets, int E, int T, Uni
     return total;
 }
 
-// Element types as sgemm_experts.h numbers them.
-template <int TYPE>
-struct ElemOf;
-template <>
-struct ElemOf<0> {
-    using T = float;
-};
-template <>
-struct ElemOf<1> {
-    using T = __nv_bfloat16;
-};
-template <>
-struct ElemOf<2> {
-    using T = __half;
-};
-
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }

@@ -171,15 +171,6 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, 
         : "memory");
 }
 
-// Untiled bulk copy global -> this CTA's shared memory: both addresses 16-byte
-// aligned, `bytes` a multiple of 16.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
 // The same copy with an L2 cache policy (from l2_policy_evict_last) for the
 // lines it reads.
 __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const void* map, uint32_t bar, int c0, int c1,
