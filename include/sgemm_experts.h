@@ -59,7 +59,9 @@ enum { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_BF16 = 1, SGEMM_TYPE_F16 = 2 };
  *   Y, ldy     T x N, overwritten
  * Accuracy: float32 operands as the other entries, |Y - exact| <= 5e-5 *
  * sum_k |X_tk||op(W)_kn|; bf16 and f16 operands that bound plus one rounding
- * to the type.  A non-finite operand reaches only its own row (X) or its own
+ * to the type.  (float32 operands that go to the tensor cores as parts are
+ * taken to a multiple of 2^-133, which those below 2^-118 in magnitude notice:
+ * 5e-5 holds from about 2^-122 on.)  A non-finite operand reaches only its own row (X) or its own
  * column of its expert's rows (W); where it reaches, float32 results are not
  * finite, but may be NaN where the exact result is an infinity.
  */

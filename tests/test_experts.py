@@ -555,3 +555,24 @@ def test_many_tiles_of_ragged_groups(dtype):
     o = sorted(offsets * 3)[: 25]
     dw = g.sgemm_grouped_wgrad(X, dY, dev(o))
     check(dw, *wgrad64(X, dY, o, 24))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exponent", [-100, -118, -124, -130, 100])
+def test_float32_magnitudes(exponent):
+    """Operands near the ends of float32's range: the parts hold each to within half of 2^-133, so a row's error grows by
+    2^-134 sum |w| at most; everything else is relative."""
+    T, E, K, N, offsets = 100, 2, 256, 136, [0, 50, 100]
+    X, W = operands(T, E, K, N, torch.float32, 50)
+    X = (X.double() * 2.0 ** exponent).float()
+    if exponent > 0:
+        W = (W.double() * 2.0 ** -exponent).float()
+    exact, bound = forward64(X, W, offsets)
+    granule, _ = forward64(torch.full_like(X, 2.0 ** -134), W.abs(), offsets)
+    err = (g.sgemm_grouped(X, W, dev(offsets)).double() - exact).abs()
+    if exponent > 0:
+        granule = granule + forward64(X.abs(), torch.full_like(W, 2.0 ** -134), offsets)[0]
+    assert (err <= TOL * bound + granule + 2.0 ** -149).all(), (err / bound).max().item()
+    few = g.sgemm_grouped(X[:8], W, dev([0, 4, 8])).double()  # (no parts)
+    exact, bound = forward64(X[:8], W, [0, 4, 8])
+    assert ((few - exact).abs() <= TOL * bound + K * 2.0 ** -149).all()
