@@ -11,13 +11,17 @@ namespace gb300 {
 // One operand copied for the tensor maps (experts_pack.cu): `count` matrices
 // of rows x cols at src (`ld` elements a row, `se` a matrix) to dst, rows of
 // dld elements (a multiple of 8) one after the other; float32 to three bf16
-// planes one after the other.  dst null: nothing to do.
+// planes one after the other.  dst null: nothing to do.  offsets: matrix e is
+// expert e's, and one without rows need not be copied (T: the rows in all).
 struct PackJob {
     const void* src;
     long long count, rows, ld, se;
     int cols;
     void* dst;
     long long dld;
+    const int* offsets;
+    int T;
+    long long each;  // rows of a matrix where `rows` holds all (set by experts_pack)
 };
 int experts_pack(const PackJob& a, const PackJob& b, bool f32, cudaStream_t s);
 

@@ -177,7 +177,8 @@ int grouped_tc(const GroupedCall& c, int dev, DeviceState& st, cudaStream_t s) {
         const bool copy = f32 || !tma_readable(m[i]);
         const long long dld = (m[i].cols + 7) / 8 * 8;
         if (copy) {
-            job[i] = {m[i].p, m[i].count, m[i].rows, m[i].ld, m[i].se, static_cast<int>(m[i].cols), nullptr, dld};
+            job[i] = {m[i].p, m[i].count, m[i].rows, m[i].ld, m[i].se, static_cast<int>(m[i].cols), nullptr, dld,
+                      i == 0 && !c.wgrad ? c.offsets : nullptr, c.T, 0};
             bytes[i] = (static_cast<size_t>(f32 ? 3 : 1) * m[i].count * m[i].rows * dld * 2 + 255) & ~size_t{255};
             o[i] = {nullptr, m[i].cols, m[i].rows, (f32 ? 3 : 1) * m[i].count, dld, m[i].rows * dld};
         } else {
