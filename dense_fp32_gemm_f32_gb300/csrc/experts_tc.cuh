@@ -59,13 +59,13 @@
 // than the MMAs: 775 cycles a stage of the wide tile, whose MMAs take 512.)
 //
 // Measured on GB300 (bf16 unless said; warm): 16 experts of 4096 x 4096, 16384
-// rows 293 us, 1.87 PFLOP/s, the rate of the library's plain product (1.88); the
+// rows 288 us, 1.91 PFLOP/s, the rate of the library's plain product (1.88); the
 // weights' gradient of the same 291 us; 32 experts of 2048 x 4096, 64 rows
-// 77 us, 6.9 TB/s (the weights' bytes); 8 experts of 4096 x 2048, 8192 rows 83 us
-// (dX) and 80 us (dW), 1.65 and 1.73 PFLOP/s, bound by the last round of
-// tiles; float32, 4 experts of 1024 x 2048, 2048 rows 52 us with its operands' copies
-// (15 us), 160 TFLOP/s of float32, six times that of bf16: two rounds of 128 tiles on 76
-// pairs bound it.
+// 77 us, 6.9 TB/s (the weights' bytes); 8 experts of 4096 x 2048, 8192 rows 78 us
+// (dX) and 78 us (dW), 1.76 PFLOP/s, bound by the last round of tiles (83 us
+// before its tiles were split; 90 with uneven groups); float32, 4 experts of 1024
+// x 2048, 2048 rows 52 us with its operands' copies (15 us), 160 TFLOP/s of
+// float32, six times that of bf16: two rounds of 128 tiles on 76 pairs bound it.
 //
 // Every wait is bounded by `timeout_ns`; on expiry the thread records the
 // timeout in the status word and goes to the final barrier.

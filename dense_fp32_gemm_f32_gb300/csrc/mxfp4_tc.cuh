@@ -20,7 +20,7 @@
 // for 16384 rows, 8 experts of 8192 x 4096, where the smaller tile's loads cost
 // what the overlap saves; 4096 x 4096 x 8192 43 and 40 us.)  7.1 PFLOP/s; with the
 // loads switched off 126 us, the MMAs' own time, with the MMAs off 136.  One row
-// x 8192 x 8192: 7.7 us, 4.6 TB/s, 64 tiles on 152 SMs.  Tiles are
+// x 8192 x 8192, 64 tiles shared by two CTAs each: 7.6 us, 4.7 TB/s.  Tiles are
 // multiples of 64 columns, so that a tile's scales begin 0 or 2 tensor-memory
 // columns into their block: B's scales have to begin at an even column.
 #pragma once

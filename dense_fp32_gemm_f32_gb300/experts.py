@@ -298,7 +298,8 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
             t, dev, (rows, bytes_) = _TYPES[dtype], codes.get_device(), codes.shape
             K = 2 * bytes_ if cols is None else cols
             usual = (not bytes_ % 16 and 0 <= 2 * bytes_ - K < 32 and dev >= 0
-                     and _usual_mxfp4(codes, scales, dev, (rows + 127) // 128, bytes_) and _current_device() == dev)
+                     and _usual_mxfp4(codes, scales, dev, ((rows + 127) // 128, (2 * bytes_ + 127) // 128, 32, 4, 4))
+                     and _current_device() == dev)
         except (AttributeError, ValueError, KeyError):
             usual = False
         if usual:
@@ -336,12 +337,10 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
     return out
 
 
-def _usual_mxfp4(codes, scales, dev: int, blocks, bytes_: int) -> bool:
-    """Whether an MXFP4 operand is as it should be; `blocks` its scales' row blocks (after their leading dimension, if any)."""
-    got = scales.shape
+def _usual_mxfp4(codes, scales, dev: int, shape) -> bool:
+    """Whether an MXFP4 operand is as it should be; `shape` of its scales."""
     return (codes.dtype is _uint8 and scales.dtype is _uint8 and codes.get_device() == dev and scales.get_device() == dev
-            and codes.is_contiguous() and scales.is_contiguous()
-            and got[-5:] == (blocks, (2 * bytes_ + 127) // 128, 32, 4, 4) and got[:-5] == codes.shape[:-2])
+            and scales.shape == shape and codes.is_contiguous() and scales.is_contiguous())
 
 
 def sgemm_mxfp4(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor,
@@ -350,8 +349,10 @@ def sgemm_mxfp4(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scal
     if out is None and stream is None:
         try:
             t, dev, (M, bytes_), (N, other) = _TYPES[dtype], A.get_device(), A.shape, B.shape
-            usual = (bytes_ == other and not bytes_ % 16 and dev >= 0 and _usual_mxfp4(A, a_scales, dev, (M + 127) // 128, bytes_)
-                     and _usual_mxfp4(B, b_scales, dev, (N + 127) // 128, bytes_) and _current_device() == dev)
+            kq = (2 * bytes_ + 127) // 128
+            usual = (bytes_ == other and not bytes_ % 16 and dev >= 0
+                     and _usual_mxfp4(A, a_scales, dev, ((M + 127) // 128, kq, 32, 4, 4))
+                     and _usual_mxfp4(B, b_scales, dev, ((N + 127) // 128, kq, 32, 4, 4)) and _current_device() == dev)
         except (AttributeError, ValueError, KeyError):
             usual = False
         if usual:
@@ -389,10 +390,11 @@ def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor
     if out is None and stream is None:
         try:
             t, dev, (T, bytes_), (E, N, other) = _TYPES[dtype], X.get_device(), X.shape, W.shape
+            kq = (2 * bytes_ + 127) // 128
             usual = (bytes_ == other and not bytes_ % 16 and dev >= 0 and offsets.dtype is _int32
                      and offsets.get_device() == dev and offsets.shape == (E + 1,) and offsets.is_contiguous()
-                     and _usual_mxfp4(X, x_scales, dev, _grouped_blocks(T, E), bytes_)
-                     and _usual_mxfp4(W, w_scales, dev, (N + 127) // 128, bytes_) and _current_device() == dev)
+                     and _usual_mxfp4(X, x_scales, dev, (_grouped_blocks(T, E), kq, 32, 4, 4))
+                     and _usual_mxfp4(W, w_scales, dev, (E, (N + 127) // 128, kq, 32, 4, 4)) and _current_device() == dev)
         except (AttributeError, ValueError, KeyError):
             usual = False
         if usual:
