@@ -59,7 +59,7 @@
 // than the MMAs: 775 cycles a stage of the wide tile, whose MMAs take 512.)
 //
 // Measured on GB300 (bf16 unless said; warm): 16 experts of 4096 x 4096, 16384
-// rows 288 us, 1.91 PFLOP/s, the rate of the library's plain product (1.88); the
+// rows 284 us, 1.94 PFLOP/s, the rate of the library's plain product (1.88); the
 // weights' gradient of the same 291 us; 32 experts of 2048 x 4096, 64 rows
 // 77 us, 6.9 TB/s (the weights' bytes); 8 experts of 4096 x 2048, 8192 rows 78 us
 // (dX) and 78 us (dW), 1.76 PFLOP/s, bound by the last round of tiles (83 us
@@ -153,6 +153,21 @@ __device__ __forceinline__ int grouped_tiles(const GroupedTcParams& p) {
         return group_total(p.offsets, p.E, p.T, [&](int n) { return (n + TN - 1) / TN * p.ftiles; });
 }
 
+// Place of a group's tile `local` of `n` (row tiles) x `ftiles`: feature tiles
+// in bands of 16, in which the features run fastest.  The tiles in flight then
+// share a band of the weights (4096 features at most) and a few of the rows, and
+// the shorter last tiles of a group fall on different clusters.  Against rows
+// running fastest over the whole group: 8192^3 580 -> 546 us, 16384 x 4096 x 4096
+// as one group 327 -> 312 us, over 16 uneven groups 312 -> 305 us; bands of 8
+// are no faster, and bands of 4 slow even groups down (284 -> 311 us).
+__device__ __forceinline__ void tile_place(int local, int n, int ftiles, int& f, int& row) {
+    constexpr int kBand = 16;
+    const int band = local / (kBand * n);
+    const int rest = local - band * kBand * n, width = min(kBand, ftiles - band * kBand);
+    row = rest / width;
+    f = band * kBand + rest - row * width;
+}
+
 // Tile number `i` (there is one), from the same cursor in increasing order
 // (whole warp).
 template <bool WGRAD, int TN, int FT>
@@ -169,8 +184,10 @@ __device__ __forceinline__ void grouped_tile(const GroupedTcParams& p, int i, Gr
     } else {
         (void)group_find(p.offsets, p.E, p.T, i, cur, [&](int n) { return (n + TN - 1) / TN * p.ftiles; }, h);
         const int n = max(1, (h.end - h.start + TN - 1) / TN);
-        t.f0 = h.local / n * FT;
-        t.c0 = h.start + h.local % n * TN;
+        int f, row;
+        tile_place(h.local, n, p.ftiles, f, row);
+        t.f0 = f * FT;
+        t.c0 = h.start + row * TN;
         t.cols = min(TN, h.end - t.c0);
         t.k0 = 0;
         t.klen = p.K;

@@ -85,9 +85,11 @@ __device__ __forceinline__ void mxfp4_tile(const Mxfp4TcParams& p, int i, GroupC
     if (p.offsets)
         (void)group_find(p.offsets, p.E, p.T, i, cur, [&](int n) { return (n + TN - 1) / TN * p.ftiles; }, h);
     const int n = max(1, (h.end - h.start + TN - 1) / TN);
-    const int off = h.local % n * TN;
+    int f, row;
+    tile_place(h.local, n, p.ftiles, f, row);
+    const int off = row * TN;
     t.e = h.e;
-    t.f0 = h.local / n * FT;
+    t.f0 = f * FT;
     t.c0 = h.start + off;
     t.cols = min(TN, h.end - t.c0);
     t.k0 = 0;
