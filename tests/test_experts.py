@@ -576,3 +576,16 @@ def test_float32_magnitudes(exponent):
     few = g.sgemm_grouped(X[:8], W, dev([0, 4, 8])).double()  # (no parts)
     exact, bound = forward64(X[:8], W, [0, 4, 8])
     assert ((few - exact).abs() <= TOL * bound + K * 2.0 ** -149).all()
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("shape", [(1500, 3, 72, 8704, [0, 3, 900, 1490]), (2000, 2, 40, 4200, [0, 1999, 2000]), (90, 3, 72, 6300, [0, 30, 31, 90])],
+                         ids=lambda s: "x".join(map(str, s[:4])))
+def test_forward_wide_features(shape, dtype):
+    """More feature tiles than a band of the tile order holds, the last band part full, and rows of several tiles."""
+    T, E, K, N, offsets = shape
+    X, W = operands(T, E, K, N, dtype, 60)
+    exact, bound = forward64(X, W, offsets)
+    out = torch.full((T, N), float("nan"), dtype=dtype, device="cuda")
+    check(g.sgemm_grouped(X, W, dev(offsets), out=out), exact, bound)
