@@ -29,6 +29,10 @@ namespace detail {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kChunk = 512;
+// Chunks after which a thread's sums are put by: 512 additions in a row at most
+// (128 for the transposed form) stay below 512 * 2^-24 = 3.1e-5 of the sum of
+// magnitudes, whatever the operands.
+constexpr int kChunksInARow = 8;
 
 struct FewParams {
     const float* X;
@@ -78,7 +82,28 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
         const int per = ((p.K + p.ks - 1) / p.ks + 127) & ~127;  // (parts begin on vectors)
         const int kbeg = min(p.K, rank * per), kend = min(p.K, kbeg + per);
         float acc[RT][4] = {};
-        for (int k0 = kbeg; k0 < kend; k0 += kChunk) {
+        [[maybe_unused]] float total[TRANS ? 1 : RT][4] = {};
+        // Sums so far, to `total`, or (transposed: over the lanes, one of which owns each) to `part`.
+        auto put_by = [&](bool first) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (TRANS) {
+                        float s = acc[r][j];
+#pragma unroll
+                        for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+                        float* const at = part + r * 32 + 4 * warp + j;
+                        if (lane == (r * 4 + j) % 32) *at = first ? s : *at + s;
+                    } else {
+                        total[r][j] += acc[r][j];
+                    }
+                    acc[r][j] = 0.f;
+                }
+        };
+        int chunks = 0;  // gone by
+        for (int k0 = kbeg; k0 < kend; k0 += kChunk, ++chunks) {
+            if (chunks > 0 && chunks % kChunksInARow == 0) put_by(chunks == kChunksInARow);
             const int len = min(kChunk, kend - k0);
             __syncthreads();
             // X's values: [k][row] for the plain form, [row][k] for the other; zeros past the rows and the end.
@@ -148,13 +173,14 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
                 }
             }
         }
+        put_by(chunks <= kChunksInARow);
         // The CTA's sums, to `part`.
         __syncthreads();
         if constexpr (!TRANS) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
                 *reinterpret_cast<float4*>(sm + (warp * RT + r) * 128 + 4 * lane) =
-                    make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+                    make_float4(total[r][0], total[r][1], total[r][2], total[r][3]);
             __syncthreads();
             for (int i = threadIdx.x; i < RT * 128; i += kThreads) {
                 float s = 0.f;
@@ -162,16 +188,6 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
                 for (int w = 0; w < kWarps; ++w) s += sm[w * RT * 128 + i];
                 part[i] = s;
             }
-        } else {
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float s = acc[r][j];
-#pragma unroll
-                    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-                    if (lane == (r * 4 + j) % 32) part[r * 32 + 4 * warp + j] = s;
-                }
         }
         __syncthreads();
         if (p.ks > 1) cluster_sync_all();  // the others' parts are there
