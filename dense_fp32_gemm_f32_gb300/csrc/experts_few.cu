@@ -29,10 +29,12 @@ namespace detail {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kChunk = 512;
-// Chunks after which a thread's sums are put by: 512 additions in a row at most
-// (128 for the transposed form) stay below 512 * 2^-24 = 3.1e-5 of the sum of
-// magnitudes, whatever the operands.
-constexpr int kChunksInARow = 8;
+// Contraction after which a thread's sums are put by: 512 additions in a row at
+// most stay below 512 * 2^-24 = 3.1e-5 of the sum of magnitudes, whatever the
+// operands.  Kernels of their own (LONG) do so: the loop around the chunks alone
+// costs the transposed form a fifth (32 rows, 8 experts of 1024 x 2048 17 -> 21 us).
+template <bool TRANS>
+constexpr int kInARow = (TRANS ? 32 : 8) * kChunk;
 
 struct FewParams {
     const float* X;
@@ -42,13 +44,15 @@ struct FewParams {
     const int* offsets;
     int T, E, N, K;
     int ks;  // CTAs a tile's contraction is split over
+    int per; // and the contraction of each
 };
 
 template <bool TRANS>
 constexpr int kCols = TRANS ? 32 : 128;
 
+// X's values, and for the plain form the warps' sums.
 template <bool TRANS, int RT>
-constexpr int kSmemFloats = (RT * kChunk > kWarps * RT * 128 || TRANS) ? RT * kChunk : kWarps * RT * 128;
+constexpr int kSmemFloats = RT * kChunk + (TRANS ? 0 : kWarps * RT * 128);
 
 __device__ __forceinline__ float4 load4(const float* p, int n, bool vec) {
     if (vec && n >= 4) return __ldg(reinterpret_cast<const float4*>(p));
@@ -56,7 +60,7 @@ __device__ __forceinline__ float4 load4(const float* p, int n, bool vec) {
                        n > 3 ? __ldg(p + 3) : 0.f);
 }
 
-template <bool TRANS, int RT>
+template <bool TRANS, int RT, bool LONG>
 __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
     extern __shared__ float sm[];
     __shared__ GroupHit hit;
@@ -79,14 +83,19 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
     if (found) {  // (all CTAs of a cluster alike)
         const int r0 = hit.start + hit.local * RT, rows = min(RT, hit.end - r0);
         const float* const W = p.W + hit.e * p.sw;
-        const int per = ((p.K + p.ks - 1) / p.ks + 127) & ~127;  // (parts begin on vectors)
-        const int kbeg = min(p.K, rank * per), kend = min(p.K, kbeg + per);
+        const int kbeg = min(p.K, rank * p.per), kend = min(p.K, kbeg + p.per);
         float acc[RT][4] = {};
-        [[maybe_unused]] float total[TRANS ? 1 : RT][4] = {};
-        // Sums so far, to `total`, or (transposed: over the lanes, one of which owns each) to `part`.
+        float* const sums = sm + RT * kChunk + (warp * RT * 128 + 4 * lane);  // (plain form: 128 apart)
+        // The sums in `acc` to shared memory: the thread's own, or (transposed) over the lanes, one of which owns each.
         auto put_by = [&](bool first) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RT; ++r) {
+                if constexpr (!TRANS) {
+                    float4* const at = reinterpret_cast<float4*>(sums + r * 128);
+                    float4 v = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+                    if (!first) v = make_float4(at->x + v.x, at->y + v.y, at->z + v.z, at->w + v.w);
+                    *at = v;
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if constexpr (TRANS) {
@@ -95,97 +104,94 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
                         for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
                         float* const at = part + r * 32 + 4 * warp + j;
                         if (lane == (r * 4 + j) % 32) *at = first ? s : *at + s;
-                    } else {
-                        total[r][j] += acc[r][j];
                     }
                     acc[r][j] = 0.f;
                 }
-        };
-        int chunks = 0;  // gone by
-        for (int k0 = kbeg; k0 < kend; k0 += kChunk, ++chunks) {
-            if (chunks > 0 && chunks % kChunksInARow == 0) put_by(chunks == kChunksInARow);
-            const int len = min(kChunk, kend - k0);
-            __syncthreads();
-            // X's values: [k][row] for the plain form, [row][k] for the other; zeros past the rows and the end.
-            for (int i = threadIdx.x; i < RT * kChunk; i += kThreads) {
-                const int r = i / kChunk, k = i % kChunk;
-                const float v = r < rows && k < len ? __ldg(p.X + (r0 + r) * p.ldx + k0 + k) : 0.f;
-                sm[TRANS ? i : k * RT + r] = v;
             }
-            __syncthreads();
-            if constexpr (!TRANS) {
-                const int c = c0 + 4 * lane, n = p.N - c;
-                const float* w0 = W + static_cast<long long>(k0) * p.ldw + c;
-                const bool vec = (reinterpret_cast<uintptr_t>(w0) & 15) == 0 && p.ldw % 4 == 0;
-                constexpr int kU = 8;  // loads under way
-                for (int k = warp; k < len; k += kWarps * kU) {
-                    float4 w[kU];
+        };
+        int from = kbeg;
+        do {
+            const int to = LONG ? min(kend, from + kInARow<TRANS>) : kend;
+            for (int k0 = from; k0 < to; k0 += kChunk) {
+                const int len = min(kChunk, kend - k0);
+                __syncthreads();
+                // X's values: [k][row] for the plain form, [row][k] for the other; zeros past the rows and the end.
+                for (int i = threadIdx.x; i < RT * kChunk; i += kThreads) {
+                    const int r = i / kChunk, k = i % kChunk;
+                    const float v = r < rows && k < len ? __ldg(p.X + (r0 + r) * p.ldx + k0 + k) : 0.f;
+                    sm[TRANS ? i : k * RT + r] = v;
+                }
+                __syncthreads();
+                if constexpr (!TRANS) {
+                    const int c = c0 + 4 * lane, n = p.N - c;
+                    const float* w0 = W + static_cast<long long>(k0) * p.ldw + c;
+                    const bool vec = (reinterpret_cast<uintptr_t>(w0) & 15) == 0 && p.ldw % 4 == 0;
+                    constexpr int kU = 8;  // loads under way
+                    for (int k = warp; k < len; k += kWarps * kU) {
+                        float4 w[kU];
 #pragma unroll
-                    for (int u = 0; u < kU; ++u) {
-                        const int kk = k + u * kWarps;
-                        w[u] = load4(w0 + kk * p.ldw, kk < len ? n : 0, vec);
-                    }
+                        for (int u = 0; u < kU; ++u) {
+                            const int kk = k + u * kWarps;
+                            w[u] = load4(w0 + kk * p.ldw, kk < len ? n : 0, vec);
+                        }
 #pragma unroll
-                    for (int u = 0; u < kU; ++u) {
-                        const int kk = min(k + u * kWarps, kChunk - 1);  // (past the chunk: w is 0)
-                        const float4* x = reinterpret_cast<const float4*>(sm + kk * RT);
+                        for (int u = 0; u < kU; ++u) {
+                            const int kk = min(k + u * kWarps, kChunk - 1);  // (past the chunk: w is 0)
+                            const float4* x = reinterpret_cast<const float4*>(sm + kk * RT);
 #pragma unroll
-                        for (int r = 0; r < RT; r += 4) {
-                            const float4 v = x[r / 4];
-                            const float xs[4] = {v.x, v.y, v.z, v.w};
+                            for (int r = 0; r < RT; r += 4) {
+                                const float4 v = x[r / 4];
+                                const float xs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                acc[r + i][0] = fmaf(xs[i], w[u].x, acc[r + i][0]);
-                                acc[r + i][1] = fmaf(xs[i], w[u].y, acc[r + i][1]);
-                                acc[r + i][2] = fmaf(xs[i], w[u].z, acc[r + i][2]);
-                                acc[r + i][3] = fmaf(xs[i], w[u].w, acc[r + i][3]);
+                                for (int i = 0; i < 4; ++i) {
+                                    acc[r + i][0] = fmaf(xs[i], w[u].x, acc[r + i][0]);
+                                    acc[r + i][1] = fmaf(xs[i], w[u].y, acc[r + i][1]);
+                                    acc[r + i][2] = fmaf(xs[i], w[u].z, acc[r + i][2]);
+                                    acc[r + i][3] = fmaf(xs[i], w[u].w, acc[r + i][3]);
+                                }
                             }
                         }
                     }
-                }
-            } else {
-                const int c = c0 + 4 * warp;
-                const bool vec = p.ldw % 4 == 0 && (reinterpret_cast<uintptr_t>(W + k0) & 15) == 0;
-                for (int k = 4 * lane; k < len; k += 256) {  // two steps of 128 k under way
-                    float4 w[2][4];
+                } else {
+                    const int c = c0 + 4 * warp;
+                    const bool vec = p.ldw % 4 == 0 && (reinterpret_cast<uintptr_t>(W + k0) & 15) == 0;
+                    for (int k = 4 * lane; k < len; k += 256) {  // two steps of 128 k under way
+                        float4 w[2][4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int kk = k + 128 * u;
-                            w[u][j] = load4(W + (c + j) * p.ldw + k0 + kk, c + j < p.N ? len - kk : 0, vec);
-                        }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int kk = min(k + 128 * u, kChunk - 4);
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            const float4 x = *reinterpret_cast<const float4*>(sm + r * kChunk + kk);
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                acc[r][j] = fmaf(x.x, w[u][j].x, acc[r][j]);
-                                acc[r][j] = fmaf(x.y, w[u][j].y, acc[r][j]);
-                                acc[r][j] = fmaf(x.z, w[u][j].z, acc[r][j]);
-                                acc[r][j] = fmaf(x.w, w[u][j].w, acc[r][j]);
+                                const int kk = k + 128 * u;
+                                w[u][j] = load4(W + (c + j) * p.ldw + k0 + kk, c + j < p.N ? len - kk : 0, vec);
+                            }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int kk = min(k + 128 * u, kChunk - 4);
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                const float4 x = *reinterpret_cast<const float4*>(sm + r * kChunk + kk);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    acc[r][j] = fmaf(x.x, w[u][j].x, acc[r][j]);
+                                    acc[r][j] = fmaf(x.y, w[u][j].y, acc[r][j]);
+                                    acc[r][j] = fmaf(x.z, w[u][j].z, acc[r][j]);
+                                    acc[r][j] = fmaf(x.w, w[u][j].w, acc[r][j]);
+                                }
                             }
                         }
                     }
                 }
             }
-        }
-        put_by(chunks <= kChunksInARow);
+            put_by(!LONG || from == kbeg);
+            from = to;
+        } while (LONG && from < kend);
         // The CTA's sums, to `part`.
         __syncthreads();
         if constexpr (!TRANS) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-                *reinterpret_cast<float4*>(sm + (warp * RT + r) * 128 + 4 * lane) =
-                    make_float4(total[r][0], total[r][1], total[r][2], total[r][3]);
-            __syncthreads();
             for (int i = threadIdx.x; i < RT * 128; i += kThreads) {
                 float s = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) s += sm[w * RT * 128 + i];
+                for (int w = 0; w < kWarps; ++w) s += sm[RT * kChunk + w * RT * 128 + i];
                 part[i] = s;
             }
         }
@@ -228,6 +234,7 @@ int launch(FewParams p, int sms, cudaStream_t s) {
     // instead of 12 for 32 rows, 8 experts of 1024 x 2048.)
     p.ks = 1;
     while (p.ks < 8 && 2 * p.ks * cols * std::min(p.T, p.E) <= sms && p.K >= 2 * p.ks * 128) p.ks *= 2;
+    p.per = ((p.K + p.ks - 1) / p.ks + 127) & ~127;  // (parts begin on vectors)
     if (tiles > 65535 || cols * p.ks > 0x7fffffffll) return SGEMM_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cols * p.ks), static_cast<unsigned>(tiles));
@@ -240,7 +247,8 @@ int launch(FewParams p, int sms, cudaStream_t s) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = p.ks > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, few_kernel<TRANS, RT>, p) != cudaSuccess) {
+    const auto kernel = p.per > kInARow<TRANS> ? few_kernel<TRANS, RT, true> : few_kernel<TRANS, RT, false>;
+    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -249,10 +257,11 @@ int launch(FewParams p, int sms, cudaStream_t s) {
 
 template <bool TRANS, int RT>
 int set_up() {
-    return cudaFuncSetAttribute(few_kernel<TRANS, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSmemFloats<TRANS, RT> * sizeof(float)) == cudaSuccess
-               ? SGEMM_OK
-               : SGEMM_ERR_CUDA;
+    for (const auto kernel : {few_kernel<TRANS, RT, false>, few_kernel<TRANS, RT, true>})
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmemFloats<TRANS, RT> * sizeof(float)) != cudaSuccess)
+            return SGEMM_ERR_CUDA;
+    return SGEMM_OK;
 }
 
 }  // namespace
