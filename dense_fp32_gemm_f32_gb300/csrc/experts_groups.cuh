@@ -129,4 +129,16 @@ __device__ __forceinline__ __half from_f32<__half>(float v) {
     return __float2half_rn(v);
 }
 
+// Two of them, the first in the low bits (one instruction).
+template <typename T>
+__device__ __forceinline__ uint32_t pair_from_f32(float lo, float hi) {
+    if constexpr (__is_same(T, __nv_bfloat16)) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
 }  // namespace gb300

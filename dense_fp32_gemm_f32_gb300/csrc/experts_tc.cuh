@@ -26,8 +26,8 @@
 // dropped ones are below 2^-24 |a||b| together.  The error grows with the number
 // of additions into one accumulator (as if each cut and did not round), so
 // x0 y0 has an accumulator of its own, the five small products another (256
-// times smaller), and every kGrChunk of the contraction both go to float32
-// registers, which round to nearest.  Measured against 64 bits, in the 2-norm,
+// times smaller), and every 512 of the contraction both go to float32
+// registers, which round to nearest (kGrChunk; 16-bit operands every 1024).  Measured against 64 bits, in the 2-norm,
 // for a contraction of 2048: 2.1e-6 with one accumulator, 5e-7 so.
 //
 // Persistent CTAs (CG = 1) or CTA pairs (CG = 2: one instruction of the pair's
@@ -84,8 +84,15 @@ namespace gb300 {
 constexpr int kGrBK = 64;                // contraction per ring stage (128 bytes of 16-bit values)
 constexpr unsigned int kGrStatusTimeout = 4u;  // the library's timeout bit
 
-// Contraction after which float32's accumulators go to registers.
-constexpr int kGrChunk = 512;
+// Contraction after which the accumulators go to float32 registers.  Measured:
+// an instruction cuts each of its 16 products 25 bits below the largest of
+// them and the accumulator, and their sum to 24 bits, so that it loses up to
+// 16 * 2^-25 + 2^-23 = 6e-7 of the sum of magnitudes so far; 64 instructions
+// stay below 3.9e-5 of it whatever the operands.  With one accumulator for the
+// whole contraction, positive bf16 operands were off by 7.9e-5 for 16384 rows
+// and 8e-4 for 131072.
+template <int PARTS>
+constexpr int kGrChunk = PARTS > 1 ? 512 : 1024;
 
 struct GroupedTcParams {
     const int* offsets;
@@ -389,9 +396,7 @@ __device__ __forceinline__ void store_rows(uint32_t patch, int align, T* o, long
                     if constexpr (sizeof(T) == 4) {
                         w[j] = __float_as_uint(as_f32(v[c + 4 * i + j]));
                     } else {
-                        const T lo = from_f32<T>(as_f32(v[8 * i + 2 * j])), hi = from_f32<T>(as_f32(v[8 * i + 2 * j + 1]));
-                        w[j] = *reinterpret_cast<const unsigned short*>(&lo) |
-                               static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(&hi)) << 16;
+                        w[j] = pair_from_f32<T>(as_f32(v[8 * i + 2 * j]), as_f32(v[8 * i + 2 * j + 1]));
                     }
                 }
                 sts128i(patch_at(patch, lane, 16 * i), make_int4(w[0], w[1], w[2], w[3]));
@@ -436,11 +441,12 @@ __device__ __forceinline__ void split_contraction(GroupedTile& t, int part, int 
 
 // Its sums, columns c .. c + 31 of feature f, to the (idle) ring: a column a
 // row of 128.
-__device__ __forceinline__ void leave_part(uint32_t ring, int c, int f, const uint32_t (&v)[32], bool zero) {
+template <typename V>
+__device__ __forceinline__ void leave_part(uint32_t ring, int c, int f, const V (&v)[32]) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ring + static_cast<uint32_t>(((c + j) * 128 + f) * 4)),
-                     "r"(zero ? 0u : v[j])
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(ring + static_cast<uint32_t>(((c + j) * 128 + f) * 4)),
+                     "f"(as_f32(v[j]))
                      : "memory");
 }
 
@@ -635,7 +641,7 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
             if (rank != 0 && !WGRAD) continue;  // (the first CTA issues for both)
             const uint32_t idesc = p.idesc | static_cast<uint32_t>((t.cols + 15) >> 4) << 18;
             const bool tail = WGRAD && grouped_tail(t.klen % kGrBK ? t.klen % kGrBK : kGrBK);
-            const int chunk = PARTS > 1 ? kGrChunk : t.klen;
+            constexpr int chunk = kGrChunk<PARTS>;
             int k = 0;
             do {
                 const int buf = unit & 1;
@@ -786,43 +792,78 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
                 __syncwarp();
                 ++unit;
             };
+            constexpr int kStep = 8 * S::kEpiWarps;  // the warp's columns: 32 of every kStep, from 32 `half` on
             uint32_t acc;
-            if constexpr (SPLIT) {
+            if constexpr (PARTS == 1) {
                 if (!wait(acc)) {
                     timed_out = true;
                     break;
                 }
-                for (int c = 32 * half; c < t.cols; c += 8 * S::kEpiWarps) {
+                if (t.klen > kGrChunk<PARTS>) {
+                    // All accumulators' sums, left in the last.  (So the stores below have the
+                    // registers to themselves; 16 columns a load for the same reason.)
+                    float sum[TN / kStep][32] = {};
+                    for (int k = kGrChunk<PARTS>;; k += kGrChunk<PARTS>) {
+#pragma unroll
+                        for (int i = 0; i < TN / kStep; ++i) {
+                            const int c = 32 * half + kStep * i;
+                            if (c < t.cols) {
+#pragma unroll
+                                for (int h = 0; h < 32; h += 16) {
+                                    uint32_t v[16];
+                                    __syncwarp();
+                                    tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(c + h), v);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) sum[i][h + j] += __uint_as_float(v[j]);
+                                }
+                            }
+                        }
+                        if (k >= t.klen) break;
+                        release();
+                        if (!wait(acc)) {
+                            timed_out = true;
+                            break;
+                        }
+                    }
+                    if (timed_out) break;
+#pragma unroll
+                    for (int i = 0; i < TN / kStep; ++i) {
+                        const int c = 32 * half + kStep * i;
+                        if (c < t.cols) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t v[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(sum[i][h + j]);
+                                __syncwarp();
+                                tmem_st_32x32b_x16(acc + static_cast<uint32_t>(c + h), v);
+                            }
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                for (int c = 32 * half; c < t.cols; c += kStep) {
                     uint32_t v[32];
                     __syncwarp();
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
                     tmem_wait_ld();
-                    leave_part(base, c, 32 * q + lane, v, t.klen == 0);
-                }
-                split = t;
-                release();
-            } else if constexpr (PARTS == 1) {
-                if (!wait(acc)) {
-                    timed_out = true;
-                    break;
-                }
-                for (int c = 32 * half; c < t.cols; c += 8 * S::kEpiWarps) {
-                    uint32_t v[32];
-                    __syncwarp();
-                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
-                    tmem_wait_ld();
-                    if (WGRAD && t.klen == 0) {  // no MMA wrote the accumulator
+                    if ((WGRAD || SPLIT) && t.klen == 0) {  // no MMA wrote the accumulator
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0;
                     }
-                    store(c, v);
+                    if constexpr (SPLIT)
+                        leave_part(base, c, 32 * q + lane, v);
+                    else
+                        store(c, v);
                 }
+                if constexpr (SPLIT) split = t;
                 release();
             } else {
                 float sum[TN];
 #pragma unroll
                 for (int j = 0; j < TN; ++j) sum[j] = 0.f;
-                for (int k = 0; k < t.klen || k == 0; k += kGrChunk) {
+                for (int k = 0; k < t.klen || k == 0; k += kGrChunk<PARTS>) {
                     if (!wait(acc)) {
                         timed_out = true;
                         break;

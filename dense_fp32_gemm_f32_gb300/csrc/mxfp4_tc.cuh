@@ -319,10 +319,15 @@ __global__ void __launch_bounds__(Mxfp4Shape<TN, CG>::kThreads, 1)
                 __syncwarp();
                 tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), v);
                 tmem_wait_ld();
-                if constexpr (SPLIT)
-                    leave_part(base, c, 32 * q + lane, v, t.klen == 0);
-                else
+                if constexpr (SPLIT) {
+                    if (t.klen == 0) {  // no MMA wrote the accumulator
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0;
+                    }
+                    leave_part(base, c, 32 * q + lane, v);
+                } else {
                     grouped_store<false>(p, patch, at + c * p.ldo, v, t.cols - c, p.F - f);
+                }
             }
             if constexpr (SPLIT) split = t;
             tc_fence_before_sync();

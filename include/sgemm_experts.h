@@ -59,11 +59,14 @@ enum { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_BF16 = 1, SGEMM_TYPE_F16 = 2 };
  *   Y, ldy     T x N, overwritten
  * Accuracy: float32 operands as the other entries, |Y - exact| <= 5e-5 *
  * sum_k |X_tk||op(W)_kn|; bf16 and f16 operands that bound plus one rounding
- * to the type.  (float32 operands that go to the tensor cores as parts are
- * taken to a multiple of 2^-133, which those below 2^-118 in magnitude notice:
- * 5e-5 holds from about 2^-122 on.)  A non-finite operand reaches only its own row (X) or its own
- * column of its expert's rows (W); where it reaches, float32 results are not
- * finite, but may be NaN where the exact result is an infinity.
+ * to the type.  It holds whatever the operands' signs and magnitudes for
+ * contractions up to 2^17 (what goes into one accumulator is limited); every
+ * further 2^10 may add 2^-22 times the sum.  (float32 operands that go to the
+ * tensor cores as parts are taken to a multiple of 2^-133, which those below
+ * 2^-118 in magnitude notice: 5e-5 holds from about 2^-122 on.)
+ * A non-finite operand reaches only its own row (X) or its own column of its
+ * expert's rows (W); where it reaches, float32 results are not finite, but may
+ * be NaN where the exact result is an infinity.
  */
 int sgemm_grouped(int type, int transw, int T, int E, int N, int K,
                   const void* X, int64_t ldx,
@@ -83,6 +86,7 @@ int sgemm_grouped(int type, int transw, int T, int E, int N, int K,
  *   out_type   of dW: `type` or SGEMM_TYPE_F32
  *   X, ldx     T x K;   dY, lddy   T x N
  *   dW, lddw, stride_dw   E matrices, overwritten
+ * Accuracy as sgemm_grouped; the contraction is an expert's rows.
  */
 int sgemm_grouped_wgrad(int type, int out_type, int T, int E, int K, int N,
                         const void* X, int64_t ldx,

@@ -3,13 +3,28 @@ or rounds away at each step adds up instead of cancelling.
 
 The acceptance is the one of test_experts.py, the bound that the header states: 5e-5 sum |a||b|, and the output's rounding.
 Where it comes from, for a contraction of K <= 2^17:
+* tensor cores, 16-bit operands: an instruction cuts each of its 16 products 2^-25 below the largest magnitude in it and the
+  sum 2^-23 below, 6e-7 of sum |a||b|; 64 of them go into one accumulator, 3.9e-5, and each accumulator is added to a
+  float32 register, 2^-24 each: K / 1024 * 2^-24 = 7.6e-6.
+* float32 in parts: 32 instructions of the leading products into one accumulator, 1.9e-5; K / 512 * 2 additions, 3.1e-5 at
+  2^17, 1.1e-5 for the 45000 here.
 * float32, few rows: 512 additions in a row at 2^-24, 3.1e-5, and K / 4096 more.
 """
 import pytest
 import torch
 
 import dense_fp32_gemm_f32_gb300 as g
-from test_experts import check, dev, forward64
+from test_experts import TYPES, check, dev, forward64, typed, wgrad64
+
+
+def positive(shape, kind, gen, dtype):
+    """Positive values, the contraction along dimension -2: "even" in [1/2, 1); "peak" with a first row 2^9 times as large
+    (2^18 in a product of two such operands)."""
+    x = torch.rand(shape, generator=gen, device="cuda") * 0.5 + 0.5
+    if kind == "peak":
+        x *= 2.0 ** -6
+        x[..., 0, :] *= 2.0 ** 9
+    return x.to(dtype)
 
 
 @pytest.fixture(autouse=True)
@@ -19,6 +34,38 @@ def no_wait_gave_up():
 
 
 pytestmark = pytest.mark.gpu
+
+
+@typed(TYPES)
+@pytest.mark.parametrize("kind", ["even", "peak"])
+@pytest.mark.parametrize("out32", [False, True])
+@pytest.mark.parametrize("K,N,E,T,offsets", [(72, 136, 3, 45000, [5, 15, 44990, 45000]), (1032, 1500, 2, 9000, [0, 8990, 9000])], ids=["narrow", "wide"])
+def test_wgrad(K, N, E, T, offsets, kind, out32, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    X, dY = positive((T, K), "even", gen, dtype), positive((T, N), "even", gen, dtype)
+    for e in range(E):
+        if offsets[e] < offsets[e + 1]:
+            rows = slice(offsets[e], offsets[e + 1])
+            X[rows], dY[rows] = (positive((rows.stop - rows.start, n), kind, gen, dtype) for n in (K, N))
+    dw = g.sgemm_grouped_wgrad(X, dY, dev(offsets), dtype=torch.float32 if out32 else None)
+    check(dw, *wgrad64(X, dY, offsets, E))
+
+
+# (rows, columns, contraction): a contraction shared by a cluster, single CTAs, pairs with both widths of tile
+FORWARD = [(3, 200, 45000), (40, 10300, 9000), (150, 400, 45000), (2000, 2000, 9000)]
+
+
+@typed(TYPES)
+@pytest.mark.parametrize("kind", ["even", "peak"])
+@pytest.mark.parametrize("transw", [False, True])
+@pytest.mark.parametrize("T,N,K", FORWARD)
+def test_forward(T, N, K, transw, kind, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    X, W = positive((K, T), kind, gen, dtype).T.contiguous(), positive((1, K, N), kind, gen, dtype)
+    if transw:
+        W = W.mT.contiguous()
+    offsets = [0, T]
+    check(g.sgemm_grouped(X, W, dev(offsets), transw=transw), *forward64(X, W, offsets, transw))
 
 
 @pytest.mark.parametrize("transw", [False, True])
