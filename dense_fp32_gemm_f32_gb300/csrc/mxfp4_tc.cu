@@ -23,10 +23,10 @@ int encode_bytes(CUtensorMap* map, const void* p, CUtensorMapDataType type, int 
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
 
-template <int TN, int CG, bool SPLIT = false>
+template <int TN, int CG, bool SPLIT = false, bool LONG = false>
 int launch(const CUtensorMap (&m)[4], const Mxfp4TcParams& p, long long tiles, const DeviceState& st,
            cudaStream_t s) {
-    using S = Mxfp4Shape<TN, CG>;
+    using S = Mxfp4Shape<TN, CG, LONG>;
     const int share = SPLIT ? p.ks : CG;  // CTAs of a cluster
     cudaLaunchConfig_t cfg = {};
     // (a pair's tiles may be split into columns of 64: LastRound)
@@ -46,17 +46,17 @@ int launch(const CUtensorMap (&m)[4], const Mxfp4TcParams& p, long long tiles, c
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = share > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, mxfp4_tc_kernel<TN, CG, SPLIT>, m[0], m[1], m[2], m[3], p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, mxfp4_tc_kernel<TN, CG, SPLIT, LONG>, m[0], m[1], m[2], m[3], p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
     return SGEMM_OK;
 }
 
-template <int TN, int CG, bool SPLIT = false>
+template <int TN, int CG, bool SPLIT = false, bool LONG = false>
 int set_up() {
-    return cudaFuncSetAttribute(mxfp4_tc_kernel<TN, CG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Mxfp4Shape<TN, CG>::kSmem) == cudaSuccess
+    return cudaFuncSetAttribute(mxfp4_tc_kernel<TN, CG, SPLIT, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Mxfp4Shape<TN, CG, LONG>::kSmem) == cudaSuccess
                ? SGEMM_OK
                : SGEMM_ERR_CUDA;
 }
@@ -64,7 +64,8 @@ int set_up() {
 }  // namespace
 
 int mxfp4_tc_set_up() {
-    if (set_up<64, 1, true>() || set_up<64, 1>() || set_up<192, 2>()) {
+    if (set_up<64, 1, true>() || set_up<64, 1>() || set_up<192, 2>() || set_up<64, 1, true, true>() ||
+        set_up<64, 1, false, true>() || set_up<192, 2, false, true>()) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -100,6 +101,10 @@ int mxfp4_tc(const Mxfp4Call& c, const DeviceState& st, cudaStream_t s) {
                           narrow ? Mxfp4Shape<64, 1>::kSbBlocks : Mxfp4Shape<192, 2>::kSbBlocks, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc != SGEMM_OK) return rc;
     p.ks = narrow ? split_parts(tiles, p.K, 1024, st.sm_count) : 1;
+    if (p.K > static_cast<long long>(kMxChunk) * p.ks) {  // (of a cluster's part)
+        if (p.ks > 1) return launch<64, 1, true, true>(m, p, tiles, st, s);
+        return narrow ? launch<64, 1, false, true>(m, p, tiles, st, s) : launch<192, 2, false, true>(m, p, tiles, st, s);
+    }
     if (p.ks > 1) return launch<64, 1, true>(m, p, tiles, st, s);
     return narrow ? launch<64, 1>(m, p, tiles, st, s) : launch<192, 2>(m, p, tiles, st, s);
 }

@@ -155,7 +155,7 @@ int sgemm_mxfp4_dequantize(int type, int batch, int rows, int K,
  * sgemm_mxfp4 -- C = A B^T of two MXFP4 matrices, A (M x K) and B (N x K), both
  * quantised along K; C (M x N) of out_type.  Products and scales are exact,
  * sums are in float32 (|C - exact| <= 5e-5 * sum_k |a||b| plus the rounding to
- * out_type).
+ * out_type, for contractions up to 2^20).
  */
 int sgemm_mxfp4(int out_type, int M, int N, int K,
                 const uint8_t* A, const uint8_t* a_scales,

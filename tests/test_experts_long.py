@@ -9,12 +9,13 @@ Where it comes from, for a contraction of K <= 2^17:
 * float32 in parts: 32 instructions of the leading products into one accumulator, 1.9e-5; K / 512 * 2 additions, 3.1e-5 at
   2^17, 1.1e-5 for the 45000 here.
 * float32, few rows: 512 additions in a row at 2^-24, 3.1e-5, and K / 4096 more.
+* MXFP4: an instruction of 64 cuts the sum 2^-23 below; 256 of them, 3.1e-5; K / 16384 additions.
 """
 import pytest
 import torch
 
 import dense_fp32_gemm_f32_gb300 as g
-from test_experts import TYPES, check, dev, forward64, typed, wgrad64
+from test_experts import TYPES, bounds_of, check, dev, forward64, typed, wgrad64
 
 
 def positive(shape, kind, gen, dtype):
@@ -82,3 +83,51 @@ def test_few_rows_of_products_just_below_a_rounding(T, transw):
     y = g.sgemm_grouped(X, W, dev([0, T]), transw=transw)
     assert torch.equal(y, y[:, :1].expand_as(y))
     check(y[:, :32], exact, bound)
+
+
+# (rows, columns, contraction): a contraction shared by a cluster (one accumulator a CTA, several), single CTAs, pairs
+PRODUCTS = [(3, 200, 100000), (3, 200, 262144), (20, 200, 140000), (40, 10300, 20000), (300, 200, 131072), (900, 700, 40000)]
+
+
+@typed([torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["peak", "blocks"])
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+def test_mxfp4(M, N, K, kind, dtype):
+    """"peak": a first block of 32 whose products are 2^20 times as large; "blocks": blocks of magnitudes within 2^12."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def operand(rows):
+        x = torch.rand((rows, K), generator=gen, device="cuda") * 0.9 + 0.1
+        if kind == "peak":
+            x[:, :32] *= 2.0 ** 10
+        else:
+            s = torch.exp2(torch.randint(-6, 7, (rows, (K + 31) // 32, 1), generator=gen, device="cuda").float())
+            x *= s.expand(-1, -1, 32).reshape(rows, -1)[:, :K]
+        codes, scales = g.sgemm_mxfp4_quantize(x)
+        return codes, scales, g.sgemm_mxfp4_dequantize(codes, scales, cols=K)
+
+    (a, sa, va), (b, sb, vb) = operand(M), operand(N)
+    c = g.sgemm_mxfp4(a, sa, b, sb, dtype=dtype)
+    vb = vb[-512:].double()  # (the last columns)
+    exact = va.double() @ vb.T
+    check(c[:, -512:], exact, exact.abs())
+
+
+@pytest.mark.parametrize("T,offsets", [(500, [3, 200, 201, 500]), (30, [0, 0, 20, 29])], ids=str)
+def test_mxfp4_grouped(T, offsets):
+    """Groups of unequal sizes, a contraction past one accumulator's that ends inside a slice."""
+    K, N, E = 33000, 264, 3
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.rand((T, K), generator=gen, device="cuda") * torch.exp2(
+        torch.randint(-6, 7, (T, 1), generator=gen, device="cuda").float())
+    w = torch.rand((E, N, K), generator=gen, device="cuda")
+    o = dev(offsets)
+    a, sa = g.sgemm_mxfp4_quantize(x, o)
+    b, sb = g.sgemm_mxfp4_quantize(w)
+    va, vb = g.sgemm_mxfp4_dequantize(a, sa, o, cols=K).double(), g.sgemm_mxfp4_dequantize(b, sb, cols=K).double()
+    bounds = bounds_of(offsets, T)
+    exact = torch.zeros((T, N), dtype=torch.float64, device="cuda")
+    for e in range(E):
+        exact[bounds[e]: bounds[e + 1]] = va[bounds[e]: bounds[e + 1]] @ vb[e].T
+    out = torch.full((T, N), float("nan"), device="cuda")
+    check(g.sgemm_mxfp4_grouped(a, sa, b, sb, o, out), exact, exact.abs())
