@@ -133,7 +133,6 @@ int init_device(int dev, DeviceState& st) {
         set_smem_attr(tf32x3_wide_kernel()) != SGEMM_OK || set_smem_attr(tf32x3_wide_pb_kernel()) != SGEMM_OK ||
         set_smem_attr(tf32x3_res_kernel()) != SGEMM_OK)
         return SGEMM_ERR_CUDA;
-    if (experts_tc_set_up(st) != SGEMM_OK || experts_few_set_up() != SGEMM_OK || mxfp4_tc_set_up() != SGEMM_OK) return SGEMM_ERR_CUDA;
     const KernelEntry ref = ffma_kernel_tma(4, kMathFfma2);
     st.max_clusters_split[1] = st.sm_count;
     for (int s = 2; s <= 8; ++s) st.max_clusters_split[s] = max_active_clusters(ref, 1, s);
@@ -144,6 +143,10 @@ int init_device(int dev, DeviceState& st) {
     // stream capture has to create it (which the capture would not allow).
     // (Without it, those calls fail; the rest work.)
     (void)workspace_pool(dev, st);
+    // The grouped and MXFP4 products; the other entries work without them.
+    st.experts_status = experts_tc_set_up(st) != SGEMM_OK || experts_few_set_up() != SGEMM_OK || mxfp4_tc_set_up() != SGEMM_OK
+                            ? SGEMM_ERR_CUDA
+                            : SGEMM_OK;
     return SGEMM_OK;
 }
 
@@ -318,6 +321,11 @@ int current_device(int* dev_out, DeviceState** st_out) {
     *dev_out = dev;
     *st_out = &st;
     return st.status;
+}
+
+int experts_device(int* dev_out, DeviceState** st_out) {
+    const int rc = current_device(dev_out, st_out);
+    return rc != SGEMM_OK ? rc : (*st_out)->experts_status;
 }
 
 }  // namespace detail

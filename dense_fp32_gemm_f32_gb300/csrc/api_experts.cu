@@ -83,7 +83,7 @@ int sgemm_grouped(int type, int transw, int T, int E, int N, int K, const void* 
     if (y.empty()) return SGEMM_OK;
     int dev = 0;
     DeviceState* st = nullptr;
-    const int rc = current_device(&dev, &st);
+    const int rc = experts_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (E == 0 || K == 0) return zero_rows(Y, 1, T, N, ldy, 0, size, s);
@@ -112,7 +112,7 @@ int sgemm_grouped_wgrad(int type, int out_type, int T, int E, int K, int N, cons
     if (dw.empty()) return SGEMM_OK;
     int dev = 0;
     DeviceState* st = nullptr;
-    const int rc = current_device(&dev, &st);
+    const int rc = experts_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return zero_rows(dW, E, K, N, lddw, stride_dw, osize, s);
@@ -186,7 +186,7 @@ static int mxfp4_product(int out_type, int T, int E, int N, int K, const uint8_t
     if (y.empty()) return SGEMM_OK;
     int dev = 0;
     DeviceState* st = nullptr;
-    const int rc = current_device(&dev, &st);
+    const int rc = experts_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (E == 0 || K == 0) return zero_rows(Y, 1, T, N, ldy, 0, size, s);

@@ -54,6 +54,7 @@ struct DeviceState {
     int status = SGEMM_ERR_CUDA;  // result of the one-time set-up
     int sm_count = 0;
     int max_clusters_split[9] = {0};
+    int experts_status = SGEMM_ERR_CUDA;  // of the grouped and MXFP4 products' set-up
     int max_pairs = 0;            // co-resident CTA pairs of the grouped products' wide kernels
     bool regsplit_ok = false;     // the register-split kernels were built at kRegsLaunch registers
     int fused_per_sm[7] = {0};    // co-resident fused-producer CTAs per SM, by stage count
@@ -243,6 +244,8 @@ struct Scale {
 
 // ---- api_device.cu: device set-up, per-stream stream-K scratch
 int current_device(int* dev_out, DeviceState** st_out);
+// The same for the grouped and MXFP4 products.
+int experts_device(int* dev_out, DeviceState** st_out);
 int sk_lease(DeviceState& st, cudaStream_t cs, size_t ws_bytes, size_t nflags, SkLease* out);
 void sk_return(DeviceState& st, cudaStream_t cs, SkLease& lease);
 
