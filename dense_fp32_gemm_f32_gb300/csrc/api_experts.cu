@@ -51,8 +51,19 @@ View scales_view(const uint8_t* p, int64_t count, int64_t row_blocks, int64_t K)
 // Row blocks of T rows grouped by E experts, at most.
 int64_t grouped_blocks(int64_t T, int64_t E) { return (T + 127 * std::min(T, E)) / 128; }
 
+// Zeros to `count` matrices of rows x cols: in one operation, unless both the rows
+// and the matrices lie apart.
 int zero_rows(void* p, int64_t count, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int size,
               cudaStream_t s) {
+    if (count > 1 && stride == rows * ld) {  // (rows of one matrix)
+        rows *= count;
+        count = 1;
+    } else if (count > 1 && (ld == cols || rows == 1)) {  // (a matrix is a row)
+        cols *= rows;
+        rows = count;
+        ld = stride;
+        count = 1;
+    }
     for (int64_t e = 0; e < count; ++e)
         if (rows > 0 && cols > 0 &&
             cudaMemset2DAsync(static_cast<char*>(p) + e * stride * size, ld * size, 0, cols * size, rows, s) !=
