@@ -16,6 +16,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import dense_fp32_gemm_f32_gb300 as g  # noqa: E402
@@ -30,10 +31,13 @@ class GroupedProduct(torch.autograd.Function):
         return g.sgemm_grouped(X, W, offsets)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, W, offsets = ctx.saved_tensors
         dY = dY.contiguous()
-        return g.sgemm_grouped(dY, W, offsets, transw=True), g.sgemm_grouped_wgrad(X, dY, offsets), None
+        dX = g.sgemm_grouped(dY, W, offsets, transw=True) if ctx.needs_input_grad[0] else None
+        dW = g.sgemm_grouped_wgrad(X, dY, offsets) if ctx.needs_input_grad[1] else None
+        return dX, dW, None
 
 
 def route(x, router):
