@@ -17,7 +17,9 @@
  *
  * Memory.  All pointers are DEVICE pointers owned by the caller and aligned
  * to their element type; leading dimensions and strides are in elements.
- * Outputs must not overlap inputs.  Row padding is never read or written.
+ * Outputs must not overlap inputs.  Row padding is never written and never
+ * reaches a result.  It may be read, and so may what lies around an operand,
+ * but only bytes that share an aligned 16 with one of its elements.
  * Entry points that may allocate device memory from the library's
  * stream-ordered pool (see sgemm.h), freed in stream order at the end of the
  * call, and those that never do:
