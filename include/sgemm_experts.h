@@ -145,7 +145,8 @@ int sgemm_mxfp4_quantize(int type, int batch, int rows, int K,
  * sgemm_mxfp4_dequantize -- the values that codes and scales stand for, to Y
  * (batch matrices of rows x K of `type`, stride_y apart); E and offsets as
  * given to the quantiser.  Rows that belong to no expert get zeros.  Values
- * are exact in float32 and bf16.
+ * are exact in float32 and bf16 up to scale byte 252, the quantiser's largest;
+ * above it those beyond the type's range are infinities.
  */
 int sgemm_mxfp4_dequantize(int type, int batch, int rows, int K,
                            const uint8_t* codes, const uint8_t* scales,
@@ -155,9 +156,10 @@ int sgemm_mxfp4_dequantize(int type, int batch, int rows, int K,
 
 /*
  * sgemm_mxfp4 -- C = A B^T of two MXFP4 matrices, A (M x K) and B (N x K), both
- * quantised along K; C (M x N) of out_type.  Products and scales are exact,
- * sums are in float32 (|C - exact| <= 5e-5 * sum_k |a||b| plus the rounding to
- * out_type, for contractions up to 2^20).
+ * quantised along K; C (M x N) of out_type.  Products are exact, sums are in
+ * float32: |C - exact| <= 5e-5 * sum_k |a||b| plus the rounding to out_type, for
+ * contractions up to 2^20 and sums of magnitudes within float32's range; below
+ * its normal numbers every 64 of the contraction may add 2^-149.
  */
 int sgemm_mxfp4(int out_type, int M, int N, int K,
                 const uint8_t* A, const uint8_t* a_scales,
