@@ -3,6 +3,10 @@
 Thin binding over include/sgemm_experts.h, which defines the operations, the
 layout of MXFP4 operands and the accuracy.  ``offsets`` is an int32 CUDA tensor of E + 1 row boundaries;
 it is never read on the host, so no call here waits for the GPU.
+
+As with the library's other entries, results are detached: torch does not differentiate through a call, also where an
+operand requires a gradient.  A layer calls the gradients itself, from a torch.autograd.Function around the product
+(examples/expert_layer.py has one).
 """
 from __future__ import annotations
 
