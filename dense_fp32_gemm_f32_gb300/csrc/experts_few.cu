@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
                     const float* w0 = W + static_cast<long long>(k0) * p.ldw + c;
                     const bool vec = (reinterpret_cast<uintptr_t>(w0) & 15) == 0 && p.ldw % 4 == 0;
                     constexpr int kU = 8;  // loads under way
+                    static_assert(kChunk % (kWarps * kU) == 0, "steps do not pass the chunk");
                     for (int k = warp; k < len; k += kWarps * kU) {
                         float4 w[kU];
 #pragma unroll
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
                         }
 #pragma unroll
                         for (int u = 0; u < kU; ++u) {
-                            const int kk = min(k + u * kWarps, kChunk - 1);  // (past the chunk: w is 0)
-                            const float4* x = reinterpret_cast<const float4*>(sm + kk * RT);
+                            // (inside the chunk: k < kChunk - (kU - 1) kWarps; past its end both are 0)
+                            const float4* x = reinterpret_cast<const float4*>(sm + (k + u * kWarps) * RT);
 #pragma unroll
                             for (int r = 0; r < RT; r += 4) {
                                 const float4 v = x[r / 4];
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
                             }
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const int kk = min(k + 128 * u, kChunk - 4);
+                            const int kk = k + 128 * u;  // (k < kChunk - 128: inside the chunk; past its end both are 0)
 #pragma unroll
                             for (int r = 0; r < RT; ++r) {
                                 const float4 x = *reinterpret_cast<const float4*>(sm + r * kChunk + kk);
