@@ -93,12 +93,21 @@ class _Switch:
         self.context.__exit__(None, None, None)
 
 
-def _enter(dev: int, stream):
+def _enter(dev: int, stream, *tensors):
     """(stream handle, what to close after the call or None).  Nothing is switched in the usual case, the current device
-    and stream: a switch costs as much as a launch."""
+    and stream: a switch costs as much as a launch.  With a ``stream`` the call's tensors (or None) are recorded on it, so
+    that the memory of one that the caller drops is not handed out again before the kernels have read it."""
     if stream is None:
         return _raw_stream(dev), (None if torch.cuda.current_device() == dev else _Switch(dev, None))
-    return int(stream.cuda_stream), _Switch(dev, stream)
+    switch = _Switch(dev, stream)
+    try:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    except BaseException:
+        switch.close()
+        raise
+    return int(stream.cuda_stream), switch
 
 
 def _out(out, like, shape, dtype, name="out"):
@@ -147,7 +156,7 @@ def sgemm_grouped(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, out: 
         raise ValueError(f"offsets must hold {E + 1} boundaries, got {offsets.numel()}")
     ldx = _strides(X, (T, K), "X")[0]
     ldw, sw = _strides(W, ws, "W")
-    s, switch = _enter(dev, stream)
+    s, switch = _enter(dev, stream, X, W, offsets, out)
     try:
         out, ldy = _out(out, X, (T, N), dtype)
         rc = _lib.load().sgemm_grouped(t, 1 if transw else 0, T, E, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, sw,
@@ -193,7 +202,7 @@ def sgemm_grouped_wgrad(X: torch.Tensor, dY: torch.Tensor, offsets: torch.Tensor
         raise ValueError(f"X has {T} rows, dY {rows}")
     E = _offsets(offsets, dev)
     ldx, ldy = _strides(X, (T, K), "X")[0], _strides(dY, (T, N), "dY")[0]
-    s, switch = _enter(dev, stream)
+    s, switch = _enter(dev, stream, X, dY, offsets, out)
     try:
         so = K * N if out is None else None
         out, ldo = _out(out, X, (E, K, N), dtype)
@@ -253,7 +262,7 @@ def sgemm_mxfp4_quantize(X: torch.Tensor, offsets: torch.Tensor | None = None, *
         E = _offsets(offsets, dev)
         nb = _grouped_blocks(rows, E)
     ldx, sx = _strides(X, shape, "X")
-    s, switch = _enter(dev, stream)
+    s, switch = _enter(dev, stream, X, offsets, codes, scales)
     try:
         given = codes is not None or scales is not None
         codes, _ = _out(codes, X, lead + (rows, 16 * ((K + 31) // 32)), torch.uint8, "codes")
@@ -325,7 +334,7 @@ def sgemm_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, offsets: t
         K = cols
     shape = tuple(codes.shape[:-1]) + (K,)
 
-    s, switch = _enter(dev, stream)
+    s, switch = _enter(dev, stream, codes, scales, offsets, out)
     try:
         sy = rows * K if out is None else None
         out, ldy = _out(out, codes, shape, dtype)
@@ -374,7 +383,7 @@ def sgemm_mxfp4(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scal
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
 
-    s, switch = _enter(dev, stream)
+    s, switch = _enter(dev, stream, A, a_scales, B, b_scales, out)
     try:
         out, ldc = _out(out, A, (M, N), dtype)
         rc = _lib.load().sgemm_mxfp4(t, M, N, K, A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(),
@@ -417,7 +426,7 @@ def sgemm_mxfp4_grouped(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor
     dtype = out.dtype if out is not None else dtype
     t = _type(dtype, "dtype")
 
-    s, switch = _enter(dev, stream)
+    s, switch = _enter(dev, stream, X, x_scales, W, w_scales, offsets, out)
     try:
         out, ldy = _out(out, X, (T, N), dtype)
         rc = _lib.load().sgemm_mxfp4_grouped(t, T, E, N, K, X.data_ptr(), x_scales.data_ptr(), W.data_ptr(),
