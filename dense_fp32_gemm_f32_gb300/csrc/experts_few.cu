@@ -15,8 +15,8 @@
 //     lanes' sums meet by shuffles.
 // Where tiles are few, the contraction is split over a cluster of up to 8 CTAs
 // that add their parts in rank order through each other's shared memory.
-// Measured for 32 / 64 rows, 8 experts of 1024 x 2048 (67 MB of weights): 12 / 17
-// us (5.5 / 3.9 TB/s), transposed 15 / 22; 48 by parts.  Up to 4 rows a group it
+// Measured for 32 / 64 rows, 8 experts of 1024 x 2048 (67 MB of weights): 13 / 19
+// us (5.0 / 3.6 TB/s), transposed 14 / 21; 50 by parts.  Up to 4 rows a group it
 // is the weights' bytes that bound it, from 8 on the multiply-adds' issue.
 #include "../../include/sgemm_experts.h"
 #include "api_internal.h"

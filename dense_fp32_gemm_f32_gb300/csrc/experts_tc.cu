@@ -11,8 +11,12 @@ namespace detail {
 namespace {
 
 // Rows an expert on average up to which float32 products run on the CUDA cores
-// (experts_few.cu).  Measured for 8 experts of 1024 x 2048, us there / by parts:
-// 4 12 / 48, 8 17 / 48, 16 32 / 48, 24 50 / 48 (transposed 15, 22, 41, 63).
+// (experts_few.cu).  Measured for 8 experts of 1024 x 2048, us there (by parts 50):
+// 4 13, 8 19, 16 26, 18 49 (transposed 14, 21, 44, 57); for 64 experts of that size (by
+// parts 353): 8 130, 12 199, 18 281 (transposed 189, 307, 442).  Uneven groups take
+// less there, not more: the same 18 on average with a fifth of all rows in one
+// expert 244, all in one 194 (transposed 390, 309): a long group's tiles share
+// their weights.
 constexpr long long kFewRows = 18;
 
 // An operand as the tensor maps read it: 16-bit elements, third dimension the

@@ -18,7 +18,7 @@
 //               stored.  (Nothing is ragged in f and c here, and a lane that
 //               holds a row's neighbouring elements packs them by itself: for
 //               32 groups of 2 rows, 2048 x 4096, bound by the epilogue, 164 us
-//               the other way round and 140 so.)
+//               the other way round, 140 so, and 109 with the rest below.)
 //
 // float32 operands come as three bf16 parts each, x = x0 + x1 + x2 (8 bits
 // each, rounded to nearest: what is left is below 2^-25 |x|), and the sum runs
@@ -51,20 +51,20 @@
 // cluster of 2 to 8 CTAs shares one (SPLIT): each takes a part of the
 // contraction, leaves its sums in its shared memory, and adds up the columns
 // that are its own from all parts, in their order.  (4 rows, 40 experts of 6690 x
-// 480: 21 us on 16 SMs, 14 so.)
+// 480: 21 us on 16 SMs, 16 so.)
 //
 // The load and MMA warps' loops are uniform over the warp, with one elected
 // lane issuing: the operands of the instructions then live in uniform
 // registers.  (In a loop of one lane they do not, and moving them cost more
 // than the MMAs: 775 cycles a stage of the wide tile, whose MMAs take 512.)
 //
-// Measured on GB300 (bf16 unless said; warm): 16 experts of 4096 x 4096, 16384
-// rows 284 us, 1.94 PFLOP/s, the rate of the library's plain product (1.88); the
-// weights' gradient of the same 291 us; 32 experts of 2048 x 4096, 64 rows
-// 77 us, 6.9 TB/s (the weights' bytes); 8 experts of 4096 x 2048, 8192 rows 78 us
-// (dX) and 78 us (dW), 1.76 PFLOP/s, bound by the last round of tiles (83 us
+// Measured on GB300 (bf16 and even groups unless said; warm): 16 experts of 4096 x
+// 4096, 16384 rows 293 us, 1.88 PFLOP/s, the rate of the library's plain product;
+// the weights' gradient of the same 297 us; 32 experts of 2048 x 4096, 64 rows
+// 77 us, 7.0 TB/s (the weights' bytes); 8 experts of 4096 x 2048, 8192 rows 79 us
+// (dX) and 80 us (dW), 1.74 PFLOP/s, bound by the last round of tiles (83 us
 // before its tiles were split; 90 with uneven groups); float32, 4 experts of 1024
-// x 2048, 2048 rows 52 us with its operands' copies (15 us), 160 TFLOP/s of
+// x 2048, 2048 rows 54 us with its operands' copies (15 us), 160 TFLOP/s of
 // float32, six times that of bf16: two rounds of 128 tiles on 76 pairs bound it.
 //
 // Every wait is bounded by `timeout_ns`; on expiry the thread records the
@@ -801,7 +801,8 @@ __global__ void __launch_bounds__(GroupedShape<TN, CG, PARTS>::kThreads, 1)
                 }
                 if (t.klen > kGrChunk<PARTS>) {
                     // All accumulators' sums, left in the last.  (So the stores below have the
-                    // registers to themselves; 16 columns a load for the same reason.)
+                    // registers to themselves; 16 columns a load for the same reason.  8 experts of
+                    // 2048 x 2048 by 8192 rows: 288 us with one accumulator, 291 so.)
                     float sum[TN / kStep][32] = {};
                     for (int k = kGrChunk<PARTS>;; k += kGrChunk<PARTS>) {
 #pragma unroll
