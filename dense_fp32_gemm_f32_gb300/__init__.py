@@ -1,5 +1,6 @@
-"""GB300 (sm_103a) single-precision matrix multiply, C = A x B, and products
-grouped by expert and on 4-bit microscaled operands (``experts.py``).
+"""GB300 (sm_103a) single-precision matrix multiply, C = A x B, products grouped
+by expert and on 4-bit microscaled operands (``experts.py``), and the routing
+of tokens to experts around them (``routing.py``).
 
 Thin Python binding over the C ABI in ``include/sgemm.h``: it checks tensor
 types, reads sizes and strides, passes raw device pointers and the current
@@ -22,6 +23,7 @@ from .experts import (
     sgemm_mxfp4_grouped,
     sgemm_mxfp4_quantize,
 )
+from .routing import Routing, sgemm_combine, sgemm_combine_grad, sgemm_route, sgemm_route_grad, sgemm_spread
 
 __all__ = [
     "sgemm_f32",
@@ -37,6 +39,12 @@ __all__ = [
     "sgemm_mxfp4_dequantize",
     "sgemm_mxfp4",
     "sgemm_mxfp4_grouped",
+    "sgemm_route",
+    "sgemm_route_grad",
+    "sgemm_spread",
+    "sgemm_combine",
+    "sgemm_combine_grad",
+    "Routing",
     "check_status",
     "describe",
     "Options",

@@ -1,5 +1,5 @@
-"""ctypes view of the C ABI declared in include/sgemm.h, include/sgemm_experts.h
-and include/sgemm_bench.h.
+"""ctypes view of the C ABI declared in include/sgemm.h, include/sgemm_experts.h,
+include/sgemm_routing.h and include/sgemm_bench.h.
 
 Loading never falls back to anything: if the shared library is missing it is
 built (nvcc), and if that fails the import error propagates.
@@ -25,6 +25,9 @@ ERR_NOT_IMPLEMENTED = 5
 
 # Element types (include/sgemm_experts.h).
 TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
+
+# Scores (include/sgemm_routing.h).
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 PRODUCER_AUTO, PRODUCER_TMA, PRODUCER_CPASYNC, PRODUCER_TMA_WG, PRODUCER_FUSED, PRODUCER_TMA_X, PRODUCER_SMALL = 0, 1, 2, 3, 4, 5, 6
 
@@ -74,6 +77,11 @@ SIGNATURES = {
     "sgemm_mxfp4_dequantize": (_i, [_i, _i, _i, _i, _p, _p, _i, _p, _p, _i64, _i64, _p]),
     "sgemm_mxfp4": (_i, [_i, _i, _i, _i, _p, _p, _p, _p, _p, _i64, _p]),
     "sgemm_mxfp4_grouped": (_i, [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _i64, _p]),
+    "sgemm_route": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _i, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p, _p]),
+    "sgemm_route_grad": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _p, _i, ctypes.c_float, _p, _i64, _p]),
+    "sgemm_spread": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _i, _p, _p, _i64, _p]),
+    "sgemm_combine": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _p, _p, _i64, _p]),
+    "sgemm_combine_grad": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _i64, _p, _p, _i, _p, _p, _i64, _p, _p]),
     "sgemm_bench_fma_peak": (_i, [_i, _i, _i, _p, _p, ctypes.POINTER(_d)]),
     "sgemm_bench_copy": (_i, [_p, _p, ctypes.c_longlong, _i, _p]),
 }

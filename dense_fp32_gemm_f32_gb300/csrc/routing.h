@@ -1,0 +1,71 @@
+// Internal interface of routing and of the rows' way to their experts
+// (include/sgemm_routing.h): kernel parameters and launch functions.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace gb300 {
+
+struct RouteParams {
+    const void* logits;
+    long long ld;
+    const float* bias;  // null: none
+    int T, E, k;
+    int sigmoid, renormalize;
+    int groups, top_groups, group_best;
+    float scale;
+    int* experts;
+    float* weights;
+    int* offsets;
+    int* slots;
+    int vec;      // the rows begin on 16 bytes: whole vectors are loaded
+    int steps;    // steps of kRouteStep tokens a CTA takes
+    int* counts;  // CTAs x E: choices of each expert (null: one CTA does it all)
+};
+
+// Tokens of a CTA's step: a bit each in an expert's word.
+constexpr int kRouteStep = 32;
+
+// The grid of a routing: CTAs and their steps.
+struct RoutePlan {
+    int ctas, steps;
+};
+RoutePlan route_plan(int T, int E, int sms);
+int route(const RouteParams& p, const RoutePlan& plan, int type, cudaStream_t s);
+
+struct RouteGradParams {
+    const void* logits;
+    long long ld;
+    const int* experts;
+    const float* dweights;
+    void* dlogits;
+    long long ldd;
+    int T, E, k;
+    int sigmoid, renormalize;
+    float scale;
+    int vec, vec_out;
+};
+int route_grad(const RouteGradParams& p, int type, cudaStream_t s);
+
+// Rows to their slots and back (rows.cu).
+struct RowsParams {
+    const void* X;  // spread: X; gradient of a combination: dout
+    long long ldx;
+    const void* Y;  // combination and its gradient: rows by slot
+    long long ldy;
+    void* out;  // spread: Y; combination: out; its gradient: dY (may be null)
+    long long ldo;
+    const int* slots;
+    const float* weights;  // null: ones
+    float* dweights;       // may be null
+    const int* used;       // &offsets[E]: rows from here on are zeroed
+    int T, k, R, H;
+    int vec;  // elements a vector, as the operands' alignment allows
+};
+int rows_spread(const RowsParams& p, int type, int sms, cudaStream_t s);
+int rows_combine(const RowsParams& p, int type, int sms, cudaStream_t s);
+int rows_combine_grad(const RowsParams& p, int type, int sms, cudaStream_t s);
+
+}  // namespace gb300
