@@ -1,6 +1,7 @@
 """GB300 (sm_103a) single-precision matrix multiply, C = A x B, products grouped
-by expert and on 4-bit microscaled operands (``experts.py``), and the routing
-of tokens to experts around them (``routing.py``).
+by expert and on 4-bit microscaled operands (``experts.py``), the routing of
+tokens to experts around them (``routing.py``), and orthogonalised weight
+updates (``ortho.py``).
 
 Thin Python binding over the C ABI in ``include/sgemm.h``: it checks tensor
 types, reads sizes and strides, passes raw device pointers and the current
@@ -23,6 +24,7 @@ from .experts import (
     sgemm_mxfp4_grouped,
     sgemm_mxfp4_quantize,
 )
+from .ortho import sgemm_orthogonalize
 from .routing import Routing, sgemm_combine, sgemm_combine_grad, sgemm_route, sgemm_route_grad, sgemm_spread
 
 __all__ = [
@@ -45,6 +47,7 @@ __all__ = [
     "sgemm_combine",
     "sgemm_combine_grad",
     "Routing",
+    "sgemm_orthogonalize",
     "check_status",
     "describe",
     "Options",

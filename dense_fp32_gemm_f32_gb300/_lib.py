@@ -1,5 +1,5 @@
 """ctypes view of the C ABI declared in include/sgemm.h, include/sgemm_experts.h,
-include/sgemm_routing.h and include/sgemm_bench.h.
+include/sgemm_routing.h, include/sgemm_ortho.h and include/sgemm_bench.h.
 
 Loading never falls back to anything: if the shared library is missing it is
 built (nvcc), and if that fails the import error propagates.
@@ -82,6 +82,7 @@ SIGNATURES = {
     "sgemm_spread": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _i, _p, _p, _i64, _p]),
     "sgemm_combine": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _p, _p, _i64, _p]),
     "sgemm_combine_grad": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _i64, _p, _p, _i, _p, _p, _i64, _p, _p]),
+    "sgemm_orthogonalize": (_i, [_i, _i, _i, _i, _p, _i64, _i64, _i, ctypes.c_float, ctypes.c_float, ctypes.c_float, _d, _p, _i64, _i64, _p]),
     "sgemm_bench_fma_peak": (_i, [_i, _i, _i, _p, _p, ctypes.POINTER(_d)]),
     "sgemm_bench_copy": (_i, [_p, _p, ctypes.c_longlong, _i, _p]),
 }

@@ -55,6 +55,8 @@ struct DeviceState {
     int sm_count = 0;
     int max_clusters_split[9] = {0};
     int experts_status = SGEMM_ERR_CUDA;  // of the grouped and MXFP4 products' set-up
+    std::once_flag ortho_once;
+    int ortho_status = SGEMM_ERR_CUDA;    // of the orthogonalised updates' set-up (at their first call)
     int max_pairs = 0;            // co-resident CTA pairs of the grouped products' wide kernels
     bool regsplit_ok = false;     // the register-split kernels were built at kRegsLaunch registers
     int fused_per_sm[7] = {0};    // co-resident fused-producer CTAs per SM, by stage count

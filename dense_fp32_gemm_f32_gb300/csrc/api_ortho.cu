@@ -1,0 +1,77 @@
+// The entry point of include/sgemm_ortho.h: argument checks.
+#include <cmath>
+
+#include "../../include/sgemm_ortho.h"
+#include "api_internal.h"
+#include "ortho.h"
+#include "views.h"
+
+using namespace gb300;
+using namespace gb300::detail;
+
+namespace {
+
+// The largest |b u + c u^2| and |a s + b s^3 + c s^5| for s in [0, most], u = s^2:
+// at the ends, and where the derivatives are zero.
+double largest_correction(double b, double c, double most) {
+    const double u = most * most;
+    double top = std::fabs(b * u + c * u * u);
+    if (c != 0) {
+        const double at = -b / (2 * c);
+        if (at > 0 && at < u) top = std::fmax(top, std::fabs(b * at + c * at * at));
+    }
+    return top;
+}
+double largest_value(double a, double b, double c, double most) {
+    auto value = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+    double top = value(most);
+    auto root = [&](double u) {
+        if (u > 0 && u < most * most) top = std::fmax(top, value(std::sqrt(u)));
+    };
+    if (c != 0) {  // 5 c u^2 + 3 b u + a = 0
+        const double disc = 9 * b * b - 20 * a * c;
+        if (disc >= 0) {
+            root((-3 * b + std::sqrt(disc)) / (10 * c));
+            root((-3 * b - std::sqrt(disc)) / (10 * c));
+        }
+    } else if (b != 0) {
+        root(-a / (3 * b));
+    }
+    return top;
+}
+
+// Whether the polynomial keeps every singular value that can occur within 2, and
+// what is added within 15 (see the scales in ortho_tc.cuh).
+bool polynomial_ok(int steps, double a, double b, double c) {
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    double most = 1;
+    for (int i = 0; i < steps; ++i) {
+        if (!(largest_correction(b, c, most) <= 15)) return false;
+        const double next = largest_value(a, b, c, most);
+        if (!(next <= 2)) return false;
+        most = std::fmax(most, next);
+    }
+    return true;
+}
+
+}  // namespace
+
+extern "C" int sgemm_orthogonalize(int type, int E, int M, int N, const void* G, int64_t ldg, int64_t stride_g, int steps,
+                                   float a, float b, float c, double eps, void* out, int64_t ldo, int64_t stride_out,
+                                   void* stream) {
+    if (!type_ok(type) || E < 0 || M < 0 || N < 0 || E > kMost || M > kMost || N > kMost) return SGEMM_ERR_INVALID_ARG;
+    if (steps < 1 || steps > 64 || !(eps >= 0) || !std::isfinite(eps) || !polynomial_ok(steps, a, b, c))
+        return SGEMM_ERR_INVALID_ARG;
+    const int size = type_bytes(type);
+    const View g{G, E, M, N, ldg, stride_g, size}, o{out, E, M, N, ldo, stride_out, size};
+    if (!g.ok(size) || !o.ok(size) || overlap(g, o)) return SGEMM_ERR_INVALID_ARG;
+    if (o.empty()) return SGEMM_OK;
+    constexpr int64_t most = int64_t{1} << 46;  // elements: what the workspace's size fits
+    if (static_cast<int64_t>(M) > most / N || static_cast<int64_t>(M) * N > most / E) return SGEMM_ERR_INVALID_ARG;
+    int dev = 0;
+    DeviceState* st = nullptr;
+    const int rc = experts_device(&dev, &st);
+    if (rc != SGEMM_OK) return rc;
+    const OrthoCall call = {G, ldg, stride_g, out, ldo, stride_out, type, E, M, N, steps, a, b, c, eps};
+    return orthogonalize(call, dev, *st, static_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,55 @@
+/*
+ * sgemm_ortho.h -- orthogonalised weight updates (GB300, sm_103a).  Companion
+ * of sgemm_experts.h, whose weight gradients it takes: same status codes,
+ * types, streams, error behaviour and scratch pool.
+ *   ORTHO-ALLOCATING: sgemm_orthogonalize
+ */
+#ifndef GB300_SGEMM_ORTHO_H
+#define GB300_SGEMM_ORTHO_H
+
+#include <stdint.h>
+
+#include "sgemm_experts.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * sgemm_orthogonalize -- E matrices (M x N) with their singular values brought
+ * near 1 by Newton-Schulz products:
+ *
+ *     X = G / (|G|_F + eps),   then `steps` times
+ *     A = X X^T,  X = a X + (b A + c A A) X      (X^T X where M > N),
+ *
+ * which takes each singular value s to a s + b s^3 + c s^5 and leaves the
+ * singular vectors where they are.
+ *   type       of G and out
+ *   G, ldg, stride_g       E matrices M x N, stride_g elements apart
+ *   out, ldo, stride_out   the same, overwritten
+ *   steps      1 .. 64
+ *   a, b, c    the polynomial.  It may take no singular value that can occur
+ *              (from [0, 1] on) above 2 in magnitude after any step, and
+ *              b s^2 + c s^4 not above 15: refused otherwise
+ *   eps        >= 0, finite.  With eps = 0 a matrix of zeros gives NaN
+ * Accuracy.  Each step's products take X, A and b A + c A A less their
+ * diagonals as f16 operands (A's and X's rounding errors, and the diagonals,
+ * are carried along outside of the products) and sum in float32.  For bf16 one
+ * f16 value each (11 bits); for float32 and f16 two (22 bits), three products
+ * of which stand for one in float32.  A step multiplies an error in the
+ * direction of small singular values by up to a, as it does those values
+ * themselves; against the result in 64 bits that comes to less than 2^-8 of its
+ * norm for bf16, and for float32 and f16 to about what the same steps with
+ * float32 products have, besides the rounding to the output's type.
+ * A non-finite element makes its whole matrix NaN or infinite, and no other.
+ */
+int sgemm_orthogonalize(int type, int E, int M, int N,
+                        const void* G, int64_t ldg, int64_t stride_g,
+                        int steps, float a, float b, float c, double eps,
+                        void* out, int64_t ldo, int64_t stride_out,
+                        void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif
