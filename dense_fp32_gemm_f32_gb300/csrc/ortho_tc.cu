@@ -36,7 +36,7 @@ int set_up() {
 template <int TN, int CG, int PARTS>
 int set_up_all() {
     return set_up<kOrthoGram, false, false, TN, CG, PARTS>() || set_up<kOrthoGram, true, true, TN, CG, PARTS>() ||
-           set_up<kOrthoSquare, false, false, TN, CG, PARTS>() || set_up<kOrthoUpdate, true, false, TN, CG, PARTS>() ||
+           set_up<kOrthoSquare, false, false, TN, CG, PARTS>() || set_up<kOrthoUpdate, false, true, TN, CG, PARTS>() ||
            set_up<kOrthoUpdate, false, false, TN, CG, PARTS>();
 }
 
@@ -97,14 +97,14 @@ int steps(const OrthoCall& c, const OrthoPrep& prep, char* const (&x)[2], char* 
           const DeviceState& st, cudaStream_t s) {
     const bool tall = c.M > c.N;
     const int m = std::min(c.M, c.N), n = std::max(c.M, c.N);
-    const long long mp = (m + 7) / 8 * 8, xs = static_cast<long long>(c.M) * prep.pitch, ms = m * mp;
+    const long long mp = (m + 15) / 16 * 16, xs = static_cast<long long>(c.M) * prep.pitch, ms = m * mp;
     alignas(64) CUtensorMap tx[2], ta, tb;
     for (int i = 0; i < 2; ++i)
         if (const int rc = encode_planes(&tx[i], x[i], c.N, c.M, 2ll * c.E, prep.pitch)) return rc;
     if (const int rc = encode_planes(&ta, a, m, m, 2ll * c.E, mp)) return rc;
     if (const int rc = encode_planes(&tb, b, m, m, static_cast<long long>(PARTS) * c.E, mp)) return rc;
     OrthoTcParams p = {};
-    p.E = c.E, p.diag = m;
+    p.E = c.E, p.diag = mp;
     p.a = c.a, p.b = c.b, p.c = c.c;
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
@@ -126,9 +126,9 @@ int steps(const OrthoCall& c, const OrthoPrep& prep, char* const (&x)[2], char* 
         rc = launch<kOrthoSquare, false, false, TN, CG, PARTS>(ta, ta, q, st, s);
         if (rc != SGEMM_OK) return rc;
         OrthoTcParams u = p;
-        u.F = c.N, u.C = c.M, u.K = m;
+        u.F = c.M, u.C = c.N, u.K = m;
         u.in_hi = plane(x[from], 0, c.E * xs), u.in_lo = plane(x[from], 1, c.E * xs), u.ld_in = prep.pitch, u.s_in = xs;
-        u.d_in = e, u.by_feature = tall;
+        u.d_in = e, u.by_column = tall;
         if (step + 1 < c.steps) {
             u.out_hi = plane(x[to], 0, c.E * xs), u.out_lo = plane(x[to], 1, c.E * xs);
             u.ld_out = prep.pitch, u.s_out = xs;
@@ -136,9 +136,9 @@ int steps(const OrthoCall& c, const OrthoPrep& prep, char* const (&x)[2], char* 
             u.out = c.out, u.ldo = c.ldo, u.so = c.so, u.out_type = c.type;
             u.align = row_alignment(c.out, c.type == SGEMM_TYPE_F32 ? 4 : 2, c.M > 1 ? c.ldo : 0, c.E > 1 ? c.so : 0);
         }
-        // wide: f = column of X, c = its row; the operands X (by columns) and P.  Tall, X^T stored: P and X.
-        rc = tall ? launch<kOrthoUpdate, false, false, TN, CG, PARTS>(tb, tx[from], u, st, s)
-                  : launch<kOrthoUpdate, true, false, TN, CG, PARTS>(tx[from], tb, u, st, s);
+        // X' = P X; tall, X^T stored: X'^T = X^T P.
+        rc = tall ? launch<kOrthoUpdate, false, false, TN, CG, PARTS>(tx[from], tb, u, st, s)
+                  : launch<kOrthoUpdate, false, true, TN, CG, PARTS>(tb, tx[from], u, st, s);
         if (rc != SGEMM_OK) return rc;
     }
     return SGEMM_OK;
@@ -150,7 +150,7 @@ int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s) 
     std::call_once(st.ortho_once, [&] { st.ortho_status = set_up_kernels(); });
     if (st.ortho_status != SGEMM_OK) return st.ortho_status;
     const int m = std::min(c.M, c.N);
-    const long long pitch = (c.N + 7ll) / 8 * 8, mp = (m + 7ll) / 8 * 8;
+    const long long pitch = (c.N + 15ll) / 16 * 16, mp = (m + 15ll) / 16 * 16;  // (the epilogue's accesses of 32 bytes)
     const int parts = c.type == SGEMM_TYPE_BF16 ? 1 : 2;
     // Row chunks of about 8192 elements, a few rounds of the GPU at most.
     OrthoPrep prep = {};
@@ -161,7 +161,7 @@ int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s) 
     if (static_cast<long long>(c.E) * prep.chunks > 0x7fffffffll) return SGEMM_ERR_INVALID_ARG;
     auto whole = [](long long bytes) { return (bytes + 255) / 256 * 256; };
     const long long xb = whole(2ll * 2 * c.E * c.M * pitch), ab = whole(2ll * 2 * c.E * m * mp);
-    const long long db = whole(4ll * c.E * m), pb = whole(8ll * c.E * prep.chunks);
+    const long long db = whole(4ll * c.E * mp), pb = whole(8ll * c.E * prep.chunks);
     Workspace ws;
     ws.s = s;
     cudaMemPool_t pool = workspace_pool(dev, st);

@@ -30,10 +30,10 @@
 // A and B are symmetric: only tiles that reach the diagonal or lie on its one
 // side are computed, and every 32 x 32 block off it is stored twice.
 //
-// The tile, the roles of the warps, the ring and the accumulators are those of
-// experts_tc.cuh: the output's contiguous dimension f on the tensor core's
-// rows, its rows c on the columns, D[f, c] = sum_k P[f, k] Q[c, k]; load warp,
-// MMA warp, epilogue warps, and persistent CTAs or CTA pairs.  With two planes
+// The roles of the warps, the ring and the accumulators are those of
+// experts_tc.cuh: load warp, MMA warp, epilogue warps, and persistent CTAs or
+// CTA pairs.  The output's rows f lie on the tensor core's rows, its contiguous
+// dimension c on the columns, D[f, c] = sum_k P[f, k] Q[c, k] (see the epilogue).  With two planes
 // hi hi has an accumulator of its own, the small products another, and both go
 // to float32 registers every 512 of the contraction (an instruction cuts
 // sums to 24 bits).
@@ -51,16 +51,16 @@ enum OrthoMode { kOrthoGram, kOrthoSquare, kOrthoUpdate };
 struct OrthoTcParams {
     int tiles, per;        // output tiles in all, of a matrix
     int ftiles, ctiles;
-    int F, C, K, E;        // output C x F (F contiguous), contraction
+    int F, C, K, E;        // output F x C (C contiguous), contraction
     const __half* in_hi;   // square: A's planes; update: X's (as the output lies)
     const __half* in_lo;
     __half* out_hi;        // gram: A's planes; square: B's; update: X's next
     __half* out_lo;        // null: not needed
     long long ld_in, s_in, ld_out, s_out;  // elements a row, a matrix
-    const float* d_in;     // square: A's diagonals; update: B's (`diag` a matrix)
+    const float* d_in;     // square: A's diagonals; update: B's (`diag` a matrix, a multiple of 16)
     float* d_out;          // gram: A's diagonals; square: B's
-    int diag;
-    int by_feature;        // update: e goes by f (else by c)
+    long long diag;
+    int by_column;         // update: e goes by column (else by row)
     float a, b, c;
     void* out;             // the last update's result, of out_type (null: planes)
     long long ldo, so;
@@ -116,6 +116,143 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoTcParams& p, int i) {
     t.f0 = f * FT;
     t.c0 = c * TN;
     return t;
+}
+
+// ------------------------------------------------------------------ epilogue
+//
+// A warp takes blocks of 32 rows x 32 columns, a row a lane, so that what a lane
+// loads and stores of a plane are 64 neighbouring bytes: two accesses of 32,
+// whole sectors, and no way through shared memory.  (With the rows' contiguous
+// dimension on the lanes, the products waited for the epilogue: update of 8
+// matrices 2048 x 4096 315 us with 2 bytes an access, 188 us with a transposition
+// through shared memory.)
+
+struct alignas(32) Half16 {  // 16 f16 values
+    uint32_t w[8];
+};
+
+// (past the first-level cache, which need not see what the kernel before wrote)
+__device__ __forceinline__ Half16 load_half16(const __half* p) {
+    Half16 x;
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7])
+                 : "l"(p));
+    return x;
+}
+__device__ __forceinline__ void store_half16(__half* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// What is carried beside the products at a lane's part of a block: two planes.
+template <int MODE>
+struct OrthoState {
+    Half16 hi[2], lo[2];
+    __device__ __forceinline__ void load(const OrthoTcParams& p, int e, int row, int c) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            hi[i] = lo[i] = Half16{};
+            if (row < p.F && c + 16 * i < p.C) {
+                const long long at = e * p.s_in + row * p.ld_in + c + 16 * i;
+                hi[i] = load_half16(p.in_hi + at);
+                lo[i] = load_half16(p.in_lo + at);
+            }
+        }
+    }
+    __device__ __forceinline__ float value(int j) const {  // (a constant after unrolling)
+        const uint32_t h = hi[j / 16].w[j % 16 / 2], l = lo[j / 16].w[j % 16 / 2];
+        const __half2 x = *reinterpret_cast<const __half2*>(&h), y = *reinterpret_cast<const __half2*>(&l);
+        return j & 1 ? __high2float(x) + __high2float(y) : __low2float(x) + __low2float(y);
+    }
+};
+template <>
+struct OrthoState<kOrthoGram> {
+    __device__ __forceinline__ void load(const OrthoTcParams&, int, int, int) {}
+};
+
+// The diagonals' part of a warp's rows and columns of a tile: the lane's row, and columns 4 lane .. 4 lane + 3.
+struct OrthoDiagonal {
+    float row = 0.f, column[4] = {};
+};
+
+// A block of rows r0 .. and columns c .., from its sums; `first`: its first column among the warp's.
+template <int MODE>
+__device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t patch, int e, int r0, int c, int first,
+                                            const OrthoState<MODE>& state, const OrthoDiagonal& d, float (&v)[32]) {
+    constexpr bool SYM = MODE != kOrthoUpdate;
+    const int lane = threadIdx.x & 31, row = r0 + lane;
+    const bool diagonal = SYM && r0 == c;
+    float* const d_out = p.d_out + e * p.diag;
+    const float dr = d.row;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        float dj[4] = {};
+        if (MODE == kOrthoSquare || (MODE == kOrthoUpdate && p.by_column)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dj[i] = __shfl_sync(0xffffffffu, d.column[i], (first + j) / 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float& x = v[j + i];
+            const bool on = diagonal && j + i == lane;
+            if constexpr (MODE == kOrthoGram) {
+                if (on && row < p.F) d_out[row] = x * 0x1p-26f;
+                x *= 0x1p-14f;
+            } else if constexpr (MODE == kOrthoSquare) {
+                if (on && row < p.F) d_out[row] = fmaf(p.c, fmaf(dr, dr, x * 0x1p-24f), p.b * dr);
+                const float o = state.value(j + i);
+                x = fmaf(p.c, fmaf(dr + dj[i], o, x * 0x1p-12f), p.b * o);
+            } else {
+                x = fmaf(p.a + (p.by_column ? dj[i] : dr), state.value(j + i), x * 0x1p-12f);
+            }
+            if (on) x = 0.f;
+        }
+    }
+    if constexpr (MODE == kOrthoUpdate) {
+        if (p.out) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= 0x1p-13f;
+            const long long at = e * p.so + r0 * p.ldo + c;
+            if (p.out_type == 0)
+                store_rows(patch, p.align, static_cast<float*>(p.out) + at, p.ldo, v, p.F - r0, p.C - c);
+            else if (p.out_type == 1)
+                store_rows(patch, p.align, static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, v, p.F - r0, p.C - c);
+            else
+                store_rows(patch, p.align, static_cast<__half*>(p.out) + at, p.ldo, v, p.F - r0, p.C - c);
+            return;
+        }
+    }
+    // hi, then what it leaves.  (Rows of the planes are whole vectors: writing to
+    // their ends is harmless.)
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        __half* const plane = part == 0 ? p.out_hi : p.out_lo;
+        if (part == 1 && !plane) break;
+        __half* const to = plane + e * p.s_out;
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            v[2 * j] -= __low2float(h);
+            v[2 * j + 1] -= __high2float(h);
+        }
+        if (row < p.F) {
+            __half* const at = to + row * p.ld_out + c;
+            store_half16(at, w);
+            if (c + 16 < p.C) store_half16(at + 16, w + 8);
+        }
+        if (SYM && !diagonal && row < p.F) {
+            // The block's mirror image: rows are columns, a value a lane.
+            uint16_t* at = reinterpret_cast<uint16_t*>(to + c * p.ld_out + row);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (c + j < p.C) *at = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+                at += p.ld_out;
+            }
+        }
+    }
 }
 
 template <int MODE, bool AMN, bool BMN, int TN, int CG, int PARTS>
@@ -311,88 +448,36 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         };
         for (int i = cluster; i < p.tiles && !timed_out; i += clusters) {
             const OrthoTile t = ortho_tile<SYM, FT, TN>(p, i);
-            const int fw = t.f0 + rank * 128 + 32 * q, f = fw + lane;  // the warp's and the lane's feature
-            // A block of 32 features x 32 columns from c on, from its sums.
-            auto block = [&](int c, float (&v)[32]) {
-                // Nothing there, or on the diagonal's other side.
-                if (fw >= p.F || c >= p.C || (SYM && fw < c)) return;
-                const int n = min(32, p.C - c);
-                const bool diagonal = SYM && fw == c;
-                if constexpr (MODE == kOrthoGram) {
-                    if (diagonal && f < p.F) {
+            const int r0 = t.f0 + rank * 128 + 32 * q;  // the warp's first row
+            // Blocks of 32 rows x 32 columns: some are not there, or on the diagonal's other side.
+            auto wanted = [&](int c) { return r0 < p.F && c < p.C && !(SYM && r0 < c); };
+            const int c0 = t.c0 + half * S::kWarpCols;
+            // While the MMAs run: the first block's planes, the others' to the second-level cache, the diagonals' parts.
+            OrthoState<MODE> next;
+            OrthoDiagonal diagonal;
+            if (wanted(c0)) next.load(p, t.e, r0 + lane, c0);
+            if constexpr (MODE != kOrthoGram) {
+                const int row = r0 + lane;
+                const float* const d = p.d_in + t.e * p.diag;
+                if (row < p.F) {
+                    if (MODE == kOrthoSquare || !p.by_column) diagonal.row = __ldcg(d + row);
+                    const long long at = t.e * p.s_in + row * p.ld_in + c0;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j == lane) p.d_out[static_cast<long long>(t.e) * p.diag + f] = v[j] * 0x1p-26f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= 0x1p-14f;
-                } else {
-                    // The carried planes at this block, and the diagonal's part.
-                    const long long at = t.e * p.s_in + c * p.ld_in + f;
-                    const float* d = p.d_in + static_cast<long long>(t.e) * p.diag;
-                    const bool by_lane = MODE == kOrthoSquare || p.by_feature;
-                    const float df = by_lane && f < p.F ? d[f] : 0.f;
-                    const float dl = (MODE == kOrthoSquare || !p.by_feature) && lane < n ? d[c + lane] : 0.f;
-                    float x[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        x[j] = 0.f;
-                        if (j < n && f < p.F) {
-                            const long long o = at + j * p.ld_in;
-                            x[j] = __half2float(p.in_hi[o]) + __half2float(p.in_lo[o]);
+                    for (int j = 32; j < S::kWarpCols; j += 32)
+                        if (wanted(c0 + j)) {
+                            prefetch_l2(p.in_hi + at + j);
+                            prefetch_l2(p.in_lo + at + j);
                         }
-                    }
-                    if constexpr (MODE == kOrthoSquare) {
-                        if (diagonal && f < p.F) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j == lane)
-                                    p.d_out[static_cast<long long>(t.e) * p.diag + f] =
-                                        fmaf(p.c, fmaf(df, df, v[j] * 0x1p-24f), p.b * df);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float dc = __shfl_sync(0xffffffffu, dl, j);
-                            v[j] = fmaf(p.c, fmaf(df + dc, x[j], v[j] * 0x1p-12f), p.b * x[j]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float dc = __shfl_sync(0xffffffffu, dl, j);
-                            v[j] = fmaf(p.a + (p.by_feature ? df : dc), x[j], v[j] * 0x1p-12f);
-                        }
-                    }
                 }
-                if (diagonal) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j == lane) v[j] = 0.f;
+                if ((MODE == kOrthoSquare || p.by_column) && 4 * lane < S::kWarpCols && c0 + 4 * lane < p.C) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(d + c0) + lane);
+                    diagonal.column[0] = x.x, diagonal.column[1] = x.y, diagonal.column[2] = x.z, diagonal.column[3] = x.w;
                 }
-                if (MODE == kOrthoUpdate && p.out) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= 0x1p-13f;
-                    const long long at = t.e * p.so + c * p.ldo + fw;
-                    if (p.out_type == 0)
-                        store_features(patch, p.align, static_cast<float*>(p.out) + at, p.ldo, v, n, p.F - fw);
-                    else if (p.out_type == 1)
-                        store_features(patch, p.align, static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, v, n, p.F - fw);
-                    else
-                        store_features(patch, p.align, static_cast<__half*>(p.out) + at, p.ldo, v, n, p.F - fw);
-                    return;
-                }
-                // hi, then what it leaves.  (Rows of the planes are whole vectors: writing to their ends is harmless.)
-                auto store = [&](__half* plane) {
-                    __half* const to = plane + t.e * p.s_out;
-                    store_features(patch, 16, to + c * p.ld_out + fw, p.ld_out, v, n, static_cast<int>(p.ld_out) - fw);
-                    if (SYM && !diagonal)
-                        store_rows(patch, 16, to + fw * p.ld_out + c, p.ld_out, v, p.F - fw, static_cast<int>(p.ld_out) - c);
-                };
-                store(p.out_hi);
-                if (p.out_lo) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
-                    store(p.out_lo);
-                }
+            }
+            auto block = [&](int j, float (&v)[32]) {
+                const OrthoState<MODE> state = next;
+                if (32 * (j + 1) < S::kWarpCols && wanted(c0 + 32 * (j + 1))) next.load(p, t.e, r0 + lane, c0 + 32 * (j + 1));
+                if (wanted(c0 + 32 * j)) ortho_block<MODE>(p, patch, t.e, r0, c0 + 32 * j, 32 * j, state, diagonal, v);
             };
             uint32_t acc;
             if constexpr (PARTS == 1) {
@@ -401,16 +486,15 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                     break;
                 }
 #pragma unroll 1
-                for (int j = 0; j < S::kWarpCols; j += 32) {
-                    const int c = half * S::kWarpCols + j;
+                for (int j = 0; j < S::kWarpCols / 32; ++j) {
                     uint32_t r[32];
                     float v[32];
                     __syncwarp();
-                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(half * S::kWarpCols + 32 * j), r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int u = 0; u < 32; ++u) v[u] = __uint_as_float(r[u]);
-                    block(t.c0 + c, v);
+                    block(j, v);
                 }
                 release();
             } else {
@@ -426,20 +510,24 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < S::kWarpCols / 32; ++j) {
-                        const uint32_t c = static_cast<uint32_t>(half * S::kWarpCols + 32 * j);
-                        uint32_t big[32], small[32];
-                        __syncwarp();
-                        tmem_ld_32x32b_x32(acc + TN + c, small);
-                        tmem_ld_32x32b_x32(acc + c, big);
-                        tmem_wait_ld();
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) sum[j][u] += __uint_as_float(big[u]) + __uint_as_float(small[u]);
+                        for (int h = 0; h < 32; h += 16) {
+                            const uint32_t c = static_cast<uint32_t>(half * S::kWarpCols + 32 * j + h);
+                            uint32_t big[16], small[16];
+                            __syncwarp();
+                            tmem_ld_32x32b_x16(acc + TN + c, small);
+                            tmem_ld_32x32b_x16(acc + c, big);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 16; ++u)
+                                sum[j][h + u] += __uint_as_float(big[u]) + __uint_as_float(small[u]);
+                        }
                     }
                     release();
                 }
                 if (timed_out) break;
 #pragma unroll
-                for (int j = 0; j < S::kWarpCols / 32; ++j) block(t.c0 + half * S::kWarpCols + 32 * j, sum[j]);
+                for (int j = 0; j < S::kWarpCols / 32; ++j) block(j, sum[j]);
             }
         }
     }
