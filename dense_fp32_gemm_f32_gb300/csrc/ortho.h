@@ -22,6 +22,8 @@ struct OrthoPrep {
     double eps;
     uint16_t* hi;        // planes of E x rows x pitch; `plane` elements apart
     long long pitch, plane;
+    int* zero;           // counters to set to 0
+    long long zeros;
 };
 int ortho_prepare(const OrthoPrep& p, int type, cudaStream_t s);
 

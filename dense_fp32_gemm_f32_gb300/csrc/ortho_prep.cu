@@ -50,6 +50,9 @@ template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const OrthoPrep p) {
     __shared__ double scratch[kPrepThreads / 32];
     grid_dependency_launch();
+    for (long long i = blockIdx.x * static_cast<long long>(kPrepThreads) + threadIdx.x; i < p.zeros;
+         i += static_cast<long long>(gridDim.x) * kPrepThreads)
+        p.zero[i] = 0;
     const int e = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
     const int octs = (p.cols + 7) / 8;
     const int r0 = chunk * p.per, rows = min(p.per, p.rows - r0);

@@ -1,7 +1,7 @@
 // Newton-Schulz products on the fifth-generation tensor cores (tcgen05).
 //
 // A step on X (m x n, m <= n; where the matrix is taller than wide, what is
-// stored is X^T) is three products, each a launch over all matrices:
+// stored is X^T) is three products:
 //
 //   gram     A = X X^T            both operands X
 //   square   B = b A + c A A      both operands A
@@ -30,10 +30,25 @@
 // A and B are symmetric: only tiles that reach the diagonal or lie on its one
 // side are computed, and every 32 x 32 block off it is stored twice.
 //
+// All steps are one launch.  Its CTAs (or CTA pairs) are resident together (a
+// cooperative launch) and take the output tiles of all products in one order,
+// every P-th each; a tile waits until the row panels that it reads are there:
+//
+//   gram tile (i, j)       rows i and j of X           (panels of FT rows)
+//   square tile (i, j)     rows i and j of A
+//   update tile (r, c)     rows r of B (taller than wide: c), and so all of A and X
+//
+// A counter a panel holds the epilogue warps that have finished a tile with
+// rows in it, over all steps.  Tiles come in an order in which every tile waits for
+// earlier ones alone, so the first unfinished one can always proceed.  A buffer
+// is written again only by tiles that wait, through others, for all that read it
+// before (X alternates between two).  Products of several matrices then follow one another without a
+// gap, and those of one matrix with gaps of about a tile.
+//
 // The roles of the warps, the ring and the accumulators are those of
-// experts_tc.cuh: load warp, MMA warp, epilogue warps, and persistent CTAs or
-// CTA pairs.  The output's rows f lie on the tensor core's rows, its contiguous
-// dimension c on the columns, D[f, c] = sum_k P[f, k] Q[c, k] (see the epilogue).  With two planes
+// experts_tc.cuh: load warp, MMA warp, epilogue warps.  The output's rows f lie on
+// the tensor core's rows, its contiguous dimension c on the columns, D[f, c] =
+// sum_k P[f, k] Q[c, k] (see the epilogue).  With two planes
 // hi hi has an accumulator of its own, the small products another, and both go
 // to float32 registers every 512 of the contraction (an instruction cuts
 // sums to 24 bits).
@@ -46,26 +61,27 @@
 
 namespace gb300 {
 
-enum OrthoMode { kOrthoGram, kOrthoSquare, kOrthoUpdate };
+enum OrthoPhase { kOrthoGram, kOrthoSquare, kOrthoUpdate };
+
+// Matrices in two f16 planes, E in each.
+struct OrthoPlanes {
+    __half *hi, *lo;       // lo null: not kept
+    long long ld, matrix;  // elements a row, a matrix
+};
 
 struct OrthoTcParams {
-    int tiles, per;        // output tiles in all, of a matrix
-    int ftiles, ctiles;
-    int F, C, K, E;        // output F x C (C contiguous), contraction
-    const __half* in_hi;   // square: A's planes; update: X's (as the output lies)
-    const __half* in_lo;
-    __half* out_hi;        // gram: A's planes; square: B's; update: X's next
-    __half* out_lo;        // null: not needed
-    long long ld_in, s_in, ld_out, s_out;  // elements a row, a matrix
-    const float* d_in;     // square: A's diagonals; update: B's (`diag` a matrix, a multiple of 16)
-    float* d_out;          // gram: A's diagonals; square: B's
+    int E, m, rows, cols;     // X as stored: rows x cols, m the shorter
+    int steps, items;         // output tiles in all
+    int sym_tiles, up_tiles;  // of a matrix: gram or square, update
+    OrthoPlanes x[2], a, p;   // X (by turns), A and B less their diagonals
+    float *d, *e;             // the diagonals of A and B, `diag` (a multiple of 16) a matrix
     long long diag;
-    int by_column;         // update: e goes by column (else by row)
-    float a, b, c;
-    void* out;             // the last update's result, of out_type (null: planes)
+    int* done;                // counters: 3 kinds (X, A, B) x E x panels, zero at the start
+    int panels;
+    float c1, c3, c5;         // the polynomial
+    void* out;
     long long ldo, so;
     int out_type, align;
-    uint32_t idesc;
     unsigned long long timeout_ns;
     unsigned int* status;
 };
@@ -75,47 +91,122 @@ constexpr int kOrthoChunk = 512;  // contraction in one accumulator, with two pl
 template <int TN_, int CG_, int PARTS_>
 struct OrthoShape {
     static constexpr int TN = TN_, CG = CG_, PARTS = PARTS_;
+    static constexpr int FT = 128 * CG, R = FT / TN;  // a tile's rows; column tiles of a panel
     static constexpr int kCols = TN / CG;
     static constexpr int kABytes = 128 * 128, kBBytes = kCols * 128;  // of a part, 64 of the contraction
     static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
     static constexpr int kEpiWarps = 8;
     static constexpr int kThreads = 32 * (2 + kEpiWarps);
-    static constexpr int kPatches = kEpiWarps * kGrPatchBytes;
+    // (the widest tile has a seventh stage instead of patches for results off the 16-byte grid)
+    static constexpr bool kPatched = !(TN == 256 && PARTS == 1);
+    static constexpr int kPatches = kPatched ? kEpiWarps * kGrPatchBytes : 0;
     static constexpr int kStages = kRing(kStageBytes, kPatches);
     static constexpr int kAccCols = PARTS * TN, kTmemCols = 2 * kAccCols;
     static constexpr int kBars = 2 * kStages + 4;
     static constexpr int kSmem = kStages * kStageBytes + kPatches + 8 * kBars + 16 + 1024;
-    static constexpr int kWarpCols = TN / 2;  // an epilogue warp's columns
-    static_assert(kSmem <= 227 * 1024 && kStages >= 2 && kCols % 64 == 0 && kTmemCols <= 512, "shape");
+    static constexpr int kWarpCols = TN / 2;    // an epilogue warp's columns
+    static constexpr int kDone = kEpiWarps * CG;  // what a tile adds to a panel's counter
+    static_assert(kSmem <= 227 * 1024 && kStages >= 2 && kCols % 64 == 0 && kTmemCols <= 512 && FT % TN == 0, "shape");
 };
+
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
 struct OrthoTile {
-    int e, f0, c0;
+    int step, phase, e, f0, c0;
+    int need0, need1;  // panels that it reads
 };
 
-// Tile i: matrix by matrix; of a symmetric output the tiles with a column at or
-// below their last feature, feature tile by feature tile (tile f has the first
-// (f + 1) FT / TN column tiles, as far as there are any); of the others in
-// bands, as the grouped products'.
-template <bool SYM, int FT, int TN>
+// Item i: step by step, product by product, matrix by matrix.  A gram tile's
+// panels are those that the update before it finishes first (row by row, up to
+// the diagonal), a square tile's order finishes panel after panel of B for the
+// update (column panel by column panel, from the diagonal down).
+template <typename S, bool TALL>
 __device__ __forceinline__ OrthoTile ortho_tile(const OrthoTcParams& p, int i) {
     OrthoTile t;
-    t.e = i / p.per;
-    const int local = i - t.e * p.per;
-    int f, c;
-    if constexpr (SYM) {
-        constexpr int R = FT / TN;
-        f = static_cast<int>((sqrtf(8.f * local / R + 1.f) - 1.f) * 0.5f);
-        while (R * f * (f + 1) / 2 > local) --f;
-        while (R * (f + 1) * (f + 2) / 2 <= local) ++f;
-        f = min(f, p.ftiles - 1);
-        c = local - R * f * (f + 1) / 2;
+    const int sym = p.E * p.sym_tiles, all = 2 * sym + p.E * p.up_tiles;
+    t.step = i / all;
+    int local = i - t.step * all;
+    if (local < 2 * sym) {
+        t.phase = local < sym ? kOrthoGram : kOrthoSquare;
+        if (t.phase == kOrthoSquare) local -= sym;
+        t.e = local / p.sym_tiles;
+        local -= t.e * p.sym_tiles;
+        const int ft = div_up(p.m, S::FT), ct = div_up(p.m, S::TN);
+        int f = 0, c;
+        if (t.phase == kOrthoGram) {
+            while (true) {
+                const int n = min(ct, (f + 1) * S::R);
+                if (local < n) break;
+                local -= n;
+                ++f;
+            }
+            c = local;
+        } else {
+            int q = 0, width;
+            while (true) {
+                width = min(S::R, ct - q * S::R);
+                const int n = (ft - q) * width;
+                if (local < n) break;
+                local -= n;
+                ++q;
+            }
+            f = q + local / width;
+            c = q * S::R + local % width;
+        }
+        t.f0 = f * S::FT;
+        t.c0 = c * S::TN;
+        t.need0 = f;
+        t.need1 = c / S::R;
     } else {
-        tile_place(local, p.ctiles, p.ftiles, f, c);
+        t.phase = kOrthoUpdate;
+        local -= 2 * sym;
+        t.e = local / p.up_tiles;
+        local -= t.e * p.up_tiles;
+        int f, c;
+        if constexpr (TALL) {
+            const int ft = div_up(p.rows, S::FT);
+            c = local / ft;
+            f = local - c * ft;
+            t.need0 = t.need1 = c / S::R;
+        } else {
+            const int ct = div_up(p.cols, S::TN);
+            f = local / ct;
+            c = local - f * ct;
+            t.need0 = t.need1 = f;
+        }
+        t.f0 = f * S::FT;
+        t.c0 = c * S::TN;
     }
-    t.f0 = f * FT;
-    t.c0 = c * TN;
     return t;
+}
+
+// The counter that panel `q` of what tile t reads has reached when it is there.
+template <typename S, bool TALL>
+__device__ __forceinline__ int ortho_needed(const OrthoTcParams& p, const OrthoTile& t, int q) {
+    const int ft = div_up(p.m, S::FT), ct = div_up(p.m, S::TN);
+    const int width = min(S::R, ct - q * S::R);  // column tiles of the panel
+    if (t.phase == kOrthoGram)  // X, of the step before
+        return t.step * S::kDone * (TALL ? div_up(p.rows, S::FT) * width : div_up(p.cols, S::TN));
+    return (t.step + 1) * S::kDone * (min(ct, (q + 1) * S::R) + (ft - 1 - q) * width);
+}
+
+// Whole warp: waits until the panels that tile t reads are there.
+template <typename S, bool TALL>
+__device__ __forceinline__ bool ortho_wait(const OrthoTcParams& p, const OrthoTile& t) {
+    const int lane = threadIdx.x & 31, q = lane == 0 ? t.need0 : t.need1;
+    const int* counter = p.done + (static_cast<long long>(t.phase) * p.E + t.e) * p.panels + q;
+    const int needed = ortho_needed<S, TALL>(p, t, q);
+    auto ready = [&] { return __all_sync(0xffffffffu, lane > 1 || load_acquire_gpu(counter) >= needed) != 0; };
+    uint64_t t0 = 0;
+    while (!ready()) {
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0)
+            t0 = now;
+        else if (__any_sync(0xffffffffu, now - t0 > p.timeout_ns))
+            return false;
+    }
+    __syncwarp();  // (what two lanes have acquired, all may read)
+    return true;
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -131,12 +222,13 @@ struct alignas(32) Half16 {  // 16 f16 values
     uint32_t w[8];
 };
 
-// (past the first-level cache, which need not see what the kernel before wrote)
+// (past the first-level cache: other SMs write what is read here)
 __device__ __forceinline__ Half16 load_half16(const __half* p) {
     Half16 x;
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7])
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
     return x;
 }
 __device__ __forceinline__ void store_half16(__half* p, const uint32_t* w) {
@@ -146,49 +238,70 @@ __device__ __forceinline__ void store_half16(__half* p, const uint32_t* w) {
 }
 
 // What is carried beside the products at a lane's part of a block: two planes.
-template <int MODE>
 struct OrthoState {
     Half16 hi[2], lo[2];
-    __device__ __forceinline__ void load(const OrthoTcParams& p, int e, int row, int c) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            hi[i] = lo[i] = Half16{};
-            if (row < p.F && c + 16 * i < p.C) {
-                const long long at = e * p.s_in + row * p.ld_in + c + 16 * i;
-                hi[i] = load_half16(p.in_hi + at);
-                lo[i] = load_half16(p.in_lo + at);
-            }
-        }
+    __device__ __forceinline__ void load(const __half* h, const __half* l, bool first, bool second) {
+        hi[0] = hi[1] = lo[0] = lo[1] = Half16{};
+        if (first) hi[0] = load_half16(h), lo[0] = load_half16(l);
+        if (second) hi[1] = load_half16(h + 16), lo[1] = load_half16(l + 16);
     }
-    __device__ __forceinline__ float value(int j) const {  // (a constant after unrolling)
+    __device__ __forceinline__ float value(int j) const {  // (j: a constant after unrolling)
         const uint32_t h = hi[j / 16].w[j % 16 / 2], l = lo[j / 16].w[j % 16 / 2];
         const __half2 x = *reinterpret_cast<const __half2*>(&h), y = *reinterpret_cast<const __half2*>(&l);
         return j & 1 ? __high2float(x) + __high2float(y) : __low2float(x) + __low2float(y);
     }
 };
-template <>
-struct OrthoState<kOrthoGram> {
-    __device__ __forceinline__ void load(const OrthoTcParams&, int, int, int) {}
-};
 
 // The diagonals' part of a warp's rows and columns of a tile: the lane's row, and columns 4 lane .. 4 lane + 3.
 struct OrthoDiagonal {
-    float row = 0.f, column[4] = {};
+    float row, column[4];
 };
 
-// A block of rows r0 .. and columns c .., from its sums; `first`: its first column among the warp's.
-template <int MODE>
-__device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t patch, int e, int r0, int c, int first,
-                                            const OrthoState<MODE>& state, const OrthoDiagonal& d, float (&v)[32]) {
-    constexpr bool SYM = MODE != kOrthoUpdate;
+// A block of the result in its own type, a row a lane; rows and columns that there are.
+template <typename S, typename T>
+__device__ __forceinline__ void ortho_result(const OrthoTcParams& p, uint32_t patch, long long at, const float (&v)[32],
+                                             int rows, int cols) {
+    T* const o = static_cast<T*>(p.out) + at;
+    const int lane = threadIdx.x & 31;
+    if (p.align == 16 && cols >= 32) {
+        if (lane < rows) {
+            uint4* to = reinterpret_cast<uint4*>(o + lane * p.ldo);
+#pragma unroll
+            for (int j = 0; j < 32; j += 16 / static_cast<int>(sizeof(T))) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (sizeof(T) == 4)
+                        w[i] = __float_as_uint(v[j + i]);
+                    else
+                        w[i] = pair_from_f32<T>(v[j + 2 * i], v[j + 2 * i + 1]);
+                }
+                *to++ = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    } else if constexpr (S::kPatched) {
+        store_rows(patch, p.align, o, p.ldo, v, rows, cols);
+    } else if (lane < rows) {
+        T* to = o + lane * p.ldo;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cols) to[j] = from_f32<T>(v[j]);
+    }
+}
+
+// A block of rows r0 .. and columns c .. of tile t, from its sums; `first`: its first column among the warp's.
+template <typename S, bool TALL, int PHASE>
+__device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t patch, const OrthoTile& t, int r0, int c,
+                                            int first, const OrthoState& state, const OrthoDiagonal& d, float (&v)[32]) {
+    constexpr bool SYM = PHASE != kOrthoUpdate;
     const int lane = threadIdx.x & 31, row = r0 + lane;
+    const int F = SYM ? p.m : p.rows, C = SYM ? p.m : p.cols;
     const bool diagonal = SYM && r0 == c;
-    float* const d_out = p.d_out + e * p.diag;
-    const float dr = d.row;
+    float* const d_out = (PHASE == kOrthoGram ? p.d : p.e) + t.e * p.diag;
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
         float dj[4] = {};
-        if (MODE == kOrthoSquare || (MODE == kOrthoUpdate && p.by_column)) {
+        if (PHASE == kOrthoSquare || (PHASE == kOrthoUpdate && TALL)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dj[i] = __shfl_sync(0xffffffffu, d.column[i], (first + j) / 4);
         }
@@ -196,40 +309,41 @@ __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t pat
         for (int i = 0; i < 4; ++i) {
             float& x = v[j + i];
             const bool on = diagonal && j + i == lane;
-            if constexpr (MODE == kOrthoGram) {
-                if (on && row < p.F) d_out[row] = x * 0x1p-26f;
+            if constexpr (PHASE == kOrthoGram) {
+                if (on && row < F) d_out[row] = x * 0x1p-26f;
                 x *= 0x1p-14f;
-            } else if constexpr (MODE == kOrthoSquare) {
-                if (on && row < p.F) d_out[row] = fmaf(p.c, fmaf(dr, dr, x * 0x1p-24f), p.b * dr);
+            } else if constexpr (PHASE == kOrthoSquare) {
+                if (on && row < F) d_out[row] = fmaf(p.c5, fmaf(d.row, d.row, x * 0x1p-24f), p.c3 * d.row);
                 const float o = state.value(j + i);
-                x = fmaf(p.c, fmaf(dr + dj[i], o, x * 0x1p-12f), p.b * o);
+                x = fmaf(p.c5, fmaf(d.row + dj[i], o, x * 0x1p-12f), p.c3 * o);
             } else {
-                x = fmaf(p.a + (p.by_column ? dj[i] : dr), state.value(j + i), x * 0x1p-12f);
+                x = fmaf(p.c1 + (TALL ? dj[i] : d.row), state.value(j + i), x * 0x1p-12f);
             }
             if (on) x = 0.f;
         }
     }
-    if constexpr (MODE == kOrthoUpdate) {
-        if (p.out) {
+    if constexpr (PHASE == kOrthoUpdate) {
+        if (t.step + 1 == p.steps) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= 0x1p-13f;
-            const long long at = e * p.so + r0 * p.ldo + c;
-            if (p.out_type == 0)
-                store_rows(patch, p.align, static_cast<float*>(p.out) + at, p.ldo, v, p.F - r0, p.C - c);
-            else if (p.out_type == 1)
-                store_rows(patch, p.align, static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, v, p.F - r0, p.C - c);
-            else
-                store_rows(patch, p.align, static_cast<__half*>(p.out) + at, p.ldo, v, p.F - r0, p.C - c);
+            const long long at = t.e * p.so + r0 * p.ldo + c;
+            if (p.out_type == 0) {
+                if constexpr (S::PARTS == 2) ortho_result<S, float>(p, patch, at, v, F - r0, C - c);
+            } else if (p.out_type == 1) {
+                if constexpr (S::PARTS == 1) ortho_result<S, __nv_bfloat16>(p, patch, at, v, F - r0, C - c);
+            } else {
+                if constexpr (S::PARTS == 2) ortho_result<S, __half>(p, patch, at, v, F - r0, C - c);
+            }
             return;
         }
     }
     // hi, then what it leaves.  (Rows of the planes are whole vectors: writing to
     // their ends is harmless.)
+    const OrthoPlanes& to = PHASE == kOrthoGram ? p.a : PHASE == kOrthoSquare ? p.p : p.x[(t.step & 1) ^ 1];
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
-        __half* const plane = part == 0 ? p.out_hi : p.out_lo;
-        if (part == 1 && !plane) break;
-        __half* const to = plane + e * p.s_out;
+        if (part == 1 && PHASE == kOrthoSquare && S::PARTS == 1) break;  // (products take B's hi alone)
+        __half* const plane = (part == 0 ? to.hi : to.lo) + t.e * to.matrix;
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -238,33 +352,33 @@ __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t pat
             v[2 * j] -= __low2float(h);
             v[2 * j + 1] -= __high2float(h);
         }
-        if (row < p.F) {
-            __half* const at = to + row * p.ld_out + c;
+        if (row < F) {
+            __half* const at = plane + row * to.ld + c;
             store_half16(at, w);
-            if (c + 16 < p.C) store_half16(at + 16, w + 8);
+            if (c + 16 < C) store_half16(at + 16, w + 8);
         }
-        if (SYM && !diagonal && row < p.F) {
+        if (SYM && !diagonal && row < F) {
             // The block's mirror image: rows are columns, a value a lane.
-            uint16_t* at = reinterpret_cast<uint16_t*>(to + c * p.ld_out + row);
+            uint16_t* at = reinterpret_cast<uint16_t*>(plane + c * to.ld + row);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                if (c + j < p.C) *at = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
-                at += p.ld_out;
+                if (c + j < C) *at = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+                at += to.ld;
             }
         }
     }
 }
 
-template <int MODE, bool AMN, bool BMN, int TN, int CG, int PARTS>
+template <int TN, int CG, int PARTS, bool TALL>
 __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
-    ortho_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    ortho_tc_kernel(const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_x1,
+                    const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_p,
                     const OrthoTcParams p) {
     using S = OrthoShape<TN, CG, PARTS>;
-    constexpr bool PAIR = CG == 2, SYM = MODE != kOrthoUpdate;
-    constexpr int FT = 128 * CG;
+    constexpr bool PAIR = CG == 2;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t baseB = base + PARTS * S::kABytes;  // B's parts follow A's in a stage
+    const uint32_t baseB = base + PARTS * S::kABytes;  // the second operand's parts follow the first's in a stage
     const uint32_t patches = base + S::kStages * S::kStageBytes;
     const uint32_t bars = patches + S::kPatches;
     const uint32_t full0 = bars, empty0 = bars + 8 * S::kStages;
@@ -286,8 +400,10 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
             mbar_init(acc_empty0 + 8 * b, S::kEpiWarps * CG);
         }
         fence_mbarrier_init();
-        prefetch_tensormap(&tmA);
-        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tm_x0);
+        prefetch_tensormap(&tm_x1);
+        prefetch_tensormap(&tm_a);
+        prefetch_tensormap(&tm_p);
     }
     __syncwarp();
     if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, S::kTmemCols);
@@ -298,9 +414,8 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
     tmem = warp_uniform(tmem);
-    grid_dependency_launch();
-    grid_dependency_wait();  // the set-up above ran beside the end of the kernel before
 
+    auto contraction = [&](int phase) { return phase == kOrthoGram ? (TALL ? p.rows : p.cols) : p.m; };
     bool timed_out = false;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -308,10 +423,20 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         const bool issuer = elect_one();
         uint32_t s = 0, phase = 1;  // (the first round finds every stage empty)
         int issued = 0;
-        for (int i = cluster; i < p.tiles && !timed_out; i += clusters) {
-            const OrthoTile t = ortho_tile<SYM, FT, TN>(p, i);
-            const int f0 = t.f0 + rank * 128, c0 = t.c0 + rank * S::kCols;
-            for (int k = 0; k < p.K; k += kGrBK) {
+        for (int i = cluster; i < p.items && !timed_out; i += clusters) {
+            const OrthoTile t = ortho_tile<S, TALL>(p, i);
+            if (!ortho_wait<S, TALL>(p, t)) {
+                timed_out = true;
+                break;
+            }
+            fence_proxy_async_global();  // (the copies read what other SMs stored)
+            const CUtensorMap* const x = t.step & 1 ? &tm_x1 : &tm_x0;
+            const CUtensorMap* const first = t.phase == kOrthoGram ? x : t.phase == kOrthoSquare ? &tm_a : TALL ? x : &tm_p;
+            const CUtensorMap* const second = t.phase == kOrthoGram ? x : t.phase == kOrthoSquare ? &tm_a : TALL ? &tm_p : x;
+            const bool first_mn = TALL && t.phase == kOrthoGram;
+            const bool second_mn = TALL ? t.phase == kOrthoGram : t.phase == kOrthoUpdate;
+            const int f0 = t.f0 + rank * 128, c0 = t.c0 + rank * S::kCols, K = contraction(t.phase);
+            for (int k = 0; k < K; k += kGrBK) {
                 if (!mbar_wait_warp<false>(empty0 + 8 * s, phase, tmo)) {
                     timed_out = true;
                     break;
@@ -320,21 +445,22 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                 if (issuer) {
                     const uint32_t bar = bar0 + 8 * s;
                     if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, CG * S::kStageBytes);
-                    auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                    auto load = [&](uint32_t dst, const CUtensorMap* map, bool mn, int at, int z) {
+                        const int x0 = mn ? at : k, y0 = mn ? k : at;
                         if constexpr (PAIR)
-                            tma_load_3d_pair(dst, map, bar, x, y, z);
+                            tma_load_3d_pair(dst, map, bar, x0, y0, z);
                         else
-                            tma_load_3d(dst, map, bar, x, y, z);
+                            tma_load_3d(dst, map, bar, x0, y0, z);
                     };
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         const int z = part * p.E + t.e;
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            load(a + part * S::kABytes + j * 64 * 128, &tmA, AMN ? f0 + 64 * j : k, AMN ? k : f0 + 64 * j, z);
+                            load(a + part * S::kABytes + j * 64 * 128, first, first_mn, f0 + 64 * j, z);
 #pragma unroll
                         for (int j = 0; j < S::kCols / 64; ++j)
-                            load(b + part * S::kBBytes + j * 64 * 128, &tmB, BMN ? c0 + 64 * j : k, BMN ? k : c0 + 64 * j, z);
+                            load(b + part * S::kBBytes + j * 64 * 128, second, second_mn, c0 + 64 * j, z);
                     }
                 }
                 __syncwarp();
@@ -354,29 +480,33 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         if (rank == 0) {  // (the first CTA issues for both)
-            const uint64_t descA = AMN ? umma_desc_mnmajor_sw128(base, 64 * 128) : umma_desc_kmajor_sw128(base);
-            const uint64_t descB = BMN ? umma_desc_mnmajor_sw128(baseB, 64 * 128) : umma_desc_kmajor_sw128(baseB);
-            // 16 k: 32 bytes of each row (K-major), 16 rows of 128 bytes (MN-major); addresses in units of 16
-            constexpr uint32_t ka = AMN ? 128 : 2, kb = BMN ? 128 : 2;
             constexpr uint32_t pa = S::kABytes / 16, pb = S::kBBytes / 16;
             const uint32_t peer_empty0 = PAIR ? warp_uniform(map_shared_rank(empty0, 1)) : 0;
             const uint32_t peer_acc_full0 = PAIR ? warp_uniform(map_shared_rank(acc_full0, 1)) : 0;
             const bool issuer = elect_one();
-            const uint32_t idesc = p.idesc;
             uint32_t s = 0, phase = 0;
             int unit = 0;  // accumulators filled
-            for (int i = cluster; i < p.tiles && !timed_out; i += clusters) {
-                for (int k = 0; k < p.K;) {
+            for (int i = cluster; i < p.items && !timed_out; i += clusters) {
+                const int of = ortho_tile<S, TALL>(p, i).phase, K = contraction(of);
+                const bool a_mn = TALL && of == kOrthoGram, b_mn = TALL ? of == kOrthoGram : of == kOrthoUpdate;
+                const uint64_t descA = a_mn ? umma_desc_mnmajor_sw128(base, 64 * 128) : umma_desc_kmajor_sw128(base);
+                const uint64_t descB = b_mn ? umma_desc_mnmajor_sw128(baseB, 64 * 128) : umma_desc_kmajor_sw128(baseB);
+                // 16 k: 32 bytes of each row (K-major), 16 rows of 128 bytes (MN-major); addresses in units of 16
+                const uint32_t ka = a_mn ? 128 : 2, kb = b_mn ? 128 : 2;
+                const uint32_t idesc = 1u << 4 | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) |
+                                       static_cast<uint32_t>(TN / 8) << 17 | static_cast<uint32_t>(S::FT / 16) << 24;
+                for (int k = 0; k < K;) {
                     const int buf = unit & 1;
                     const uint32_t acc = tmem + static_cast<uint32_t>(buf * S::kAccCols);
-                    const int end = PARTS > 1 ? min(p.K, k + kOrthoChunk) : p.K;
+                    const int end = PARTS > 1 ? min(K, k + kOrthoChunk) : K;
                     if (unit >= 2 && !mbar_wait_warp<PAIR>(acc_empty0 + 8 * buf, ((unit >> 1) - 1) & 1, tmo)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after_sync();
                     for (int q = k; q < end; q += kGrBK) {
-                        if (!mbar_wait_warp<false>(full0 + 8 * s, phase, tmo)) {
+                        // (the load warp waits for what it reads up to the limit, and then for the stage)
+                        if (!mbar_wait_warp<false>(full0 + 8 * s, phase, 2 * tmo)) {
                             timed_out = true;
                             break;
                         }
@@ -429,7 +559,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         int unit = 0;
         auto wait = [&](uint32_t& acc) {
             const int buf = unit & 1;
-            if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, tmo)) return false;
+            if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, 3 * tmo)) return false;
             tc_fence_after_sync();
             acc = tmem + static_cast<uint32_t>(buf * S::kAccCols) + (static_cast<uint32_t>(32 * q) << 16);
             return true;
@@ -446,45 +576,51 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
             __syncwarp();
             ++unit;
         };
-        for (int i = cluster; i < p.tiles && !timed_out; i += clusters) {
-            const OrthoTile t = ortho_tile<SYM, FT, TN>(p, i);
-            const int r0 = t.f0 + rank * 128 + 32 * q;  // the warp's first row
+        // A tile of product PHASE; false on a timeout.
+        auto tile = [&](const OrthoTile& t, auto which) -> bool {
+            constexpr int PHASE = decltype(which)::value;
+            constexpr bool SYM = PHASE != kOrthoUpdate;
+            const int F = SYM ? p.m : p.rows, C = SYM ? p.m : p.cols, K = contraction(PHASE);
+            const int r0 = t.f0 + rank * 128 + 32 * q, c0 = t.c0 + half * S::kWarpCols;  // the warp's first row and column
             // Blocks of 32 rows x 32 columns: some are not there, or on the diagonal's other side.
-            auto wanted = [&](int c) { return r0 < p.F && c < p.C && !(SYM && r0 < c); };
-            const int c0 = t.c0 + half * S::kWarpCols;
+            auto wanted = [&](int c) { return r0 < F && c < C && !(SYM && r0 < c); };
             // While the MMAs run: the first block's planes, the others' to the second-level cache, the diagonals' parts.
-            OrthoState<MODE> next;
-            OrthoDiagonal diagonal;
-            if (wanted(c0)) next.load(p, t.e, r0 + lane, c0);
-            if constexpr (MODE != kOrthoGram) {
-                const int row = r0 + lane;
-                const float* const d = p.d_in + t.e * p.diag;
-                if (row < p.F) {
-                    if (MODE == kOrthoSquare || !p.by_column) diagonal.row = __ldcg(d + row);
-                    const long long at = t.e * p.s_in + row * p.ld_in + c0;
+            OrthoState next = {};
+            OrthoDiagonal diagonal = {};
+            const __half *hi = nullptr, *lo = nullptr;
+            const bool mine = r0 + lane < F;
+            if constexpr (PHASE != kOrthoGram) {
+                if (!ortho_wait<S, TALL>(p, t)) return false;
+                const OrthoPlanes& from = PHASE == kOrthoSquare ? p.a : p.x[t.step & 1];
+                const long long at = t.e * from.matrix + (r0 + lane) * from.ld + c0;
+                hi = from.hi + at;
+                lo = from.lo + at;
+                const float* const d = (PHASE == kOrthoSquare ? p.d : p.e) + t.e * p.diag;
+                if (wanted(c0)) next.load(hi, lo, mine, mine && c0 + 16 < C);
+                if (mine) {
+                    if (PHASE == kOrthoSquare || !TALL) diagonal.row = __ldcg(d + r0 + lane);
 #pragma unroll
                     for (int j = 32; j < S::kWarpCols; j += 32)
                         if (wanted(c0 + j)) {
-                            prefetch_l2(p.in_hi + at + j);
-                            prefetch_l2(p.in_lo + at + j);
+                            prefetch_l2(hi + j);
+                            prefetch_l2(lo + j);
                         }
                 }
-                if ((MODE == kOrthoSquare || p.by_column) && 4 * lane < S::kWarpCols && c0 + 4 * lane < p.C) {
+                if ((PHASE == kOrthoSquare || TALL) && 4 * lane < S::kWarpCols && c0 + 4 * lane < C) {
                     const float4 x = __ldcg(reinterpret_cast<const float4*>(d + c0) + lane);
                     diagonal.column[0] = x.x, diagonal.column[1] = x.y, diagonal.column[2] = x.z, diagonal.column[3] = x.w;
                 }
             }
             auto block = [&](int j, float (&v)[32]) {
-                const OrthoState<MODE> state = next;
-                if (32 * (j + 1) < S::kWarpCols && wanted(c0 + 32 * (j + 1))) next.load(p, t.e, r0 + lane, c0 + 32 * (j + 1));
-                if (wanted(c0 + 32 * j)) ortho_block<MODE>(p, patch, t.e, r0, c0 + 32 * j, 32 * j, state, diagonal, v);
+                const OrthoState state = next;
+                const int c = c0 + 32 * j;
+                if (PHASE != kOrthoGram && 32 * (j + 1) < S::kWarpCols && wanted(c + 32))
+                    next.load(hi + 32 * (j + 1), lo + 32 * (j + 1), mine, mine && c + 48 < C);
+                if (wanted(c)) ortho_block<S, TALL, PHASE>(p, patch, t, r0, c, 32 * j, state, diagonal, v);
             };
             uint32_t acc;
             if constexpr (PARTS == 1) {
-                if (!wait(acc)) {
-                    timed_out = true;
-                    break;
-                }
+                if (!wait(acc)) return false;
 #pragma unroll 1
                 for (int j = 0; j < S::kWarpCols / 32; ++j) {
                     uint32_t r[32];
@@ -503,11 +639,8 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                 for (int j = 0; j < S::kWarpCols / 32; ++j)
 #pragma unroll
                     for (int u = 0; u < 32; ++u) sum[j][u] = 0.f;
-                for (int k = 0; k < p.K; k += kOrthoChunk) {
-                    if (!wait(acc)) {
-                        timed_out = true;
-                        break;
-                    }
+                for (int k = 0; k < K; k += kOrthoChunk) {
+                    if (!wait(acc)) return false;
 #pragma unroll
                     for (int j = 0; j < S::kWarpCols / 32; ++j) {
 #pragma unroll
@@ -525,10 +658,30 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                     }
                     release();
                 }
-                if (timed_out) break;
 #pragma unroll
                 for (int j = 0; j < S::kWarpCols / 32; ++j) block(j, sum[j]);
             }
+            // The tile's rows, and those of its mirror image, are one warp nearer.
+            fence_proxy_async_global();
+            __syncwarp();
+            if (lane == 0 && (PHASE != kOrthoUpdate || t.step + 1 < p.steps)) {
+                // kinds: gram finishes A (1), square B (2), update X (0)
+                constexpr int kind = PHASE == kOrthoUpdate ? 0 : PHASE + 1;
+                int* const counter = p.done + (static_cast<long long>(kind) * p.E + t.e) * p.panels;
+                if (SYM) {
+                    add_release_gpu(counter + t.need0, 1);
+                    if (t.need1 != t.need0) add_release_gpu(counter + t.need1, 1);
+                } else {
+                    add_release_gpu(counter + t.need0, 1);
+                }
+            }
+            return true;
+        };
+        for (int i = cluster; i < p.items && !timed_out; i += clusters) {
+            const OrthoTile t = ortho_tile<S, TALL>(p, i);
+            timed_out = !(t.phase == kOrthoGram     ? tile(t, std::integral_constant<int, kOrthoGram>())
+                          : t.phase == kOrthoSquare ? tile(t, std::integral_constant<int, kOrthoSquare>())
+                                                    : tile(t, std::integral_constant<int, kOrthoUpdate>()));
         }
     }
 
