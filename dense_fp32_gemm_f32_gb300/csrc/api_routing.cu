@@ -82,12 +82,12 @@ int sgemm_route(int type, int score, int T, int E, int k, const void* logits, in
     p.top_groups = top_groups, p.group_best = group_best;
     p.experts = experts, p.weights = weights, p.offsets = offsets, p.slots = slots;
     p.vec = whole_vectors(in[0]);
-    const RoutePlan plan = route_plan(T, E, st->sm_count);
+    const RoutePlan plan = route_plan(T, st->sm_count);
     p.steps = plan.steps;
-    if (plan.ctas > 1) {
+    if (plan.clusters > 1) {
         cudaMemPool_t pool = workspace_pool(dev, *st);
         void* ws = nullptr;
-        if (!pool || cudaMallocFromPoolAsync(&ws, sizeof(int) * plan.ctas * E, pool, s) != cudaSuccess) {
+        if (!pool || cudaMallocFromPoolAsync(&ws, sizeof(int) * plan.clusters * E, pool, s) != cudaSuccess) {
             (void)cudaGetLastError();
             return SGEMM_ERR_CUDA;
         }

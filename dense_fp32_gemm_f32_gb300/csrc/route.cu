@@ -16,9 +16,13 @@
 // Places.  A CTA takes tokens 32 at a time and sets a bit a token in a word of
 // each chosen expert (an OR: its order does not matter); a choice's place
 // among the expert's rows in this CTA is then the number of bits below its own
-// plus those of the steps before.  With several CTAs their counts go to a
-// table, and place_kernel adds up, in every CTA, the counts of the CTAs before
-// it and of the experts before each.
+// plus those of the steps before.  The CTAs of a cluster add up their counts
+// through distributed shared memory.  Up to 512 tokens are one cluster, which
+// then knows all; else the clusters' counts go to a table, and place_kernel adds
+// up, in a CTA a cluster, those of the clusters and of the experts before.
+#include <algorithm>
+#include <type_traits>
+
 #include "../../include/sgemm_routing.h"
 #include "experts_groups.cuh"
 #include "ptx.cuh"
@@ -113,6 +117,70 @@ __device__ __forceinline__ void load_row(const T* row, int E, bool vec, float (&
 
 // ------------------------------------------------------------------ the choice
 
+// The lane's keys, the largest first (equal ones by their number), and their
+// numbers, 4 bits each.  Neighbours trade places, so that equal ones keep theirs.
+template <int NPL, typename Key>
+__device__ __forceinline__ uint32_t sort_lane(Key (&key)[NPL]) {
+    static_assert(NPL <= 8, "4 bits each");
+    uint32_t at[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) at[i] = i;
+#pragma unroll
+    for (int round = 0; round < NPL; ++round)
+#pragma unroll
+        for (int i = round & 1; i + 1 < NPL; i += 2) {
+            const bool swap = key[i] < key[i + 1];
+            const Key a = key[i], b = key[i + 1];
+            key[i] = swap ? b : a;
+            key[i + 1] = swap ? a : b;
+            const uint32_t x = at[i], y = at[i + 1];
+            at[i] = swap ? y : x;
+            at[i + 1] = swap ? x : y;
+        }
+    uint32_t packed = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) packed |= at[i] << (4 * i);
+    return packed;
+}
+
+// The two largest of four keys, (a >= b) and (c >= d), to a and b.
+template <typename Key>
+__device__ __forceinline__ void merge_two(Key& a, Key& b, Key c, Key d) {
+    const Key low = min(a, c);
+    a = max(a, c);
+    b = max(low, max(b, d));
+}
+
+// The groups to choose from, a bit each: from the two best keys a, b of group g in
+// lane g (0: none).  `sure`: whether that is certain; see choose().
+template <typename V>
+__device__ __forceinline__ unsigned choose_groups(const RouteParams& p, typename Keys<V>::Key a, typename Keys<V>::Key b,
+                                                  bool checked, V near, bool& sure) {
+    using K = Keys<V>;
+    using Key = typename K::Key;
+    Key score = 0;
+    if ((threadIdx.x & 31) < p.groups && a) {
+        V value = K::value(a);
+        if (p.group_best == 2 && b) value += K::value(b);
+        score = K::of(value);
+    }
+    unsigned kept = 0;
+    Key last = 0;
+    for (int i = 0; i < p.top_groups; ++i) {
+        const Key best = K::most(score);
+        if (best == 0) return kept;
+        const unsigned lane = __ffs(__ballot_sync(kAll, score == best)) - 1;
+        kept |= 1u << lane;
+        if ((threadIdx.x & 31) == lane) score = 0;
+        last = best;
+    }
+    if (checked) {  // (what is among them or not is decided at their end alone)
+        const Key next = K::most(score);
+        if (next && !(K::value(last) - K::value(next) > 2 * near)) sure = false;
+    }
+    return kept;
+}
+
 // Of a token's keys (0: out of service), the k best in order: lane j's result
 // is the j-th expert, -1 where there is none.  checked: `sure` is false if two
 // values that decide lie within `near` of one another (the result is then not
@@ -122,59 +190,25 @@ __device__ __forceinline__ int choose(typename Keys<V>::Key (&key)[NPL], const R
                                       bool& sure) {
     using K = Keys<V>;
     using Key = typename K::Key;
+    constexpr bool SORTED = NPL <= 8 && sizeof(V) == 4;
     const int lane = threadIdx.x & 31, first = lane * NPL;
+    const int size = p.groups > 1 ? p.E / p.groups : 0, lanes = size / NPL;
+    const bool whole = size % NPL == 0 && (lanes & (lanes - 1)) == 0;  // a power of two of whole lanes a group
     sure = true;
-    if (p.groups > 1) {
-        // The two best of every group, and from them its score, in lane g.
-        const int size = p.E / p.groups;
-        auto merge = [](Key& a, Key& b, Key c, Key d) {
-            const Key low = min(a, c);
-            a = max(a, c);
-            b = max(low, max(b, d));
-        };
+    if (p.groups > 1 && !(SORTED && whole)) {
         Key a = 0, b = 0;
-        const int lanes = size / NPL;
-        const bool whole = size % NPL == 0 && (lanes & (lanes - 1)) == 0;  // a power of two of whole lanes each
-        if (whole) {
+        for (int g = 0; g < p.groups; ++g) {
+            Key c = 0, d = 0;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) merge(a, b, key[i], Key{0});
-            for (int d = 1; d < lanes; d *= 2) merge(a, b, __shfl_xor_sync(kAll, a, d), __shfl_xor_sync(kAll, b, d));
-            const int from = (lane * lanes) & 31;
-            a = __shfl_sync(kAll, a, from);
-            b = __shfl_sync(kAll, b, from);
-        } else {
-            for (int g = 0; g < p.groups; ++g) {
-                Key c = 0, d = 0;
-#pragma unroll
-                for (int i = 0; i < NPL; ++i) {
-                    const int e = first + i - g * size;
-                    if (e >= 0 && e < size) merge(c, d, key[i], Key{0});
-                }
-#pragma unroll
-                for (int s = 1; s < 32; s *= 2) merge(c, d, __shfl_xor_sync(kAll, c, s), __shfl_xor_sync(kAll, d, s));
-                if (lane == g) a = c, b = d;
+            for (int i = 0; i < NPL; ++i) {
+                const int e = first + i - g * size;
+                if (e >= 0 && e < size) merge_two(c, d, key[i], Key{0});
             }
+#pragma unroll
+            for (int s = 1; s < 32; s *= 2) merge_two(c, d, __shfl_xor_sync(kAll, c, s), __shfl_xor_sync(kAll, d, s));
+            if (lane == g) a = c, b = d;
         }
-        Key score = 0;
-        V value = 0;
-        if (lane < p.groups && a) {
-            value = K::value(a);
-            if (p.group_best == 2 && b) value += K::value(b);
-            score = K::of(value);
-        }
-        int better = 0;
-        bool close = false;
-        for (int h = 0; h < p.groups; ++h) {
-            const Key other = __shfl_sync(kAll, score, h);
-            const V v = __shfl_sync(kAll, value, h);
-            better += other > score || (other == score && h < lane);
-            close |= h != lane && score && other && !(fabs(v - value) > 2 * near);
-        }
-        if (checked && __any_sync(kAll, close)) {
-            sure = false;
-            return -1;
-        }
-        const unsigned kept = __ballot_sync(kAll, score && better < p.top_groups);
+        const unsigned kept = choose_groups<V>(p, a, b, checked, near, sure);
         int g = first / size, rest = first - g * size;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
@@ -182,16 +216,33 @@ __device__ __forceinline__ int choose(typename Keys<V>::Key (&key)[NPL], const R
             if (++rest == size) rest = 0, ++g;
         }
     }
+    uint32_t at = 0;  // sorted: numbers of the lane's keys, the first in the low bits; else the largest one's
     Key m = 0;
-    int at = 0, mine = -1;
     auto lead = [&] {
         m = key[0], at = 0;
 #pragma unroll
         for (int i = 1; i < NPL; ++i)
             if (key[i] > m) m = key[i], at = i;
     };
-    lead();
+    if constexpr (SORTED) {
+        at = sort_lane(key);
+        m = key[0];
+        if (p.groups > 1 && whole) {
+            Key a = m, b = NPL > 1 ? key[NPL > 1 ? 1 : 0] : Key{0};
+            for (int d = 1; d < lanes; d *= 2) merge_two(a, b, __shfl_xor_sync(kAll, a, d), __shfl_xor_sync(kAll, b, d));
+            const int from = (lane * lanes) & 31;
+            a = __shfl_sync(kAll, a, from);
+            b = __shfl_sync(kAll, b, from);
+            const unsigned kept = choose_groups<V>(p, a, b, checked, near, sure);
+            const int g = lane / lanes;
+            if (!(kept >> g & 1)) m = 0;  // (lanes past the last group hold no keys)
+        }
+    } else {
+        lead();
+    }
+    if (!sure) return -1;
     Key before = 0;
+    int mine = -1;
     for (int j = 0; j < p.k + (checked ? 1 : 0); ++j) {
         const Key best = K::most(m);
         if (best == 0) break;
@@ -202,13 +253,21 @@ __device__ __forceinline__ int choose(typename Keys<V>::Key (&key)[NPL], const R
         if (j == p.k) break;
         before = best;
         const int from = __ffs(__ballot_sync(kAll, m == best)) - 1;
-        const int e = __shfl_sync(kAll, first + at, from);
+        const int e = __shfl_sync(kAll, first + static_cast<int>(SORTED ? at & 15 : at), from);
         if (lane == j) mine = e;
         if (lane == from) {
+            if constexpr (SORTED) {
 #pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                if (i == at) key[i] = 0;
-            lead();
+                for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
+                key[NPL - 1] = 0;
+                at >>= 4;
+                m = key[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NPL; ++i)
+                    if (i == static_cast<int>(at)) key[i] = 0;
+                lead();
+            }
         }
     }
     return mine;
@@ -245,13 +304,11 @@ __device__ __noinline__ int choose_again(const RouteParams& p, const T* row) {
     return choose<NPL, double>(key, p, false, 0., sure);
 }
 
-// A token's experts and weights, the j-th in lane j.
+// A token's experts and weights, the j-th in lane j, from its row (l: the lane's part).
 template <int NPL, typename T>
-__device__ __forceinline__ int route_token(const RouteParams& p, int t, const float (&bias)[NPL], float& weight) {
-    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+__device__ __forceinline__ int route_token(const RouteParams& p, const T* row, const float (&l)[NPL],
+                                           const float (&bias)[NPL], float& weight) {
     const bool by_logit = !p.bias && (p.groups == 1 || p.group_best == 1);
-    float l[NPL];
-    load_row<NPL>(row, p.E, p.vec, l);
     float top = 0.f, sum = 0.f;
     uint32_t key[NPL];
     if (!p.sigmoid && (!by_logit || !p.renormalize)) {
@@ -283,7 +340,7 @@ __device__ __forceinline__ int route_token(const RouteParams& p, int t, const fl
         for (int i = 0; i < NPL; ++i) {
             key[i] = 0;
             if (l[i] != -INFINITY) {
-                const float s = p.sigmoid ? 1.f / (1.f + expf(-l[i])) : expf(l[i] - top) * inv;
+                const float s = p.sigmoid ? __fdividef(1.f, 1.f + expf(-l[i])) : expf(l[i] - top) * inv;
                 const float c = s + bias[i];
                 size = fmaxf(size, fabsf(c));
                 if (c != -INFINITY) key[i] = Keys<float>::of(c);
@@ -340,12 +397,16 @@ __device__ __forceinline__ void exclusive_sums(const int* count, int E, int* bas
     __syncthreads();
 }
 
-template <int NPL, typename T>
+// CLUSTER: CTAs of a cluster (their count of each expert's choices is summed
+// through distributed shared memory).  With p.counts there are several clusters,
+// which leave their sums there for place_kernel; else the one finishes the places.
+template <int NPL, typename T, int CLUSTER>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
     extern __shared__ int shared[];
-    int* const mask = shared;                       // E: this step's tokens
-    int* const count = shared + p.E;                // E: choices of the steps before
-    int* const scratch = shared + 2 * p.E;          // a word a warp
+    int* const mask = shared;             // E: this step's tokens
+    int* const count = shared + p.E;      // E: choices of the steps before
+    int* const before = shared + 2 * p.E; // E: of the cluster's CTAs before this one, then all that come before
+    int* const scratch = shared + 3 * p.E;  // a word a warp
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = count[e] = 0;
@@ -357,35 +418,41 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     }
     __syncthreads();
     const long long begin = static_cast<long long>(blockIdx.x) * p.steps * kRouteStep;
+    int mine[kRouteTokens] = {}, rank[kRouteTokens] = {};  // of the last step
     for (int step = 0; step < p.steps; ++step) {
-        const long long t0 = begin + step * kRouteStep;
-        int mine[kRouteTokens];
-#pragma unroll 1
+        const long long t0 = begin + step * kRouteStep + warp;
+        auto row = [&](int i) { return static_cast<const T*>(p.logits) + (t0 + i * kRouteWarps) * p.ld; };
+        float l[NPL], next[NPL];
+        if (t0 < p.T) load_row<NPL>(row(0), p.E, p.vec, l);
+#pragma unroll
         for (int i = 0; i < kRouteTokens; ++i) {
-            const long long t = t0 + warp + i * kRouteWarps;
+            const long long t = t0 + i * kRouteWarps;
+            const bool more = i + 1 < kRouteTokens && t + kRouteWarps < p.T;
+            if (NPL <= 8 && more) load_row<NPL>(row(i + 1), p.E, p.vec, next);  // (beside this token's work)
             int e = -1;
             if (t < p.T) {
                 float w;
-                e = route_token<NPL, T>(p, static_cast<int>(t), bias, w);
+                e = route_token<NPL, T>(p, row(i), l, bias, w);
                 if (lane < p.k) {
                     p.experts[t * p.k + lane] = e;
                     p.weights[t * p.k + lane] = w;
                     if (e >= 0) atomicOr(mask + e, 1 << (warp + i * kRouteWarps));
                 }
             }
+            mine[i] = lane < p.k ? e : -1;
+            if (NPL > 8 && more) load_row<NPL>(row(i + 1), p.E, p.vec, next);
+            if (more) {
 #pragma unroll
-            for (int q = 0; q < kRouteTokens; ++q)
-                if (q == i) mine[q] = e;
+                for (int j = 0; j < NPL; ++j) l[j] = next[j];
+            }
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRouteTokens; ++i) {
-            const long long t = t0 + warp + i * kRouteWarps;
-            if (t < p.T && lane < p.k) {
-                const int e = mine[i];
-                const unsigned below = (1u << (warp + i * kRouteWarps)) - 1;
-                p.slots[t * p.k + lane] = e < 0 ? -1 : count[e] + __popc(mask[e] & below);
-            }
+            const long long t = t0 + i * kRouteWarps;
+            const unsigned below = (1u << (warp + i * kRouteWarps)) - 1;
+            rank[i] = mine[i] < 0 ? -1 : count[mine[i]] + __popc(mask[mine[i]] & below);
+            if (step + 1 < p.steps && t < p.T && lane < p.k) p.slots[t * p.k + lane] = rank[i];
         }
         __syncthreads();
         for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
@@ -394,21 +461,51 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         }
         __syncthreads();
     }
-    if (p.counts) {
-        for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
-            p.counts[static_cast<long long>(blockIdx.x) * p.E + e] = count[e];
-        return;
+    // What comes before this CTA's choices of an expert, in the cluster.
+    int* total = count;
+    if constexpr (CLUSTER > 1) {
+        const int of = static_cast<int>(cluster_ctarank());
+        cluster_sync_all();
+        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+            const uint32_t at = smem_addr(count + e);
+            int sum = 0, mine_from = 0;
+#pragma unroll
+            for (int q = 0; q < CLUSTER; ++q) {
+                if (q == of) mine_from = sum;
+                sum += ld_shared_cluster_s32(map_shared_rank(at, q));
+            }
+            before[e] = mine_from;
+            mask[e] = sum;
+            if (p.counts && of == 0) p.counts[static_cast<long long>(blockIdx.x / CLUSTER) * p.E + e] = sum;
+        }
+        total = mask;
+        cluster_sync_all();  // (nobody reads this CTA's counts after this)
+    } else {
+        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) before[e] = 0;
+        __syncthreads();
     }
-    int* const base = mask;
-    exclusive_sums(count, p.E, base, p.offsets, scratch);
-    for (int i = threadIdx.x; i < p.T * p.k; i += kRouteThreads) {
-        const int e = p.experts[i];
-        if (e >= 0) p.slots[i] += base[e];
+    if (!p.counts) {
+        int* const base = CLUSTER > 1 ? count : mask;
+        exclusive_sums(total, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
+        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) before[e] += base[e];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kRouteTokens; ++i) {
+        const long long t = begin + (p.steps - 1) * kRouteStep + warp + i * kRouteWarps;
+        if (t < p.T && lane < p.k) p.slots[t * p.k + lane] = mine[i] < 0 ? -1 : rank[i] + before[mine[i]];
+    }
+    if (p.steps > 1) {  // the steps before the last, whose places are in memory
+        const long long from = begin * p.k, to = min(static_cast<long long>(p.T), begin + (p.steps - 1) * kRouteStep) * p.k;
+        for (long long i = from + threadIdx.x; i < to; i += kRouteThreads) {
+            const int e = p.experts[i];
+            if (e >= 0) p.slots[i] += before[e];
+        }
     }
 }
 
-// Places within a CTA's rows of an expert to places among all rows.
-__global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams p, int ctas) {
+// Places within a cluster's rows of an expert to places among all rows; a CTA a cluster.
+__global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams p, int clusters) {
     extern __shared__ int shared[];
     int* const total = shared;
     int* const before = shared + p.E;
@@ -424,7 +521,7 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
     for (int e = threadIdx.x % width; e < p.E; e += width) {
         int all = 0, mine = 0;
 #pragma unroll 8
-        for (int c = part; c < ctas; c += parts) {
+        for (int c = part; c < clusters; c += parts) {
             const int n = p.counts[static_cast<long long>(c) * p.E + e];
             all += n;
             if (c < static_cast<int>(blockIdx.x)) mine += n;
@@ -434,7 +531,7 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
     }
     __syncthreads();
     exclusive_sums(total, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
-    const long long per = static_cast<long long>(p.steps) * kRouteStep * p.k, all = static_cast<long long>(p.T) * p.k;
+    const long long per = static_cast<long long>(p.steps) * kRouteStep * kRouteCluster * p.k, all = static_cast<long long>(p.T) * p.k;
     const long long from = blockIdx.x * per, to = min(all, from + per);
     for (long long i = from + threadIdx.x; i < to; i += kRouteThreads) {
         const int e = p.experts[i];
@@ -564,31 +661,45 @@ int launched() {
 
 }  // namespace
 
-RoutePlan route_plan(int T, int E, int sms) {
-    (void)E;
+RoutePlan route_plan(int T, int sms) {
     const int steps = (T + kRouteStep - 1) / kRouteStep;
-    const int each = (steps + sms - 1) / sms;
-    return {(steps + each - 1) / each, each};
+    if (steps == 1) return {1, 1, 1};
+    // One cluster finishes by itself, which saves a launch: up to two steps of it.
+    const int least = (steps + kRouteCluster - 1) / kRouteCluster;
+    if (least <= 2) return {1, kRouteCluster, least};
+    // About three CTAs an SM at once.
+    const int most = std::max(1, 3 * sms / kRouteCluster);
+    const int each = (least + most - 1) / most;
+    return {(least + each - 1) / each, kRouteCluster, each};
 }
 
 int route(const RouteParams& p, const RoutePlan& plan, int type, cudaStream_t s) {
     const size_t smem = (3 * static_cast<size_t>(p.E) + kRouteWarps) * sizeof(int);
-    const int rc = by_type_and_width(type, p.E, [&](auto zero, auto npl) {
-        route_kernel<decltype(npl)::value, decltype(zero)><<<plan.ctas, kRouteThreads, smem, s>>>(p);
-        return launched();
-    });
-    if (rc != SGEMM_OK || !p.counts) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas));
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters * plan.width));
     cfg.blockDim = dim3(kRouteThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(plan.width);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = plan.width > 1 ? 1 : 0;
+    const int rc = by_type_and_width(type, p.E, [&](auto zero, auto npl) {
+        constexpr int NPL = decltype(npl)::value;
+        using T = decltype(zero);
+        const auto kernel = plan.width > 1 ? route_kernel<NPL, T, kRouteCluster> : route_kernel<NPL, T, 1>;
+        if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return static_cast<int>(SGEMM_OK);
+        (void)cudaGetLastError();
+        return static_cast<int>(SGEMM_ERR_CUDA);
+    });
+    if (rc != SGEMM_OK || !p.counts) return rc;
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters));
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, place_kernel, p, plan.ctas) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, place_kernel, p, plan.clusters) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }

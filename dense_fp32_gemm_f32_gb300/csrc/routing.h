@@ -22,17 +22,19 @@ struct RouteParams {
     int* slots;
     int vec;      // the rows begin on 16 bytes: whole vectors are loaded
     int steps;    // steps of kRouteStep tokens a CTA takes
-    int* counts;  // CTAs x E: choices of each expert (null: one CTA does it all)
+    int* counts;  // clusters x E: choices of each expert (null: one cluster does it all)
 };
 
 // Tokens of a CTA's step: a bit each in an expert's word.
 constexpr int kRouteStep = 32;
+// CTAs of a cluster, where there is more than one.
+constexpr int kRouteCluster = 8;
 
-// The grid of a routing: CTAs and their steps.
+// The grid of a routing: clusters of `width` CTAs, and each CTA's steps.
 struct RoutePlan {
-    int ctas, steps;
+    int clusters, width, steps;
 };
-RoutePlan route_plan(int T, int E, int sms);
+RoutePlan route_plan(int T, int sms);
 int route(const RouteParams& p, const RoutePlan& plan, int type, cudaStream_t s);
 
 struct RouteGradParams {

@@ -5,6 +5,9 @@
 // through the token's choices, so that the token's row stays in a register
 // and each choice's row is one stream of whole lines.
 #include "../../include/sgemm_routing.h"
+#include <algorithm>
+#include <type_traits>
+
 #include "experts_groups.cuh"
 #include "ptx.cuh"
 #include "routing.h"
@@ -15,10 +18,41 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRowsThreads = 256;
 
-// N elements of T as one access of N * sizeof(T) bytes (at most 16).
+// N elements of T as one access of N * sizeof(T) bytes (2 to 16).
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+    using type = uint4;
+};
+template <>
+struct Word<8> {
+    using type = uint2;
+};
+template <>
+struct Word<4> {
+    using type = uint32_t;
+};
+template <>
+struct Word<2> {
+    using type = uint16_t;
+};
 template <typename T, int N>
-struct alignas(N * sizeof(T)) Vec {
-    T v[N];
+struct Vec {
+    using W = typename Word<N * static_cast<int>(sizeof(T))>::type;
+    W w;
+    __device__ __forceinline__ void get(float (&v)[N]) const {
+        alignas(16) T x[N];
+        *reinterpret_cast<W*>(x) = w;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = to_f32(x[i]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[N]) {
+        alignas(16) T x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = from_f32<T>(v[i]);
+        w = *reinterpret_cast<const W*>(x);
+    }
 };
 
 __device__ __forceinline__ int slot_of(const RowsParams& p, long long i) {
@@ -36,138 +70,208 @@ __device__ __forceinline__ void zero_unused(const RowsParams& p, long long worke
         const int c = static_cast<int>(i - r * nvec) * N;
         T* o = static_cast<T*>(p.out) + (used + r) * p.ldo + c;
         if (c + N <= p.H) {
-            Vec<T, N> z;
-#pragma unroll
-            for (int j = 0; j < N; ++j) z.v[j] = from_f32<T>(0.f);
-            *reinterpret_cast<Vec<T, N>*>(o) = z;
+            *reinterpret_cast<typename Vec<T, N>::W*>(o) = typename Vec<T, N>::W{};
         } else {
             for (int j = 0; c + j < p.H; ++j) o[j] = from_f32<T>(0.f);
         }
     }
 }
 
+// A vector of a row, `left` elements before the row's end; zeros past it.
 template <typename T, int N>
 __device__ __forceinline__ Vec<T, N> load_vec(const T* p, int left) {
-    if (left >= N) return *reinterpret_cast<const Vec<T, N>*>(p);
+    using W = typename Vec<T, N>::W;
     Vec<T, N> x;
+    if (left >= N) {
+        x.w = __ldg(reinterpret_cast<const W*>(p));
+    } else {
+        alignas(16) T e[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) x.v[j] = j < left ? p[j] : from_f32<T>(0.f);
+        for (int j = 0; j < N; ++j) e[j] = j < left ? p[j] : from_f32<T>(0.f);
+        x.w = *reinterpret_cast<const W*>(e);
+    }
     return x;
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, N>& x, int left) {
+    using W = typename Vec<T, N>::W;
     if (left >= N) {
-        *reinterpret_cast<Vec<T, N>*>(p) = x;
+        *reinterpret_cast<W*>(p) = x.w;
     } else {
+        alignas(16) T e[N];
+        *reinterpret_cast<W*>(e) = x.w;
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            if (j < left) p[j] = x.v[j];
+            if (j < left) p[j] = e[j];
     }
 }
 
-template <typename T, int N>
-__global__ void __launch_bounds__(kRowsThreads) spread_kernel(const RowsParams p, uint32_t nvec) {
-    const long long id = static_cast<long long>(blockIdx.x) * kRowsThreads + threadIdx.x;
-    const long long t = id / nvec;
-    if (t < p.T) {
-        const int c = static_cast<int>(id - t * nvec) * N, left = p.H - c;
-        const Vec<T, N> x = load_vec<T, N>(static_cast<const T*>(p.X) + t * p.ldx + c, left);
+// Which token and which of its `per` threads a thread is.
+__device__ __forceinline__ bool token_of(const RowsParams& p, uint32_t per, uint32_t& t, uint32_t& v) {
+    const uint32_t id = blockIdx.x * kRowsThreads + threadIdx.x;
+    t = id / per;
+    v = id - t * per;
+    return t < static_cast<uint32_t>(p.T);
+}
+
+// A thread: U vectors of a token's row, `per` vectors apart.
+template <typename T, int N, int U>
+__global__ void __launch_bounds__(kRowsThreads) spread_kernel(const RowsParams p, uint32_t nvec, uint32_t per) {
+    uint32_t t, v;
+    if (token_of(p, per, t, v)) {
+        const T* x = static_cast<const T*>(p.X) + t * p.ldx;
+        Vec<T, N> row[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v + u * per < nvec) row[u] = load_vec<T, N>(x + (v + u * per) * N, p.H - (v + u * per) * N);
+        const long long first = static_cast<long long>(t) * p.k;
         for (int j = 0; j < p.k; ++j) {
-            const int s = slot_of(p, t * p.k + j);
-            if (s >= 0) store_vec<T, N>(static_cast<T*>(p.out) + s * p.ldo + c, x, left);
+            const int s = slot_of(p, first + j);
+            if (s < 0) continue;
+            T* y = static_cast<T*>(p.out) + s * p.ldo;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + u * per < nvec) store_vec<T, N>(y + (v + u * per) * N, row[u], p.H - (v + u * per) * N);
         }
     }
-    zero_unused<T, N>(p, id, static_cast<long long>(gridDim.x) * kRowsThreads, nvec);
+    if (p.used)
+        zero_unused<T, N>(p, blockIdx.x * static_cast<long long>(kRowsThreads) + threadIdx.x,
+                          static_cast<long long>(gridDim.x) * kRowsThreads, nvec);
 }
 
-template <typename T, int N>
-__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p, uint32_t nvec) {
-    const long long id = static_cast<long long>(blockIdx.x) * kRowsThreads + threadIdx.x;
-    const long long t = id / nvec;
-    if (t >= p.T) return;
-    const int c = static_cast<int>(id - t * nvec) * N, left = p.H - c;
-    float sum[N] = {};
-#pragma unroll 4
-    for (int j = 0; j < p.k; ++j) {
-        const int s = slot_of(p, t * p.k + j);
-        if (s >= 0) {
-            const float w = p.weights ? __ldg(p.weights + t * p.k + j) : 1.f;
-            const Vec<T, N> y = load_vec<T, N>(static_cast<const T*>(p.Y) + s * p.ldy + c, left);
+// A thread: U vectors of a token's result, B choices at a time; all loads of a
+// batch are under way before the first is used.
+template <typename T, int N, int B, int U>
+__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p, uint32_t nvec, uint32_t per) {
+    uint32_t t, v;
+    if (!token_of(p, per, t, v)) return;
+    const long long first = static_cast<long long>(t) * p.k;
+    float sum[U][N] = {};
+    for (int j0 = 0; j0 < p.k; j0 += B) {
+        Vec<T, N> y[B][U];
+        int slot[B];
+        float w[B];
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum[i] = fmaf(w, to_f32(y.v[i]), sum[i]);
+        for (int b = 0; b < B; ++b) {
+            slot[b] = j0 + b < p.k ? slot_of(p, first + j0 + b) : -1;
+            w[b] = slot[b] >= 0 && p.weights ? __ldg(p.weights + first + j0 + b) : 1.f;
         }
-    }
-    Vec<T, N> o;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(sum[i]);
-    store_vec<T, N>(static_cast<T*>(p.out) + t * p.ldo + c, o, left);
+        for (int b = 0; b < B; ++b) {
+            const T* row = static_cast<const T*>(p.Y) + slot[b] * p.ldy;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (slot[b] >= 0 && v + u * per < nvec)
+                    y[b][u] = load_vec<T, N>(row + (v + u * per) * N, p.H - (v + u * per) * N);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (slot[b] >= 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[N];
+                    y[b][u].get(x);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) sum[u][i] = fmaf(w[b], x[i], sum[u][i]);
+                }
+            }
+    }
+    T* o = static_cast<T*>(p.out) + t * p.ldo;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (v + u * per < nvec) {
+            Vec<T, N> x;
+            x.set(sum[u]);
+            store_vec<T, N>(o + (v + u * per) * N, x, p.H - (v + u * per) * N);
+        }
 }
 
-// A token to `group` threads (a power of two, 32 to 256), choices 8 at a time.
-template <typename T, int N>
+// A token to `group` threads (a power of two, 32 to 256), B choices at a time, U
+// vectors a thread and round.
+template <typename T, int N, int B, int U>
 __global__ void __launch_bounds__(kRowsThreads) combine_grad_kernel(const RowsParams p, int nvec, int group) {
-    constexpr int kBatch = 8;
-    __shared__ float part[kRowsThreads / 32][kBatch];
+    __shared__ float part[kRowsThreads / 32][B];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int member = threadIdx.x & (group - 1);
-    const long long t = static_cast<long long>(blockIdx.x) * (kRowsThreads / group) + threadIdx.x / group;
-    const bool there = t < p.T;
-    for (int j0 = 0; j0 < p.k; j0 += kBatch) {
-        int slot[kBatch];
-        float w[kBatch], dot[kBatch] = {};
+    const uint32_t t = blockIdx.x * (kRowsThreads / group) + threadIdx.x / group;
+    const bool there = t < static_cast<uint32_t>(p.T);
+    const T* const dx = static_cast<const T*>(p.X) + t * p.ldx;
+    const long long first = static_cast<long long>(t) * p.k;
+    for (int j0 = 0; j0 < p.k; j0 += B) {
+        int slot[B];
+        float w[B], dot[B] = {};
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
+        for (int b = 0; b < B; ++b) {
             const bool in = there && j0 + b < p.k;
-            slot[b] = in ? slot_of(p, t * p.k + j0 + b) : -1;
-            w[b] = in && p.weights ? __ldg(p.weights + t * p.k + j0 + b) : 1.f;
+            slot[b] = in ? slot_of(p, first + j0 + b) : -1;
+            w[b] = in && p.weights ? __ldg(p.weights + first + j0 + b) : 1.f;
         }
-        if (there) {
-            for (int v = member; v < nvec; v += group) {
-                const int c = v * N, left = p.H - c;
-                const Vec<T, N> d = load_vec<T, N>(static_cast<const T*>(p.X) + t * p.ldx + c, left);
+        for (int v = member; there && v < nvec; v += U * group) {
+            Vec<T, N> d[U], y[B][U];
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
+            for (int u = 0; u < U; ++u)
+                if (v + u * group < nvec) d[u] = load_vec<T, N>(dx + (v + u * group) * N, p.H - (v + u * group) * N);
+            if (p.dweights) {  // (all loads before the first use)
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const T* row = static_cast<const T*>(p.Y) + slot[b] * p.ldy;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (slot[b] >= 0 && v + u * group < nvec)
+                            y[b][u] = load_vec<T, N>(row + (v + u * group) * N, p.H - (v + u * group) * N);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (v + u * group >= nvec) continue;
+                float x[N];
+                d[u].get(x);
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
                     if (slot[b] < 0) continue;
+                    float z[N];
                     if (p.dweights) {
-                        const Vec<T, N> y = load_vec<T, N>(static_cast<const T*>(p.Y) + slot[b] * p.ldy + c, left);
+                        y[b][u].get(z);
 #pragma unroll
-                        for (int i = 0; i < N; ++i) dot[b] = fmaf(to_f32(d.v[i]), to_f32(y.v[i]), dot[b]);
+                        for (int i = 0; i < N; ++i) dot[b] = fmaf(x[i], z[i], dot[b]);
                     }
                     if (p.out) {
                         Vec<T, N> o;
 #pragma unroll
-                        for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(w[b] * to_f32(d.v[i]));
-                        store_vec<T, N>(static_cast<T*>(p.out) + slot[b] * p.ldo + c, o, left);
+                        for (int i = 0; i < N; ++i) z[i] = w[b] * x[i];
+                        o.set(z);
+                        store_vec<T, N>(static_cast<T*>(p.out) + slot[b] * p.ldo + (v + u * group) * N, o,
+                                        p.H - (v + u * group) * N);
                     }
                 }
             }
         }
         if (p.dweights) {
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b)
+            for (int b = 0; b < B; ++b)
 #pragma unroll
                 for (int s = 16; s; s /= 2) dot[b] += __shfl_xor_sync(kAll, dot[b], s);
             if (group > 32) {
                 if (lane == 0) {
 #pragma unroll
-                    for (int b = 0; b < kBatch; ++b) part[warp][b] = dot[b];
+                    for (int b = 0; b < B; ++b) part[warp][b] = dot[b];
                 }
                 __syncthreads();
-                if (member < kBatch && there && j0 + member < p.k) {
+                if (member < B && there && j0 + member < p.k) {
                     float sum = 0.f;
                     for (int q = 0; q < group / 32; ++q) sum += part[warp + q][member];
-                    p.dweights[t * p.k + j0 + member] = sum;
+                    p.dweights[first + j0 + member] = sum;
                 }
                 __syncthreads();
             } else if (there) {
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b)
-                    if (lane == b && j0 + b < p.k) p.dweights[t * p.k + j0 + b] = dot[b];
+                for (int b = 0; b < B; ++b)
+                    if (lane == b && j0 + b < p.k) p.dweights[first + j0 + b] = dot[b];
             }
         }
     }
-    if (p.out)
-        zero_unused<T, N>(p, static_cast<long long>(blockIdx.x) * kRowsThreads + threadIdx.x,
+    if (p.used)
+        zero_unused<T, N>(p, blockIdx.x * static_cast<long long>(kRowsThreads) + threadIdx.x,
                           static_cast<long long>(gridDim.x) * kRowsThreads, nvec);
 }
 
@@ -188,49 +292,102 @@ int by_type_and_vec(int type, int vec, F f) {
     return type == SGEMM_TYPE_BF16 ? half(__nv_bfloat16()) : half(__half());
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA; }
-
-// CTAs for `threads` threads; -1 if a grid cannot hold them.
-long long ctas_for(long long threads) {
-    const long long n = (threads + kRowsThreads - 1) / kRowsThreads;
-    return n <= 0x7fffffffll ? n : -1;
+// f(integral_constant<B>, integral_constant<U>): choices at a time and vectors
+// of each, up to 8 loads in flight a thread.  Measured, us (floor 45 / 84; 49 / 89;
+// 69 / 104), a combination / its gradient of 8192 tokens and 8 choices of 2048 bf16:
+// (8, 1) 54 / 112, (4, 2) 49 / 94, (4, 1) 49 / 93; 8192 tokens, 4 choices of 4096:
+// (4, 2) 56 / 99, (2, 4) 54 / 99, one load at a time 99 / 165; 16384 tokens, one choice of
+// 7168: (1, 4) 87 / 103, (1, 8) 85 / 112, one load 128 / 332.  64 tokens, 4 choices of
+// 4096: (4, 2) 2.2 / 3.5, (2, 4) 2.4 / 5.4.
+template <typename F>
+int by_choices(int k, F f) {
+    if (k > 2) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+    if (k > 1) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
+    return f(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
 }
+
+// Launches for tokens in parts that a 32-bit thread number holds: launch(part,
+// threads) with the arrays' beginnings moved to each part's.
+template <typename L>
+int in_parts(const RowsParams& p, int size, long long per, L launch) {
+    const int most = static_cast<int>(std::max(1ll, (1ll << 30) / per));  // (per >= 1: an int holds it)
+    int t0 = 0;
+    do {
+        RowsParams q = p;
+        q.T = std::min(most, p.T - t0);
+        const long long at = t0, row = at * p.k;
+        if (p.X) q.X = static_cast<const char*>(p.X) + at * p.ldx * size;
+        q.slots = p.slots + row;
+        if (p.weights) q.weights = p.weights + row;
+        if (p.dweights) q.dweights = p.dweights + row;
+        if (!p.X && p.out) q.out = static_cast<char*>(p.out) + at * p.ldo * size;  // (a combination's result goes by token)
+        if (t0 > 0) q.used = nullptr;
+        const int rc = launch(q, q.T * per);
+        if (rc != SGEMM_OK) return rc;
+        t0 += q.T;
+    } while (t0 < p.T);
+    return SGEMM_OK;
+}
+
+unsigned ctas_for(long long threads, int least) {
+    return static_cast<unsigned>(std::max<long long>((threads + kRowsThreads - 1) / kRowsThreads, least));
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA; }
 
 }  // namespace
 
 int rows_spread(const RowsParams& p, int type, int sms, cudaStream_t s) {
     const uint32_t nvec = static_cast<uint32_t>((p.H + p.vec - 1) / p.vec);
-    const long long n = ctas_for(static_cast<long long>(p.T) * nvec);
-    if (n < 0) return SGEMM_ERR_INVALID_ARG;
-    const unsigned ctas = static_cast<unsigned>(n > sms ? n : sms);  // (the rows to zero are shared among all)
     return by_type_and_vec(type, p.vec, [&](auto zero, auto vec) {
-        spread_kernel<decltype(zero), decltype(vec)::value><<<ctas, kRowsThreads, 0, s>>>(p, nvec);
-        return launched();
+        // (two vectors a thread where there are threads enough)
+        const bool two = static_cast<long long>(p.T) * nvec >= 4096ll * sms;
+        const uint32_t per = two ? (nvec + 1) / 2 : nvec;
+        return in_parts(p, sizeof(zero), per, [&](const RowsParams& q, long long threads) {
+            const unsigned ctas = ctas_for(threads, q.used ? sms : 1);  // (the rows to zero are shared among all)
+            if (two)
+                spread_kernel<decltype(zero), decltype(vec)::value, 2><<<ctas, kRowsThreads, 0, s>>>(q, nvec, per);
+            else
+                spread_kernel<decltype(zero), decltype(vec)::value, 1><<<ctas, kRowsThreads, 0, s>>>(q, nvec, per);
+            return launched();
+        });
     });
 }
 
 int rows_combine(const RowsParams& p, int type, int sms, cudaStream_t s) {
-    (void)sms;
     const uint32_t nvec = static_cast<uint32_t>((p.H + p.vec - 1) / p.vec);
-    const long long n = ctas_for(static_cast<long long>(p.T) * nvec);
-    if (n < 0) return SGEMM_ERR_INVALID_ARG;
     return by_type_and_vec(type, p.vec, [&](auto zero, auto vec) {
-        combine_kernel<decltype(zero), decltype(vec)::value><<<static_cast<unsigned>(n), kRowsThreads, 0, s>>>(p, nvec);
-        return launched();
+        return by_choices(p.k, [&](auto b, auto u) {
+            using T = decltype(zero);
+            constexpr int N = decltype(vec)::value, B = decltype(b)::value, U = decltype(u)::value;
+            const bool wide = U > 1 && static_cast<long long>(p.T) * nvec >= 2048ll * U * sms;
+            const uint32_t per = wide ? (nvec + U - 1) / U : nvec;
+            return in_parts(p, sizeof(T), per, [&](const RowsParams& q, long long threads) {
+                if (wide)
+                    combine_kernel<T, N, B, U><<<ctas_for(threads, 1), kRowsThreads, 0, s>>>(q, nvec, per);
+                else
+                    combine_kernel<T, N, B, 1><<<ctas_for(threads, 1), kRowsThreads, 0, s>>>(q, nvec, per);
+                return launched();
+            });
+        });
     });
 }
 
 int rows_combine_grad(const RowsParams& p, int type, int sms, cudaStream_t s) {
     const int nvec = (p.H + p.vec - 1) / p.vec;
-    // Threads a token: all that have a vector, unless there are tokens enough.
-    int group = kRowsThreads;
-    while (group > 32 && (group / 2 >= nvec || static_cast<long long>(p.T) * group > 2048ll * 8 * sms)) group /= 2;
-    const long long n = ctas_for(static_cast<long long>(p.T) * group);
-    if (n < 0) return SGEMM_ERR_INVALID_ARG;
-    const unsigned ctas = static_cast<unsigned>(p.out && n < sms ? sms : n);
     return by_type_and_vec(type, p.vec, [&](auto zero, auto vec) {
-        combine_grad_kernel<decltype(zero), decltype(vec)::value><<<ctas, kRowsThreads, 0, s>>>(p, nvec, group);
-        return launched();
+        return by_choices(p.k, [&](auto b, auto u) {
+            using T = decltype(zero);
+            constexpr int N = decltype(vec)::value, B = decltype(b)::value, U = decltype(u)::value;
+            // Threads a token: two rounds of vectors each; more where there are few tokens.
+            int group = 32;
+            while (group < kRowsThreads && (nvec > 2 * U * group || (nvec > U * group && static_cast<long long>(p.T) * group < 1024ll * sms)))
+                group *= 2;
+            return in_parts(p, sizeof(T), group, [&](const RowsParams& q, long long threads) {
+                combine_grad_kernel<T, N, B, U><<<ctas_for(threads, q.used ? sms : 1), kRowsThreads, 0, s>>>(q, nvec, group);
+                return launched();
+            });
+        });
     });
 }
 
