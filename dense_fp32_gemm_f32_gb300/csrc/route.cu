@@ -8,18 +8,20 @@
 // and k of them with the lane's own largest kept up to date make the choice.
 //
 // What the choice is by.  Without a bias (and with group_best = 1) both scores
-// grow with the logit, so logits are compared, exactly.  Otherwise float32
-// scores decide where they are further apart than their errors; a token where
-// two of those that decide are not goes through the same code in 64 bits
-// (choose_again), so that no rounding of exp or of a sum moves a choice.
+// grow with the logit, so logits are compared.  Otherwise float32 scores
+// decide where they are further apart than their errors.  First with keys that
+// hold the expert and 22 bits of the value (choose_packed); a token where two that
+// decide are too near for that goes through keys of 32 bits, and scores that are
+// too near for those are computed in 64 (choose_again), so that no rounding moves
+// a choice.
 //
-// Places.  A CTA takes tokens 32 at a time and sets a bit a token in a word of
+// Places.  A CTA takes tokens 32 (or 16) at a time and sets a bit a token in a word of
 // each chosen expert (an OR: its order does not matter); a choice's place
 // among the expert's rows in this CTA is then the number of bits below its own
 // plus those of the steps before.  The CTAs of a cluster add up their counts
 // through distributed shared memory.  Up to 512 tokens are one cluster, which
 // then knows all; else the clusters' counts go to a table, and place_kernel adds
-// up, in a CTA a cluster, those of the clusters and of the experts before.
+// up those of the clusters and of the experts before.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,8 +34,7 @@ namespace gb300 {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kRouteWarps = 16, kRouteThreads = 32 * kRouteWarps;
-constexpr int kRouteTokens = kRouteStep / kRouteWarps;  // tokens of a warp in a step
+constexpr int kRouteThreads = 32 * kRouteWarps;
 
 // ------------------------------------------------------------------ keys
 
@@ -117,32 +118,6 @@ __device__ __forceinline__ void load_row(const T* row, int E, bool vec, float (&
 
 // ------------------------------------------------------------------ the choice
 
-// The lane's keys, the largest first (equal ones by their number), and their
-// numbers, 4 bits each.  Neighbours trade places, so that equal ones keep theirs.
-template <int NPL, typename Key>
-__device__ __forceinline__ uint32_t sort_lane(Key (&key)[NPL]) {
-    static_assert(NPL <= 8, "4 bits each");
-    uint32_t at[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) at[i] = i;
-#pragma unroll
-    for (int round = 0; round < NPL; ++round)
-#pragma unroll
-        for (int i = round & 1; i + 1 < NPL; i += 2) {
-            const bool swap = key[i] < key[i + 1];
-            const Key a = key[i], b = key[i + 1];
-            key[i] = swap ? b : a;
-            key[i + 1] = swap ? a : b;
-            const uint32_t x = at[i], y = at[i + 1];
-            at[i] = swap ? y : x;
-            at[i + 1] = swap ? x : y;
-        }
-    uint32_t packed = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) packed |= at[i] << (4 * i);
-    return packed;
-}
-
 // The two largest of four keys, (a >= b) and (c >= d), to a and b.
 template <typename Key>
 __device__ __forceinline__ void merge_two(Key& a, Key& b, Key c, Key d) {
@@ -151,224 +126,437 @@ __device__ __forceinline__ void merge_two(Key& a, Key& b, Key c, Key d) {
     b = max(low, max(b, d));
 }
 
-// The groups to choose from, a bit each: from the two best keys a, b of group g in
-// lane g (0: none).  `sure`: whether that is certain; see choose().
-template <typename V>
-__device__ __forceinline__ unsigned choose_groups(const RouteParams& p, typename Keys<V>::Key a, typename Keys<V>::Key b,
-                                                  bool checked, V near, bool& sure) {
-    using K = Keys<V>;
-    using Key = typename K::Key;
-    Key score = 0;
-    if ((threadIdx.x & 31) < p.groups && a) {
-        V value = K::value(a);
-        if (p.group_best == 2 && b) value += K::value(b);
-        score = K::of(value);
-    }
-    unsigned kept = 0;
-    Key last = 0;
-    for (int i = 0; i < p.top_groups; ++i) {
-        const Key best = K::most(score);
-        if (best == 0) return kept;
-        const unsigned lane = __ffs(__ballot_sync(kAll, score == best)) - 1;
-        kept |= 1u << lane;
-        if ((threadIdx.x & 31) == lane) score = 0;
-        last = best;
-    }
-    if (checked) {  // (what is among them or not is decided at their end alone)
-        const Key next = K::most(score);
-        if (next && !(K::value(last) - K::value(next) > 2 * near)) sure = false;
-    }
-    return kept;
-}
-
-// Of a token's keys (0: out of service), the k best in order: lane j's result
-// is the j-th expert, -1 where there is none.  checked: `sure` is false if two
-// values that decide lie within `near` of one another (the result is then not
-// to be used).
-template <int NPL, typename V>
-__device__ __forceinline__ int choose(typename Keys<V>::Key (&key)[NPL], const RouteParams& p, bool checked, V near,
-                                      bool& sure) {
-    using K = Keys<V>;
-    using Key = typename K::Key;
-    constexpr bool SORTED = NPL <= 8 && sizeof(V) == 4;
-    const int lane = threadIdx.x & 31, first = lane * NPL;
-    const int size = p.groups > 1 ? p.E / p.groups : 0, lanes = size / NPL;
-    const bool whole = size % NPL == 0 && (lanes & (lanes - 1)) == 0;  // a power of two of whole lanes a group
-    sure = true;
-    if (p.groups > 1 && !(SORTED && whole)) {
-        Key a = 0, b = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            Key c = 0, d = 0;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const int e = first + i - g * size;
-                if (e >= 0 && e < size) merge_two(c, d, key[i], Key{0});
-            }
-#pragma unroll
-            for (int s = 1; s < 32; s *= 2) merge_two(c, d, __shfl_xor_sync(kAll, c, s), __shfl_xor_sync(kAll, d, s));
-            if (lane == g) a = c, b = d;
-        }
-        const unsigned kept = choose_groups<V>(p, a, b, checked, near, sure);
-        int g = first / size, rest = first - g * size;
+// The two best keys of group g, in lane g (0: none): any groups.
+template <int NPL, typename Key>
+__device__ __forceinline__ void group_best(const Key (&key)[NPL], const RouteParams& p, Key& a, Key& b) {
+    const int lane = threadIdx.x & 31, first = lane * NPL, size = p.group_size;
+    a = b = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        Key c = 0, d = 0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            if (g >= p.groups || !(kept >> g & 1)) key[i] = 0;
-            if (++rest == size) rest = 0, ++g;
+            const int e = first + i - g * size;
+            if (e >= 0 && e < size) merge_two(c, d, key[i], Key{0});
         }
+#pragma unroll
+        for (int s = 1; s < 32; s *= 2) merge_two(c, d, __shfl_xor_sync(kAll, c, s), __shfl_xor_sync(kAll, d, s));
+        if (lane == g) a = c, b = d;
     }
-    uint32_t at = 0;  // sorted: numbers of the lane's keys, the first in the low bits; else the largest one's
-    Key m = 0;
-    auto lead = [&] {
-        m = key[0], at = 0;
+}
+
+// Keys of the groups that are not kept become 0.
+template <int NPL, typename Key>
+__device__ __forceinline__ void keep_groups(Key (&key)[NPL], const RouteParams& p, unsigned kept) {
+    const int first = (threadIdx.x & 31) * NPL, size = p.group_size;
+    int g = first / size, rest = first - g * size;
 #pragma unroll
-        for (int i = 1; i < NPL; ++i)
-            if (key[i] > m) m = key[i], at = i;
-    };
-    if constexpr (SORTED) {
-        at = sort_lane(key);
-        m = key[0];
-        if (p.groups > 1 && whole) {
-            Key a = m, b = NPL > 1 ? key[NPL > 1 ? 1 : 0] : Key{0};
-            for (int d = 1; d < lanes; d *= 2) merge_two(a, b, __shfl_xor_sync(kAll, a, d), __shfl_xor_sync(kAll, b, d));
-            const int from = (lane * lanes) & 31;
-            a = __shfl_sync(kAll, a, from);
-            b = __shfl_sync(kAll, b, from);
-            const unsigned kept = choose_groups<V>(p, a, b, checked, near, sure);
-            const int g = lane / lanes;
-            if (!(kept >> g & 1)) m = 0;  // (lanes past the last group hold no keys)
-        }
-    } else {
-        lead();
+    for (int i = 0; i < NPL; ++i) {
+        if (g >= p.groups || !(kept >> g & 1)) key[i] = 0;
+        if (++rest == size) rest = 0, ++g;
     }
-    if (!sure) return -1;
-    Key before = 0;
-    int mine = -1;
-    for (int j = 0; j < p.k + (checked ? 1 : 0); ++j) {
-        const Key best = K::most(m);
-        if (best == 0) break;
-        if (checked && j > 0 && !(K::value(before) - K::value(best) > near)) {
-            sure = false;
-            return -1;
+}
+
+// e^x to 2^-22 and 2^-24 |x|, relative: the rounding of x log2(e), and the instruction's 2 units.
+__device__ __forceinline__ float fast_exp(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+__device__ __forceinline__ float fast_reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// (a NaN wins)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// A row's largest logit (NaN passed over) and the sum of exp(l - top).
+template <int NPL>
+__device__ __forceinline__ void softmax_sums(const float (&l)[NPL], float& top, float& sum) {
+    top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) top = fmaxf(top, l[i]);
+    top = warp_max(top);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) sum += l[i] == -INFINITY ? 0.f : fast_exp(l[i] - top);
+    sum = warp_sum(sum);
+}
+
+__device__ __forceinline__ bool chosen_by_logit(const RouteParams& p) {
+    return !p.bias && (p.groups == 1 || p.group_best == 1);
+}
+
+// What experts are chosen by where that is not the logits: c = score + bias, in
+// float32, -inf out of service.
+template <int NPL>
+__device__ __forceinline__ void choice_values(const RouteParams& p, const float (&l)[NPL], const float (&bias)[NPL],
+                                              float top, float sum, float (&c)[NPL]) {
+    const float inv = fast_reciprocal(sum);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const float s = p.sigmoid ? fast_reciprocal(1.f + fast_exp(-l[i])) : fast_exp(l[i] - top) * inv;
+        c[i] = l[i] == -INFINITY ? -INFINITY : s + bias[i];
+    }
+}
+
+// How far apart two of them have to be for their order to be certain; `size`: at
+// least their magnitude.  Softmax: exp(l - top) is off by |l - top| 2^-23 (the
+// roundings of the difference and of its multiple) and 2^-22; times exp(l - top), the
+// former is largest at |l - top| = 1; the sum by as much, with 10 roundings and the mean of
+// |l - top| over the softmax, below log 1024 = 7: in all below 2^-19 of the
+// largest score, 1 / sum.  Sigmoid: s (1 - s) times the exponential's error, |l| s (1 - s) < 1/4,
+// and two roundings: below 2^-21.  Then half a unit of the sum with the bias.
+__device__ __forceinline__ float choice_error(const RouteParams& p, float size, float sum) {
+    return 0x1p-22f * size + (p.sigmoid ? 0x1p-20f : 0x1p-18f * fast_reciprocal(sum));
+}
+
+// The largest key's place: (lane, number) with the lowest expert.  Whole warp; 0 if there is none.
+template <int NPL, typename V>
+__device__ __forceinline__ typename Keys<V>::Key largest(const typename Keys<V>::Key (&key)[NPL], int& e) {
+    typename Keys<V>::Key m = key[0];
+    int at = 0;
+#pragma unroll 1
+    for (int i = 1; i < NPL; ++i)
+        if (key[i] > m) m = key[i], at = i;
+    const auto best = Keys<V>::most(m);
+    const int from = __ffs(__ballot_sync(kAll, m == best)) - 1;
+    e = __shfl_sync(kAll, static_cast<int>(threadIdx.x & 31) * NPL + at, from);
+    return best;
+}
+
+// The choice with keys of 32 bits.  Where those that decide are within their
+// errors of one another, these alone are computed in 64 bits and compared so.
+// Few tokens come here, and the rest wait for them: so little is computed in 64
+// bits (2 lanes a cycle of an SM), and loops are not unrolled (instructions that
+// nobody has fetched before: 25 us for the first token of a prompt).
+template <int NPL, typename T>
+__device__ __noinline__ int choose_again(const RouteParams& p, const T* row, float top, float sum) {
+    using K = Keys<float>;
+    const int lane = threadIdx.x & 31, first = lane * NPL;
+    const bool by_logit = chosen_by_logit(p);
+    float l[NPL], bias[NPL], size = 0.f, near = 0.f;
+    uint32_t key[NPL];
+#pragma unroll 1
+    for (int i = 0; i < NPL; ++i) {
+        const bool there = first + i < p.E;
+        l[i] = there ? to_f32(row[first + i]) : -INFINITY;
+        bias[i] = there && p.bias ? p.bias[first + i] : 0.f;
+        float c = l[i];
+        if (!by_logit && c != -INFINITY) {
+            c = (p.sigmoid ? fast_reciprocal(1.f + fast_exp(-c)) : fast_exp(c - top) * fast_reciprocal(sum)) + bias[i];
+            if (fabsf(c) < INFINITY) size = fmaxf(size, fabsf(c));
         }
-        if (j == p.k) break;
-        before = best;
-        const int from = __ffs(__ballot_sync(kAll, m == best)) - 1;
-        const int e = __shfl_sync(kAll, first + static_cast<int>(SORTED ? at & 15 : at), from);
-        if (lane == j) mine = e;
-        if (lane == from) {
-            if constexpr (SORTED) {
-#pragma unroll
-                for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
-                key[NPL - 1] = 0;
-                at >>= 4;
-                m = key[0];
-            } else {
-#pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (i == static_cast<int>(at)) key[i] = 0;
-                lead();
+        key[i] = c == -INFINITY ? 0u : K::of(c);
+    }
+    if (!by_logit) near = choice_error(p, warp_max(size), sum);  // (logits are exact)
+    double all = 0;  // the softmax's sum, once it is needed
+    // 64-bit keys of the lane's values whose bit is set in `some`, 0 for the others.
+    auto evaluate = [&](uint32_t some, unsigned long long (&exact)[NPL]) {
+        if (!p.sigmoid && all == 0) {
+#pragma unroll 1
+            for (int i = 0; i < NPL; ++i) all += l[i] == -INFINITY ? 0. : exp(static_cast<double>(l[i]) - top);
+            all = warp_sum(all);
+        }
+#pragma unroll 1
+        for (int i = 0; i < NPL; ++i) {
+            exact[i] = 0;
+            if (__any_sync(kAll, some >> i & 1)) {
+                const double x = l[i];
+                const double c = (p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / all) + bias[i];
+                if (some >> i & 1) exact[i] = Keys<double>::of(c);
             }
         }
+    };
+    if (p.groups > 1) {
+        uint32_t a, b;
+        group_best<NPL>(key, p, a, b);
+        const bool there = lane < p.groups && a;
+        float score = 0.f;
+        if (there) score = K::value(a) + (p.group_best == 2 && b ? K::value(b) : 0.f);
+        const uint32_t rank = there ? K::of(score) : 0u;
+        // Surely among the best: fewer than top_groups may be better.  Surely not: as many are.
+        const float apart = p.group_best == 2 ? 2.f * near : near;
+        int may = 0, are = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint32_t other = __shfl_sync(kAll, rank, g);
+            const float v = __shfl_sync(kAll, score, g);
+            if (g == lane || !other) continue;
+            const bool close = apart > 0.f && fabsf(score) < INFINITY && fabsf(v) < INFINITY && fabsf(v - score) <= apart;
+            const bool better = other > rank || (other == rank && g < lane);
+            may += close || better;
+            are += !close && better;
+        }
+        unsigned kept = __ballot_sync(kAll, there && may < p.top_groups);
+        const unsigned open = __ballot_sync(kAll, there && may >= p.top_groups && are < p.top_groups);
+        if (open) {
+            // The open groups' scores in 64 bits, from those of their values that may be among the best two.
+            const int size = p.group_size;
+            const float second = b ? K::value(b) : -INFINITY;
+            uint32_t some = 0;
+#pragma unroll 1
+            for (int i = 0; i < NPL; ++i) {
+                const int g = min((first + i) / size, 31);
+                const float from = __shfl_sync(kAll, p.group_best == 2 ? second : there ? K::value(a) : 0.f, g) - near;
+                if (key[i] && (open >> g & 1) && !(K::value(key[i]) < from)) some |= 1u << i;
+            }
+            unsigned long long exact[NPL], best, next;
+            evaluate(some, exact);
+            group_best<NPL>(exact, p, best, next);
+            unsigned long long value = 0;
+            if (open >> lane & 1) {
+                double v = Keys<double>::value(best);
+                if (p.group_best == 2 && next) v += Keys<double>::value(next);
+                value = Keys<double>::of(v);
+            }
+            for (int left = p.top_groups - __popc(kept); left > 0; --left) {
+                const unsigned long long most = Keys<double>::most(value);
+                if (most == 0) break;
+                const int from = __ffs(__ballot_sync(kAll, value == most)) - 1;
+                kept |= 1u << from;
+                if (lane == from) value = 0;
+            }
+        }
+        keep_groups<NPL>(key, p, kept);
+    }
+    int mine = -1;
+    for (int j = 0; j < p.k; ++j) {
+        int e;
+        const uint32_t best = largest<NPL, float>(key, e);
+        if (best == 0) break;
+        const float v = K::value(best);
+        if (near > 0.f && fabsf(v) < INFINITY) {
+            const uint32_t from = K::of(v - near);
+            uint32_t some = 0;
+#pragma unroll 1
+            for (int i = 0; i < NPL; ++i)
+                if (key[i] >= from) some |= 1u << i;
+            if (__reduce_add_sync(kAll, __popc(some)) > 1) {
+                unsigned long long exact[NPL];
+                evaluate(some, exact);
+                (void)largest<NPL, double>(exact, e);
+            }
+        }
+        if (lane == j) mine = e;
+#pragma unroll 1
+        for (int i = 0; i < NPL; ++i)
+            if (first + i == e) key[i] = 0;
     }
     return mine;
 }
 
-// The choice in 64 bits.
-template <int NPL, typename T>
-__device__ __noinline__ int choose_again(const RouteParams& p, const T* row) {
-    float l[NPL];
-    load_row<NPL>(row, p.E, p.vec, l);
-    float top = -INFINITY;
+// Keys with their expert in them: 22 bits of the value, in its order, and 1023 - e
+// below.  No two are alike, so that a maximum names its expert, and equal
+// values go to the lowest.  Of a 16-bit logit the upper 22 bits of its key in
+// float32 are all there is; other values are taken to a grid of 2^22 steps from
+// the token's smallest to its largest.  Keys below 1024: out of service.
+constexpr uint32_t kExpertBits = 1023;
+constexpr int kExpertShift = 10;
+
+// Exchanges that sort the lane's keys, the largest first (merge exchange, Batcher).
+template <int NPL>
+__device__ __forceinline__ void sort_lane(uint32_t (&key)[NPL]) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) top = fmaxf(top, l[i]);
-    top = warp_max(top);
-    double sum = 0;
-    if (!p.sigmoid) {
+    for (int p = 1; p < NPL; p *= 2)
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) sum += l[i] == -INFINITY ? 0. : exp(static_cast<double>(l[i]) - top);
-        sum = warp_sum(sum);
-    }
-    const int first = (threadIdx.x & 31) * NPL;
-    unsigned long long key[NPL];
+        for (int k = p; k >= 1; k /= 2)
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        key[i] = 0;
-        if (l[i] != -INFINITY) {
-            const double x = l[i];
-            double c = p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / sum;
-            if (p.bias) c += __ldg(p.bias + first + i);
-            if (c != -INFINITY) key[i] = Keys<double>::of(c);
-        }
-    }
-    bool sure;
-    return choose<NPL, double>(key, p, false, 0., sure);
+            for (int j = k % p; j + k < NPL; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < NPL && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t x = key[i + j], y = key[i + j + k];
+                        key[i + j] = max(x, y);
+                        key[i + j + k] = min(x, y);
+                    }
 }
 
-// A token's experts and weights, the j-th in lane j, from its row (l: the lane's part).
-template <int NPL, typename T>
-__device__ __forceinline__ int route_token(const RouteParams& p, const T* row, const float (&l)[NPL],
-                                           const float (&bias)[NPL], float& weight) {
-    const bool by_logit = !p.bias && (p.groups == 1 || p.group_best == 1);
-    float top = 0.f, sum = 0.f;
-    uint32_t key[NPL];
-    if (!p.sigmoid && (!by_logit || !p.renormalize)) {
-        top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) top = fmaxf(top, l[i]);
-        top = warp_max(top);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) sum += l[i] == -INFINITY ? 0.f : expf(l[i] - top);
-        sum = warp_sum(sum);
+// The choice with packed keys: lane j's result is the j-th expert, -1 where there
+// is none.  exact: they hold all of the values; else `sure` is false where two
+// that decide are not further apart than `gap` steps of the grid (the scores of
+// groups: `group_gap`).
+template <int NPL>
+__device__ __forceinline__ int choose_packed(uint32_t (&key)[NPL], const RouteParams& p, bool exact, uint32_t gap,
+                                             uint32_t group_gap, bool& sure) {
+    const int lane = threadIdx.x & 31;
+    constexpr bool SORTED = NPL <= 8;
+    bool close = false;
+    auto most = [](uint32_t k) { return __reduce_max_sync(kAll, k); };
+    // Groups that are a power of two of whole lanes, 2^shift of them, or no groups.
+    const bool whole = SORTED && p.group_lanes >= 0;
+    const int shift = max(p.group_lanes, 0), lanes = 1 << shift;
+    if constexpr (SORTED) {
+        if (whole) sort_lane(key);
     }
-    bool sure;
-    int e;
-    if (by_logit) {
+    if (p.groups > 1) {
+        uint32_t a, b;
+        if (whole) {
+            a = key[0], b = NPL > 1 ? key[NPL > 1 ? 1 : 0] : 0u;
+            for (int d = 1; d < lanes; d *= 2) merge_two(a, b, __shfl_xor_sync(kAll, a, d), __shfl_xor_sync(kAll, b, d));
+            const int from = (lane << shift) & 31;
+            a = __shfl_sync(kAll, a, from);
+            b = __shfl_sync(kAll, b, from);
+        } else {
+            group_best<NPL>(key, p, a, b);
+        }
+        a >>= kExpertShift;
+        b >>= kExpertShift;
+        uint32_t score = lane < p.groups ? a : 0u;
+        if (p.group_best == 2) {
+            // (a sum of two and a single value are not on one grid)
+            const unsigned one = __ballot_sync(kAll, score != 0 && b == 0), two = __ballot_sync(kAll, score != 0 && b != 0);
+            close = one && two;
+            if (score) score += b;
+        }
+        unsigned kept = 0;
+        uint32_t last = ~0u;
+        for (int i = 0; i < p.top_groups; ++i) {
+            const uint32_t best = most(score);
+            const unsigned who = __ballot_sync(kAll, score == best);
+            const unsigned bit = who & (0u - who);  // the lowest
+            kept |= best ? bit : 0u;
+            if (bit >> lane & 1) score = 0;
+            last = best;
+        }
+        const uint32_t next = most(score);
+        close |= next && last - next <= group_gap;
+        if (whole) {
+            if (!(kept >> (lane >> shift) & 1)) {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) key[i] = l[i] == -INFINITY ? 0u : Keys<float>::of(l[i]);
-        e = choose<NPL, float>(key, p, false, 0.f, sure);
+                for (int i = 0; i < NPL; ++i) key[i] = 0;
+            }
+        } else {
+            keep_groups<NPL>(key, p, kept);
+        }
+    }
+    uint32_t m = key[0];
+    if constexpr (SORTED) {
+        if (!whole) sort_lane(key);
+        m = key[0];
     } else {
-        // Errors.  Softmax: exp(l - top) is off by |l - top| 2^-24 (the
-        // difference's rounding) and 2 units; times exp(l - top), the former is
-        // largest at |l - top| = 1; the sum by 12 units and by the mean of
-        // |l - top| over the softmax, below log 1024 = 7: in all below 2^-19 of
-        // the largest score.  Sigmoid: below 2^-21.  Then half a unit of the
-        // sum with the bias.  Two values are in order when they are further
-        // apart than both errors.
-        const float inv = 1.f / sum;
-        float size = 0.f;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            key[i] = 0;
-            if (l[i] != -INFINITY) {
-                const float s = p.sigmoid ? __fdividef(1.f, 1.f + expf(-l[i])) : expf(l[i] - top) * inv;
-                const float c = s + bias[i];
-                size = fmaxf(size, fabsf(c));
-                if (c != -INFINITY) key[i] = Keys<float>::of(c);
+        for (int i = 1; i < NPL; ++i) m = max(m, key[i]);
+    }
+    uint32_t before = ~0u;
+    int mine = -1;
+    for (int j = exact ? 1 : 0; j <= p.k; ++j) {  // (one more than wanted, to see how near it is)
+        const uint32_t best = most(m);
+        close |= j > 0 && best > kExpertBits && (before >> kExpertShift) - (best >> kExpertShift) <= gap;
+        if (lane == (exact ? j - 1 : j)) mine = best > kExpertBits ? static_cast<int>(kExpertBits - (best & kExpertBits)) : -1;
+        before = best;
+        if constexpr (SORTED) {
+            const bool pop = m == best;
+#pragma unroll
+            for (int i = 0; i + 1 < NPL; ++i) key[i] = pop ? key[i + 1] : key[i];
+            key[NPL - 1] = pop ? 0u : key[NPL - 1];
+            m = key[0];
+        } else if (m == best) {
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                key[i] = key[i] == best ? 0u : key[i];
+                m = max(m, key[i]);
             }
         }
-        size = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
-        const float near = 0x1p-22f * size + (p.sigmoid ? 0x1p-20f : 0x1p-18f * inv);
-        e = choose<NPL, float>(key, p, true, near, sure);
-        if (!sure) e = choose_again<NPL>(p, row);
     }
-    // Weights.  sigmoid(l) = e^min(l, 0) / (1 + e^-|l|): with the largest chosen
-    // logit's e^min(l, 0) taken out, the renormalised ones are ratios of
-    // numbers near 1 however small the scores are.
-    const float x = e >= 0 ? to_f32(row[e]) : -INFINITY;
-    float s = 0.f;
-    const float lead = p.renormalize ? warp_max(x) : top;
-    if (e >= 0) {
-        if (p.sigmoid) {
-            const float low = x > 0.f ? 0.f : x;
-            s = expf(low - (p.renormalize ? fminf(lead, 0.f) : 0.f)) / (1.f + expf(-fabsf(x)));
+    sure = exact || !close;
+    return lane < p.k ? mine : -1;
+}
+
+// The values' keys on the grid; false where there is none (values that are all
+// alike, or not finite).  A value's place is off by less than a step, and
+// places never change their order.  low, high: the smallest and the largest.
+template <int NPL>
+__device__ __forceinline__ bool grid_keys(const float (&c)[NPL], uint32_t (&key)[NPL], float& low, float& high,
+                                          float& scale) {
+    using K = Keys<float>;
+    high = -INFINITY, low = INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        high = max_nan(high, c[i]);
+        low = fminf(low, c[i] == -INFINITY ? INFINITY : c[i]);
+    }
+    high = K::value(__reduce_max_sync(kAll, K::of(high)));
+    low = K::value(__reduce_min_sync(kAll, K::of(low)));
+    const float range = high - low;
+    scale = 4194280.f * fast_reciprocal(range);  // 2^22 less 24
+    // The place is the mantissa of a number from 2^23 on, whose exponent the shift drops (as it drops all of -inf).
+    const uint32_t e0 = kExpertBits - (threadIdx.x & 31) * NPL;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+        key[i] = (__float_as_uint(fmaf(c[i] - low, scale, 8388612.f)) << kExpertShift) + (e0 - static_cast<uint32_t>(i));
+    return range > 0x1p-60f && range < 0x1p60f;
+}
+
+// A token's experts, the j-th in lane j, from its logits (the lane's part); `bias`: the lane's, in shared memory.
+template <int NPL, typename T>
+__device__ __forceinline__ int choose_experts(const RouteParams& p, const float (&l)[NPL], const float* bias, float top,
+                                              float sum, bool& sure) {
+    uint32_t key[NPL];
+    float low, high, scale;
+    if (chosen_by_logit(p)) {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const uint32_t e = (threadIdx.x & 31) * NPL + i;
+                key[i] = l[i] == -INFINITY ? 0u : (Keys<float>::of(l[i]) & ~kExpertBits) | (kExpertBits - e);
+            }
+            return choose_packed<NPL>(key, p, true, 0, 0, sure);
         } else {
-            s = expf(x - lead);
-            if (sum != sum) s = sum;  // (a NaN or +inf that was not chosen)
+            sure = grid_keys(l, key, low, high, scale);
+            if (sure) return choose_packed<NPL>(key, p, false, 0, 0, sure);
+            sure = high == -INFINITY;  // (nobody is in service)
+            return -1;
         }
     }
+    float c[NPL], b[NPL];
+    if constexpr (NPL >= 4) {
+#pragma unroll
+        for (int i = 0; i < NPL; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(bias + i);
+            b[i] = x.x, b[i + 1] = x.y, b[i + 2] = x.z, b[i + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) b[i] = bias[i];
+    }
+    choice_values(p, l, b, top, sum, c);
+    sure = grid_keys(c, key, low, high, scale);
+    if (!sure) {
+        sure = high == -INFINITY;  // (nobody is in service)
+        return -1;
+    }
+    // (a step more for each place's error)
+    const float steps = fminf(choice_error(p, fmaxf(fabsf(low), fabsf(high)), sum) * scale, 0x1p20f);
+    return choose_packed<NPL>(key, p, false, static_cast<uint32_t>(steps + 2.1f),
+                              p.group_best == 2 ? static_cast<uint32_t>(2.f * steps + 4.1f)
+                                                : static_cast<uint32_t>(steps + 2.1f),
+                              sure);
+}
+
+// The weight of the lane's expert e (-1: none).
+//
+// sigmoid(l) = e^min(l, 0) / (1 + e^-|l|): with the largest chosen logit's
+// e^min(l, 0) taken out, the renormalised ones are ratios of numbers near 1
+// however small the scores are.
+template <typename T>
+__device__ __forceinline__ float weight_of(const RouteParams& p, const T* row, int e, float top, float sum) {
+    const float x = e >= 0 ? to_f32(row[e]) : -INFINITY;
+    const float lead = p.renormalize ? warp_max(x) : top;
+    float s = 0.f;
+    if (p.sigmoid) {
+        const float low = x > 0.f ? 0.f : x;
+        s = __fdividef(expf(low - (p.renormalize ? fminf(lead, 0.f) : 0.f)), 1.f + expf(-fabsf(x)));
+    } else {
+        s = expf(x - lead);
+        if (sum != sum) s = sum;  // (a NaN or +inf that was not chosen)
+    }
+    if (e < 0) s = 0.f;
     if (p.renormalize) sum = warp_sum(s);
-    weight = e < 0 ? 0.f : p.sigmoid && !p.renormalize ? p.scale * s : p.scale * s / sum;
-    return e;
+    return e < 0 ? 0.f : p.sigmoid && !p.renormalize ? p.scale * s : p.scale * s * fast_reciprocal(sum);
 }
 
 // Exclusive sums of count[0 .. E - 1] (at most two a thread) to base, and
@@ -397,62 +585,61 @@ __device__ __forceinline__ void exclusive_sums(const int* count, int E, int* bas
     __syncthreads();
 }
 
-// CLUSTER: CTAs of a cluster (their count of each expert's choices is summed
-// through distributed shared memory).  With p.counts there are several clusters,
+// The CTAs of a cluster (p.width) add up their counts of each expert's choices
+// through distributed shared memory.  With p.counts there are several clusters,
 // which leave their sums there for place_kernel; else the one finishes the places.
-template <int NPL, typename T, int CLUSTER>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
-    extern __shared__ int shared[];
-    int* const mask = shared;             // E: this step's tokens
-    int* const count = shared + p.E;      // E: choices of the steps before
-    int* const before = shared + 2 * p.E; // E: of the cluster's CTAs before this one, then all that come before
-    int* const scratch = shared + 3 * p.E;  // a word a warp
+template <int NPL, typename T>
+__global__ void __launch_bounds__(kRouteThreads, NPL <= 8 ? 2 : 1) route_kernel(const RouteParams p) {
+    extern __shared__ __align__(16) int shared[];
+    float* const bias = reinterpret_cast<float*>(shared);  // 32 * NPL
+    int* const mask = shared + 32 * NPL;                   // E: this step's tokens
+    int* const count = mask + p.E;                         // E: choices of the steps before
+    int* const before = count + p.E;    // E: of the cluster's CTAs before this one, then all that come before
+    int* const scratch = before + p.E;  // a word a warp
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = count[e] = 0;
-    float bias[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = lane * NPL + i;
-        bias[i] = p.bias && e < p.E ? __ldg(p.bias + e) : 0.f;
-    }
+    for (int e = threadIdx.x; e < 32 * NPL; e += kRouteThreads) bias[e] = p.bias && e < p.E ? __ldg(p.bias + e) : 0.f;
     __syncthreads();
-    const long long begin = static_cast<long long>(blockIdx.x) * p.steps * kRouteStep;
-    int mine[kRouteTokens] = {}, rank[kRouteTokens] = {};  // of the last step
+    constexpr int kTokens = 2;  // of a warp in a step, at most: with 16 warps, a bit each
+    static_assert(kTokens * kRouteWarps <= 32, "a bit a token");
+    const bool sums = !p.sigmoid && (!p.renormalize || !chosen_by_logit(p));
+    const long long begin = static_cast<long long>(blockIdx.x) * p.per, end = min(static_cast<long long>(p.T), begin + p.per);
+    int mine[kTokens] = {}, rank[kTokens] = {};  // of the last step
     for (int step = 0; step < p.steps; ++step) {
-        const long long t0 = begin + step * kRouteStep + warp;
-        auto row = [&](int i) { return static_cast<const T*>(p.logits) + (t0 + i * kRouteWarps) * p.ld; };
-        float l[NPL], next[NPL];
-        if (t0 < p.T) load_row<NPL>(row(0), p.E, p.vec, l);
+        const long long t0 = begin + step * p.step + warp;
 #pragma unroll
-        for (int i = 0; i < kRouteTokens; ++i) {
+        for (int i = 0; i < kTokens; ++i) {
             const long long t = t0 + i * kRouteWarps;
-            const bool more = i + 1 < kRouteTokens && t + kRouteWarps < p.T;
-            if (NPL <= 8 && more) load_row<NPL>(row(i + 1), p.E, p.vec, next);  // (beside this token's work)
-            int e = -1;
-            if (t < p.T) {
-                float w;
-                e = route_token<NPL, T>(p, row(i), l, bias, w);
+            mine[i] = -1;
+            if (t < end && i * kRouteWarps < p.step) {
+                const T* const row = static_cast<const T*>(p.logits) + t * p.ld;
+                float top = 0.f, sum = 0.f;
+                bool sure;
+                int e;
+                {
+                    float l[NPL];
+                    load_row<NPL>(row, p.E, p.vec, l);
+                    if (sums) softmax_sums(l, top, sum);
+                    e = choose_experts<NPL, T>(p, l, bias + lane * NPL, top, sum, sure);
+                }
+                if (!sure) e = choose_again<NPL>(p, row, top, sum);
+                const float w = weight_of(p, row, e, top, sum);
                 if (lane < p.k) {
                     p.experts[t * p.k + lane] = e;
                     p.weights[t * p.k + lane] = w;
                     if (e >= 0) atomicOr(mask + e, 1 << (warp + i * kRouteWarps));
                 }
-            }
-            mine[i] = lane < p.k ? e : -1;
-            if (NPL > 8 && more) load_row<NPL>(row(i + 1), p.E, p.vec, next);
-            if (more) {
-#pragma unroll
-                for (int j = 0; j < NPL; ++j) l[j] = next[j];
+                mine[i] = e;
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kRouteTokens; ++i) {
+        for (int i = 0; i < kTokens; ++i) {
             const long long t = t0 + i * kRouteWarps;
             const unsigned below = (1u << (warp + i * kRouteWarps)) - 1;
             rank[i] = mine[i] < 0 ? -1 : count[mine[i]] + __popc(mask[mine[i]] & below);
-            if (step + 1 < p.steps && t < p.T && lane < p.k) p.slots[t * p.k + lane] = rank[i];
+            if (step + 1 < p.steps && t < end && i * kRouteWarps < p.step && lane < p.k) p.slots[t * p.k + lane] = rank[i];
         }
         __syncthreads();
         for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
@@ -462,41 +649,35 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         __syncthreads();
     }
     // What comes before this CTA's choices of an expert, in the cluster.
-    int* total = count;
-    if constexpr (CLUSTER > 1) {
-        const int of = static_cast<int>(cluster_ctarank());
-        cluster_sync_all();
-        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-            const uint32_t at = smem_addr(count + e);
-            int sum = 0, mine_from = 0;
-#pragma unroll
-            for (int q = 0; q < CLUSTER; ++q) {
-                if (q == of) mine_from = sum;
-                sum += ld_shared_cluster_s32(map_shared_rank(at, q));
-            }
-            before[e] = mine_from;
-            mask[e] = sum;
-            if (p.counts && of == 0) p.counts[static_cast<long long>(blockIdx.x / CLUSTER) * p.E + e] = sum;
+    const int of = static_cast<int>(cluster_ctarank());
+    cluster_sync_all();
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+        const uint32_t at = smem_addr(count + e);
+        int sum = 0, sum_before = 0;
+#pragma unroll 4
+        for (int q = 0; q < p.width; ++q) {
+            if (q == of) sum_before = sum;
+            sum += ld_shared_cluster_s32(map_shared_rank(at, q));
         }
-        total = mask;
-        cluster_sync_all();  // (nobody reads this CTA's counts after this)
-    } else {
-        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) before[e] = 0;
-        __syncthreads();
+        before[e] = sum_before;
+        mask[e] = sum;
+        if (p.counts && of == 0) p.counts[static_cast<long long>(blockIdx.x / p.width) * p.E + e] = sum;
     }
+    cluster_sync_all();  // (nobody reads this CTA's counts after this)
     if (!p.counts) {
-        int* const base = CLUSTER > 1 ? count : mask;
-        exclusive_sums(total, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
+        int* const base = count;
+        exclusive_sums(mask, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
         for (int e = threadIdx.x; e < p.E; e += kRouteThreads) before[e] += base[e];
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < kRouteTokens; ++i) {
-        const long long t = begin + (p.steps - 1) * kRouteStep + warp + i * kRouteWarps;
-        if (t < p.T && lane < p.k) p.slots[t * p.k + lane] = mine[i] < 0 ? -1 : rank[i] + before[mine[i]];
+    for (int i = 0; i < kTokens; ++i) {
+        const long long t = begin + (p.steps - 1) * p.step + warp + i * kRouteWarps;
+        if (t < end && i * kRouteWarps < p.step && lane < p.k)
+            p.slots[t * p.k + lane] = mine[i] < 0 ? -1 : rank[i] + before[mine[i]];
     }
     if (p.steps > 1) {  // the steps before the last, whose places are in memory
-        const long long from = begin * p.k, to = min(static_cast<long long>(p.T), begin + (p.steps - 1) * kRouteStep) * p.k;
+        const long long from = begin * p.k, to = min(end, begin + (p.steps - 1) * p.step) * p.k;
         for (long long i = from + threadIdx.x; i < to; i += kRouteThreads) {
             const int e = p.experts[i];
             if (e >= 0) p.slots[i] += before[e];
@@ -504,9 +685,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     }
 }
 
-// Places within a cluster's rows of an expert to places among all rows; a CTA a cluster.
+// Places within a cluster's rows of an expert to places among all rows.
 __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams p, int clusters) {
-    extern __shared__ int shared[];
+    extern __shared__ __align__(16) int shared[];
     int* const total = shared;
     int* const before = shared + p.E;
     int* const base = shared + 2 * p.E;
@@ -514,26 +695,38 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) total[e] = before[e] = 0;
     __syncthreads();
     grid_dependency_wait();
-    // Threads by expert, and those left over by CTA as well.
+    // (the first choices' experts on their way beside the counts)
+    const long long per = static_cast<long long>(p.per) * p.k, all = static_cast<long long>(p.T) * p.k;
+    const long long from = blockIdx.x * per, to = min(all, from + per);
+    const int mine = static_cast<int>(blockIdx.x) / p.width;
+    int expert[2], slot[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const long long i = from + threadIdx.x + u * kRouteThreads;
+        expert[u] = i < to ? p.experts[i] : -1;
+        slot[u] = i < to ? p.slots[i] : -1;
+    }
+    // Threads by expert, and those left over by cluster as well.
     int width = 32;
     while (width < p.E && width < kRouteThreads) width *= 2;
     const int parts = kRouteThreads / width, part = threadIdx.x / width;
     for (int e = threadIdx.x % width; e < p.E; e += width) {
-        int all = 0, mine = 0;
+        int sum = 0, sum_before = 0;
 #pragma unroll 8
         for (int c = part; c < clusters; c += parts) {
             const int n = p.counts[static_cast<long long>(c) * p.E + e];
-            all += n;
-            if (c < static_cast<int>(blockIdx.x)) mine += n;
+            sum += n;
+            if (c < mine) sum_before += n;
         }
-        atomicAdd(total + e, all);
-        atomicAdd(before + e, mine);
+        atomicAdd(total + e, sum);
+        atomicAdd(before + e, sum_before);
     }
     __syncthreads();
     exclusive_sums(total, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
-    const long long per = static_cast<long long>(p.steps) * kRouteStep * kRouteCluster * p.k, all = static_cast<long long>(p.T) * p.k;
-    const long long from = blockIdx.x * per, to = min(all, from + per);
-    for (long long i = from + threadIdx.x; i < to; i += kRouteThreads) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (expert[u] >= 0) p.slots[from + threadIdx.x + u * kRouteThreads] = slot[u] + base[expert[u]] + before[expert[u]];
+    for (long long i = from + threadIdx.x + 2 * kRouteThreads; i < to; i += kRouteThreads) {
         const int e = p.experts[i];
         if (e >= 0) p.slots[i] += base[e] + before[e];
     }
@@ -662,19 +855,24 @@ int launched() {
 }  // namespace
 
 RoutePlan route_plan(int T, int sms) {
-    const int steps = (T + kRouteStep - 1) / kRouteStep;
-    if (steps == 1) return {1, 1, 1};
-    // One cluster finishes by itself, which saves a launch: up to two steps of it.
-    const int least = (steps + kRouteCluster - 1) / kRouteCluster;
-    if (least <= 2) return {1, kRouteCluster, least};
-    // About three CTAs an SM at once.
-    const int most = std::max(1, 3 * sms / kRouteCluster);
-    const int each = (least + most - 1) / most;
-    return {(least + each - 1) / each, kRouteCluster, each};
+    // One cluster finishes by itself, which saves a launch.
+    if (T <= kRouteWarps) return {1, 1, T, kRouteWarps};
+    constexpr int step = 2 * kRouteWarps;
+    if (T <= 2 * kRouteCluster * step) {
+        const int per = (T + kRouteCluster - 1) / kRouteCluster;
+        return {1, kRouteCluster, per, per <= kRouteWarps ? kRouteWarps : step};
+    }
+    // Two CTAs an SM at once, whole steps each.
+    const int most = std::max(1, 2 * sms / kRouteCluster) * kRouteCluster;
+    const int per = ((T + most - 1) / most + step - 1) / step * step;
+    const int ctas = (T + per - 1) / per;
+    return {(ctas + kRouteCluster - 1) / kRouteCluster, kRouteCluster, per, step};
 }
 
-int route(const RouteParams& p, const RoutePlan& plan, int type, cudaStream_t s) {
-    const size_t smem = (3 * static_cast<size_t>(p.E) + kRouteWarps) * sizeof(int);
+int route(const RouteParams& given, const RoutePlan& plan, int type, cudaStream_t s) {
+    RouteParams p = given;
+    // (the bias to the last lane's end: E up to a power of two from 32 on)
+    const size_t smem = (5 * static_cast<size_t>(std::max(p.E, 32)) + kRouteWarps) * sizeof(int);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters * plan.width));
     cfg.blockDim = dim3(kRouteThreads);
@@ -689,13 +887,15 @@ int route(const RouteParams& p, const RoutePlan& plan, int type, cudaStream_t s)
     const int rc = by_type_and_width(type, p.E, [&](auto zero, auto npl) {
         constexpr int NPL = decltype(npl)::value;
         using T = decltype(zero);
-        const auto kernel = plan.width > 1 ? route_kernel<NPL, T, kRouteCluster> : route_kernel<NPL, T, 1>;
-        if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return static_cast<int>(SGEMM_OK);
+        const int lanes = p.group_size / NPL;
+        p.group_lanes = 0;
+        while (1 << p.group_lanes < lanes) ++p.group_lanes;
+        if (p.groups > 1 && (p.group_size % NPL || 1 << p.group_lanes != lanes)) p.group_lanes = -1;
+        if (cudaLaunchKernelEx(&cfg, route_kernel<NPL, T>, p) == cudaSuccess) return static_cast<int>(SGEMM_OK);
         (void)cudaGetLastError();
         return static_cast<int>(SGEMM_ERR_CUDA);
     });
     if (rc != SGEMM_OK || !p.counts) return rc;
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters));
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;

@@ -15,24 +15,24 @@ struct RouteParams {
     int T, E, k;
     int sigmoid, renormalize;
     int groups, top_groups, group_best;
+    int group_size, group_lanes;  // E / groups; the lanes of a group's keys as a power of two, or -1 (set by route)
     float scale;
     int* experts;
     float* weights;
     int* offsets;
     int* slots;
     int vec;      // the rows begin on 16 bytes: whole vectors are loaded
-    int steps;    // steps of kRouteStep tokens a CTA takes
-    int* counts;  // clusters x E: choices of each expert (null: one cluster does it all)
+    int width, per;    // CTAs of a cluster, tokens of a CTA
+    int steps, step;   // a CTA's steps, and the tokens of one
+    int* counts;      // clusters x E: choices of each expert (null: one cluster does it all)
 };
 
-// Tokens of a CTA's step: a bit each in an expert's word.
-constexpr int kRouteStep = 32;
-// CTAs of a cluster, where there is more than one.
-constexpr int kRouteCluster = 8;
+// Warps of a CTA, and CTAs of a cluster where there is more than one.
+constexpr int kRouteWarps = 16, kRouteCluster = 8;
 
-// The grid of a routing: clusters of `width` CTAs, and each CTA's steps.
+// The grid of a routing: clusters of `width` CTAs, each CTA's tokens, and those of a step.
 struct RoutePlan {
-    int clusters, width, steps;
+    int clusters, width, per, step;
 };
 RoutePlan route_plan(int T, int sms);
 int route(const RouteParams& p, const RoutePlan& plan, int type, cudaStream_t s);
