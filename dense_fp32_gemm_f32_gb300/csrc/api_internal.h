@@ -57,6 +57,7 @@ struct DeviceState {
     int experts_status = SGEMM_ERR_CUDA;  // of the grouped and MXFP4 products' set-up
     std::once_flag ortho_once;
     int ortho_status = SGEMM_ERR_CUDA;    // of the orthogonalised updates' set-up (at their first call)
+    int ortho_ctas = 0;           // CTAs of a cluster that their small form may have
     int max_pairs = 0;            // co-resident CTA pairs of the grouped products' wide kernels
     bool regsplit_ok = false;     // the register-split kernels were built at kRegsLaunch registers
     int fused_per_sm[7] = {0};    // co-resident fused-producer CTAs per SM, by stage count

@@ -40,6 +40,9 @@ struct OrthoCall {
     double eps;
 };
 int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s);
+// A short side of up to 128 (ortho_small.cu); SGEMM_ERR_UNSUPPORTED: not one of these.
+int ortho_small_set_up(int* most_ctas);
+int ortho_small(const OrthoCall& c, const DeviceState& st, cudaStream_t s);
 
 }  // namespace detail
 }  // namespace gb300

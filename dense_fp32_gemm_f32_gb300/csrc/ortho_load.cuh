@@ -1,0 +1,71 @@
+// Elements of an update on their way to the products of ortho_tc.cuh and
+// ortho_small.cu: loads, sums of squares, and X = G / (norm + eps) times 2^13 in
+// two f16 parts, hi = f16(x) and lo = f16(x - hi), together 22 bits.
+#pragma once
+
+#include "experts_groups.cuh"
+
+namespace gb300 {
+
+// Eight neighbouring values of a row with `left` of them there.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int left, bool vec, float (&v)[8]) {
+    if (vec && left >= 8) {
+        alignas(16) T x[8];
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+            reinterpret_cast<uint4*>(x)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
+    }
+}
+
+// The sum of eight values' squares.  They are scaled by a power of two that
+// brings the largest near 1, their squares summed in float32, and the sum scaled
+// back in 64 bits: no square overflows or vanishes.
+__device__ __forceinline__ double squares8(const float (&v)[8]) {
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));  // (a NaN is passed over here and summed below)
+    // 2^up brings it to [1, 2) or, from below 2^-126 or above, near that
+    const int up = most > 0.f ? min(126, 127 - static_cast<int>(__float_as_uint(most) >> 23)) : 0;
+    const float scale = __uint_as_float(static_cast<uint32_t>(max(up, -126) + 127) << 23);
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = v[j] * scale;
+        s = fmaf(x, x, s);
+    }
+    // (s is 0 or above 2^-50, below 2^8, and 2^-2up within a double's range)
+    return s * __longlong_as_double(static_cast<long long>(1023 - 2 * max(up, -126)) << 52);
+}
+
+// 2^13 / norm as 2^up * factor, up a power that float32 holds and the factor
+// near 1 where it can be: X's elements stay in range between.
+struct OrthoScale {
+    float power, factor;
+    __device__ __forceinline__ explicit OrthoScale(double norm) {
+        const double inv = 1. / norm;
+        const int exponent = static_cast<int>(__double_as_longlong(inv) >> 52 & 0x7ff) - 1023;
+        const int up = min(max(exponent, -126), 126);
+        power = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+        factor = static_cast<float>(inv * __longlong_as_double(static_cast<long long>(1023 - up) << 52)) * 8192.f;
+    }
+    __device__ __forceinline__ void split(const float (&v)[8], uint4& hi, uint4& lo) const {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = v[2 * j] * power * factor, y = v[2 * j + 1] * power * factor;
+            const __half2 pair = __floats2half2_rn(x, y);
+            h[j] = *reinterpret_cast<const uint32_t*>(&pair);
+            l[j] = pair_from_f32<__half>(x - __low2float(pair), y - __high2float(pair));
+        }
+        hi = make_uint4(h[0], h[1], h[2], h[3]);
+        lo = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+};
+
+}  // namespace gb300

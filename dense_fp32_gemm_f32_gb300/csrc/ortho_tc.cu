@@ -88,8 +88,11 @@ int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st
 }  // namespace
 
 int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s) {
-    std::call_once(st.ortho_once, [&] { st.ortho_status = set_up_kernels(); });
+    std::call_once(st.ortho_once, [&] {
+        st.ortho_status = set_up_kernels() != SGEMM_OK ? SGEMM_ERR_CUDA : ortho_small_set_up(&st.ortho_ctas);
+    });
     if (st.ortho_status != SGEMM_OK) return st.ortho_status;
+    if (const int rc = ortho_small(c, st, s); rc != SGEMM_ERR_UNSUPPORTED) return rc;
     const int m = std::min(c.M, c.N);
     const long long pitch = (c.N + 15ll) / 16 * 16, mp = (m + 15ll) / 16 * 16;  // (the epilogue's accesses of 32 bytes)
     const int parts = c.type == SGEMM_TYPE_BF16 ? 1 : 2;

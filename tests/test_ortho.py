@@ -112,6 +112,18 @@ def test_orthogonalize_many_tiles(E, M, N, dtype):
 
 @pytest.mark.gpu
 @typed(TYPES)
+@pytest.mark.parametrize("E,M,N", [(1, 128, 129), (2, 100, 256), (1, 128, 257), (3, 385, 17), (1, 90, 640), (2, 128, 1024), (1, 1025, 127),
+                                   (1, 60, 2049), (2, 3000, 128), (1, 128, 4096), (1, 33, 3841), (1, 128, 4097), (40, 64, 300), (170, 9, 20)])
+def test_short_sides(E, M, N, dtype):
+    """A short side of up to 128, in clusters of one to sixteen CTAs, and a long one past what those hold."""
+    G = update(E, M, N, dtype, seed=M + N, rank=2)
+    y = g.sgemm_orthogonalize(G)
+    check(y, ortho64(G))
+    assert torch.equal(y, g.sgemm_orthogonalize(G))
+
+
+@pytest.mark.gpu
+@typed(TYPES)
 def test_one_matrix_without_a_batch(dtype):
     G = update(1, 130, 70, dtype, seed=2)
     y = g.sgemm_orthogonalize(G[0])
@@ -122,7 +134,7 @@ def test_one_matrix_without_a_batch(dtype):
 @pytest.mark.gpu
 @typed(TYPES)
 @pytest.mark.parametrize("pad,shift", [(8, 0), (0, 8), (3, 0), (1, 5)])
-@pytest.mark.parametrize("M,N", [(72, 136), (136, 72), (130, 300)])
+@pytest.mark.parametrize("M,N", [(72, 136), (136, 72), (130, 300), (300, 130)])
 def test_strides_and_alignment(M, N, pad, shift, dtype):
     G = update(3, M, N, dtype, seed=3)
     out = padded(torch.zeros_like(G), pad, shift)
@@ -190,7 +202,7 @@ def test_eps_zeros_and_sparse_matrices(dtype):
 @pytest.mark.gpu
 @typed(TYPES)
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("M,N", [(66, 130), (130, 66), (300, 600)])
+@pytest.mark.parametrize("M,N", [(66, 130), (130, 66), (300, 600), (20, 1500)])
 def test_a_non_finite_element_stays_in_its_matrix(M, N, bad, dtype):
     G = update(3, M, N, dtype, seed=9)
     G[1, M // 2, N // 3] = bad
