@@ -14,7 +14,7 @@
 //   square   B = b A + c A A, in every CTA
 //   update   X = a X + B X, a CTA's own columns
 //
-// A thread has a row (its lane of tensor memory) and half of the columns, and what
+// A thread has a row (its lane of tensor memory) and a quarter of the columns, and what
 // it reads and writes of a plane between products are its own elements, so that
 // each plane is updated in place.
 //
@@ -31,7 +31,7 @@ namespace gb300 {
 namespace detail {
 namespace {
 
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 512, kSmallShare = kSmallThreads / 128;  // warps that share a quarter of the rows
 constexpr int kSmallBlock = 128 * 128;  // bytes of 64 columns of a plane (or of 64 of A's)
 
 struct OrthoSmallParams {
@@ -53,8 +53,8 @@ struct SmallShape {
     static constexpr int kXBytes = W / 64 * kSmallBlock, kABytes = 2 * kSmallBlock;  // of a plane
     static constexpr int kPlanes = 2 * kXBytes + 2 * kABytes;
     static constexpr int kTmemCols = PARTS * W;
-    // d, e: 128 floats each; the CTAs' sums and scratch: 16 + 8 doubles; a barrier; the address of tensor memory
-    static constexpr int kSmem = kPlanes + 2 * 512 + 24 * 8 + 16 + 1024;
+    // d, e: 128 floats each; the CTAs' sums and scratch: 16 + 16 doubles; a barrier; the address of tensor memory
+    static constexpr int kSmem = kPlanes + 2 * 512 + (16 + kSmallThreads / 32) * 8 + 16 + 1024;
     static_assert(kSmem <= 227 * 1024 && kTmemCols <= 512 && (W == 128 || W == 256), "shape");
 };
 
@@ -137,13 +137,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
     const uint32_t x_hi = base, x_lo = base + S::kXBytes;
     const uint32_t a_hi = base + 2 * S::kXBytes, a_lo = a_hi + S::kABytes;  // A's, then B's; with several CTAs first A's part
     const uint32_t d_at = base + S::kPlanes, e_at = d_at + 512, sums = e_at + 512, scratch = sums + 16 * 8;
-    const uint32_t bar = scratch + 8 * 8, tmem_slot = bar + 8;
+    const uint32_t bar = scratch + 8 * (kSmallThreads / 32), tmem_slot = bar + 8;
 
     const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = warp_uniform(static_cast<int>(cluster_ctarank()));
     const int e = static_cast<int>(blockIdx.x) / p.width;
     const int n0 = rank * W, cols = min(W, p.n - n0);  // the CTA's columns of X
-    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+    const int row = 32 * (warp & 3) + lane, share = warp >> 2;
+    // Rows and columns of A that are computed; what lies past them in X is zeros.  Warps of rows past them have no part.
+    const int side = (p.m + 31) & ~31;
+    const bool active = 32 * (warp & 3) < side;
     bool timed_out = false;
 
     if (threadIdx.x == 0) {
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         if (warp == 0) {
             if (elect_one()) {
                 fence_proxy_async_all();
-                const int N = update ? W : 128;
+                const int N = update ? (cols + 15) & ~15 : side;
                 const uint32_t idesc = 1u << 4 | (update ? 1u << 16 : 0) | static_cast<uint32_t>(N / 8) << 17 | 8u << 24;
                 for (int k = 0; k < k_len; k += 16) {
                     const uint32_t along = static_cast<uint32_t>((k >> 6) * kSmallBlock / 16 + (k & 63) / 16 * 2);
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         product(true, false, cols);
         if (p.width == 1) {
 #pragma unroll 1
-            for (int c = 64 * half; c < 64 * half + 64; c += 32) {
+            for (int c = 32 * share; active && c < side; c += 32 * kSmallShare) {
                 float v[32];
                 sums_of(c, v);
 #pragma unroll
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             // This CTA's part, in float32: rows of 512 bytes, whose 16-byte pieces trade places by the row's number.
             auto part = [&](int r, int u) { return a_hi + static_cast<uint32_t>(r * 512 + ((u ^ r) & 31) * 16); };
 #pragma unroll 1
-            for (int c = 64 * half; c < 64 * half + 64; c += 32) {
+            for (int c = 32 * share; active && c < side; c += 32 * kSmallShare) {
                 float v[32];
                 sums_of(c, v);
 #pragma unroll
@@ -289,15 +292,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             }
             cluster_sync_all();
             // The sums of some of the rows, from all parts in their order.
-            const int rows = (128 + p.width - 1) / p.width, r0 = rank * rows;
-            const int items = max(0, min(rows, 128 - r0)) * 32;
-            float4 a[8];
+            const int rows = (side + p.width - 1) / p.width, r0 = rank * rows, pieces = side / 4;
+            const int items = max(0, min(rows, side - r0)) * pieces;
+            constexpr int kSums = 64 * 32 / kSmallThreads;
+            float4 a[kSums];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kSums; ++i) {
                 a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 const int item = static_cast<int>(threadIdx.x) + i * kSmallThreads;
                 if (item < items) {
-                    const uint32_t at = part(r0 + item / 32, item % 32);
+                    const uint32_t at = part(r0 + item / pieces, item % pieces);
 #pragma unroll 4
                     for (int q = 0; q < p.width; ++q) {
                         const float4 v = ld_shared_cluster_v4(map_shared_rank(at, q));
@@ -307,10 +311,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             }
             cluster_sync_all();  // (all parts have been read)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kSums; ++i) {
                 const int item = static_cast<int>(threadIdx.x) + i * kSmallThreads;
                 if (item < items) {
-                    const int r = r0 + item / 32, c = item % 32 * 4;
+                    const int r = r0 + item / pieces, c = item % pieces * 4;
                     float v[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, diagonal = 0.f;
                     const bool on = r >= c && r < c + 4;
 #pragma unroll
@@ -336,9 +340,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         }
         // ------------------------------------------------------------ square
         product(false, false, p.m);
-        const float d_row = lds_f(d_at + 4 * row);
+        const float d_row = active ? lds_f(d_at + 4 * row) : 0.f;
 #pragma unroll 1
-        for (int c = 64 * half; c < 64 * half + 64; c += 32) {
+        for (int c = 32 * share; active && c < side; c += 32 * kSmallShare) {
             float v[32], o[32];
             load_planes(a_hi, a_lo, row, c, o);
             sums_of(c, v);
@@ -355,10 +359,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         }
         // ------------------------------------------------------------ update
         product(false, true, p.m);
-        const float factor = p.c1 + lds_f(e_at + 4 * row);
+        const float factor = active ? p.c1 + lds_f(e_at + 4 * row) : 0.f;
         const bool last = step + 1 == p.steps;
 #pragma unroll 1
-        for (int c = W / 2 * half; c < min(cols, W / 2 * half + W / 2); c += 32) {
+        for (int c = 32 * share; active && c < cols; c += 32 * kSmallShare) {
             float v[32], x[32];
             load_planes(x_hi, x_lo, row, c, x);
             sums_of(c, v);
@@ -472,8 +476,8 @@ int ortho_small_set_up(int* most_ctas) {
 
 int ortho_small(const OrthoCall& c, const DeviceState& st, cudaStream_t s) {
     const int m = std::min(c.M, c.N), n = std::max(c.M, c.N);
-    // 128 columns a CTA in clusters of up to 8, else 256.
-    const int w = n <= 8 * 128 ? 128 : 256;
+    // 128 columns a CTA in clusters of up to 8; 256 where one CTA then has all, or there are more.
+    const int w = n <= 128 || (n > 256 && n <= 8 * 128) ? 128 : 256;
     if (m > 128 || n > 256 * st.ortho_ctas) return SGEMM_ERR_UNSUPPORTED;
     if (c.E > 0x7fffffff / 16) return SGEMM_ERR_UNSUPPORTED;
     OrthoSmallParams p = {};

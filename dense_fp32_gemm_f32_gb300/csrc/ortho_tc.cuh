@@ -38,8 +38,8 @@
 //   square tile (i, j)     rows i and j of A
 //   update tile (r, c)     rows r of B (taller than wide: c), and so all of A and X
 //
-// A counter a panel holds the epilogue warps that have finished a tile with
-// rows in it, over all steps.  Tiles come in an order in which every tile waits for
+// A counter a panel holds the CTAs that have finished a tile with rows in it,
+// over all steps.  Tiles come in an order in which every tile waits for
 // earlier ones alone, so the first unfinished one can always proceed.  A buffer
 // is written again only by tiles that wait, through others, for all that read it
 // before (X alternates between two).  Products of several matrices then follow one another without a
@@ -87,6 +87,7 @@ struct OrthoTcParams {
 };
 
 constexpr int kOrthoChunk = 512;  // contraction in one accumulator, with two planes
+constexpr int kOrthoSlots = 4;    // tiles that the load warp tells the epilogue warps about ahead
 
 template <int TN_, int CG_, int PARTS_>
 struct OrthoShape {
@@ -95,21 +96,28 @@ struct OrthoShape {
     static constexpr int kCols = TN / CG;
     static constexpr int kABytes = 128 * 128, kBBytes = kCols * 128;  // of a part, 64 of the contraction
     static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
-    static constexpr int kEpiWarps = 8;
+    static constexpr int kEpiWarps = 16;
     static constexpr int kThreads = 32 * (2 + kEpiWarps);
     // (the widest tile has a seventh stage instead of patches for results off the 16-byte grid)
     static constexpr bool kPatched = !(TN == 256 && PARTS == 1);
     static constexpr int kPatches = kPatched ? kEpiWarps * kGrPatchBytes : 0;
     static constexpr int kStages = kRing(kStageBytes, kPatches);
     static constexpr int kAccCols = PARTS * TN, kTmemCols = 2 * kAccCols;
-    static constexpr int kBars = 2 * kStages + 4;
-    static constexpr int kSmem = kStages * kStageBytes + kPatches + 8 * kBars + 16 + 1024;
-    static constexpr int kWarpCols = TN / 2;    // an epilogue warp's columns
-    static constexpr int kDone = kEpiWarps * CG;  // what a tile adds to a panel's counter
+    static constexpr int kBars = 2 * kStages + 4 + 2 * kOrthoSlots;
+    static constexpr int kSmem = kStages * kStageBytes + kPatches + 8 * kBars + 32 + 1024;
+    static constexpr int kWarpCols = TN / (kEpiWarps / 4);  // an epilogue warp's columns
+    static constexpr int kDone = CG;                        // what a tile adds to a panel's counter
     static_assert(kSmem <= 227 * 1024 && kStages >= 2 && kCols % 64 == 0 && kTmemCols <= 512 && FT % TN == 0, "shape");
 };
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// Adds one to a word of shared memory; what it was.  Ordered as a release and an acquire.
+__device__ __forceinline__ uint32_t count_shared(uint32_t addr) {
+    uint32_t was;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(was) : "r"(addr) : "memory");
+    return was;
+}
 
 struct OrthoTile {
     int step, phase, e, f0, c0;
@@ -383,7 +391,8 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
     const uint32_t bars = patches + S::kPatches;
     const uint32_t full0 = bars, empty0 = bars + 8 * S::kStages;
     const uint32_t acc_full0 = bars + 16 * S::kStages, acc_empty0 = acc_full0 + 16;
-    const uint32_t tmem_slot = bars + 8u * S::kBars;
+    const uint32_t there0 = acc_empty0 + 16, seen0 = there0 + 8 * kOrthoSlots;  // what a tile reads is there; has been read
+    const uint32_t tmem_slot = bars + 8u * S::kBars, finished = tmem_slot + 4;  // finished: warps, by slot
 
     const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = PAIR ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
@@ -398,6 +407,11 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
             mbar_init(acc_empty0 + 8 * b, S::kEpiWarps * CG);
+        }
+        for (int j = 0; j < kOrthoSlots; ++j) {
+            mbar_init(there0 + 8 * j, 1);
+            mbar_init(seen0 + 8 * j, S::kEpiWarps);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(finished + 4 * j), "r"(0) : "memory");
         }
         fence_mbarrier_init();
         prefetch_tensormap(&tm_x0);
@@ -422,13 +436,17 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         const uint32_t bar0 = PAIR ? warp_uniform(map_shared_rank(full0, 0)) : full0;
         const bool issuer = elect_one();
         uint32_t s = 0, phase = 1;  // (the first round finds every stage empty)
-        int issued = 0;
-        for (int i = cluster; i < p.items && !timed_out; i += clusters) {
+        int issued = 0, n = 0;
+        for (int i = cluster; i < p.items && !timed_out; i += clusters, ++n) {
             const OrthoTile t = ortho_tile<S, TALL>(p, i);
-            if (!ortho_wait<S, TALL>(p, t)) {
+            const int slot = n % kOrthoSlots, round = n / kOrthoSlots;
+            if ((round > 0 && !mbar_wait_warp<false>(seen0 + 8 * slot, (round - 1) & 1, 3 * tmo)) ||
+                !ortho_wait<S, TALL>(p, t)) {
                 timed_out = true;
                 break;
             }
+            if (issuer) mbar_arrive(there0 + 8 * slot);
+            __syncwarp();
             fence_proxy_async_global();  // (the copies read what other SMs stored)
             const CUtensorMap* const x = t.step & 1 ? &tm_x1 : &tm_x0;
             const CUtensorMap* const first = t.phase == kOrthoGram ? x : t.phase == kOrthoSquare ? &tm_a : TALL ? x : &tm_p;
@@ -553,13 +571,13 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int q = warp & 3, share = (warp - 2) >> 2;
         const uint32_t acc_empty_lead = PAIR ? warp_uniform(map_shared_rank(acc_empty0, 0)) : acc_empty0;
         const uint32_t patch = patches + (warp - 2) * kGrPatchBytes;
-        int unit = 0;
+        int unit = 0, n = 0;
         auto wait = [&](uint32_t& acc) {
             const int buf = unit & 1;
-            if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, 3 * tmo)) return false;
+            if (!mbar_wait_warp<false>(acc_full0 + 8 * buf, (unit >> 1) & 1, 4 * tmo)) return false;
             tc_fence_after_sync();
             acc = tmem + static_cast<uint32_t>(buf * S::kAccCols) + (static_cast<uint32_t>(32 * q) << 16);
             return true;
@@ -581,7 +599,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
             constexpr int PHASE = decltype(which)::value;
             constexpr bool SYM = PHASE != kOrthoUpdate;
             const int F = SYM ? p.m : p.rows, C = SYM ? p.m : p.cols, K = contraction(PHASE);
-            const int r0 = t.f0 + rank * 128 + 32 * q, c0 = t.c0 + half * S::kWarpCols;  // the warp's first row and column
+            const int r0 = t.f0 + rank * 128 + 32 * q, c0 = t.c0 + share * S::kWarpCols;  // the warp's first row and column
             // Blocks of 32 rows x 32 columns: some are not there, or on the diagonal's other side.
             auto wanted = [&](int c) { return r0 < F && c < C && !(SYM && r0 < c); };
             // While the MMAs run: the first block's planes, the others' to the second-level cache, the diagonals' parts.
@@ -589,8 +607,8 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
             OrthoDiagonal diagonal = {};
             const __half *hi = nullptr, *lo = nullptr;
             const bool mine = r0 + lane < F;
+            if (!mbar_wait_warp<false>(there0 + 8 * (n % kOrthoSlots), (n / kOrthoSlots) & 1, 4 * tmo)) return false;
             if constexpr (PHASE != kOrthoGram) {
-                if (!ortho_wait<S, TALL>(p, t)) return false;
                 const OrthoPlanes& from = PHASE == kOrthoSquare ? p.a : p.x[t.step & 1];
                 const long long at = t.e * from.matrix + (r0 + lane) * from.ld + c0;
                 hi = from.hi + at;
@@ -612,11 +630,10 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                 }
             }
             auto block = [&](int j, float (&v)[32]) {
-                const OrthoState state = next;
                 const int c = c0 + 32 * j;
+                if (wanted(c)) ortho_block<S, TALL, PHASE>(p, patch, t, r0, c, 32 * j, next, diagonal, v);
                 if (PHASE != kOrthoGram && 32 * (j + 1) < S::kWarpCols && wanted(c + 32))
                     next.load(hi + 32 * (j + 1), lo + 32 * (j + 1), mine, mine && c + 48 < C);
-                if (wanted(c)) ortho_block<S, TALL, PHASE>(p, patch, t, r0, c, 32 * j, state, diagonal, v);
             };
             uint32_t acc;
             if constexpr (PARTS == 1) {
@@ -626,7 +643,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                     uint32_t r[32];
                     float v[32];
                     __syncwarp();
-                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(half * S::kWarpCols + 32 * j), r);
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(share * S::kWarpCols + 32 * j), r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int u = 0; u < 32; ++u) v[u] = __uint_as_float(r[u]);
@@ -645,7 +662,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                     for (int j = 0; j < S::kWarpCols / 32; ++j) {
 #pragma unroll
                         for (int h = 0; h < 32; h += 16) {
-                            const uint32_t c = static_cast<uint32_t>(half * S::kWarpCols + 32 * j + h);
+                            const uint32_t c = static_cast<uint32_t>(share * S::kWarpCols + 32 * j + h);
                             uint32_t big[16], small[16];
                             __syncwarp();
                             tmem_ld_32x32b_x16(acc + TN + c, small);
@@ -661,20 +678,23 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < S::kWarpCols / 32; ++j) block(j, sum[j]);
             }
-            // The tile's rows, and those of its mirror image, are one warp nearer.
+            // The CTA's last warp tells those that wait for the tile's rows and for those of its mirror image.
             fence_proxy_async_global();
             __syncwarp();
-            if (lane == 0 && (PHASE != kOrthoUpdate || t.step + 1 < p.steps)) {
-                // kinds: gram finishes A (1), square B (2), update X (0)
-                constexpr int kind = PHASE == kOrthoUpdate ? 0 : PHASE + 1;
-                int* const counter = p.done + (static_cast<long long>(kind) * p.E + t.e) * p.panels;
-                if (SYM) {
+            if (lane == 0) {
+                const int slot = n % kOrthoSlots;
+                if (count_shared(finished + 4 * slot) % S::kEpiWarps == S::kEpiWarps - 1 &&
+                    (PHASE != kOrthoUpdate || t.step + 1 < p.steps)) {
+                    // kinds: gram finishes A (1), square B (2), update X (0)
+                    constexpr int kind = PHASE == kOrthoUpdate ? 0 : PHASE + 1;
+                    int* const counter = p.done + (static_cast<long long>(kind) * p.E + t.e) * p.panels;
                     add_release_gpu(counter + t.need0, 1);
-                    if (t.need1 != t.need0) add_release_gpu(counter + t.need1, 1);
-                } else {
-                    add_release_gpu(counter + t.need0, 1);
+                    if (SYM && t.need1 != t.need0) add_release_gpu(counter + t.need1, 1);
                 }
+                mbar_arrive(seen0 + 8 * slot);  // (after the count: the slot is used again when all have arrived)
             }
+            __syncwarp();
+            ++n;
             return true;
         };
         for (int i = cluster; i < p.items && !timed_out; i += clusters) {
