@@ -23,23 +23,54 @@ __device__ __forceinline__ void load8(const T* p, int left, bool vec, float (&v)
     }
 }
 
-// The sum of eight values' squares.  They are scaled by a power of two that
-// brings the largest near 1, their squares summed in float32, and the sum scaled
-// back in 64 bits: no square overflows or vanishes.
-__device__ __forceinline__ double squares8(const float (&v)[8]) {
+// Eight values each from N places, `step` octs apart from oct `first` on, of rows of `octs` octs (`cols` elements); zeros
+// from oct `n` on.  whole: every oct is a vector (no oct of a row is cut short), and all loads are one without a branch
+// between them (with one, 4 loads of a thread followed one another: 134 MB of bf16 54 us).
+template <int N, typename T>
+__device__ __forceinline__ void load_octs(const T* G, long long ld, int first, int step, int octs, int cols, int n, bool whole,
+                                          bool vec, float (&v)[N][8]) {
+    if (whole) {
+        alignas(16) T x[N][8];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int at = min(first + u * step, n - 1), r = at / octs;
+            const uint4* from = reinterpret_cast<const uint4*>(G + r * ld + (at - r * octs) * 8);
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(x[u])[i] = __ldg(from + i);
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = first + u * step < n ? to_f32(x[u][i]) : 0.f;
+    } else {
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int at = first + u * step, r = at / octs, c = (at - r * octs) * 8;
+            load8(G + r * ld + c, at < n ? cols - c : 0, vec, v[u]);
+        }
+    }
+}
+
+// The sum of the squares of N times eight values.  They are scaled by a power of
+// two that brings the largest near 1, their squares summed in float32, and the sum
+// scaled back in 64 bits: no square overflows or vanishes.  (64 bits run at 2 lanes
+// a cycle of an SM: once in 32 values 8 matrices of 2048 x 4096 bf16 are read at
+// the memory's speed, once in 8 the sums took 50 us.)
+template <int N>
+__device__ __forceinline__ double squares(const float (&v)[N][8]) {
     float most = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));  // (a NaN is passed over here and summed below)
+    for (int i = 0; i < 8 * N; ++i) most = fmaxf(most, fabsf(v[i / 8][i % 8]));  // (a NaN is passed over here and summed below)
     // 2^up brings it to [1, 2) or, from below 2^-126 or above, near that
     const int up = most > 0.f ? min(126, 127 - static_cast<int>(__float_as_uint(most) >> 23)) : 0;
     const float scale = __uint_as_float(static_cast<uint32_t>(max(up, -126) + 127) << 23);
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = v[j] * scale;
+    for (int i = 0; i < 8 * N; ++i) {
+        const float x = v[i / 8][i % 8] * scale;
         s = fmaf(x, x, s);
     }
-    // (s is 0 or above 2^-50, below 2^8, and 2^-2up within a double's range)
+    // (s is 0 or above 2^-50, below 2^10, and 2^-2up within a double's range)
     return s * __longlong_as_double(static_cast<long long>(1023 - 2 * max(up, -126)) << 52);
 }
 

@@ -13,7 +13,7 @@
 namespace gb300 {
 namespace {
 
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 256, kPrepLoads = 4;  // (8 values a load)
 
 // The CTA's sum of `v`, in every thread.
 __device__ __forceinline__ double cta_sum(double v, double* scratch) {
@@ -40,12 +40,11 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const OrthoPre
     const int r0 = chunk * p.per, rows = min(p.per, p.rows - r0);
     const T* G = static_cast<const T*>(p.G) + e * p.sg;
     double sum = 0;
-    const long long n = static_cast<long long>(max(rows, 0)) * octs;
-    for (long long i = threadIdx.x; i < n; i += kPrepThreads) {
-        const int r = static_cast<int>(i / octs), c = static_cast<int>(i - static_cast<long long>(r) * octs) * 8;
-        float v[8];
-        load8(G + (r0 + r) * p.ldg + c, p.cols - c, p.vec, v);
-        sum += squares8(v);
+    const int n = max(rows, 0) * octs;
+    for (int i = threadIdx.x; i < n; i += kPrepLoads * kPrepThreads) {
+        float v[kPrepLoads][8];
+        load_octs(G + r0 * p.ldg, p.ldg, i, kPrepThreads, octs, p.cols, n, p.vec && p.cols % 8 == 0, p.vec, v);
+        sum += squares(v);
     }
     sum = cta_sum(sum, scratch);
     if (threadIdx.x == 0) p.part[static_cast<long long>(e) * p.chunks + chunk] = sum;
@@ -63,16 +62,21 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_split_kernel(const OrthoPr
     const int octs = (p.cols + 7) / 8;
     const int r0 = chunk * p.per, rows = min(p.per, p.rows - r0);
     const T* G = static_cast<const T*>(p.G) + e * p.sg;
-    const long long n = static_cast<long long>(max(rows, 0)) * octs;
-    for (long long i = threadIdx.x; i < n; i += kPrepThreads) {
-        const int r = static_cast<int>(i / octs), c = static_cast<int>(i - static_cast<long long>(r) * octs) * 8;
-        float v[8];
-        load8(G + (r0 + r) * p.ldg + c, p.cols - c, p.vec, v);
-        uint4 hi, lo;
-        scale.split(v, hi, lo);
-        uint16_t* d = p.hi + (static_cast<long long>(e) * p.rows + r0 + r) * p.pitch + c;
-        *reinterpret_cast<uint4*>(d) = hi;
-        *reinterpret_cast<uint4*>(d + p.plane) = lo;
+    const int n = max(rows, 0) * octs;
+    uint16_t* const to = p.hi + (static_cast<long long>(e) * p.rows + r0) * p.pitch;
+    for (int i = threadIdx.x; i < n; i += kPrepLoads * kPrepThreads) {
+        float v[kPrepLoads][8];
+        load_octs(G + r0 * p.ldg, p.ldg, i, kPrepThreads, octs, p.cols, n, p.vec && p.cols % 8 == 0, p.vec, v);
+#pragma unroll
+        for (int u = 0; u < kPrepLoads; ++u) {
+            const int at = i + u * kPrepThreads, r = at / octs, c = (at - r * octs) * 8;
+            if (at >= n) break;
+            uint4 hi, lo;
+            scale.split(v[u], hi, lo);
+            uint16_t* const d = to + r * p.pitch + c;
+            *reinterpret_cast<uint4*>(d) = hi;
+            *reinterpret_cast<uint4*>(d + p.plane) = lo;
+        }
     }
 }
 

@@ -161,11 +161,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
     const T* const G = static_cast<const T*>(p.G) + e * p.sg + (TALL ? n0 * p.ldg : n0);
     const int grows = TALL ? cols : p.m, gcols = TALL ? p.m : cols, octs = (gcols + 7) / 8;
     double sum = 0;
-    for (int i = threadIdx.x; i < grows * octs; i += kSmallThreads) {
-        const int r = i / octs, c = (i - r * octs) * 8;
-        float v[8];
-        load8(G + r * p.ldg + c, gcols - c, p.vec, v);
-        sum += squares8(v);
+    constexpr int kLoads = 4;  // (before the first use)
+    for (int i = threadIdx.x; i < grows * octs; i += kLoads * kSmallThreads) {
+        float v[kLoads][8];
+        load_octs(G, p.ldg, i, kSmallThreads, octs, gcols, grows * octs, p.vec && gcols % 8 == 0, p.vec, v);
+        sum += squares(v);
     }
 #pragma unroll
     for (int s = 16; s; s /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, s);

@@ -24,21 +24,21 @@ int encode_planes(CUtensorMap* map, const void* p, long long inner, long long ro
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
 
-template <int TN, int CG, int PARTS, bool TALL>
+template <int TN, int PARTS, bool TALL>
 int set_up() {
-    return cudaFuncSetAttribute(ortho_tc_kernel<TN, CG, PARTS, TALL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                OrthoShape<TN, CG, PARTS>::kSmem) == cudaSuccess
+    return cudaFuncSetAttribute(ortho_tc_kernel<TN, PARTS, TALL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                OrthoShape<TN, PARTS>::kSmem) == cudaSuccess
                ? SGEMM_OK
                : SGEMM_ERR_CUDA;
 }
 
-template <int TN, int CG, int PARTS>
+template <int TN, int PARTS>
 int set_up_both() {
-    return set_up<TN, CG, PARTS, false>() || set_up<TN, CG, PARTS, true>();
+    return set_up<TN, PARTS, false>() || set_up<TN, PARTS, true>();
 }
 
 int set_up_kernels() {
-    if (set_up_both<256, 2, 1>() || set_up_both<128, 1, 1>() || set_up_both<128, 2, 2>() || set_up_both<128, 1, 2>()) {
+    if (set_up_both<256, 1>() || set_up_both<128, 1>() || set_up_both<128, 2>()) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -53,9 +53,9 @@ struct Workspace {
     }
 };
 
-template <int TN, int CG, int PARTS>
+template <int TN, int PARTS>
 int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st, cudaStream_t s) {
-    using S = OrthoShape<TN, CG, PARTS>;
+    using S = OrthoShape<TN, PARTS>;
     const bool tall = p.rows > p.cols;
     const long long ft = ceil_div(p.m, S::FT), ct = ceil_div(p.m, TN);
     long long sym = 0;
@@ -65,7 +65,7 @@ int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st
     if (items > 0x7fffffffll - 65536) return SGEMM_ERR_INVALID_ARG;
     p.sym_tiles = static_cast<int>(sym), p.up_tiles = static_cast<int>(up), p.items = static_cast<int>(items);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(CG * std::min<long long>(most, CG == 2 ? st.max_pairs : st.sm_count)));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(most, st.max_pairs)));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -73,11 +73,11 @@ int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st
     attr[0].id = cudaLaunchAttributeCooperative;  // tiles wait for those of other CTAs
     attr[0].val.cooperative = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
-    const auto kernel = tall ? ortho_tc_kernel<TN, CG, PARTS, true> : ortho_tc_kernel<TN, CG, PARTS, false>;
+    cfg.numAttrs = 2;
+    const auto kernel = tall ? ortho_tc_kernel<TN, PARTS, true> : ortho_tc_kernel<TN, PARTS, false>;
     if (cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
@@ -104,7 +104,7 @@ int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s) 
     prep.chunks = static_cast<int>(ceil_div(c.M, prep.per));
     if (static_cast<long long>(c.E) * prep.chunks > 0x7fffffffll) return SGEMM_ERR_INVALID_ARG;
     auto whole = [](long long bytes) { return (bytes + 255) / 256 * 256; };
-    const int panels = static_cast<int>(ceil_div(m, 128));  // (of 128 or 256 rows)
+    const int panels = static_cast<int>(ceil_div(m, 256));
     const long long xb = whole(2ll * 2 * c.E * c.M * pitch), ab = whole(2ll * 2 * c.E * m * mp);
     const long long db = whole(4ll * c.E * mp), pb = whole(8ll * c.E * prep.chunks), nb = whole(4ll * 3 * c.E * panels);
     Workspace ws;
@@ -158,13 +158,14 @@ int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s) 
     prep.hi = reinterpret_cast<uint16_t*>(p.x[0].hi), prep.pitch = pitch, prep.plane = static_cast<long long>(c.E) * c.M * pitch;
     const int rc = ortho_prepare(prep, c.type, s);
     if (rc != SGEMM_OK) return rc;
-    // Pairs of CTAs where their tiles are half as many as the pairs at least, else
-    // single CTAs with tiles of 128 x 128.
-    const long long wide = parts == 1 ? 256 : 128;
-    const long long tiles = c.E * ceil_div(c.M, wide) * ceil_div(c.N, 256);
-    const bool pairs = 2 * tiles >= st.max_pairs;
-    if (parts == 1) return pairs ? launch<256, 2, 1>(p, maps, st, s) : launch<128, 1, 1>(p, maps, st, s);
-    return pairs ? launch<128, 2, 2>(p, maps, st, s) : launch<128, 1, 2>(p, maps, st, s);
+    // Tiles of a pair of CTAs: 256 rows by 128 columns; bf16 256 where the GPU's pairs then have two and a half each in an update.
+    // Measured, us for 256 columns / 128 / single CTAs with 128 x 128 (bf16): 512 x 512 173 / 110 / 112, 1024 x 1024
+    // 213 / 135 / 136, 8 of 200 x 4000 232 / 186 / 198, 2048 x 4096 406 / 338 / 354 (128 tiles of 256 columns, 76 pairs),
+    // 2 of 3000 x 3000 (288) 768 / 897 / 942.  float32, two planes of either operand, 128 columns of a pair / single
+    // CTAs: 200 x 300 122 / 125, 2048 x 2048 420 / 445, 2 of 3000 x 3000 2178 / 2492.
+    if (parts == 2) return launch<128, 2>(p, maps, st, s);
+    const long long tiles = c.E * ceil_div(c.M, 256) * ceil_div(c.N, 256);
+    return 2 * tiles >= 5 * st.max_pairs ? launch<256, 1>(p, maps, st, s) : launch<128, 1>(p, maps, st, s);
 }
 
 }  // namespace detail

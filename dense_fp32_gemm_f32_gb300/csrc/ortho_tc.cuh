@@ -30,8 +30,8 @@
 // A and B are symmetric: only tiles that reach the diagonal or lie on its one
 // side are computed, and every 32 x 32 block off it is stored twice.
 //
-// All steps are one launch.  Its CTAs (or CTA pairs) are resident together (a
-// cooperative launch) and take the output tiles of all products in one order,
+// All steps are one launch.  Its CTA pairs are resident together (a cooperative
+// launch) and take the output tiles of all products in one order,
 // every P-th each; a tile waits until the row panels that it reads are there:
 //
 //   gram tile (i, j)       rows i and j of X           (panels of FT rows)
@@ -89,14 +89,16 @@ struct OrthoTcParams {
 constexpr int kOrthoChunk = 512;  // contraction in one accumulator, with two planes
 constexpr int kOrthoSlots = 4;    // tiles that the load warp tells the epilogue warps about ahead
 
-template <int TN_, int CG_, int PARTS_>
+template <int TN_, int PARTS_>
 struct OrthoShape {
-    static constexpr int TN = TN_, CG = CG_, PARTS = PARTS_;
-    static constexpr int FT = 128 * CG, R = FT / TN;  // a tile's rows; column tiles of a panel
-    static constexpr int kCols = TN / CG;
+    static constexpr int TN = TN_, PARTS = PARTS_;
+    static constexpr int FT = 256, R = FT / TN;  // a tile's rows; column tiles of a panel
+    static constexpr int kCols = TN / 2;         // of a CTA
     static constexpr int kABytes = 128 * 128, kBBytes = kCols * 128;  // of a part, 64 of the contraction
     static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
-    static constexpr int kEpiWarps = 16;
+    // Measured, 8 and 16 warps (168 and 96 registers a thread): tiles of 256 columns, 8 x 2048 x 4096 bf16 1740 and 1880
+    // us; of 128 columns and two planes, 4 x 2048 x 2048 float32 1470 and 1415 us.
+    static constexpr int kEpiWarps = TN == 256 ? 8 : 16;
     static constexpr int kThreads = 32 * (2 + kEpiWarps);
     // (the widest tile has a seventh stage instead of patches for results off the 16-byte grid)
     static constexpr bool kPatched = !(TN == 256 && PARTS == 1);
@@ -106,7 +108,7 @@ struct OrthoShape {
     static constexpr int kBars = 2 * kStages + 4 + 2 * kOrthoSlots;
     static constexpr int kSmem = kStages * kStageBytes + kPatches + 8 * kBars + 32 + 1024;
     static constexpr int kWarpCols = TN / (kEpiWarps / 4);  // an epilogue warp's columns
-    static constexpr int kDone = CG;                        // what a tile adds to a panel's counter
+    static constexpr int kDone = 2;                         // what a tile's CTAs add to a panel's counter
     static_assert(kSmem <= 227 * 1024 && kStages >= 2 && kCols % 64 == 0 && kTmemCols <= 512 && FT % TN == 0, "shape");
 };
 
@@ -377,13 +379,12 @@ __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t pat
     }
 }
 
-template <int TN, int CG, int PARTS, bool TALL>
-__global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
+template <int TN, int PARTS, bool TALL>
+__global__ void __launch_bounds__(OrthoShape<TN, PARTS>::kThreads, 1)
     ortho_tc_kernel(const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_x1,
                     const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_p,
                     const OrthoTcParams p) {
-    using S = OrthoShape<TN, CG, PARTS>;
-    constexpr bool PAIR = CG == 2;
+    using S = OrthoShape<TN, PARTS>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t baseB = base + PARTS * S::kABytes;  // the second operand's parts follow the first's in a stage
@@ -395,8 +396,8 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
     const uint32_t tmem_slot = bars + 8u * S::kBars, finished = tmem_slot + 4;  // finished: warps, by slot
 
     const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const int rank = PAIR ? warp_uniform(static_cast<int>(cluster_ctarank())) : 0;
-    const int cluster = static_cast<int>(blockIdx.x) / CG, clusters = static_cast<int>(gridDim.x) / CG;
+    const int rank = warp_uniform(static_cast<int>(cluster_ctarank()));
+    const int cluster = static_cast<int>(blockIdx.x) / 2, clusters = static_cast<int>(gridDim.x) / 2;
     const unsigned long long tmo = p.timeout_ns;
 
     if (threadIdx.x == 0) {
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, S::kEpiWarps * CG);
+            mbar_init(acc_empty0 + 8 * b, 2 * S::kEpiWarps);
         }
         for (int j = 0; j < kOrthoSlots; ++j) {
             mbar_init(there0 + 8 * j, 1);
@@ -420,10 +421,10 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         prefetch_tensormap(&tm_p);
     }
     __syncwarp();
-    if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, S::kTmemCols);
+    if (warp == 1) tmem_alloc_cg<2>(tmem_slot, S::kTmemCols);
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();  // the peer's barriers are ready
+    cluster_sync_all();  // the peer's barriers are ready
     tc_fence_after_sync();
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
     bool timed_out = false;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        const uint32_t bar0 = PAIR ? warp_uniform(map_shared_rank(full0, 0)) : full0;
+        const uint32_t bar0 = warp_uniform(map_shared_rank(full0, 0));
         const bool issuer = elect_one();
         uint32_t s = 0, phase = 1;  // (the first round finds every stage empty)
         int issued = 0, n = 0;
@@ -462,13 +463,10 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                 const uint32_t a = base + s * S::kStageBytes, b = baseB + s * S::kStageBytes;
                 if (issuer) {
                     const uint32_t bar = bar0 + 8 * s;
-                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, CG * S::kStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * S::kStageBytes);
                     auto load = [&](uint32_t dst, const CUtensorMap* map, bool mn, int at, int z) {
                         const int x0 = mn ? at : k, y0 = mn ? k : at;
-                        if constexpr (PAIR)
-                            tma_load_3d_pair(dst, map, bar, x0, y0, z);
-                        else
-                            tma_load_3d(dst, map, bar, x0, y0, z);
+                        tma_load_3d_pair(dst, map, bar, x0, y0, z);
                     };
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
@@ -499,8 +497,8 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
         // ------------------------------------------------------------ MMAs
         if (rank == 0) {  // (the first CTA issues for both)
             constexpr uint32_t pa = S::kABytes / 16, pb = S::kBBytes / 16;
-            const uint32_t peer_empty0 = PAIR ? warp_uniform(map_shared_rank(empty0, 1)) : 0;
-            const uint32_t peer_acc_full0 = PAIR ? warp_uniform(map_shared_rank(acc_full0, 1)) : 0;
+            const uint32_t peer_empty0 = warp_uniform(map_shared_rank(empty0, 1));
+            const uint32_t peer_acc_full0 = warp_uniform(map_shared_rank(acc_full0, 1));
             const bool issuer = elect_one();
             uint32_t s = 0, phase = 0;
             int unit = 0;  // accumulators filled
@@ -517,7 +515,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                     const int buf = unit & 1;
                     const uint32_t acc = tmem + static_cast<uint32_t>(buf * S::kAccCols);
                     const int end = PARTS > 1 ? min(K, k + kOrthoChunk) : K;
-                    if (unit >= 2 && !mbar_wait_warp<PAIR>(acc_empty0 + 8 * buf, ((unit >> 1) - 1) & 1, tmo)) {
+                    if (unit >= 2 && !mbar_wait_warp<true>(acc_empty0 + 8 * buf, ((unit >> 1) - 1) & 1, tmo)) {
                         timed_out = true;
                         break;
                     }
@@ -537,15 +535,15 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                             for (int kk = 0; kk < kGrBK / 16; ++kk) {
                                 if (left > kk * 16) {  // (what lies past the contraction's end is zeros)
                                     const bool add = q > k || kk > 0;
-                                    umma_f16<CG>(acc, a + kk * ka, b + kk * kb, idesc, add);
+                                    umma_f16<2>(acc, a + kk * ka, b + kk * kb, idesc, add);
                                     if constexpr (PARTS == 2) {
-                                        umma_f16<CG>(acc + TN, a + kk * ka, b + pb + kk * kb, idesc, add);
-                                        umma_f16<CG>(acc + TN, a + pa + kk * ka, b + kk * kb, idesc, true);
+                                        umma_f16<2>(acc + TN, a + kk * ka, b + pb + kk * kb, idesc, add);
+                                        umma_f16<2>(acc + TN, a + pa + kk * ka, b + kk * kb, idesc, true);
                                     }
                                 }
                             }
-                            umma_commit_cg<CG>(empty0 + 8 * s);
-                            if constexpr (PAIR) umma_commit_cg<CG>(peer_empty0 + 8 * s);
+                            umma_commit_cg<2>(empty0 + 8 * s);
+                            umma_commit_cg<2>(peer_empty0 + 8 * s);
                         }
                         __syncwarp();
                         if (++s == S::kStages) {
@@ -555,8 +553,8 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                     }
                     if (timed_out) break;
                     if (issuer) {
-                        umma_commit_cg<CG>(acc_full0 + 8 * buf);
-                        if constexpr (PAIR) umma_commit_cg<CG>(peer_acc_full0 + 8 * buf);
+                        umma_commit_cg<2>(acc_full0 + 8 * buf);
+                        umma_commit_cg<2>(peer_acc_full0 + 8 * buf);
                     }
                     __syncwarp();
                     ++unit;
@@ -564,7 +562,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                 }
             }
             if (timed_out) {  // the MMAs in flight end before tensor memory is freed
-                if (issuer) umma_commit_cg<CG>(acc_full0 + 8 * (unit & 1));
+                if (issuer) umma_commit_cg<2>(acc_full0 + 8 * (unit & 1));
                 __syncwarp();
                 (void)mbar_wait_warp<false>(acc_full0 + 8 * (unit & 1), (unit >> 1) & 1, tmo);
             }
@@ -572,7 +570,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3, share = (warp - 2) >> 2;
-        const uint32_t acc_empty_lead = PAIR ? warp_uniform(map_shared_rank(acc_empty0, 0)) : acc_empty0;
+        const uint32_t acc_empty_lead = warp_uniform(map_shared_rank(acc_empty0, 0));
         const uint32_t patch = patches + (warp - 2) * kGrPatchBytes;
         int unit = 0, n = 0;
         auto wait = [&](uint32_t& acc) {
@@ -586,7 +584,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (!PAIR || rank == 0)
+                if (rank == 0)
                     mbar_arrive(acc_empty0 + 8 * (unit & 1));
                 else
                     mbar_arrive_cluster_relaxed(acc_empty_lead + 8 * (unit & 1));
@@ -602,7 +600,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
             const int r0 = t.f0 + rank * 128 + 32 * q, c0 = t.c0 + share * S::kWarpCols;  // the warp's first row and column
             // Blocks of 32 rows x 32 columns: some are not there, or on the diagonal's other side.
             auto wanted = [&](int c) { return r0 < F && c < C && !(SYM && r0 < c); };
-            // While the MMAs run: the first block's planes, the others' to the second-level cache, the diagonals' parts.
+            // While the MMAs run: the first block's planes, the diagonals' parts.
             OrthoState next = {};
             OrthoDiagonal diagonal = {};
             const __half *hi = nullptr, *lo = nullptr;
@@ -615,15 +613,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
                 lo = from.lo + at;
                 const float* const d = (PHASE == kOrthoSquare ? p.d : p.e) + t.e * p.diag;
                 if (wanted(c0)) next.load(hi, lo, mine, mine && c0 + 16 < C);
-                if (mine) {
-                    if (PHASE == kOrthoSquare || !TALL) diagonal.row = __ldcg(d + r0 + lane);
-#pragma unroll
-                    for (int j = 32; j < S::kWarpCols; j += 32)
-                        if (wanted(c0 + j)) {
-                            prefetch_l2(hi + j);
-                            prefetch_l2(lo + j);
-                        }
-                }
+                if (mine && (PHASE == kOrthoSquare || !TALL)) diagonal.row = __ldcg(d + r0 + lane);
                 if ((PHASE == kOrthoSquare || TALL) && 4 * lane < S::kWarpCols && c0 + 4 * lane < C) {
                     const float4 x = __ldcg(reinterpret_cast<const float4*>(d + c0) + lane);
                     diagonal.column[0] = x.x, diagonal.column[1] = x.y, diagonal.column[2] = x.z, diagonal.column[3] = x.w;
@@ -709,11 +699,11 @@ __global__ void __launch_bounds__(OrthoShape<TN, CG, PARTS>::kThreads, 1)
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();  // nothing of the peer's is under way in this CTA's memory
+    cluster_sync_all();  // nothing of the peer's is under way in this CTA's memory
     __syncwarp();
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc_cg<CG>(tmem, S::kTmemCols);
+        tmem_dealloc_cg<2>(tmem, S::kTmemCols);
     }
 }
 
