@@ -58,8 +58,12 @@ int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st
     using S = OrthoShape<TN, PARTS>;
     const bool tall = p.rows > p.cols;
     const long long ft = ceil_div(p.m, S::FT), ct = ceil_div(p.m, TN);
-    long long sym = 0;
-    for (long long f = 0; f < ft; ++f) sym += std::min(ct, (f + 1) * S::R);
+    long long sym = ft * ct;
+    p.mirror = p.E * sym > st.max_pairs || ft > 32;
+    if (p.mirror) {
+        sym = 0;
+        for (long long f = 0; f < ft; ++f) sym += std::min(ct, (f + 1) * S::R);
+    }
     const long long up = ceil_div(p.rows, S::FT) * ceil_div(p.cols, TN), most = p.E * std::max(sym, up);
     const long long items = p.steps * p.E * (2 * sym + up);
     if (items > 0x7fffffffll - 65536) return SGEMM_ERR_INVALID_ARG;

@@ -27,8 +27,10 @@
 // (the entry refuses polynomials that go beyond) make elements up to 2^14, 2^14
 // and 15 * 2^12, below f16's largest.
 //
-// A and B are symmetric: only tiles that reach the diagonal or lie on its one
-// side are computed, and every 32 x 32 block off it is stored twice.
+// A and B are symmetric: where there are more tiles than the GPU's pairs of CTAs,
+// only those that reach the diagonal or lie on its one side are computed, and every
+// 32 x 32 block off it is stored twice.  (Where there are fewer, the second
+// store, 2 bytes a lane, is the longer way: 129 x 129 bf16 79 us with it.)
 //
 // All steps are one launch.  Its CTA pairs are resident together (a cooperative
 // launch) and take the output tiles of all products in one order,
@@ -73,6 +75,7 @@ struct OrthoTcParams {
     int E, m, rows, cols;     // X as stored: rows x cols, m the shorter
     int steps, items;         // output tiles in all
     int sym_tiles, up_tiles;  // of a matrix: gram or square, update
+    int mirror;               // gram and square: tiles on one side of the diagonal alone, stored twice
     OrthoPlanes x[2], a, p;   // X (by turns), A and B less their diagonals
     float *d, *e;             // the diagonals of A and B, `diag` (a multiple of 16) a matrix
     long long diag;
@@ -143,7 +146,10 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoTcParams& p, int i) {
         local -= t.e * p.sym_tiles;
         const int ft = div_up(p.m, S::FT), ct = div_up(p.m, S::TN);
         int f = 0, c;
-        if (t.phase == kOrthoGram) {
+        if (!p.mirror) {
+            f = local / ct;
+            c = local - f * ct;
+        } else if (t.phase == kOrthoGram) {
             while (true) {
                 const int n = min(ct, (f + 1) * S::R);
                 if (local < n) break;
@@ -197,16 +203,20 @@ __device__ __forceinline__ int ortho_needed(const OrthoTcParams& p, const OrthoT
     const int width = min(S::R, ct - q * S::R);  // column tiles of the panel
     if (t.phase == kOrthoGram)  // X, of the step before
         return t.step * S::kDone * (TALL ? div_up(p.rows, S::FT) * width : div_up(p.cols, S::TN));
-    return (t.step + 1) * S::kDone * (min(ct, (q + 1) * S::R) + (ft - 1 - q) * width);
+    return (t.step + 1) * S::kDone * (p.mirror ? min(ct, (q + 1) * S::R) + (ft - 1 - q) * width : ct);
 }
 
-// Whole warp: waits until the panels that tile t reads are there.
+// Whole warp: waits until the panels that tile t reads are there.  Without
+// mirrored tiles a gram tile waits for all of X (at most 32 panels; the host sees
+// to it): it overwrites rows of A that square tiles of other panels have read.
 template <typename S, bool TALL>
 __device__ __forceinline__ bool ortho_wait(const OrthoTcParams& p, const OrthoTile& t) {
-    const int lane = threadIdx.x & 31, q = lane == 0 ? t.need0 : t.need1;
+    const int lane = threadIdx.x & 31;
+    const bool all = !p.mirror && t.phase == kOrthoGram;
+    const int q = all ? min(lane, p.panels - 1) : lane == 0 ? t.need0 : t.need1;
     const int* counter = p.done + (static_cast<long long>(t.phase) * p.E + t.e) * p.panels + q;
     const int needed = ortho_needed<S, TALL>(p, t, q);
-    auto ready = [&] { return __all_sync(0xffffffffu, lane > 1 || load_acquire_gpu(counter) >= needed) != 0; };
+    auto ready = [&] { return __all_sync(0xffffffffu, (lane > 1 && !all) || load_acquire_gpu(counter) >= needed) != 0; };
     uint64_t t0 = 0;
     while (!ready()) {
         const uint64_t now = global_timer_ns();
@@ -367,7 +377,7 @@ __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t pat
             store_half16(at, w);
             if (c + 16 < C) store_half16(at + 16, w + 8);
         }
-        if (SYM && !diagonal && row < F) {
+        if (SYM && p.mirror && !diagonal && row < F) {
             // The block's mirror image: rows are columns, a value a lane.
             uint16_t* at = reinterpret_cast<uint16_t*>(plane + c * to.ld + row);
 #pragma unroll
@@ -599,7 +609,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, PARTS>::kThreads, 1)
             const int F = SYM ? p.m : p.rows, C = SYM ? p.m : p.cols, K = contraction(PHASE);
             const int r0 = t.f0 + rank * 128 + 32 * q, c0 = t.c0 + share * S::kWarpCols;  // the warp's first row and column
             // Blocks of 32 rows x 32 columns: some are not there, or on the diagonal's other side.
-            auto wanted = [&](int c) { return r0 < F && c < C && !(SYM && r0 < c); };
+            auto wanted = [&](int c) { return r0 < F && c < C && !(SYM && p.mirror && r0 < c); };
             // While the MMAs run: the first block's planes, the diagonals' parts.
             OrthoState next = {};
             OrthoDiagonal diagonal = {};
@@ -679,7 +689,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, PARTS>::kThreads, 1)
                     constexpr int kind = PHASE == kOrthoUpdate ? 0 : PHASE + 1;
                     int* const counter = p.done + (static_cast<long long>(kind) * p.E + t.e) * p.panels;
                     add_release_gpu(counter + t.need0, 1);
-                    if (SYM && t.need1 != t.need0) add_release_gpu(counter + t.need1, 1);
+                    if (SYM && p.mirror && t.need1 != t.need0) add_release_gpu(counter + t.need1, 1);
                 }
                 mbar_arrive(seen0 + 8 * slot);  // (after the count: the slot is used again when all have arrived)
             }
