@@ -82,7 +82,8 @@ SIGNATURES = {
     "sgemm_spread": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _i, _p, _p, _i64, _p]),
     "sgemm_combine": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _p, _p, _i64, _p]),
     "sgemm_combine_grad": (_i, [_i, _i, _i, _i, _i, _p, _i64, _p, _i64, _p, _p, _i, _p, _p, _i64, _p, _p]),
-    "sgemm_orthogonalize": (_i, [_i, _i, _i, _i, _p, _i64, _i64, _i, ctypes.c_float, ctypes.c_float, ctypes.c_float, _d, _p, _i64, _i64, _p]),
+    "sgemm_orthogonalize": (_i, [_i, _i, _i, _i, _p, _i64, _i64, _i, ctypes.c_float, ctypes.c_float, ctypes.c_float, _d, _p, _i64, _i64, _p, _i64, _p]),
+    "sgemm_orthogonalize_workspace": (_i64, [_i, _i, _i, _i, _i]),
     "sgemm_bench_fma_peak": (_i, [_i, _i, _i, _p, _p, ctypes.POINTER(_d)]),
     "sgemm_bench_copy": (_i, [_p, _p, ctypes.c_longlong, _i, _p]),
 }

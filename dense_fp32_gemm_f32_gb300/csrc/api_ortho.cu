@@ -54,24 +54,38 @@ bool polynomial_ok(int steps, double a, double b, double c) {
     return true;
 }
 
+// Sizes that the workspace's size fits.
+bool sizes_ok(int type, int E, int M, int N, int steps) {
+    if (!type_ok(type) || E < 0 || M < 0 || N < 0 || E > kMost || M > kMost || N > kMost || steps < 1 || steps > 64)
+        return false;
+    constexpr int64_t most = int64_t{1} << 46;  // elements
+    return N == 0 || E == 0 || (M <= most / N && static_cast<int64_t>(M) * N <= most / E);
+}
+
 }  // namespace
+
+extern "C" int64_t sgemm_orthogonalize_workspace(int type, int E, int M, int N, int steps) {
+    if (!sizes_ok(type, E, M, N, steps)) return -1;
+    if (E == 0 || M == 0 || N == 0 || ortho_always_small(M, N)) return 0;
+    return ortho_layout(E, M, N, steps).bytes;
+}
 
 extern "C" int sgemm_orthogonalize(int type, int E, int M, int N, const void* G, int64_t ldg, int64_t stride_g, int steps,
                                    float a, float b, float c, double eps, void* out, int64_t ldo, int64_t stride_out,
-                                   void* stream) {
-    if (!type_ok(type) || E < 0 || M < 0 || N < 0 || E > kMost || M > kMost || N > kMost) return SGEMM_ERR_INVALID_ARG;
-    if (steps < 1 || steps > 64 || !(eps >= 0) || !std::isfinite(eps) || !polynomial_ok(steps, a, b, c))
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!sizes_ok(type, E, M, N, steps) || !(eps >= 0) || !std::isfinite(eps) || !polynomial_ok(steps, a, b, c))
         return SGEMM_ERR_INVALID_ARG;
     const int size = type_bytes(type);
     const View g{G, E, M, N, ldg, stride_g, size}, o{out, E, M, N, ldo, stride_out, size};
     if (!g.ok(size) || !o.ok(size) || overlap(g, o)) return SGEMM_ERR_INVALID_ARG;
     if (o.empty()) return SGEMM_OK;
-    constexpr int64_t most = int64_t{1} << 46;  // elements: what the workspace's size fits
-    if (static_cast<int64_t>(M) > most / N || static_cast<int64_t>(M) * N > most / E) return SGEMM_ERR_INVALID_ARG;
+    const int64_t needed = sgemm_orthogonalize_workspace(type, E, M, N, steps);
+    const View ws{workspace, 1, 1, needed, needed, 0, 1};
+    if (workspace_bytes < needed || !ws.ok(256) || overlap(ws, g) || overlap(ws, o)) return SGEMM_ERR_INVALID_ARG;
     int dev = 0;
     DeviceState* st = nullptr;
     const int rc = experts_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
-    const OrthoCall call = {G, ldg, stride_g, out, ldo, stride_out, type, E, M, N, steps, a, b, c, eps};
-    return orthogonalize(call, dev, *st, static_cast<cudaStream_t>(stream));
+    const OrthoCall call = {G, ldg, stride_g, out, ldo, stride_out, type, E, M, N, steps, a, b, c, eps, workspace};
+    return orthogonalize(call, *st, static_cast<cudaStream_t>(stream));
 }

@@ -38,8 +38,20 @@ struct OrthoCall {
     int type, E, M, N, steps;
     float a, b, c;
     double eps;
+    void* workspace;
 };
-int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s);
+// The workspace's parts, in bytes from its beginning.
+struct OrthoLayout {
+    int chunks, per, panels;       // of the preparation and of the counters
+    long long pitch, square_pitch;  // elements a row of X's planes and of A's
+    long long part, done, d, e, a, p, x[2], bytes;
+};
+OrthoLayout ortho_layout(int E, int M, int N, int steps);
+int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s);
+// Whether every device takes the call in its small form, which needs no workspace.
+inline bool ortho_always_small(int M, int N) {
+    return (M < N ? M : N) <= 128 && (M < N ? N : M) <= 8 * 256;
+}
 // A short side of up to 128 (ortho_small.cu); SGEMM_ERR_UNSUPPORTED: not one of these.
 int ortho_small_set_up(int* most_ctas);
 int ortho_small(const OrthoCall& c, const DeviceState& st, cudaStream_t s);

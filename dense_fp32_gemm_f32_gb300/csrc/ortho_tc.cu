@@ -1,5 +1,5 @@
-// Launches of an orthogonalised update: workspace, tensor maps, tile shape
-// (ortho_tc.cuh).
+// Launches of an orthogonalised update: the workspace's parts, tensor maps, tile
+// shape (ortho_tc.cuh).
 #include "../../include/sgemm_ortho.h"
 #include "ortho_tc.cuh"
 
@@ -45,14 +45,6 @@ int set_up_kernels() {
     return SGEMM_OK;
 }
 
-struct Workspace {
-    void* p = nullptr;
-    cudaStream_t s = nullptr;
-    ~Workspace() {
-        if (p) (void)cudaFreeAsync(p, s);
-    }
-};
-
 template <int TN, int PARTS>
 int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st, cudaStream_t s) {
     using S = OrthoShape<TN, PARTS>;
@@ -91,58 +83,60 @@ int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st
 
 }  // namespace
 
-int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s) {
+OrthoLayout ortho_layout(int E, int M, int N, int steps) {
+    const long long m = std::min(M, N);
+    OrthoLayout l = {};
+    l.pitch = (N + 15ll) / 16 * 16, l.square_pitch = (m + 15) / 16 * 16;  // (the epilogue's accesses of 32 bytes)
+    // Row chunks of about 8192 elements, a few rounds of the GPU at most.
+    l.chunks = static_cast<int>(std::max(1ll, std::min({static_cast<long long>(kOrthoMostChunks), static_cast<long long>(M),
+                                                        M * l.pitch / 8192})));
+    l.per = static_cast<int>(ceil_div(M, l.chunks));
+    l.chunks = static_cast<int>(ceil_div(M, l.per));
+    l.panels = static_cast<int>(ceil_div(m, 256));
+    auto take = [&](long long bytes) {
+        const long long at = l.bytes;
+        l.bytes += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    l.part = take(8ll * E * l.chunks);
+    l.done = take(4ll * 3 * E * l.panels);
+    l.d = take(4ll * E * l.square_pitch);
+    l.e = take(4ll * E * l.square_pitch);
+    l.a = take(2ll * 2 * E * m * l.square_pitch);
+    l.p = take(2ll * 2 * E * m * l.square_pitch);
+    l.x[0] = take(2ll * 2 * E * M * l.pitch);
+    l.x[1] = steps > 1 ? take(2ll * 2 * E * M * l.pitch) : l.x[0];
+    return l;
+}
+
+int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     std::call_once(st.ortho_once, [&] {
         st.ortho_status = set_up_kernels() != SGEMM_OK ? SGEMM_ERR_CUDA : ortho_small_set_up(&st.ortho_ctas);
     });
     if (st.ortho_status != SGEMM_OK) return st.ortho_status;
     if (const int rc = ortho_small(c, st, s); rc != SGEMM_ERR_UNSUPPORTED) return rc;
-    const int m = std::min(c.M, c.N);
-    const long long pitch = (c.N + 15ll) / 16 * 16, mp = (m + 15ll) / 16 * 16;  // (the epilogue's accesses of 32 bytes)
-    const int parts = c.type == SGEMM_TYPE_BF16 ? 1 : 2;
-    // Row chunks of about 8192 elements, a few rounds of the GPU at most.
-    OrthoPrep prep = {};
-    prep.chunks = static_cast<int>(std::max(1ll, std::min({static_cast<long long>(kOrthoMostChunks), static_cast<long long>(c.M),
-                                                           static_cast<long long>(c.M) * pitch / 8192})));
-    prep.per = static_cast<int>(ceil_div(c.M, prep.chunks));
-    prep.chunks = static_cast<int>(ceil_div(c.M, prep.per));
-    if (static_cast<long long>(c.E) * prep.chunks > 0x7fffffffll) return SGEMM_ERR_INVALID_ARG;
-    auto whole = [](long long bytes) { return (bytes + 255) / 256 * 256; };
-    const int panels = static_cast<int>(ceil_div(m, 256));
-    const long long xb = whole(2ll * 2 * c.E * c.M * pitch), ab = whole(2ll * 2 * c.E * m * mp);
-    const long long db = whole(4ll * c.E * mp), pb = whole(8ll * c.E * prep.chunks), nb = whole(4ll * 3 * c.E * panels);
-    Workspace ws;
-    ws.s = s;
-    cudaMemPool_t pool = workspace_pool(dev, st);
-    const long long bytes = (c.steps > 1 ? 2 : 1) * xb + 2 * ab + 2 * db + pb + nb;
-    if (!pool || cudaMallocFromPoolAsync(&ws.p, static_cast<size_t>(bytes), pool, s) != cudaSuccess) {
-        (void)cudaGetLastError();
-        ws.p = nullptr;
-        return SGEMM_ERR_CUDA;
-    }
-    char* at = static_cast<char*>(ws.p);
-    auto take = [&](long long n) {
-        char* const q = at;
-        at += n;
-        return q;
-    };
-    auto planes = [&](long long size, long long ld, long long matrix) {
-        __half* const hi = reinterpret_cast<__half*>(take(size));
+    const int m = std::min(c.M, c.N), parts = c.type == SGEMM_TYPE_BF16 ? 1 : 2;
+    const OrthoLayout l = ortho_layout(c.E, c.M, c.N, c.steps);
+    if (static_cast<long long>(c.E) * l.chunks > 0x7fffffffll) return SGEMM_ERR_INVALID_ARG;
+    char* const ws = static_cast<char*>(c.workspace);
+    auto planes = [&](long long at, long long ld, long long matrix) {
+        __half* const hi = reinterpret_cast<__half*>(ws + at);
         return OrthoPlanes{hi, hi + c.E * matrix, ld, matrix};
     };
+    OrthoPrep prep = {};
+    prep.chunks = l.chunks, prep.per = l.per;
     OrthoTcParams p = {};
     p.E = c.E, p.m = m, p.rows = c.M, p.cols = c.N, p.steps = c.steps;
-    prep.part = reinterpret_cast<double*>(take(pb));
-    prep.zero = p.done = reinterpret_cast<int*>(take(nb));
-    prep.zeros = 3ll * c.E * panels;
-    p.panels = panels;
-    p.d = reinterpret_cast<float*>(take(db));
-    p.e = reinterpret_cast<float*>(take(db));
-    p.diag = mp;
-    p.a = planes(ab, mp, m * mp);
-    p.p = planes(ab, mp, m * mp);
-    p.x[0] = planes(xb, pitch, c.M * pitch);
-    p.x[1] = c.steps > 1 ? planes(xb, pitch, c.M * pitch) : p.x[0];
+    prep.part = reinterpret_cast<double*>(ws + l.part);
+    prep.zero = p.done = reinterpret_cast<int*>(ws + l.done);
+    prep.zeros = 3ll * c.E * l.panels;
+    p.panels = l.panels;
+    p.d = reinterpret_cast<float*>(ws + l.d);
+    p.e = reinterpret_cast<float*>(ws + l.e);
+    p.diag = l.square_pitch;
+    p.a = planes(l.a, l.square_pitch, m * l.square_pitch);
+    p.p = planes(l.p, l.square_pitch, m * l.square_pitch);
+    for (int i = 0; i < 2; ++i) p.x[i] = planes(l.x[i], l.pitch, c.M * l.pitch);
     p.c1 = c.a, p.c3 = c.b, p.c5 = c.c;
     p.out = c.out, p.ldo = c.ldo, p.so = c.so, p.out_type = c.type;
     p.align = row_alignment(c.out, c.type == SGEMM_TYPE_F32 ? 4 : 2, c.M > 1 ? c.ldo : 0, c.E > 1 ? c.so : 0);
@@ -151,15 +145,15 @@ int orthogonalize(const OrthoCall& c, int dev, DeviceState& st, cudaStream_t s) 
     alignas(64) CUtensorMap maps[4];
     const OrthoPlanes* const of[4] = {&p.x[0], &p.x[1], &p.a, &p.p};
     for (int i = 0; i < 4; ++i) {
-        const int rc = i < 2 ? encode_planes(&maps[i], of[i]->hi, c.N, c.M, 2ll * c.E, pitch)
-                             : encode_planes(&maps[i], of[i]->hi, m, m, 2ll * c.E, mp);
+        const int rc = i < 2 ? encode_planes(&maps[i], of[i]->hi, c.N, c.M, 2ll * c.E, l.pitch)
+                             : encode_planes(&maps[i], of[i]->hi, m, m, 2ll * c.E, l.square_pitch);
         if (rc != SGEMM_OK) return rc;
     }
     prep.G = c.G, prep.ldg = c.ldg, prep.sg = c.sg;
     prep.E = c.E, prep.rows = c.M, prep.cols = c.N;
     prep.vec = row_alignment(c.G, c.type == SGEMM_TYPE_F32 ? 4 : 2, c.M > 1 ? c.ldg : 0, c.E > 1 ? c.sg : 0) == 16;
     prep.eps = c.eps;
-    prep.hi = reinterpret_cast<uint16_t*>(p.x[0].hi), prep.pitch = pitch, prep.plane = static_cast<long long>(c.E) * c.M * pitch;
+    prep.hi = reinterpret_cast<uint16_t*>(p.x[0].hi), prep.pitch = l.pitch, prep.plane = c.E * p.x[0].matrix;
     const int rc = ortho_prepare(prep, c.type, s);
     if (rc != SGEMM_OK) return rc;
     // Tiles of a pair of CTAs: 256 rows by 128 columns; bf16 256 where the GPU's pairs then have two and a half each in an update.

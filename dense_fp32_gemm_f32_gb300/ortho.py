@@ -7,9 +7,16 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .experts import _TYPES, _current_device, _empty, _enter, _operand, _out, _raw_stream, _strides, _type
+from .experts import _TYPES, _current_device, _empty, _enter, _operand, _out, _raw_stream, _strides, _type, _uint8
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def _scratch(lib, t: int, E: int, M: int, N: int, steps: int, device):
+    """The call's scratch from torch's allocator, on the current stream, to which it goes back when the call has been
+    enqueued; (None, 0) where there is none (sizes that the entry refuses among them)."""
+    n = lib.sgemm_orthogonalize_workspace(t, E, M, N, steps)
+    return (_empty((n,), dtype=_uint8, device=device), n) if n > 0 else (None, 0)
 
 
 def sgemm_orthogonalize(G: torch.Tensor, out: torch.Tensor | None = None, *, steps: int = 5,
@@ -30,9 +37,11 @@ def sgemm_orthogonalize(G: torch.Tensor, out: torch.Tensor | None = None, *, ste
         except (AttributeError, ValueError, KeyError):
             usual = False
         if usual:
+            lib = _lib.load()
             out = _empty(shape, dtype=G.dtype, device=G.device)
-            rc = _lib.load().sgemm_orthogonalize(t, E, M, N, G.data_ptr(), N, M * N, steps, a, b, c, eps, out.data_ptr(), N, M * N,
-                                                 _raw_stream(dev))
+            scratch, n = _scratch(lib, t, E, M, N, steps, G.device)
+            rc = lib.sgemm_orthogonalize(t, E, M, N, G.data_ptr(), N, M * N, steps, a, b, c, eps, out.data_ptr(), N, M * N,
+                                         None if scratch is None else scratch.data_ptr(), n, _raw_stream(dev))
             if rc:
                 _lib.check(rc, "sgemm_orthogonalize")
             return out
@@ -48,7 +57,10 @@ def sgemm_orthogonalize(G: torch.Tensor, out: torch.Tensor | None = None, *, ste
         out, ldo = _out(out, G, tuple(shape), G.dtype)
         if so is None:
             so = _strides(out, shape, "out")[1]
-        rc = _lib.load().sgemm_orthogonalize(t, E, M, N, G.data_ptr(), ldg, sg, steps, a, b, c, eps, out.data_ptr(), ldo, so, s)
+        lib = _lib.load()
+        scratch, n = _scratch(lib, t, E, M, N, steps, G.device)
+        rc = lib.sgemm_orthogonalize(t, E, M, N, G.data_ptr(), ldg, sg, steps, a, b, c, eps, out.data_ptr(), ldo, so,
+                                     None if scratch is None else scratch.data_ptr(), n, s)
     finally:
         if switch is not None:
             switch.close()

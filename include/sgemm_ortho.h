@@ -1,8 +1,9 @@
 /*
  * sgemm_ortho.h -- orthogonalised weight updates (GB300, sm_103a).  Companion
  * of sgemm_experts.h, whose weight gradients it takes: same status codes,
- * types, streams, error behaviour and scratch pool.
- *   ORTHO-ALLOCATING: sgemm_orthogonalize
+ * types, streams and error behaviour.  The entries take no device memory: the
+ * scratch, which is several times an update's size, is the caller's.
+ *   ORTHO-NON-ALLOCATING: sgemm_orthogonalize sgemm_orthogonalize_workspace
  */
 #ifndef GB300_SGEMM_ORTHO_H
 #define GB300_SGEMM_ORTHO_H
@@ -32,6 +33,9 @@ extern "C" {
  *              (from [0, 1] on) above 2 in magnitude after any step, and
  *              b s^2 + c s^4 not above 15: refused otherwise
  *   eps        >= 0, finite.  With eps = 0 a matrix of zeros gives NaN
+ *   workspace  DEVICE memory of workspace_bytes, at least what
+ *              sgemm_orthogonalize_workspace says, 256-byte aligned, for this call alone until
+ *              its work on the stream is done (NULL where it says 0)
  * Accuracy.  Each step's products take X, A and b A + c A A less their
  * diagonals as f16 operands (A's and X's rounding errors, and the diagonals,
  * are carried along outside of the products) and sum in float32.  For bf16 one
@@ -47,7 +51,16 @@ int sgemm_orthogonalize(int type, int E, int M, int N,
                         const void* G, int64_t ldg, int64_t stride_g,
                         int steps, float a, float b, float c, double eps,
                         void* out, int64_t ldo, int64_t stride_out,
+                        void* workspace, int64_t workspace_bytes,
                         void* stream);
+
+/*
+ * sgemm_orthogonalize_workspace -- the bytes of workspace that a call of these
+ * sizes takes (about 16 an element for several steps, 8 for one, and 16 an element
+ * of the square of the shorter side; 0 for a shorter side of up to 128 and a longer
+ * one of up to 2048), or -1 for sizes that it refuses.  It asks no device.
+ */
+int64_t sgemm_orthogonalize_workspace(int type, int E, int M, int N, int steps);
 
 #ifdef __cplusplus
 }

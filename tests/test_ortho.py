@@ -55,16 +55,22 @@ def update(E, M, N, dtype, seed=0, rank=0, size=1e-3):
 
 # ------------------------------------------------------------------ refusals, on the CPU
 
-A, B = 0x10000000, 0x20000000  # never dereferenced
+A, B, C = 0x10000000, 0x20000000, 0x30000000  # never dereferenced
 
 
 @pytest.mark.parametrize("change", [
     dict(type=3), dict(E=-1), dict(M=-1), dict(N=-1), dict(G=0), dict(out=0), dict(G=A + 1), dict(ldg=31), dict(ldo=31), dict(sg=400),
     dict(so=100), dict(out=A + 64), dict(steps=0), dict(steps=65), dict(a=math.nan), dict(b=math.inf), dict(eps=-1.0), dict(eps=math.nan),
     dict(eps=math.inf), dict(a=4.0, b=0.0, c=0.0), dict(a=1.5, b=0.0, c=0.0), dict(c=30.0), dict(a=0.0, b=-100.0, c=100.0),
-    dict(M=2 ** 24, N=2 ** 24, ldg=2 ** 24, ldo=2 ** 24, sg=2 ** 48, so=2 ** 48, out=1 << 55)], ids=str)
+    dict(M=2 ** 24, N=2 ** 24, ldg=2 ** 24, ldo=2 ** 24, sg=2 ** 48, so=2 ** 48, out=1 << 55),
+    # a workspace that is missing, too small, not aligned, or G's or the result's
+    dict(M=200, N=256, ldg=256, ldo=256, sg=51200, so=51200), dict(M=200, N=256, ldg=256, ldo=256, sg=51200, so=51200, workspace=C, bytes=10 ** 6),
+    dict(M=200, N=256, ldg=256, ldo=256, sg=51200, so=51200, workspace=C + 128, bytes=10 ** 8),
+    dict(M=200, N=256, ldg=256, ldo=256, sg=51200, so=51200, workspace=A + 4096, bytes=10 ** 8),
+    dict(M=200, N=256, ldg=256, ldo=256, sg=51200, so=51200, workspace=B - 4096, bytes=10 ** 8)], ids=str)
 def test_refusals(change):
-    p = dict(type=1, E=2, M=16, N=32, G=A, ldg=32, sg=512, steps=5, a=3.4445, b=-4.775, c=2.0315, eps=1e-7, out=B, ldo=32, so=512, stream=None)
+    p = dict(type=1, E=2, M=16, N=32, G=A, ldg=32, sg=512, steps=5, a=3.4445, b=-4.775, c=2.0315, eps=1e-7, out=B, ldo=32, so=512, workspace=0, bytes=0,
+             stream=None)
     p.update(change)
     assert _lib.load().sgemm_orthogonalize(*p.values()) == _lib.ERR_INVALID_ARG
 
@@ -72,7 +78,7 @@ def test_refusals(change):
 @pytest.mark.parametrize("coefficients", [QUINTIC, (2.0, -1.5, 0.5), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (1.0, 0.0, 0.0)])
 def test_usual_polynomials_are_taken(coefficients):
     """(Of no matrices: nothing is launched.)"""
-    assert _lib.load().sgemm_orthogonalize(1, 0, 16, 32, 0, 32, 512, 64, *coefficients, 0.0, 0, 32, 512, None) == _lib.OK
+    assert _lib.load().sgemm_orthogonalize(1, 0, 16, 32, 0, 32, 512, 64, *coefficients, 0.0, 0, 32, 512, 0, 0, None) == _lib.OK
 
 
 def test_binding_refuses_cpu_tensors():
@@ -80,11 +86,22 @@ def test_binding_refuses_cpu_tensors():
         g.sgemm_orthogonalize(torch.zeros(4, 4))
 
 
-def test_header_states_that_it_allocates():
+def test_workspace():
+    """What a call takes: nothing for short sides, the planes of X twice and of A and B once, each of two f16 values an element;
+    no size for what is refused."""
+    size = _lib.load().sgemm_orthogonalize_workspace
+    assert size(1, 8, 128, 2048, 5) == size(0, 1, 2000, 100, 5) == size(1, 0, 500, 500, 5) == size(1, 2, 500, 0, 5) == 0
+    least = 2 * 2 * 8 * (2 * 2048 * 4096 + 2 * 2048 * 2048)
+    assert least <= size(1, 8, 2048, 4096, 5) <= 1.01 * least
+    assert size(1, 8, 2048, 4096, 1) <= least - 2 * 2 * 8 * 2048 * 4096 * 0.99
+    assert size(3, 1, 500, 500, 5) == size(1, -1, 500, 500, 5) == size(1, 1, 500, 500, 0) == size(1, 1, 2 ** 25, 2 ** 25, 5) == -1
+
+
+def test_header_states_that_it_does_not_allocate():
     import os
 
     path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "sgemm_ortho.h")
-    assert "ORTHO-ALLOCATING: sgemm_orthogonalize\n" in open(path).read()
+    assert "ORTHO-NON-ALLOCATING: sgemm_orthogonalize sgemm_orthogonalize_workspace\n" in open(path).read()
 
 
 # ------------------------------------------------------------------ results
@@ -273,6 +290,19 @@ def test_streams_and_recorded_calls(dtype):
         for x, y in zip(G, out):
             assert torch.equal(g.sgemm_orthogonalize(x), y)
     assert g.check_status() == 0
+
+
+@pytest.mark.gpu
+def test_a_workspace_of_anything():
+    """What the scratch held before has no part in the result (NaN, counters that are not zero)."""
+    G = update(2, 300, 520, torch.bfloat16, seed=35)
+    want, lib = g.sgemm_orthogonalize(G), _lib.load()
+    n = lib.sgemm_orthogonalize_workspace(_lib.TYPE_BF16, 2, 300, 520, 5)
+    for fill in (0, 0xFF, 0x7F):
+        scratch, out = torch.full((n,), fill, dtype=torch.uint8, device="cuda"), torch.empty_like(G)
+        rc = lib.sgemm_orthogonalize(_lib.TYPE_BF16, 2, 300, 520, G.data_ptr(), 520, 300 * 520, 5, *QUINTIC, 1e-7, out.data_ptr(), 520,
+                                     300 * 520, scratch.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+        assert rc == _lib.OK and torch.equal(out, want)
 
 
 @pytest.mark.gpu
