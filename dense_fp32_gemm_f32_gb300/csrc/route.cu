@@ -743,9 +743,20 @@ constexpr int kGradWarps = 8;
 
 template <int NPL, typename T>
 __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const RouteGradParams p) {
+    constexpr int kQuad = NPL >= 4 ? 4 : 1;
+    __shared__ __align__(16) float rows[kGradWarps][32 * NPL];
     const int lane = threadIdx.x & 31, first = lane * NPL;
     const long long t = static_cast<long long>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5);
     if (t >= p.T) return;
+    float* const mine = rows[threadIdx.x >> 5];
+#pragma unroll
+    for (int i = 0; i < NPL; i += kQuad) {
+        if constexpr (kQuad == 4)
+            *reinterpret_cast<float4*>(mine + first + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        else
+            mine[first + i] = 0.f;
+    }
+    __syncwarp();
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     int e = -1;
     float d = 0.f, x = -INFINITY;
@@ -767,13 +778,14 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
         float s = 0.f, rest = 1.f;  // rest: 1 - s, of a sigmoid
         if (e >= 0 && p.sigmoid) {
             const float low = x > 0.f ? 0.f : x, tail = expf(-fabsf(x));
-            s = expf(low - (p.renormalize ? fminf(top, 0.f) : 0.f)) / (1.f + tail);
-            rest = (x > 0.f ? tail : 1.f) / (1.f + tail);
+            const float inv = fast_reciprocal(1.f + tail);
+            s = expf(low - (p.renormalize ? fminf(top, 0.f) : 0.f)) * inv;
+            rest = (x > 0.f ? tail : 1.f) * inv;
         } else if (e >= 0) {
             s = expf(x - top);
         }
         if (p.renormalize) {
-            s /= warp_sum(s);
+            s *= fast_reciprocal(warp_sum(s));
             const float mean = warp_sum(d * s);
             if (e >= 0) g = p.scale * s * (d - mean) * rest;
         } else if (p.sigmoid) {
@@ -788,23 +800,27 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - most);
+                l[i] = l[i] == -INFINITY ? 0.f : fast_exp(l[i] - most);
                 sum += l[i];
             }
-            sum = warp_sum(sum);
-            s = e >= 0 ? expf(x - most) / sum : 0.f;
-            const float mean = warp_sum(d * s);
+            const float inv = fast_reciprocal(warp_sum(sum));
+            s = e >= 0 ? fast_exp(x - most) * inv : 0.f;
+            const float less = -p.scale * inv * warp_sum(d * s);
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) v[i] = -p.scale * (l[i] / sum) * mean;
+            for (int i = 0; i < NPL; ++i) v[i] = l[i] * less;
             if (e >= 0) g = p.scale * s * d;
         }
-        for (int j = 0; j < p.k; ++j) {
-            const int at = __shfl_sync(kAll, e, j);
-            const float more = __shfl_sync(kAll, g, j);
-            const int i0 = at - first;
+        // The chosen experts' parts, by way of a row in shared memory.
+        if (e >= 0) atomicAdd(mine + e, g);
+        __syncwarp();
 #pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                if (at >= 0 && i == i0) v[i] += more;
+        for (int i = 0; i < NPL; i += kQuad) {
+            if constexpr (kQuad == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(mine + first + i);
+                v[i] += x.x, v[i + 1] += x.y, v[i + 2] += x.z, v[i + 3] += x.w;
+            } else {
+                v[i] += mine[first + i];
+            }
         }
     }
     T* out = static_cast<T*>(p.dlogits) + t * p.ldd + first;
