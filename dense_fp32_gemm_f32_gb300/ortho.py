@@ -25,7 +25,7 @@ def sgemm_orthogonalize(G: torch.Tensor, out: torch.Tensor | None = None, *, ste
 
     X = G / (|G| + eps), then ``steps`` times X = a X + (b A + c A A) X with A = X X^T (or X^T X, the smaller) and (a, b, c)
     the ``coefficients``: each singular value s becomes a s + b s^3 + c s^5.  The default brings all that are above about
-    1/500 of the norm to between 0.7 and 1.2 in five steps; (2, -1.5, 0.5) converges to 1.
+    1/500 of the norm to between 0.7 and 1.2 in five steps; (2, -1.5, 0.5) converges to 1.  M and N are up to 262144.
     """
     a, b, c = coefficients
     if out is None and stream is None:

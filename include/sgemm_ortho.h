@@ -26,7 +26,8 @@ extern "C" {
  * which takes each singular value s to a s + b s^3 + c s^5 and leaves the
  * singular vectors where they are.
  *   type       of G and out
- *   G, ldg, stride_g       E matrices M x N, stride_g elements apart
+ *   G, ldg, stride_g       E matrices M x N, stride_g elements apart; M and N up to
+ *              262144 (sums over longer rows lose more than what follows)
  *   out, ldo, stride_out   the same, overwritten
  *   steps      1 .. 64
  *   a, b, c    the polynomial.  It may take no singular value that can occur
@@ -44,7 +45,8 @@ extern "C" {
  * direction of small singular values by up to a, as it does those values
  * themselves; against the result in 64 bits that comes to less than 2^-8 of its
  * norm for bf16, and for float32 and f16 to about what the same steps with
- * float32 products have, besides the rounding to the output's type.
+ * float32 products have (2^-18 up to rows of 65536), besides the rounding to the
+ * output's type.
  * A non-finite element makes its whole matrix NaN or infinite, and no other.
  */
 int sgemm_orthogonalize(int type, int E, int M, int N,
