@@ -7,8 +7,8 @@
 // an expert out of service: the warp's largest is then one redux instruction,
 // and k of them with the lane's own largest kept up to date make the choice.
 //
-// What the choice is by.  Without a bias (and with group_best = 1) both scores
-// grow with the logit, so logits are compared.  Otherwise float32 scores
+// What the choice is by.  Without a bias, or with one that is the same for all (and
+// with group_best = 1), both scores grow with the logit, so logits are compared.  Otherwise float32 scores
 // decide where they are further apart than their errors.  First with keys that
 // hold the expert and 22 bits of the value (choose_packed); a token where two that
 // decide are too near for that goes through keys of 32 bits, and scores that are
@@ -195,8 +195,9 @@ __device__ __forceinline__ void softmax_sums(const float (&l)[NPL], float& top, 
     sum = warp_sum(sum);
 }
 
-__device__ __forceinline__ bool chosen_by_logit(const RouteParams& p) {
-    return !p.bias && (p.groups == 1 || p.group_best == 1);
+// `one_bias`: there is none, or it is the same finite number for all experts.
+__device__ __forceinline__ bool chosen_by_logit(const RouteParams& p, bool one_bias) {
+    return one_bias && (p.groups == 1 || p.group_best == 1);
 }
 
 // What experts are chosen by where that is not the logits: c = score + bias, in
@@ -238,15 +239,16 @@ __device__ __forceinline__ typename Keys<V>::Key largest(const typename Keys<V>:
 }
 
 // The choice with keys of 32 bits.  Where those that decide are within their
-// errors of one another, these alone are computed in 64 bits and compared so.
+// errors of one another, these alone are compared again: by their logits if they
+// have one bias (a bias of zeros, or equal scores of which a token of
+// padding has many), else computed in 64 bits.
 // Few tokens come here, and the rest wait for them: so little is computed in 64
 // bits (2 lanes a cycle of an SM), and loops are not unrolled (instructions that
 // nobody has fetched before: 25 us for the first token of a prompt).
 template <int NPL, typename T>
-__device__ __noinline__ int choose_again(const RouteParams& p, const T* row, float top, float sum) {
+__device__ __noinline__ int choose_again(const RouteParams& p, const T* row, bool by_logit, float top, float sum) {
     using K = Keys<float>;
     const int lane = threadIdx.x & 31, first = lane * NPL;
-    const bool by_logit = chosen_by_logit(p);
     float l[NPL], bias[NPL], size = 0.f, near = 0.f;
     uint32_t key[NPL];
 #pragma unroll 1
@@ -270,14 +272,17 @@ __device__ __noinline__ int choose_again(const RouteParams& p, const T* row, flo
             for (int i = 0; i < NPL; ++i) all += l[i] == -INFINITY ? 0. : exp(static_cast<double>(l[i]) - top);
             all = warp_sum(all);
         }
+        float last = NAN, last_bias = 0.f;  // (neighbours that are alike are computed once)
+        unsigned long long last_key = 0;
 #pragma unroll 1
         for (int i = 0; i < NPL; ++i) {
-            exact[i] = 0;
-            if (__any_sync(kAll, some >> i & 1)) {
+            const bool wanted = some >> i & 1, known = l[i] == last && bias[i] == last_bias;
+            if (__any_sync(kAll, wanted && !known)) {
                 const double x = l[i];
-                const double c = (p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / all) + bias[i];
-                if (some >> i & 1) exact[i] = Keys<double>::of(c);
+                last_key = Keys<double>::of((p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / all) + bias[i]);
+                last = l[i], last_bias = bias[i];
             }
+            exact[i] = wanted ? last_key : 0;
         }
     };
     if (p.groups > 1) {
@@ -344,9 +349,21 @@ __device__ __noinline__ int choose_again(const RouteParams& p, const T* row, flo
             for (int i = 0; i < NPL; ++i)
                 if (key[i] >= from) some |= 1u << i;
             if (__reduce_add_sync(kAll, __popc(some)) > 1) {
-                unsigned long long exact[NPL];
-                evaluate(some, exact);
-                (void)largest<NPL, double>(exact, e);
+                const float one = p.bias ? p.bias[e] : 0.f;
+                bool other = false;
+                uint32_t logit[NPL];
+#pragma unroll 1
+                for (int i = 0; i < NPL; ++i) {
+                    logit[i] = some >> i & 1 ? K::of(l[i]) : 0u;
+                    other |= (some >> i & 1) && bias[i] != one;
+                }
+                if (__any_sync(kAll, other)) {
+                    unsigned long long exact[NPL];
+                    evaluate(some, exact);
+                    (void)largest<NPL, double>(exact, e);
+                } else {
+                    (void)largest<NPL, float>(logit, e);
+                }
             }
         }
         if (lane == j) mine = e;
@@ -502,11 +519,11 @@ __device__ __forceinline__ bool grid_keys(const float (&c)[NPL], uint32_t (&key)
 
 // A token's experts, the j-th in lane j, from its logits (the lane's part); `bias`: the lane's, in shared memory.
 template <int NPL, typename T>
-__device__ __forceinline__ int choose_experts(const RouteParams& p, const float (&l)[NPL], const float* bias, float top,
-                                              float sum, bool& sure) {
+__device__ __forceinline__ int choose_experts(const RouteParams& p, const float (&l)[NPL], bool by_logit, const float* bias,
+                                              float top, float sum, bool& sure) {
     uint32_t key[NPL];
     float low, high, scale;
-    if (chosen_by_logit(p)) {
+    if (by_logit) {
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
@@ -608,11 +625,17 @@ __global__ void __launch_bounds__(kRouteThreads, NPL <= 8 ? 2 : 1) route_kernel(
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = count[e] = 0;
-    for (int e = threadIdx.x; e < 32 * NPL; e += kRouteThreads) bias[e] = p.bias && e < p.E ? __ldg(p.bias + e) : 0.f;
-    __syncthreads();
+    const float first_bias = p.bias ? __ldg(p.bias) : 0.f;
+    bool same = fabsf(first_bias) < INFINITY;
+    for (int e = threadIdx.x; e < 32 * NPL; e += kRouteThreads) {
+        const float b = p.bias && e < p.E ? __ldg(p.bias + e) : first_bias;
+        same &= b == first_bias;
+        bias[e] = b;
+    }
+    const bool by_logit = chosen_by_logit(p, __syncthreads_and(same));
     constexpr int kTokens = 2;  // of a warp in a step, at most: with 16 warps, a bit each
     static_assert(kTokens * kRouteWarps <= 32, "a bit a token");
-    const bool sums = !p.sigmoid && (!p.renormalize || !chosen_by_logit(p));
+    const bool sums = !p.sigmoid && (!p.renormalize || !by_logit);
     const long long begin = static_cast<long long>(blockIdx.x) * p.per, end = min(static_cast<long long>(p.T), begin + p.per);
     int mine[kTokens] = {}, rank[kTokens] = {};  // of the last step
     for (int step = 0; step < p.steps; ++step) {
@@ -630,9 +653,9 @@ __global__ void __launch_bounds__(kRouteThreads, NPL <= 8 ? 2 : 1) route_kernel(
                     float l[NPL];
                     load_row<NPL>(row, p.E, p.vec, l);
                     if (sums) softmax_sums(l, top, sum);
-                    e = choose_experts<NPL, T>(p, l, bias + lane * NPL, top, sum, sure);
+                    e = choose_experts<NPL, T>(p, l, by_logit, bias + lane * NPL, top, sum, sure);
                 }
-                if (!sure) e = choose_again<NPL>(p, row, top, sum);
+                if (!sure) e = choose_again<NPL>(p, row, by_logit, top, sum);
                 const float w = weight_of(p, row, e, top, sum);
                 if (lane < p.k) {
                     p.experts[t * p.k + lane] = e;
