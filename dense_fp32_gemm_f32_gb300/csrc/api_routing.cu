@@ -82,8 +82,7 @@ int sgemm_route(int type, int score, int T, int E, int k, const void* logits, in
     p.top_groups = top_groups, p.group_best = group_best, p.group_size = E / groups;
     p.experts = experts, p.weights = weights, p.offsets = offsets, p.slots = slots;
     p.vec = whole_vectors(in[0]);
-    const RoutePlan plan = route_plan(T, st->sm_count);
-    p.width = plan.width, p.per = plan.per, p.step = plan.step, p.steps = (plan.per + plan.step - 1) / plan.step;
+    const RoutePlan plan = route_plan(p, st->sm_count);
     if (plan.clusters > 1) {
         cudaMemPool_t pool = workspace_pool(dev, *st);
         void* ws = nullptr;

@@ -99,10 +99,9 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // ------------------------------------------------------------------ rows
 
-// Lane l's values of a row of E: elements l * NPL ..., -inf past the row's end.
+// A lane's values of a row of E: elements `first` ..., -inf past the row's end.
 template <int NPL, typename T>
-__device__ __forceinline__ void load_row(const T* row, int E, bool vec, float (&v)[NPL]) {
-    const int first = (threadIdx.x & 31) * NPL;
+__device__ __forceinline__ void load_row(const T* row, int first, int E, bool vec, float (&v)[NPL]) {
     constexpr int kBytes = NPL * static_cast<int>(sizeof(T)), kWord = kBytes < 16 ? kBytes : 16;
     if (kWord >= 4 && vec && first + NPL <= E) {
         alignas(16) T x[NPL];
@@ -200,17 +199,11 @@ __device__ __forceinline__ bool chosen_by_logit(const RouteParams& p, bool one_b
     return one_bias && (p.groups == 1 || p.group_best == 1);
 }
 
-// What experts are chosen by where that is not the logits: c = score + bias, in
-// float32, -inf out of service.
-template <int NPL>
-__device__ __forceinline__ void choice_values(const RouteParams& p, const float (&l)[NPL], const float (&bias)[NPL],
-                                              float top, float sum, float (&c)[NPL]) {
-    const float inv = fast_reciprocal(sum);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const float s = p.sigmoid ? fast_reciprocal(1.f + fast_exp(-l[i])) : fast_exp(l[i] - top) * inv;
-        c[i] = l[i] == -INFINITY ? -INFINITY : s + bias[i];
-    }
+// What an expert is chosen by where that is not the logit: c = score + bias, in
+// float32, -inf out of service.  inv: 1 / sum.
+__device__ __forceinline__ float choice_value(const RouteParams& p, float l, float bias, float top, float inv) {
+    const float s = p.sigmoid ? fast_reciprocal(1.f + fast_exp(-l)) : fast_exp(l - top) * inv;
+    return l == -INFINITY ? -INFINITY : s + bias;
 }
 
 // How far apart two of them have to be for their order to be certain; `size`: at
@@ -492,29 +485,50 @@ __device__ __forceinline__ int choose_packed(uint32_t (&key)[NPL], const RoutePa
     return lane < p.k ? mine : -1;
 }
 
-// The values' keys on the grid; false where there is none (values that are all
-// alike, or not finite).  A value's place is off by less than a step, and
-// places never change their order.  low, high: the smallest and the largest.
+// The largest of the lane's values (NaN before all) and the smallest of those in service.
 template <int NPL>
-__device__ __forceinline__ bool grid_keys(const float (&c)[NPL], uint32_t (&key)[NPL], float& low, float& high,
-                                          float& scale) {
-    using K = Keys<float>;
+__device__ __forceinline__ void range_of(const float (&c)[NPL], float& high, float& low) {
     high = -INFINITY, low = INFINITY;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         high = max_nan(high, c[i]);
         low = fminf(low, c[i] == -INFINITY ? INFINITY : c[i]);
     }
-    high = K::value(__reduce_max_sync(kAll, K::of(high)));
-    low = K::value(__reduce_min_sync(kAll, K::of(low)));
-    const float range = high - low;
-    scale = 4194280.f * fast_reciprocal(range);  // 2^22 less 24
+}
+
+// Keys on a grid from the smallest value of a token to its largest, `range` in all.  A value's place is off
+// by less than a step, and places never change their order.  There is no grid for values that are all alike, or not finite.
+__device__ __forceinline__ bool on_grid(float range) { return range > 0x1p-60f && range < 0x1p60f; }
+__device__ __forceinline__ float grid_scale(float range) { return 4194280.f * fast_reciprocal(range); }  // 2^22 less 24
+template <int NPL>
+__device__ __forceinline__ void place_on_grid(const float (&c)[NPL], float low, float scale, int first, uint32_t (&key)[NPL]) {
     // The place is the mantissa of a number from 2^23 on, whose exponent the shift drops (as it drops all of -inf).
-    const uint32_t e0 = kExpertBits - (threadIdx.x & 31) * NPL;
+    const uint32_t e0 = kExpertBits - first;
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
         key[i] = (__float_as_uint(fmaf(c[i] - low, scale, 8388612.f)) << kExpertShift) + (e0 - static_cast<uint32_t>(i));
-    return range > 0x1p-60f && range < 0x1p60f;
+}
+
+// A warp's keys on the grid; false where there is none.
+template <int NPL>
+__device__ __forceinline__ bool grid_keys(const float (&c)[NPL], uint32_t (&key)[NPL], float& low, float& high,
+                                          float& scale) {
+    using K = Keys<float>;
+    range_of(c, high, low);
+    high = K::value(__reduce_max_sync(kAll, K::of(high)));
+    low = K::value(__reduce_min_sync(kAll, K::of(low)));
+    scale = grid_scale(high - low);
+    place_on_grid(c, low, scale, (threadIdx.x & 31) * NPL, key);
+    return on_grid(high - low);
+}
+
+// How many steps of the grid apart two scores have to be (a step more for each place's error), and two scores of groups.
+__device__ __forceinline__ float choice_steps(const RouteParams& p, float low, float high, float sum, float scale) {
+    return fminf(choice_error(p, fmaxf(fabsf(low), fabsf(high)), sum) * scale, 0x1p20f);
+}
+__device__ __forceinline__ uint32_t choice_gap(float steps) { return static_cast<uint32_t>(steps + 2.1f); }
+__device__ __forceinline__ uint32_t score_gap(const RouteParams& p, float steps) {
+    return p.group_best == 2 ? static_cast<uint32_t>(2.f * steps + 4.1f) : choice_gap(steps);
 }
 
 // A token's experts, the j-th in lane j, from its logits (the lane's part); `bias`: the lane's, in shared memory.
@@ -549,38 +563,37 @@ __device__ __forceinline__ int choose_experts(const RouteParams& p, const float 
 #pragma unroll
         for (int i = 0; i < NPL; ++i) b[i] = bias[i];
     }
-    choice_values(p, l, b, top, sum, c);
+    const float inv = fast_reciprocal(sum);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) c[i] = choice_value(p, l[i], b[i], top, inv);
     sure = grid_keys(c, key, low, high, scale);
     if (!sure) {
         sure = high == -INFINITY;  // (nobody is in service)
         return -1;
     }
-    // (a step more for each place's error)
-    const float steps = fminf(choice_error(p, fmaxf(fabsf(low), fabsf(high)), sum) * scale, 0x1p20f);
-    return choose_packed<NPL>(key, p, false, static_cast<uint32_t>(steps + 2.1f),
-                              p.group_best == 2 ? static_cast<uint32_t>(2.f * steps + 4.1f)
-                                                : static_cast<uint32_t>(steps + 2.1f),
-                              sure);
+    const float steps = choice_steps(p, low, high, sum, scale);
+    return choose_packed<NPL>(key, p, false, choice_gap(steps), score_gap(p, steps), sure);
 }
 
-// The weight of the lane's expert e (-1: none).
+// The score of logit x, less the factor of `lead` that all of a token's have.
 //
 // sigmoid(l) = e^min(l, 0) / (1 + e^-|l|): with the largest chosen logit's
 // e^min(l, 0) taken out, the renormalised ones are ratios of numbers near 1
 // however small the scores are.
+__device__ __forceinline__ float score_over(const RouteParams& p, float x, float lead, float sum) {
+    if (p.sigmoid) {
+        const float low = x > 0.f ? 0.f : x;
+        return __fdividef(expf(low - (p.renormalize ? fminf(lead, 0.f) : 0.f)), 1.f + expf(-fabsf(x)));
+    }
+    return sum != sum ? sum : expf(x - lead);  // (a NaN or +inf that was not chosen)
+}
+
+// The weight of the lane's expert e (-1: none).
 template <typename T>
 __device__ __forceinline__ float weight_of(const RouteParams& p, const T* row, int e, float top, float sum) {
     const float x = e >= 0 ? to_f32(row[e]) : -INFINITY;
     const float lead = p.renormalize ? warp_max(x) : top;
-    float s = 0.f;
-    if (p.sigmoid) {
-        const float low = x > 0.f ? 0.f : x;
-        s = __fdividef(expf(low - (p.renormalize ? fminf(lead, 0.f) : 0.f)), 1.f + expf(-fabsf(x)));
-    } else {
-        s = expf(x - lead);
-        if (sum != sum) s = sum;  // (a NaN or +inf that was not chosen)
-    }
-    if (e < 0) s = 0.f;
+    float s = e < 0 ? 0.f : score_over(p, x, lead, sum);
     if (p.renormalize) sum = warp_sum(s);
     return e < 0 ? 0.f : p.sigmoid && !p.renormalize ? p.scale * s : p.scale * s * fast_reciprocal(sum);
 }
@@ -609,6 +622,25 @@ __device__ __forceinline__ void exclusive_sums(const int* count, int E, int* bas
         if (i + 1 == E || i + 2 == E) out[E] = from + a + b;
     }
     __syncthreads();
+}
+
+// The CTAs of a cluster add up their counts: `before` those of the CTAs before this one, `sums` those of all, which
+// also go to p.counts.  A cluster's barrier has to follow before a CTA's counts change.
+__device__ __forceinline__ void cluster_counts(const RouteParams& p, const int* count, int* before, int* sums) {
+    const int of = static_cast<int>(cluster_ctarank());
+    cluster_sync_all();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        const uint32_t at = smem_addr(count + e);
+        int sum = 0, sum_before = 0;
+#pragma unroll 4
+        for (int q = 0; q < p.width; ++q) {
+            if (q == of) sum_before = sum;
+            sum += ld_shared_cluster_s32(map_shared_rank(at, q));
+        }
+        before[e] = sum_before;
+        sums[e] = sum;
+        if (p.counts && of == 0) p.counts[static_cast<long long>(blockIdx.x / p.width) * p.E + e] = sum;
+    }
 }
 
 // The CTAs of a cluster (p.width) add up their counts of each expert's choices
@@ -651,7 +683,7 @@ __global__ void __launch_bounds__(kRouteThreads, NPL <= 8 ? 2 : 1) route_kernel(
                 int e;
                 {
                     float l[NPL];
-                    load_row<NPL>(row, p.E, p.vec, l);
+                    load_row<NPL>(row, lane * NPL, p.E, p.vec, l);
                     if (sums) softmax_sums(l, top, sum);
                     e = choose_experts<NPL, T>(p, l, by_logit, bias + lane * NPL, top, sum, sure);
                 }
@@ -680,21 +712,7 @@ __global__ void __launch_bounds__(kRouteThreads, NPL <= 8 ? 2 : 1) route_kernel(
         }
         __syncthreads();
     }
-    // What comes before this CTA's choices of an expert, in the cluster.
-    const int of = static_cast<int>(cluster_ctarank());
-    cluster_sync_all();
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-        const uint32_t at = smem_addr(count + e);
-        int sum = 0, sum_before = 0;
-#pragma unroll 4
-        for (int q = 0; q < p.width; ++q) {
-            if (q == of) sum_before = sum;
-            sum += ld_shared_cluster_s32(map_shared_rank(at, q));
-        }
-        before[e] = sum_before;
-        mask[e] = sum;
-        if (p.counts && of == 0) p.counts[static_cast<long long>(blockIdx.x / p.width) * p.E + e] = sum;
-    }
+    cluster_counts(p, count, before, mask);
     cluster_sync_all();  // (nobody reads this CTA's counts after this)
     if (!p.counts) {
         int* const base = count;
@@ -717,6 +735,290 @@ __global__ void __launch_bounds__(kRouteThreads, NPL <= 8 ? 2 : 1) route_kernel(
     }
 }
 
+// ------------------------------------------------------------------ many tokens
+//
+// Four lanes a token, N = 16, 32 or 64 neighbouring experts a lane, the choice the
+// same as choose_packed's.  What a warp does once for a token above (a maximum of all lanes for each choice and
+// each group, the weights), it does here once for eight.  A lane's keys are sorted eight
+// at a time (19 exchanges) and merged to the best eight; then two merges across the four.  Of what a merge drops the
+// largest is kept, to see how near the ninth is.
+constexpr int kQuadWarps = 4, kQuadThreads = 32 * kQuadWarps;
+static_assert(8 * kQuadWarps == kQuadStep, "a bit a token");
+
+// The best eight of two sorted eights to `a`, sorted; `next`: the largest that is dropped.
+__device__ __forceinline__ void merge_best(uint32_t (&a)[8], const uint32_t (&b)[8], uint32_t& next) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        next = max(next, min(a[i], b[7 - i]));
+        a[i] = max(a[i], b[7 - i]);
+    }
+#pragma unroll
+    for (int d = 4; d; d /= 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) {
+                const uint32_t x = a[i], y = a[i + d];
+                a[i] = max(x, y);
+                a[i + d] = min(x, y);
+            }
+}
+
+// Over the four lanes of a token.
+template <typename V, typename F>
+__device__ __forceinline__ V over_quad(V v, F f) {
+    v = f(v, __shfl_xor_sync(kAll, v, 1));
+    return f(v, __shfl_xor_sync(kAll, v, 2));
+}
+
+// choose_packed of four lanes: their keys to the best eight, sorted, in `best`.  Groups are powers of two from 8 on.
+template <int N>
+__device__ __forceinline__ bool choose_quad(uint32_t (&key)[N], const RouteParams& p, uint32_t gap, uint32_t group_gap,
+                                            uint32_t (&best)[8]) {
+    constexpr int B = N / 8;  // blocks of eight keys
+    const int block = (threadIdx.x & 3) * B;
+    const auto most = [](uint32_t x, uint32_t y) { return max(x, y); };
+    bool close = false;
+    if (p.groups > 1) {
+        const int blocks = p.group_size >> 3, shift = 31 - __clz(blocks);
+        uint32_t a[B], b[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            a[j] = b[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) merge_two(a[j], b[j], key[8 * j + i], 0u);
+        }
+        // A group's first block gets what the others have.
+#pragma unroll
+        for (int w = 1; w < B; w *= 2)
+            if (blocks > w) {
+#pragma unroll
+                for (int j = 0; j + w < B; j += 2 * w) merge_two(a[j], b[j], a[j + w], b[j + w]);
+            }
+        if (blocks > B) merge_two(a[0], b[0], __shfl_xor_sync(kAll, a[0], 1), __shfl_xor_sync(kAll, b[0], 1));
+        if (blocks > 2 * B) merge_two(a[0], b[0], __shfl_xor_sync(kAll, a[0], 2), __shfl_xor_sync(kAll, b[0], 2));
+        // Scores with their group in them, as keys hold their expert.
+        uint32_t score[B];
+        bool one = false, two = false;
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            const bool first = ((block + j) & (blocks - 1)) == 0;
+            uint32_t v = first ? a[j] >> kExpertShift : 0u;
+            const uint32_t second = p.group_best == 2 ? b[j] >> kExpertShift : 0u;
+            one |= v && !second;
+            two |= v && second;
+            if (v) v += second;
+            score[j] = v ? v << 5 | (31 - ((block + j) >> shift)) : 0u;
+        }
+        // (a sum of two and a single value are not on one grid)
+        const unsigned ones = __ballot_sync(kAll, one), twos = __ballot_sync(kAll, two);
+        const int quad = threadIdx.x & 28;
+        close = (ones >> quad & 15) && (twos >> quad & 15);
+        unsigned kept = 0;
+        uint32_t last = ~0u;
+        for (int i = 0; i <= p.top_groups; ++i) {
+            uint32_t m = score[0];
+#pragma unroll
+            for (int j = 1; j < B; ++j) m = max(m, score[j]);
+            m = over_quad(m, most);
+            if (i == p.top_groups) {
+                close |= m && last - (m >> 5) <= group_gap;
+            } else {
+                kept |= m ? 1u << (31 - (m & 31)) : 0u;
+                last = m >> 5;
+#pragma unroll
+                for (int j = 0; j < B; ++j) score[j] = score[j] == m ? 0u : score[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (!(kept >> ((block + j) >> shift & 31) & 1)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) key[8 * j + i] = 0;
+            }
+    }
+    uint32_t next = 0;
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+        uint32_t some[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) some[i] = key[8 * j + i];
+        sort_lane(some);
+        if (j == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) best[i] = some[i];
+        } else {
+            merge_best(best, some, next);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d <= 2; d *= 2) {
+        uint32_t other[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, best[i], d);
+        next = max(next, __shfl_xor_sync(kAll, next, d));
+        merge_best(best, other, next);
+    }
+#pragma unroll
+    for (int j = 1; j <= 8; ++j) {
+        const uint32_t here = j < 8 ? best[j & 7] : next;
+        close |= j <= p.k && here > kExpertBits && (best[j - 1] >> kExpertShift) - (here >> kExpertShift) <= gap;
+    }
+    return !close;
+}
+
+// As route_kernel with several clusters, for k <= 8 and E <= 4 N.
+template <int N, typename T>
+__global__ void __launch_bounds__(kQuadThreads, 4) route_quads_kernel(const RouteParams p) {
+    constexpr int kPitch = N + 4;  // (the four lanes' vectors of the bias from other banks)
+    extern __shared__ __align__(16) int shared[];
+    float* const bias = reinterpret_cast<float*>(shared);  // 4 kPitch
+    int* const mask = shared + 4 * kPitch;                 // E each, as route_kernel's
+    int* const count = mask + p.E;
+    int* const before = count + p.E;
+    grid_dependency_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane & 3, first = q * N;
+    for (int e = threadIdx.x; e < p.E; e += kQuadThreads) mask[e] = count[e] = 0;
+    const float first_bias = p.bias ? __ldg(p.bias) : 0.f;
+    bool same = fabsf(first_bias) < INFINITY;
+    for (int e = threadIdx.x; e < 4 * N; e += kQuadThreads) {
+        const float b = p.bias && e < p.E ? __ldg(p.bias + e) : first_bias;
+        same &= b == first_bias;
+        bias[e / N * kPitch + e % N] = b;
+    }
+    const bool by_logit = chosen_by_logit(p, __syncthreads_and(same));
+    const bool sums = !p.sigmoid && (!p.renormalize || !by_logit);
+    const auto most = [](float x, float y) { return fmaxf(x, y); };
+    const auto plus = [](float x, float y) { return x + y; };
+    const long long begin = static_cast<long long>(blockIdx.x) * p.per, end = min(static_cast<long long>(p.T), begin + p.per);
+    const int bit = threadIdx.x >> 2;
+    int mine[2] = {-1, -1}, rank[2] = {-1, -1};  // choices q and q + 4 of the last step
+    for (int step = 0; step < p.steps; ++step) {
+        const long long t = begin + step * p.step + bit;
+        const bool there = t < end;
+        const T* const row = static_cast<const T*>(p.logits) + (there ? t : begin) * p.ld;
+        float top = 0.f, sum = 0.f, low = 0.f, high = 0.f;
+        bool sure;
+        {
+            float v[N];
+            if (there) {
+                load_row<N>(row, first, p.E, p.vec, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = -INFINITY;
+            }
+            if (sums) {
+                top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < N; ++i) top = fmaxf(top, v[i]);
+                top = over_quad(top, most);
+                float part[8] = {};  // (few roundings; see choice_error)
+#pragma unroll
+                for (int i = 0; i < N; ++i) part[i % 8] += v[i] == -INFINITY ? 0.f : fast_exp(v[i] - top);
+#pragma unroll
+                for (int d = 4; d; d /= 2)
+#pragma unroll
+                    for (int i = 0; i < d; ++i) part[i] += part[i + d];
+                sum = over_quad(part[0], plus);
+            }
+            uint32_t key[N], best[8], gap = 0, group_gap = 0;
+            bool grid = true;
+            if (sizeof(T) == 2 && by_logit) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    key[i] = v[i] == -INFINITY ? 0u : (Keys<float>::of(v[i]) & ~kExpertBits) | (kExpertBits - (first + i));
+            } else {
+                if (!by_logit) {
+                    const float inv = fast_reciprocal(sum);
+#pragma unroll
+                    for (int i = 0; i < N; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(bias + q * kPitch + i);
+                        const float b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) v[i + u] = choice_value(p, v[i + u], b[u], top, inv);
+                    }
+                }
+                high = -INFINITY, low = INFINITY;
+                range_of(v, high, low);
+                high = over_quad(high, [](float x, float y) { return max_nan(x, y); });
+                low = over_quad(low, [](float x, float y) { return fminf(x, y); });
+                const float scale = grid_scale(high - low);
+                grid = on_grid(high - low);
+                place_on_grid(v, low, scale, first, key);
+                if (!by_logit) {
+                    const float steps = choice_steps(p, low, high, sum, scale);
+                    gap = choice_gap(steps), group_gap = score_gap(p, steps);
+                }
+            }
+            sure = choose_quad(key, p, gap, group_gap, best) || (sizeof(T) == 2 && by_logit);
+            if (!grid) sure = high == -INFINITY;  // (nobody is in service)
+            // choices q and q + 4
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t x = q & 1 ? best[4 * i + 1] : best[4 * i], y = q & 1 ? best[4 * i + 3] : best[4 * i + 2];
+                const uint32_t b = q & 2 ? y : x;
+                mine[i] = grid && b > kExpertBits && q + 4 * i < p.k ? static_cast<int>(kExpertBits - (b & kExpertBits)) : -1;
+            }
+        }
+        // The tokens that are not sure, one after another, by the whole warp.
+        for (unsigned left = __ballot_sync(kAll, !sure && q == 0); left; left &= left - 1) {
+            const int from = __ffs(left) - 1;
+            const long long other = __shfl_sync(kAll, t, from);
+            const int e = choose_again<N / 8>(p, static_cast<const T*>(p.logits) + other * p.ld, by_logit,
+                                              __shfl_sync(kAll, top, from), __shfl_sync(kAll, sum, from));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int theirs = __shfl_sync(kAll, e, q + 4 * i);
+                if ((lane & 28) == from) mine[i] = theirs;
+            }
+        }
+        float x[2], s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[i] = mine[i] >= 0 ? to_f32(row[mine[i]]) : -INFINITY;
+        const float lead = p.renormalize ? over_quad(fmaxf(x[0], x[1]), most) : top;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s[i] = mine[i] < 0 ? 0.f : score_over(p, x[i], lead, sum);
+        if (p.renormalize) sum = over_quad(s[0] + s[1], plus);
+        const float share = p.sigmoid && !p.renormalize ? 1.f : fast_reciprocal(sum);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = q + 4 * i;
+            if (there && j < p.k) {
+                p.experts[t * p.k + j] = mine[i];
+                p.weights[t * p.k + j] = mine[i] < 0 ? 0.f : p.scale * s[i] * share;
+                if (mine[i] >= 0) atomicOr(mask + mine[i], 1 << bit);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = q + 4 * i;
+            rank[i] = mine[i] < 0 ? -1 : count[mine[i]] + __popc(mask[mine[i]] & ((1u << bit) - 1));
+            if (step + 1 < p.steps && there && j < p.k) p.slots[t * p.k + j] = rank[i];
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += kQuadThreads) {
+            count[e] += __popc(mask[e]);
+            mask[e] = 0;
+        }
+        __syncthreads();
+    }
+    cluster_counts(p, count, before, mask);
+    cluster_sync_all();  // (nobody reads this CTA's counts after this)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const long long t = begin + (p.steps - 1) * p.step + bit;
+        const int j = q + 4 * i;
+        if (t < end && j < p.k) p.slots[t * p.k + j] = mine[i] < 0 ? -1 : rank[i] + before[mine[i]];
+    }
+    if (p.steps > 1) {  // the steps before the last, whose places are in memory
+        const long long from = begin * p.k, to = min(end, begin + (p.steps - 1) * p.step) * p.k;
+        for (long long i = from + threadIdx.x; i < to; i += kQuadThreads) {
+            const int e = p.experts[i];
+            if (e >= 0) p.slots[i] += before[e];
+        }
+    }
+}
+
 // Places within a cluster's rows of an expert to places among all rows.
 __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams p, int clusters) {
     extern __shared__ __align__(16) int shared[];
@@ -728,12 +1030,13 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
     __syncthreads();
     grid_dependency_wait();
     // (the first choices' experts on their way beside the counts)
-    const long long per = static_cast<long long>(p.per) * p.k, all = static_cast<long long>(p.T) * p.k;
+    const long long per = static_cast<long long>(p.place_per) * p.k, all = static_cast<long long>(p.T) * p.k;
     const long long from = blockIdx.x * per, to = min(all, from + per);
-    const int mine = static_cast<int>(blockIdx.x) / p.width;
-    int expert[2], slot[2];
+    const int mine = static_cast<int>(blockIdx.x) / p.place_width;
+    constexpr int kAhead = 4;
+    int expert[kAhead], slot[kAhead];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
         const long long i = from + threadIdx.x + u * kRouteThreads;
         expert[u] = i < to ? p.experts[i] : -1;
         slot[u] = i < to ? p.slots[i] : -1;
@@ -756,9 +1059,9 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
     __syncthreads();
     exclusive_sums(total, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kAhead; ++u)
         if (expert[u] >= 0) p.slots[from + threadIdx.x + u * kRouteThreads] = slot[u] + base[expert[u]] + before[expert[u]];
-    for (long long i = from + threadIdx.x + 2 * kRouteThreads; i < to; i += kRouteThreads) {
+    for (long long i = from + threadIdx.x + kAhead * kRouteThreads; i < to; i += kRouteThreads) {
         const int e = p.experts[i];
         if (e >= 0) p.slots[i] += base[e] + before[e];
     }
@@ -826,7 +1129,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
             if (e >= 0) g = p.scale * d * s * rest;
         } else {
             float l[NPL];
-            load_row<NPL>(row, p.E, p.vec, l);
+            load_row<NPL>(row, lane * NPL, p.E, p.vec, l);
             float most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) most = fmaxf(most, l[i]);
@@ -904,29 +1207,29 @@ int launched() {
 
 }  // namespace
 
-RoutePlan route_plan(int T, int sms) {
+RoutePlan route_plan(const RouteParams& p, int sms) {
+    const int T = p.T;
     // One cluster finishes by itself, which saves a launch.
-    if (T <= kRouteWarps) return {1, 1, T, kRouteWarps};
-    constexpr int step = 2 * kRouteWarps;
-    if (T <= 2 * kRouteCluster * step) {
+    if (T <= kRouteWarps) return {1, 1, T, kRouteWarps, false};
+    constexpr int whole = 2 * kRouteWarps;
+    if (T <= 2 * kRouteCluster * whole) {
         const int per = (T + kRouteCluster - 1) / kRouteCluster;
-        return {1, kRouteCluster, per, per <= kRouteWarps ? kRouteWarps : step};
+        return {1, kRouteCluster, per, per <= kRouteWarps ? kRouteWarps : whole, false};
     }
-    // Two CTAs an SM at once, whole steps each.
-    const int most = std::max(1, 2 * sms / kRouteCluster) * kRouteCluster;
+    // Two CTAs an SM at once (four of a quarter of the threads), whole steps each.
+    const bool quads = p.k <= 8 && p.E <= 256 && (p.groups == 1 || (p.group_size >= 8 && !(p.group_size & (p.group_size - 1))));
+    const int step = quads ? kQuadStep : whole;
+    const int most = std::max(1, (quads ? 4 : 2) * sms / kRouteCluster) * kRouteCluster;
     const int per = ((T + most - 1) / most + step - 1) / step * step;
     const int ctas = (T + per - 1) / per;
-    return {(ctas + kRouteCluster - 1) / kRouteCluster, kRouteCluster, per, step};
+    return {(ctas + kRouteCluster - 1) / kRouteCluster, kRouteCluster, per, step, quads};
 }
 
 int route(const RouteParams& given, const RoutePlan& plan, int type, cudaStream_t s) {
     RouteParams p = given;
-    // (the bias to the last lane's end: E up to a power of two from 32 on)
-    const size_t smem = (5 * static_cast<size_t>(std::max(p.E, 32)) + kRouteWarps) * sizeof(int);
+    p.width = plan.width, p.per = plan.per, p.step = plan.step, p.steps = (plan.per + plan.step - 1) / plan.step;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters * plan.width));
-    cfg.blockDim = dim3(kRouteThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -934,18 +1237,39 @@ int route(const RouteParams& given, const RoutePlan& plan, int type, cudaStream_
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = plan.width > 1 ? 1 : 0;
+    const auto start = [&](auto kernel) {
+        if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return static_cast<int>(SGEMM_OK);
+        (void)cudaGetLastError();
+        return static_cast<int>(SGEMM_ERR_CUDA);
+    };
+    // (the bias to the last lane's end: E up to a power of two from 32 on)
+    const size_t smem = (5 * static_cast<size_t>(std::max(p.E, 32)) + kRouteWarps) * sizeof(int);
     const int rc = by_type_and_width(type, p.E, [&](auto zero, auto npl) {
         constexpr int NPL = decltype(npl)::value;
         using T = decltype(zero);
+        if constexpr (NPL <= 8) {
+            if (plan.quads) {
+                constexpr int N = std::max(16, 8 * NPL);
+                cfg.blockDim = dim3(kQuadThreads);
+                cfg.dynamicSmemBytes = (4 * (N + 4) + 3 * static_cast<size_t>(p.E)) * sizeof(int);
+                return start(route_quads_kernel<N, T>);
+            }
+        }
         const int lanes = p.group_size / NPL;
         p.group_lanes = 0;
         while (1 << p.group_lanes < lanes) ++p.group_lanes;
         if (p.groups > 1 && (p.group_size % NPL || 1 << p.group_lanes != lanes)) p.group_lanes = -1;
-        if (cudaLaunchKernelEx(&cfg, route_kernel<NPL, T>, p) == cudaSuccess) return static_cast<int>(SGEMM_OK);
-        (void)cudaGetLastError();
-        return static_cast<int>(SGEMM_ERR_CUDA);
+        cfg.blockDim = dim3(kRouteThreads);
+        cfg.dynamicSmemBytes = smem;
+        return start(route_kernel<NPL, T>);
     });
     if (rc != SGEMM_OK || !p.counts) return rc;
+    // Places by CTA, or, of the smaller CTAs, by cluster.
+    p.place_per = plan.quads ? plan.per * plan.width : plan.per;
+    p.place_width = plan.quads ? 1 : plan.width;
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters * p.place_width));
+    cfg.blockDim = dim3(kRouteThreads);
+    cfg.dynamicSmemBytes = smem;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;

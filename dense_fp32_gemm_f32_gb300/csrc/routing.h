@@ -22,19 +22,22 @@ struct RouteParams {
     int* offsets;
     int* slots;
     int vec;      // the rows begin on 16 bytes: whole vectors are loaded
-    int width, per;    // CTAs of a cluster, tokens of a CTA
+    int width, per;    // CTAs of a cluster, tokens of a CTA (these to place_width are set by route)
     int steps, step;   // a CTA's steps, and the tokens of one
+    int place_per, place_width;  // of the second kernel: tokens of a CTA, CTAs for a cluster's
     int* counts;      // clusters x E: choices of each expert (null: one cluster does it all)
 };
 
 // Warps of a CTA, and CTAs of a cluster where there is more than one.
 constexpr int kRouteWarps = 16, kRouteCluster = 8;
+constexpr int kQuadStep = 32;  // tokens of a CTA's step with four lanes a token
 
-// The grid of a routing: clusters of `width` CTAs, each CTA's tokens, and those of a step.
+// The grid of a routing: clusters of `width` CTAs, each CTA's tokens, and those of a step; four lanes a token or a warp.
 struct RoutePlan {
     int clusters, width, per, step;
+    bool quads;
 };
-RoutePlan route_plan(int T, int sms);
+RoutePlan route_plan(const RouteParams& p, int sms);
 int route(const RouteParams& p, const RoutePlan& plan, int type, cudaStream_t s);
 
 struct RouteGradParams {
