@@ -217,12 +217,16 @@ __device__ __forceinline__ float choice_error(const RouteParams& p, float size, 
     return 0x1p-22f * size + (p.sigmoid ? 0x1p-20f : 0x1p-18f * fast_reciprocal(sum));
 }
 
+// Loops over a lane's values are unrolled as long as registers hold these.
+template <int NPL>
+constexpr int kUnrolled = NPL <= 8 ? NPL : 1;
+
 // The largest key's place: (lane, number) with the lowest expert.  Whole warp; 0 if there is none.
 template <int NPL, typename V>
 __device__ __forceinline__ typename Keys<V>::Key largest(const typename Keys<V>::Key (&key)[NPL], int& e) {
     typename Keys<V>::Key m = key[0];
     int at = 0;
-#pragma unroll 1
+#pragma unroll kUnrolled<NPL>
     for (int i = 1; i < NPL; ++i)
         if (key[i] > m) m = key[i], at = i;
     const auto best = Keys<V>::most(m);
@@ -231,51 +235,61 @@ __device__ __forceinline__ typename Keys<V>::Key largest(const typename Keys<V>:
     return best;
 }
 
+__device__ __noinline__ double exp64(double x) { return exp(x); }
+
 // The choice with keys of 32 bits.  Where those that decide are within their
 // errors of one another, these alone are compared again: by their logits if they
 // have one bias (a bias of zeros, or equal scores of which a token of
 // padding has many), else computed in 64 bits.
 // Few tokens come here, and the rest wait for them: so little is computed in 64
-// bits (2 lanes a cycle of an SM), and loops are not unrolled (instructions that
-// nobody has fetched before: 25 us for the first token of a prompt).
+// bits (2 lanes a cycle of an SM), in one place (instructions that
+// nobody has fetched before: 25 us for the first token of a prompt with the loops around them unrolled).
 template <int NPL, typename T>
 __device__ __noinline__ int choose_again(const RouteParams& p, const T* row, bool by_logit, float top, float sum) {
     using K = Keys<float>;
     const int lane = threadIdx.x & 31, first = lane * NPL;
     float l[NPL], bias[NPL], size = 0.f, near = 0.f;
     uint32_t key[NPL];
-#pragma unroll 1
+#pragma unroll kUnrolled<NPL>
     for (int i = 0; i < NPL; ++i) {
         const bool there = first + i < p.E;
         l[i] = there ? to_f32(row[first + i]) : -INFINITY;
         bias[i] = there && p.bias ? p.bias[first + i] : 0.f;
+    }
+    const float inv = fast_reciprocal(sum);
+#pragma unroll kUnrolled<NPL>
+    for (int i = 0; i < NPL; ++i) {
         float c = l[i];
-        if (!by_logit && c != -INFINITY) {
-            c = (p.sigmoid ? fast_reciprocal(1.f + fast_exp(-c)) : fast_exp(c - top) * fast_reciprocal(sum)) + bias[i];
+        if (!by_logit) {
+            c = choice_value(p, c, bias[i], top, inv);
             if (fabsf(c) < INFINITY) size = fmaxf(size, fabsf(c));
         }
         key[i] = c == -INFINITY ? 0u : K::of(c);
     }
     if (!by_logit) near = choice_error(p, warp_max(size), sum);  // (logits are exact)
     double all = 0;  // the softmax's sum, once it is needed
-    // 64-bit keys of the lane's values whose bit is set in `some`, 0 for the others.
-    auto evaluate = [&](uint32_t some, unsigned long long (&exact)[NPL]) {
+    // use(i, 64-bit key) for the lane's values whose bit is set in `some`, one after another; one that is as the one before
+    // is not computed again.
+    auto evaluate = [&](uint32_t some, auto use) {
+        const double less = p.sigmoid ? 0. : static_cast<double>(top);
         if (!p.sigmoid && all == 0) {
 #pragma unroll 1
-            for (int i = 0; i < NPL; ++i) all += l[i] == -INFINITY ? 0. : exp(static_cast<double>(l[i]) - top);
+            for (int i = 0; i < NPL; ++i) all += first + i < p.E ? exp64(to_f32(row[first + i]) - less) : 0.;
             all = warp_sum(all);
         }
-        float last = NAN, last_bias = 0.f;  // (neighbours that are alike are computed once)
-        unsigned long long last_key = 0;
-#pragma unroll 1
-        for (int i = 0; i < NPL; ++i) {
-            const bool wanted = some >> i & 1, known = l[i] == last && bias[i] == last_bias;
-            if (__any_sync(kAll, wanted && !known)) {
-                const double x = l[i];
-                last_key = Keys<double>::of((p.sigmoid ? 1. / (1. + exp(-x)) : exp(x - top) / all) + bias[i]);
-                last = l[i], last_bias = bias[i];
+        float before = NAN, before_bias = 0.f;
+        unsigned long long value = 0;
+        for (; __any_sync(kAll, some); some &= some - 1) {
+            if (some) {
+                const int i = __ffs(some) - 1;
+                const float logit = to_f32(row[first + i]), b = p.bias ? p.bias[first + i] : 0.f;
+                if (!(logit == before && b == before_bias)) {
+                    const double x = logit - less, y = exp64(p.sigmoid ? -x : x);
+                    value = Keys<double>::of((p.sigmoid ? 1. / (1. + y) : y / all) + b);
+                    before = logit, before_bias = b;
+                }
+                use(i, value);
             }
-            exact[i] = wanted ? last_key : 0;
         }
     };
     if (p.groups > 1) {
@@ -304,14 +318,19 @@ __device__ __noinline__ int choose_again(const RouteParams& p, const T* row, boo
             const int size = p.group_size;
             const float second = b ? K::value(b) : -INFINITY;
             uint32_t some = 0;
-#pragma unroll 1
+            unsigned long long exact[NPL] = {}, best, next;
+            int g = first / size, rest = first - g * size;
+#pragma unroll kUnrolled<NPL>
             for (int i = 0; i < NPL; ++i) {
-                const int g = min((first + i) / size, 31);
                 const float from = __shfl_sync(kAll, p.group_best == 2 ? second : there ? K::value(a) : 0.f, g) - near;
-                if (key[i] && (open >> g & 1) && !(K::value(key[i]) < from)) some |= 1u << i;
+                if (key[i] && g < 32 && (open >> g & 1) && !(K::value(key[i]) < from)) some |= 1u << i;
+                if (++rest == size) rest = 0, ++g;
             }
-            unsigned long long exact[NPL], best, next;
-            evaluate(some, exact);
+            evaluate(some, [&](int at, unsigned long long x) {
+#pragma unroll kUnrolled<NPL>
+                for (int i = 0; i < NPL; ++i)
+                    if (i == at) exact[i] = x;
+            });
             group_best<NPL>(exact, p, best, next);
             unsigned long long value = 0;
             if (open >> lane & 1) {
@@ -338,29 +357,33 @@ __device__ __noinline__ int choose_again(const RouteParams& p, const T* row, boo
         if (near > 0.f && fabsf(v) < INFINITY) {
             const uint32_t from = K::of(v - near);
             uint32_t some = 0;
-#pragma unroll 1
+#pragma unroll kUnrolled<NPL>
             for (int i = 0; i < NPL; ++i)
                 if (key[i] >= from) some |= 1u << i;
             if (__reduce_add_sync(kAll, __popc(some)) > 1) {
                 const float one = p.bias ? p.bias[e] : 0.f;
                 bool other = false;
                 uint32_t logit[NPL];
-#pragma unroll 1
+#pragma unroll kUnrolled<NPL>
                 for (int i = 0; i < NPL; ++i) {
                     logit[i] = some >> i & 1 ? K::of(l[i]) : 0u;
                     other |= (some >> i & 1) && bias[i] != one;
                 }
                 if (__any_sync(kAll, other)) {
-                    unsigned long long exact[NPL];
-                    evaluate(some, exact);
-                    (void)largest<NPL, double>(exact, e);
+                    unsigned long long top64 = 0;
+                    int at = 0;
+                    evaluate(some, [&](int i, unsigned long long x) {
+                        if (x > top64) top64 = x, at = i;
+                    });
+                    const unsigned long long best64 = Keys<double>::most(top64);
+                    e = __shfl_sync(kAll, first + at, __ffs(__ballot_sync(kAll, top64 == best64)) - 1);
                 } else {
                     (void)largest<NPL, float>(logit, e);
                 }
             }
         }
         if (lane == j) mine = e;
-#pragma unroll 1
+#pragma unroll kUnrolled<NPL>
         for (int i = 0; i < NPL; ++i)
             if (first + i == e) key[i] = 0;
     }
