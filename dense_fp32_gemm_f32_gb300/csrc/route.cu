@@ -648,7 +648,7 @@ __device__ __forceinline__ void exclusive_sums(const int* count, int E, int* bas
 }
 
 // The CTAs of a cluster add up their counts: `before` those of the CTAs before this one, `sums` those of all, which
-// also go to p.counts.  A cluster's barrier has to follow before a CTA's counts change.
+// also go to p.counts.
 __device__ __forceinline__ void cluster_counts(const RouteParams& p, const int* count, int* before, int* sums) {
     const int of = static_cast<int>(cluster_ctarank());
     cluster_sync_all();
@@ -664,6 +664,14 @@ __device__ __forceinline__ void cluster_counts(const RouteParams& p, const int* 
         sums[e] = sum;
         if (p.counts && of == 0) p.counts[static_cast<long long>(blockIdx.x / p.width) * p.E + e] = sum;
     }
+    cluster_sync_all();  // (nobody reads this CTA's counts after this)
+}
+
+// One cluster did it all: what comes before a CTA's choices of an expert among all, to `before`, and the boundaries.
+__device__ __forceinline__ void finish_counts(const RouteParams& p, int* base, int* before, const int* sums, int* scratch) {
+    exclusive_sums(sums, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) before[e] += base[e];
+    __syncthreads();
 }
 
 // The CTAs of a cluster (p.width) add up their counts of each expert's choices
@@ -736,13 +744,7 @@ __global__ void __launch_bounds__(kRouteThreads, NPL <= 8 ? 2 : 1) route_kernel(
         __syncthreads();
     }
     cluster_counts(p, count, before, mask);
-    cluster_sync_all();  // (nobody reads this CTA's counts after this)
-    if (!p.counts) {
-        int* const base = count;
-        exclusive_sums(mask, p.E, base, blockIdx.x == 0 ? p.offsets : nullptr, scratch);
-        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) before[e] += base[e];
-        __syncthreads();
-    }
+    if (!p.counts) finish_counts(p, count, before, mask, scratch);
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
         const long long t = begin + (p.steps - 1) * p.step + warp + i * kRouteWarps;
@@ -889,7 +891,7 @@ __device__ __forceinline__ bool choose_quad(uint32_t (&key)[N], const RouteParam
     return !close;
 }
 
-// As route_kernel with several clusters, for k <= 8 and E <= 4 N.
+// As route_kernel, for k <= 8 and E <= 4 N.
 template <int N, typename T>
 __global__ void __launch_bounds__(kQuadThreads, 4) route_quads_kernel(const RouteParams p) {
     constexpr int kPitch = N + 4;  // (the four lanes' vectors of the bias from other banks)
@@ -898,8 +900,9 @@ __global__ void __launch_bounds__(kQuadThreads, 4) route_quads_kernel(const Rout
     int* const mask = shared + 4 * kPitch;                 // E each, as route_kernel's
     int* const count = mask + p.E;
     int* const before = count + p.E;
+    int* const scratch = before + p.E;  // a word a warp
     grid_dependency_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane & 3, first = q * N;
+    const int lane = threadIdx.x & 31, q = lane & 3, first = q * N;
     for (int e = threadIdx.x; e < p.E; e += kQuadThreads) mask[e] = count[e] = 0;
     const float first_bias = p.bias ? __ldg(p.bias) : 0.f;
     bool same = fabsf(first_bias) < INFINITY;
@@ -1026,7 +1029,7 @@ __global__ void __launch_bounds__(kQuadThreads, 4) route_quads_kernel(const Rout
         __syncthreads();
     }
     cluster_counts(p, count, before, mask);
-    cluster_sync_all();  // (nobody reads this CTA's counts after this)
+    if (!p.counts) finish_counts(p, count, before, mask, scratch);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const long long t = begin + (p.steps - 1) * p.step + bit;
@@ -1232,20 +1235,23 @@ int launched() {
 
 RoutePlan route_plan(const RouteParams& p, int sms) {
     const int T = p.T;
-    // One cluster finishes by itself, which saves a launch.
-    if (T <= kRouteWarps) return {1, 1, T, kRouteWarps, false};
-    constexpr int whole = 2 * kRouteWarps;
-    if (T <= 2 * kRouteCluster * whole) {
+    // Four lanes a token where they can, but for many experts and a token a warp at most: its 32 lanes are done sooner. us
+    // (four lanes / a warp), 64 experts: 1 to 16 tokens 3.3 / 3.7, 64 4.1 / 4.6, 256 4.2 / 6.1, 512 6.5 / 9.5; 256 experts in
+    // groups: 16 7.4 / 6.1, 64 8.9 / 6.2, 200 9.5 / 9.8, 512 12 / 16, 16384 28 / 40.
+    const bool quads = p.k <= 8 && p.E <= 256 && (p.groups == 1 || (p.group_size >= 8 && !(p.group_size & (p.group_size - 1)))) &&
+                       (p.E <= 64 || T > kRouteCluster * kRouteWarps);
+    // One CTA or one cluster finishes by itself, which saves a launch.
+    const int whole = quads ? kQuadStep : 2 * kRouteWarps;
+    if (T <= kRouteWarps) return {1, 1, T, quads ? whole : kRouteWarps, quads};
+    if (T <= (quads ? 1 : 2) * kRouteCluster * whole) {
         const int per = (T + kRouteCluster - 1) / kRouteCluster;
-        return {1, kRouteCluster, per, per <= kRouteWarps ? kRouteWarps : whole, false};
+        return {1, kRouteCluster, per, !quads && per <= kRouteWarps ? kRouteWarps : whole, quads};
     }
     // Two CTAs an SM at once (four of a quarter of the threads), whole steps each.
-    const bool quads = p.k <= 8 && p.E <= 256 && (p.groups == 1 || (p.group_size >= 8 && !(p.group_size & (p.group_size - 1))));
-    const int step = quads ? kQuadStep : whole;
     const int most = std::max(1, (quads ? 4 : 2) * sms / kRouteCluster) * kRouteCluster;
-    const int per = ((T + most - 1) / most + step - 1) / step * step;
+    const int per = ((T + most - 1) / most + whole - 1) / whole * whole;
     const int ctas = (T + per - 1) / per;
-    return {(ctas + kRouteCluster - 1) / kRouteCluster, kRouteCluster, per, step, quads};
+    return {(ctas + kRouteCluster - 1) / kRouteCluster, kRouteCluster, per, whole, quads};
 }
 
 int route(const RouteParams& given, const RoutePlan& plan, int type, cudaStream_t s) {
@@ -1274,7 +1280,7 @@ int route(const RouteParams& given, const RoutePlan& plan, int type, cudaStream_
             if (plan.quads) {
                 constexpr int N = std::max(16, 8 * NPL);
                 cfg.blockDim = dim3(kQuadThreads);
-                cfg.dynamicSmemBytes = (4 * (N + 4) + 3 * static_cast<size_t>(p.E)) * sizeof(int);
+                cfg.dynamicSmemBytes = (4 * (N + 4) + 3 * static_cast<size_t>(p.E) + kQuadWarps) * sizeof(int);
                 return start(route_quads_kernel<N, T>);
             }
         }
