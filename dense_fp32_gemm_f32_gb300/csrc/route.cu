@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
     const int parts = kRouteThreads / width, part = threadIdx.x / width;
     for (int e = threadIdx.x % width; e < p.E; e += width) {
         int sum = 0, sum_before = 0;
-#pragma unroll 8
+#pragma unroll 16
         for (int c = part; c < clusters; c += parts) {
             const int n = p.counts[static_cast<long long>(c) * p.E + e];
             sum += n;
