@@ -1,11 +1,13 @@
 // Routing of tokens to experts, and its gradient (include/sgemm_routing.h).
 //
-// A warp takes a token.  Lane l holds the scores of experts l * NPL .. l * NPL
-// + NPL - 1, so that a row comes in with wide loads, a lane's experts are
+// Two forms.  A warp takes a token (route_kernel): lane l holds the scores of experts l * NPL
+// .. l * NPL + NPL - 1, so that a row comes in with wide loads, a lane's experts are
 // neighbours (groups span whole lanes) and the lowest of equal experts is the
 // lowest lane's.  Scores are compared as unsigned keys in their order, 0 for
 // an expert out of service: the warp's largest is then one redux instruction,
 // and k of them with the lane's own largest kept up to date make the choice.
+// Or four lanes take a token (route_quads_kernel), up to 8 of 256 experts: what the other
+// form does once a warp for a token is done for eight at a time.
 //
 // What the choice is by.  Without a bias, or with one that is the same for all (and
 // with group_best = 1), both scores grow with the logit, so logits are compared.  Otherwise float32 scores
@@ -19,18 +21,20 @@
 // each chosen expert (an OR: its order does not matter); a choice's place
 // among the expert's rows in this CTA is then the number of bits below its own
 // plus those of the steps before.  The CTAs of a cluster add up their counts
-// through distributed shared memory.  Up to 512 tokens are one cluster, which
+// through distributed shared memory.  Up to 256 (512) tokens are one cluster, which
 // then knows all; else the clusters' counts go to a table, and place_kernel adds
 // up those of the clusters and of the experts before.
 //
 // Bound by instructions, not by bytes (16384 x 256 bf16: 10 MB, 1.5 us): about 1000 of
-// a warp a token for scores, grid, sort and k rounds, on SMs that issue half of the time;
+// a warp a token for scores, grid, sort and k rounds, 420 with four lanes a token, whose warps also wait for the
+// instructions themselves (50 KB without a loop);
 // for a few tokens by latency.  Measured on GB300 (replayed from a CUDA graph): 16384 tokens, 8 of 256
-// experts, sigmoid, bias, 4 of 8 groups 43 us (the counts' second kernel 6 of them), by
-// softmax alone 22 us; 64 tokens 6.1 us; one token, 4 of 64 3.5 us.  What carried it:
-// two CTAs an SM (67 -> 60 us), keys that hold their expert (51 -> 26 us by softmax), no
+// experts, sigmoid, bias, 4 of 8 groups 28 us (43 with a warp a token; 22 where no scores lie so near one another
+// that choose_again decides, which all wait for), by softmax alone 17 us (22), 64 tokens of the former 6.2 us; 65536
+// tokens, 6 of 64 25 us; one token, 4 of 64 3.3 us.  What carried it:
+// keys that hold their expert (51 -> 26 us by softmax), no
 // division and no float64 but for the contested values (60 -> 47 us), clusters instead of a
-// second launch (64 tokens 16 -> 6 us).
+// second launch (64 tokens 16 -> 6 us), four lanes a token (43 -> 37 us), choose_again's values in registers (37 -> 28 us).
 #include <algorithm>
 #include <type_traits>
 
