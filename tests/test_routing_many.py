@@ -78,3 +78,54 @@ def test_rows_apart(pad, shift, dtype):
     view.copy_(logits)
     for a, b in zip(g.sgemm_route(view, 8), g.sgemm_route(logits, 8)):
         assert torch.equal(a, b)
+
+
+SIZES = [(5000, 256, 8, dict(score="sigmoid", bias=1, groups=8, top_groups=4, group_best=2)), (300, 64, 6, dict()), (70000, 32, 2, dict(bias=1))]
+
+
+def case(T, E, how, seed):
+    how = dict(how)
+    if "bias" in how:
+        how["bias"] = 0.1 * randn(E, seed=3)
+    return randn(T, E, seed=seed, dtype=torch.bfloat16), how
+
+
+@pytest.mark.parametrize("T, E, k, how", SIZES, ids=str)
+def test_many_recorded_calls(T, E, k, how):
+    """Two graphs on two streams at once, replayed with other logits."""
+    graphs = []
+    for seed in (1, 2):
+        logits, kw = case(T, E, how, seed)
+        g.sgemm_route(logits, k, **kw)
+        torch.cuda.synchronize()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            r = g.sgemm_route(logits, k, **kw)
+        graphs.append((graph, stream, logits, kw, r))
+    for again in range(3):
+        for i, (graph, stream, logits, kw, r) in enumerate(graphs):
+            logits.copy_(case(T, E, how, 10 * again + i)[0])
+        torch.cuda.synchronize()
+        for graph, stream, *_ in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, stream, logits, kw, r in graphs:
+            for a, b in zip(r, g.sgemm_route(logits, k, **kw)):
+                assert torch.equal(a, b)
+    assert g.check_status() == 0
+
+
+@pytest.mark.parametrize("T, E, k, how", SIZES, ids=str)
+def test_many_calls_at_once(T, E, k, how):
+    """On four streams, each over other logits; every result is that of the call alone."""
+    cases = [case(T, E, how, seed) for seed in range(4)]
+    alone = [g.sgemm_route(logits, k, **kw) for logits, kw in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    results = [[g.sgemm_route(logits, k, stream=s, **kw) for (logits, kw), s in zip(cases, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for some in results:
+        for r, want in zip(some, alone):
+            assert all(torch.equal(a, b) for a, b in zip(r, want))
+    assert g.check_status() == 0
