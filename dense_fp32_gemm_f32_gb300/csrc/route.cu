@@ -29,8 +29,9 @@
 // a warp a token for scores, grid, sort and k rounds, 420 with four lanes a token, whose warps also wait for the
 // instructions themselves (50 KB without a loop);
 // for a few tokens by latency.  Measured on GB300 (replayed from a CUDA graph): 16384 tokens, 8 of 256
-// experts, sigmoid, bias, 4 of 8 groups 28 us (43 with a warp a token; 22 where no scores lie so near one another
-// that choose_again decides, which all wait for), by softmax alone 17 us (22), 64 tokens of the former 6.2 us; 65536
+// experts, sigmoid, bias, 4 of 8 groups 28 to 31 us (43 with a warp a token; 22 where no scores lie so near one another
+// that choose_again decides, which all wait for; with a bias of zeros, where equal bf16 logits are many, 40, and 75 if these
+// all went there), by softmax alone 17 us (22), 64 tokens of the former 6.2 us; 65536
 // tokens, 6 of 64 25 us; one token, 4 of 64 3.3 us.  What carried it:
 // keys that hold their expert (51 -> 26 us by softmax), no
 // division and no float64 but for the contested values (60 -> 47 us), clusters instead of a
@@ -800,9 +801,10 @@ __device__ __forceinline__ V over_quad(V v, F f) {
 }
 
 // choose_packed of four lanes: their keys to the best eight, sorted, in `best`.  Groups are powers of two from 8 on.
+// False where it is not certain which these are; bit j of `near` where it is not that the j-th is behind the one before.
 template <int N>
 __device__ __forceinline__ bool choose_quad(uint32_t (&key)[N], const RouteParams& p, uint32_t gap, uint32_t group_gap,
-                                            uint32_t (&best)[8]) {
+                                            uint32_t (&best)[8], uint32_t& near) {
     constexpr int B = N / 8;  // blocks of eight keys
     const int block = (threadIdx.x & 3) * B;
     const auto most = [](uint32_t x, uint32_t y) { return max(x, y); };
@@ -890,7 +892,9 @@ __device__ __forceinline__ bool choose_quad(uint32_t (&key)[N], const RouteParam
 #pragma unroll
     for (int j = 1; j <= 8; ++j) {
         const uint32_t here = j < 8 ? best[j & 7] : next;
-        close |= j <= p.k && here > kExpertBits && (best[j - 1] >> kExpertShift) - (here >> kExpertShift) <= gap;
+        const bool two = here > kExpertBits && (best[j - 1] >> kExpertShift) - (here >> kExpertShift) <= gap;
+        close |= j == p.k && two;
+        near |= j < p.k && two ? 1u << j : 0u;
     }
     return !close;
 }
@@ -928,6 +932,7 @@ __global__ void __launch_bounds__(kQuadThreads, 4) route_quads_kernel(const Rout
         const T* const row = static_cast<const T*>(p.logits) + (there ? t : begin) * p.ld;
         float top = 0.f, sum = 0.f, low = 0.f, high = 0.f;
         bool sure;
+        uint32_t near = 0;
         {
             float v[N];
             if (there) {
@@ -979,8 +984,9 @@ __global__ void __launch_bounds__(kQuadThreads, 4) route_quads_kernel(const Rout
                     gap = choice_gap(steps), group_gap = score_gap(p, steps);
                 }
             }
-            sure = choose_quad(key, p, gap, group_gap, best) || (sizeof(T) == 2 && by_logit);
-            if (!grid) sure = high == -INFINITY;  // (nobody is in service)
+            sure = choose_quad(key, p, gap, group_gap, best, near);
+            if (sizeof(T) == 2 && by_logit) sure = true, near = 0;
+            if (!grid) sure = high == -INFINITY, near = 0;  // (nobody is in service)
             // choices q and q + 4
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -988,6 +994,28 @@ __global__ void __launch_bounds__(kQuadThreads, 4) route_quads_kernel(const Rout
                 const uint32_t b = q & 2 ? y : x;
                 mine[i] = grid && b > kExpertBits && q + 4 * i < p.k ? static_cast<int>(kExpertBits - (b & kExpertBits)) : -1;
             }
+        }
+        // Choices that lie near one another are in order where their logits are, if they have one bias.
+        if (__any_sync(kAll, near)) {
+            const int behind = (lane & 28) | ((lane + 1) & 3);
+            float l[2], b[2], next_l[2], next_b[2];
+            int next_e[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] = mine[i] >= 0 ? to_f32(row[mine[i]]) : -INFINITY;
+                b[i] = mine[i] >= 0 ? bias[mine[i] / N * kPitch + mine[i] % N] : 0.f;
+                next_l[i] = __shfl_sync(kAll, l[i], behind);
+                next_b[i] = __shfl_sync(kAll, b[i], behind);
+                next_e[i] = __shfl_sync(kAll, mine[i], behind);
+            }
+            if (q == 3) next_l[0] = next_l[1], next_b[0] = next_b[1], next_e[0] = next_e[1];  // (the fifth is the first lane's)
+            bool wrong = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool ordered = b[i] == next_b[i] && (l[i] > next_l[i] || (l[i] == next_l[i] && mine[i] < next_e[i]));
+                wrong |= (near >> (q + 4 * i + 1) & 1) && !ordered;
+            }
+            if (__ballot_sync(kAll, wrong) >> (lane & 28) & 15) sure = false;
         }
         // The tokens that are not sure, one after another, by the whole warp.
         for (unsigned left = __ballot_sync(kAll, !sure && q == 0); left; left &= left - 1) {
