@@ -38,7 +38,8 @@ int set_up_both() {
 }
 
 int set_up_kernels() {
-    if (set_up_both<256, 1>() || set_up_both<128, 1>() || set_up_both<128, 2>()) {
+    if (set_up_both<256, 1>() || set_up_both<128, 1>() || set_up_both<64, 1>() || set_up_both<128, 2>() ||
+        set_up_both<64, 2>()) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -161,6 +162,8 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     // 213 / 135 / 136, 8 of 200 x 4000 232 / 186 / 198, 2048 x 4096 406 / 338 / 354 (128 tiles of 256 columns, 76 pairs),
     // 2 of 3000 x 3000 (288) 768 / 897 / 942.  float32, two planes of either operand, 128 columns of a pair / single
     // CTAs: 200 x 300 122 / 125, 2048 x 2048 420 / 445, 2 of 3000 x 3000 2178 / 2492.
+    const long long narrow = c.E * ceil_div(c.M, 256) * ceil_div(c.N, 64);
+    if (narrow <= st.max_pairs) return parts == 2 ? launch<64, 2>(p, maps, st, s) : launch<64, 1>(p, maps, st, s);
     if (parts == 2) return launch<128, 2>(p, maps, st, s);
     const long long tiles = c.E * ceil_div(c.M, 256) * ceil_div(c.N, 256);
     return 2 * tiles >= 5 * st.max_pairs ? launch<256, 1>(p, maps, st, s) : launch<128, 1>(p, maps, st, s);

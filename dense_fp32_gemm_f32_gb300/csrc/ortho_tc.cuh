@@ -103,11 +103,12 @@ struct OrthoShape {
     static constexpr int TN = TN_, PARTS = PARTS_;
     static constexpr int FT = 256, R = FT / TN;  // a tile's rows; column tiles of a panel
     static constexpr int kCols = TN / 2;         // of a CTA
-    static constexpr int kABytes = 128 * 128, kBBytes = kCols * 128;  // of a part, 64 of the contraction
+    // of a part, 64 of the contraction (boxes of 64 rows or columns, of which the narrowest tile takes the first 32)
+    static constexpr int kBoxes = (kCols + 63) / 64, kABytes = 128 * 128, kBBytes = kBoxes * 64 * 128;
     static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
     // Measured, 8 and 16 warps (168 and 96 registers a thread): tiles of 256 columns, 8 x 2048 x 4096 bf16 1740 and 1880
     // us; of 128 columns and two planes, 4 x 2048 x 2048 float32 1470 and 1415 us.
-    static constexpr int kEpiWarps = TN == 256 ? 8 : 16;
+    static constexpr int kEpiWarps = TN == 128 ? 16 : 8;
     static constexpr int kThreads = 32 * (2 + kEpiWarps);
     // (the widest tile has a seventh stage instead of patches for results off the 16-byte grid)
     static constexpr bool kPatched = !(TN == 256 && PARTS == 1);
@@ -118,7 +119,7 @@ struct OrthoShape {
     static constexpr int kSmem = kStages * kStageBytes + kPatches + 8 * kBars + 32 + 1024;
     static constexpr int kWarpCols = TN / (kEpiWarps / 4);  // an epilogue warp's columns
     static constexpr int kDone = 2;                         // what a tile's CTAs add to a panel's counter
-    static_assert(kSmem <= 227 * 1024 && kStages >= 2 && kCols % 64 == 0 && kTmemCols <= 512 && FT % TN == 0, "shape");
+    static_assert(kSmem <= 227 * 1024 && kStages >= 2 && kCols % 32 == 0 && kWarpCols % 32 == 0 && kTmemCols <= 512 && FT % TN == 0, "shape");
 };
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, PARTS>::kThreads, 1)
                         for (int j = 0; j < 2; ++j)
                             load(a + part * S::kABytes + j * 64 * 128, first, first_mn, f0 + 64 * j, z);
 #pragma unroll
-                        for (int j = 0; j < S::kCols / 64; ++j)
+                        for (int j = 0; j < S::kBoxes; ++j)
                             load(b + part * S::kBBytes + j * 64 * 128, second, second_mn, c0 + 64 * j, z);
                     }
                 }
