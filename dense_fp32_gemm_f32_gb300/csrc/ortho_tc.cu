@@ -162,8 +162,13 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     // 213 / 135 / 136, 8 of 200 x 4000 232 / 186 / 198, 2048 x 4096 406 / 338 / 354 (128 tiles of 256 columns, 76 pairs),
     // 2 of 3000 x 3000 (288) 768 / 897 / 942.  float32, two planes of either operand, 128 columns of a pair / single
     // CTAs: 200 x 300 122 / 125, 2048 x 2048 420 / 445, 2 of 3000 x 3000 2178 / 2492.
+    // 64 columns where there are few tiles: each is done sooner, and its epilogue has registers enough. us for 64 columns / 128, float32:
+    // 129 x 129 75 / 105, 1024 x 1024 (64 tiles of 64 columns) 139 / 193, 2 of 1024 x 1024 (128) 177 / 199, 2 of 1025 x 1023 (160) 205 / 219,
+    // 3 of 1024 x 1024 (192) 221 / 255, 4 of them (256) 269 / 261, 2048 x 2048 (256) 467 / 402; bf16: 300 x 700 (22) 79 / 98, 1024 x 1024
+    // 99 / 119, 1152 x 1152 (90) 128 / 124, 1500 x 1500 (144) 173 / 149.
     const long long narrow = c.E * ceil_div(c.M, 256) * ceil_div(c.N, 64);
-    if (narrow <= st.max_pairs) return parts == 2 ? launch<64, 2>(p, maps, st, s) : launch<64, 1>(p, maps, st, s);
+    if (narrow <= (parts == 2 ? 8ll * st.max_pairs / 3 : st.max_pairs))
+        return parts == 2 ? launch<64, 2>(p, maps, st, s) : launch<64, 1>(p, maps, st, s);
     if (parts == 2) return launch<128, 2>(p, maps, st, s);
     const long long tiles = c.E * ceil_div(c.M, 256) * ceil_div(c.N, 256);
     return 2 * tiles >= 5 * st.max_pairs ? launch<256, 1>(p, maps, st, s) : launch<128, 1>(p, maps, st, s);

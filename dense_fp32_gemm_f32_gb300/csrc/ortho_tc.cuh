@@ -57,8 +57,8 @@
 //
 // Measured on GB300, five steps: 8 matrices 2048 x 4096 bf16 1.74 ms (with 5 / 8 of the symmetric
 // products' flops 1.5 PFLOP/s; the GPU runs at its power limit, 1.6 GHz, at which the tensor pipe
-// would need 1.5 ms; preparation 95 us), in float32 5.2 ms; 1024 x 1024 bf16 121 us and 512 x 512 97 us, bound by
-// latency: of a tile's 8000 to 9000 cycles on the way from one product to the next 1100 are the
+// would need 1.5 ms; preparation 95 us), in float32 5.2 ms; 1024 x 1024 bf16 99 us and 512 x 512 78 us, bound by
+// latency: of the 8000 to 9000 cycles of a tile of 128 columns on the way from one product to the next 1100 are the
 // first copy's, 1000 to 2400 the products', 3300 the epilogue's and 1900 the counters'.
 //
 // Every wait is bounded by `timeout_ns`; on expiry the thread records the

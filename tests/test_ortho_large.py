@@ -102,3 +102,16 @@ def test_a_matrix_past_2_31_elements(dtype):
             assert (y[i, :, i, j].double() - x).norm() <= LIMIT[dtype] * x.norm()
         assert not y[i, :, (i + 1) % blocks].any()
     assert g.check_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E, M, N", [(1, 1100, 130), (1, 500, 1100), (1, 1100, 500), (2, 1000, 1200), (2, 1200, 1000), (3, 1025, 1023), (5, 450, 900),
+                                     (5, 900, 450), (1, 1600, 1500), (2, 1281, 769)])
+@typed(TYPES)
+def test_between_few_tiles_and_many(E, M, N, dtype):
+    """Sizes on either side of where tiles get wider, and of where symmetric products take one side alone."""
+    G = randn((E, M, N), dtype, seed=M)
+    y, want = g.sgemm_orthogonalize(G), ortho64(G)
+    off = (y.double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    assert (off <= LIMIT[dtype]).all(), off.max().item()
+    assert g.check_status() == 0
