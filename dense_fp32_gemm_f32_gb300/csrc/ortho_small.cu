@@ -21,10 +21,11 @@
 // Bound by latency: five steps of three dependent products, each a barrier, 6 to 16
 // instructions of the tensor core for each product of planes, and about 450 instructions a
 // warp to put its sums back (a quarter of the issue slots are used).  Measured on GB300, five steps: 64 x 64
-// bf16 34 us, 128 x 96 bf16 41 and float32 49 us, 128 x 512 66 and 77 us (4 CTAs; the sums
-// of their parts 3 us a step), 4096 x 128 94 and 110 us (16 CTAs).  The many-tile form
-// (ortho_tc.cuh) took 71 and 102 us for 128 x 96, most of it on the way of tiles through HBM;
-// 8 warps, half as many as here, 49 and 57.
+// bf16 24 us, 128 x 96 bf16 31 and float32 40 us, 128 x 512 56 and 67 us (4 CTAs; the sums
+// of their parts 3 us a step).  Of 128 x 96 40 and 48 us before what a thread updates was loaded while the product
+// runs, G read once and a row of the diagonal four values a load.  The many-tile form
+// (ortho_tc.cuh) took 71 and 102 us, most of it on the way of tiles through HBM;
+// 8 warps, half as many as here, 49 and 57 when these were 41 and 49.
 #include "../../include/sgemm_ortho.h"
 #include "api_internal.h"
 #include "experts_tc.cuh"
@@ -163,14 +164,39 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
     // ---------------------------------------------------------------- norm
     // The slice as it is stored: rows of X, or of X^T.
     const T* const G = static_cast<const T*>(p.G) + e * p.sg + (TALL ? n0 * p.ldg : n0);
-    const int grows = TALL ? cols : p.m, gcols = TALL ? p.m : cols, octs = (gcols + 7) / 8;
-    double sum = 0;
-    constexpr int kLoads = 4;  // (before the first use)
-    for (int i = threadIdx.x; i < grows * octs; i += kLoads * kSmallThreads) {
-        float v[kLoads][8];
-        load_octs(G, p.ldg, i, kSmallThreads, octs, gcols, grows * octs, p.vec && gcols % 8 == 0, p.vec, v);
-        sum += squares(v);
+    // A thread's octs of X: rows and columns of X, zeros where there are none.  They stay in registers until the norm is known.
+    constexpr int kMine = 128 * (W / 8) / kSmallThreads;
+    float g[kMine][8];
+    // (neighbouring threads read neighbouring elements)
+    auto row_of = [&](int u) { return TALL ? (threadIdx.x + u * kSmallThreads) & 127 : (threadIdx.x + u * kSmallThreads) / (W / 8); };
+    auto column_of = [&](int u) {
+        return static_cast<int>(TALL ? (threadIdx.x + u * kSmallThreads) >> 7 : (threadIdx.x + u * kSmallThreads) % (W / 8)) * 8;
+    };
+    if (!TALL && p.vec && cols % 8 == 0) {  // (every oct is a vector: all loads under way at once)
+        alignas(16) T x[kMine][8];
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const uint4* from = reinterpret_cast<const uint4*>(G + min(static_cast<int>(row_of(u)), p.m - 1) * p.ldg + min(column_of(u), cols - 8));
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(x[u])[i] = __ldg(from + i);
+        }
+#pragma unroll
+        for (int u = 0; u < kMine; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[u][j] = row_of(u) < p.m && column_of(u) < cols ? to_f32(x[u][j]) : 0.f;
+    } else {
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const int r = row_of(u), c = column_of(u);
+            if constexpr (TALL) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[u][j] = r < p.m && c + j < cols ? to_f32(G[(c + j) * p.ldg + r]) : 0.f;
+            } else {
+                load8(G + r * p.ldg + c, r < p.m ? cols - c : 0, p.vec, g[u]);
+            }
+        }
     }
+    double sum = squares(g);
 #pragma unroll
     for (int s = 16; s; s /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, s);
     if (lane == 0) asm volatile("st.shared.f64 [%0], %1;" ::"r"(scratch + 8 * warp), "d"(sum) : "memory");
@@ -195,28 +221,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
     const OrthoScale scale(sqrt(sum) + p.eps);
 
     // ---------------------------------------------------------------- X
-    for (int i = threadIdx.x; i < 128 * (W / 8); i += kSmallThreads) {
-        // (neighbouring threads read neighbouring elements)
-        const int r = TALL ? i & 127 : i / (W / 8), c = (TALL ? i >> 7 : i % (W / 8)) * 8;
-        float v[8];
-        if constexpr (TALL) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = r < p.m && c + j < cols ? to_f32(G[(c + j) * p.ldg + r]) : 0.f;
-        } else {
-            load8(G + r * p.ldg + c, r < p.m ? cols - c : 0, p.vec, v);
-        }
+    for (int u = 0; u < kMine; ++u) {
+        const int r = row_of(u), c = column_of(u);
         uint4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-        if (r < p.m && c < cols) scale.split(v, hi, lo);
+        if (r < p.m && c < cols) scale.split(g[u], hi, lo);
         sts_u4(x_hi + piece(r, c), hi);
         sts_u4(x_lo + piece(r, c), lo);
     }
 
     // A product: D (128 x N) = sum over k of the first operand's rows (K-major) and the second's.  What threads
-    // wrote to shared memory before is there for it, and its sums for them after.
+    // wrote to shared memory before is there for it, and its sums for them after.  `meanwhile`: what a warp loads
+    // beside it.
     const uint64_t x_k = umma_desc_kmajor_sw128(x_hi), x_mn = umma_desc_mnmajor_sw128(x_hi, kSmallBlock);
     const uint64_t a_k = umma_desc_kmajor_sw128(a_hi);
     uint32_t phase = 0;
-    auto product = [&](bool gram, bool update, int k_len) {
+    auto product = [&](bool gram, bool update, int k_len, auto meanwhile) {
         fence_proxy_async_all();
         tc_fence_before_sync();
         if (p.width > 1 && !gram && !update)
@@ -244,6 +264,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             }
             __syncwarp();
         }
+        meanwhile();
         if (!mbar_wait_warp<false>(bar, phase, p.timeout_ns)) timed_out = true;
         phase ^= 1;
         tc_fence_after_sync();
@@ -265,9 +286,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         }
     };
 
+    static_assert(32 * kSmallShare == 128, "32 columns of A a warp");
+    const int c0 = 32 * share;  // the warp's columns of A, and its first ones of X
+    const bool mine = active && c0 < side;
     for (int step = 0; step < p.steps; ++step) {
         // ------------------------------------------------------------ gram
-        product(true, false, cols);
+        product(true, false, cols, [] {});
         if (p.width == 1) {
 #pragma unroll 1
             for (int c = 32 * share; active && c < side; c += 32 * kSmallShare) {
@@ -343,32 +367,44 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             }
         }
         // ------------------------------------------------------------ square
-        product(false, false, p.m);
-        const float d_row = active ? lds_f(d_at + 4 * row) : 0.f;
-#pragma unroll 1
-        for (int c = 32 * share; active && c < side; c += 32 * kSmallShare) {
-            float v[32], o[32];
-            load_planes(a_hi, a_lo, row, c, o);
-            sums_of(c, v);
+        float o[32], d_row = 0.f;
+        product(false, false, p.m, [&] {
+            if (!mine) return;
+            load_planes(a_hi, a_lo, row, c0, o);
+            d_row = lds_f(d_at + 4 * row);
+        });
+        if (mine) {
+            float v[32];
+            sums_of(c0, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (c + j == row) {
-                    sts_f(e_at + 4 * row, fmaf(p.c5, fmaf(d_row, d_row, v[j] * 0x1p-24f), p.c3 * d_row));
-                    v[j] = 0.f;
-                } else {
-                    v[j] = fmaf(p.c5, fmaf(d_row + lds_f(d_at + 4 * (c + j)), o[j], v[j] * 0x1p-12f), p.c3 * o[j]);
+            for (int j = 0; j < 32; j += 4) {
+                const float4 d4 = lds128(d_at + 4 * (c0 + j));
+                const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float& x = v[j + i];
+                    if (c0 + j + i == row) {
+                        sts_f(e_at + 4 * row, fmaf(p.c5, fmaf(d_row, d_row, x * 0x1p-24f), p.c3 * d_row));
+                        x = 0.f;
+                    } else {
+                        x = fmaf(p.c5, fmaf(d_row + d[i], o[j + i], x * 0x1p-12f), p.c3 * o[j + i]);
+                    }
                 }
             }
-            store_planes(a_hi, a_lo, row, c, v);
+            store_planes(a_hi, a_lo, row, c0, v);
         }
         // ------------------------------------------------------------ update
-        product(false, true, p.m);
-        const float factor = active ? p.c1 + lds_f(e_at + 4 * row) : 0.f;
+        float x[32], factor = 0.f;
+        product(false, true, p.m, [&] {
+            if (!active || c0 >= cols) return;
+            load_planes(x_hi, x_lo, row, c0, x);
+            factor = p.c1 + lds_f(e_at + 4 * row);
+        });
         const bool last = step + 1 == p.steps;
 #pragma unroll 1
-        for (int c = 32 * share; active && c < cols; c += 32 * kSmallShare) {
-            float v[32], x[32];
-            load_planes(x_hi, x_lo, row, c, x);
+        for (int c = c0; active && c < cols; c += 32 * kSmallShare) {
+            float v[32];
+            if (c != c0) load_planes(x_hi, x_lo, row, c, x);
             sums_of(c, v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = fmaf(factor, x[j], v[j] * 0x1p-12f);
