@@ -29,6 +29,9 @@ TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
 # Scores (include/sgemm_routing.h).
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
+# Added to the type of an update (include/sgemm_ortho.h).
+ORTHO_QUICK = 256
+
 PRODUCER_AUTO, PRODUCER_TMA, PRODUCER_CPASYNC, PRODUCER_TMA_WG, PRODUCER_FUSED, PRODUCER_TMA_X, PRODUCER_SMALL = 0, 1, 2, 3, 4, 5, 6
 
 # Every symbol the headers declare, with its ctypes signature.

@@ -55,9 +55,17 @@ bool polynomial_ok(int steps, double a, double b, double c) {
 }
 
 // A side's most.  The tensor cores cut a sum each time that they add to it, always towards zero, n / 16 times over a
-// row of n: with bf16 the result is off by 1.7e-3 of its norm (1.7e-3 of it its rounding) up to 65536 columns, 2.1e-3 at
+// row of n where one plane is multiplied (two: at most 32 times): the bf16 result is then off by 1.7e-3 of its norm (1.7e-3 of it its rounding) up to 65536 columns, 2.1e-3 at
 // 262144, 5.1e-3 at a million and 2.9e-2 at seven.
 constexpr int kLongest = 1 << 18;
+
+// The flag of products with one f16 value an operand out of `type`, where that may have it.
+bool take_quick(int* type, int* parts) {
+    const bool quick = (*type & SGEMM_ORTHO_QUICK) != 0;
+    *type &= ~SGEMM_ORTHO_QUICK;
+    if (quick && parts) *parts = 1;
+    return !quick || *type == SGEMM_TYPE_BF16;
+}
 
 bool sizes_ok(int type, int E, int M, int N, int steps) {
     if (!type_ok(type) || E < 0 || M < 0 || N < 0 || E > kMost || M > kLongest || N > kLongest || steps < 1 || steps > 64)
@@ -69,7 +77,7 @@ bool sizes_ok(int type, int E, int M, int N, int steps) {
 }  // namespace
 
 extern "C" int64_t sgemm_orthogonalize_workspace(int type, int E, int M, int N, int steps) {
-    if (!sizes_ok(type, E, M, N, steps)) return -1;
+    if (!take_quick(&type, nullptr) || !sizes_ok(type, E, M, N, steps)) return -1;
     if (E == 0 || M == 0 || N == 0 || ortho_always_small(M, N)) return 0;
     return ortho_layout(E, M, N, steps).bytes;
 }
@@ -77,19 +85,21 @@ extern "C" int64_t sgemm_orthogonalize_workspace(int type, int E, int M, int N, 
 extern "C" int sgemm_orthogonalize(int type, int E, int M, int N, const void* G, int64_t ldg, int64_t stride_g, int steps,
                                    float a, float b, float c, double eps, void* out, int64_t ldo, int64_t stride_out,
                                    void* workspace, int64_t workspace_bytes, void* stream) {
-    if (!sizes_ok(type, E, M, N, steps) || !(eps >= 0) || !std::isfinite(eps) || !polynomial_ok(steps, a, b, c))
+    const int asked = type;
+    int parts = 2;
+    if (!take_quick(&type, &parts) || !sizes_ok(type, E, M, N, steps) || !(eps >= 0) || !std::isfinite(eps) || !polynomial_ok(steps, a, b, c))
         return SGEMM_ERR_INVALID_ARG;
     const int size = type_bytes(type);
     const View g{G, E, M, N, ldg, stride_g, size}, o{out, E, M, N, ldo, stride_out, size};
     if (!g.ok(size) || !o.ok(size) || overlap(g, o)) return SGEMM_ERR_INVALID_ARG;
     if (o.empty()) return SGEMM_OK;
-    const int64_t needed = sgemm_orthogonalize_workspace(type, E, M, N, steps);
+    const int64_t needed = sgemm_orthogonalize_workspace(asked, E, M, N, steps);
     const View ws{workspace, 1, 1, needed, needed, 0, 1};
     if (workspace_bytes < needed || !ws.ok(256) || overlap(ws, g) || overlap(ws, o)) return SGEMM_ERR_INVALID_ARG;
     int dev = 0;
     DeviceState* st = nullptr;
     const int rc = experts_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
-    const OrthoCall call = {G, ldg, stride_g, out, ldo, stride_out, type, E, M, N, steps, a, b, c, eps, workspace};
+    const OrthoCall call = {G, ldg, stride_g, out, ldo, stride_out, type, E, M, N, steps, parts, a, b, c, eps, workspace};
     return orthogonalize(call, *st, static_cast<cudaStream_t>(stream));
 }

@@ -36,6 +36,7 @@ struct OrthoCall {
     void* out;
     long long ldo, so;
     int type, E, M, N, steps;
+    int parts;  // f16 values that stand for an operand in the products: 2, or 1 (bf16 alone)
     float a, b, c;
     double eps;
     void* workspace;

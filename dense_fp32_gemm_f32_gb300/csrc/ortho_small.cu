@@ -20,9 +20,9 @@
 //
 // Bound by latency: five steps of three dependent products, each a barrier, 6 to 16
 // instructions of the tensor core for each product of planes, and about 450 instructions a
-// warp to put its sums back (a quarter of the issue slots are used).  Measured on GB300, five steps: 64 x 64
-// bf16 24 us, 128 x 96 bf16 31 and float32 40 us, 128 x 512 56 and 67 us (4 CTAs; the sums
-// of their parts 3 us a step).  Of 128 x 96 40 and 48 us before what a thread updates was loaded while the product
+// warp to put its sums back (a quarter of the issue slots are used).  Measured on GB300, five steps, products of
+// one plane and of two: 64 x 64 24 and 29 us, 128 x 96 31 and 40 us, 128 x 512 56 and 67 us (4 CTAs; the sums
+// of their parts 3 us a step).  (What follows was measured with one plane for bf16, two for float32.)  Of 128 x 96 40 and 48 us before what a thread updates was loaded while the product
 // runs, G read once and a row of the diagonal four values a load.  The many-tile form
 // (ortho_tc.cuh) took 71 and 102 us, most of it on the way of tiles through HBM;
 // 8 warps, half as many as here, 49 and 57 when these were 41 and 49.
@@ -52,9 +52,8 @@ struct OrthoSmallParams {
     unsigned int* status;
 };
 
-template <typename T, int W>
+template <int W, int PARTS>
 struct SmallShape {
-    static constexpr int PARTS = sizeof(T) == 2 && !__is_same(T, __half) ? 1 : 2;  // (bf16: products of hi alone)
     static constexpr int kXBytes = W / 64 * kSmallBlock, kABytes = 2 * kSmallBlock;  // of a plane
     static constexpr int kPlanes = 2 * kXBytes + 2 * kABytes;
     static constexpr int kTmemCols = PARTS * W;
@@ -133,10 +132,9 @@ __device__ __forceinline__ void store_planes(uint32_t hi, uint32_t lo, int row, 
     }
 }
 
-template <typename T, int W, bool TALL>
+template <typename T, int W, int PARTS, bool TALL>
 __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const OrthoSmallParams p) {
-    using S = SmallShape<T, W>;
-    constexpr int PARTS = S::PARTS;
+    using S = SmallShape<W, PARTS>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t x_hi = base, x_lo = base + S::kXBytes;
@@ -452,10 +450,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
     }
 }
 
-template <typename T, int W>
+template <typename T, int W, int PARTS>
 int set_up_width(int* most) {
-    for (const auto kernel : {ortho_small_kernel<T, W, false>, ortho_small_kernel<T, W, true>}) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallShape<T, W>::kSmem) != cudaSuccess)
+    for (const auto kernel : {ortho_small_kernel<T, W, PARTS, false>, ortho_small_kernel<T, W, PARTS, true>}) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SmallShape<W, PARTS>::kSmem) != cudaSuccess)
             return SGEMM_ERR_CUDA;
         if (W == 256 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return SGEMM_ERR_CUDA;
@@ -464,7 +462,7 @@ int set_up_width(int* most) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(16);
         cfg.blockDim = dim3(kSmallThreads);
-        cfg.dynamicSmemBytes = SmallShape<T, W>::kSmem;
+        cfg.dynamicSmemBytes = SmallShape<W, PARTS>::kSmem;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = 16;
@@ -472,7 +470,7 @@ int set_up_width(int* most) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, ortho_small_kernel<T, W, true>, &cfg) != cudaSuccess || clusters < 1) {
+        if (cudaOccupancyMaxActiveClusters(&clusters, ortho_small_kernel<T, W, PARTS, true>, &cfg) != cudaSuccess || clusters < 1) {
             (void)cudaGetLastError();
             *most = 8;
         }
@@ -480,12 +478,12 @@ int set_up_width(int* most) {
     return SGEMM_OK;
 }
 
-template <typename T, int W>
+template <typename T, int W, int PARTS>
 int launch(const OrthoCall& c, const OrthoSmallParams& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(c.E) * static_cast<unsigned>(p.width));
     cfg.blockDim = dim3(kSmallThreads);
-    cfg.dynamicSmemBytes = SmallShape<T, W>::kSmem;
+    cfg.dynamicSmemBytes = SmallShape<W, PARTS>::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -493,7 +491,7 @@ int launch(const OrthoCall& c, const OrthoSmallParams& p, cudaStream_t s) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = p.width > 1 ? 1 : 0;
-    const auto kernel = c.M > c.N ? ortho_small_kernel<T, W, true> : ortho_small_kernel<T, W, false>;
+    const auto kernel = c.M > c.N ? ortho_small_kernel<T, W, PARTS, true> : ortho_small_kernel<T, W, PARTS, false>;
     if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
@@ -501,13 +499,22 @@ int launch(const OrthoCall& c, const OrthoSmallParams& p, cudaStream_t s) {
     return SGEMM_OK;
 }
 
+template <typename T, int PARTS>
+int set_up_type(int* most) {
+    return set_up_width<T, 128, PARTS>(most) || set_up_width<T, 256, PARTS>(most);
+}
+
+template <typename T, int PARTS>
+int launch_width(int w, const OrthoCall& c, const OrthoSmallParams& p, cudaStream_t s) {
+    return w == 128 ? launch<T, 128, PARTS>(c, p, s) : launch<T, 256, PARTS>(c, p, s);
+}
+
 }  // namespace
 
 int ortho_small_set_up(int* most_ctas) {
     *most_ctas = 16;
-    if (set_up_width<float, 128>(most_ctas) || set_up_width<float, 256>(most_ctas) ||
-        set_up_width<__nv_bfloat16, 128>(most_ctas) || set_up_width<__nv_bfloat16, 256>(most_ctas) ||
-        set_up_width<__half, 128>(most_ctas) || set_up_width<__half, 256>(most_ctas)) {
+    if (set_up_type<float, 2>(most_ctas) || set_up_type<__nv_bfloat16, 2>(most_ctas) ||
+        set_up_type<__nv_bfloat16, 1>(most_ctas) || set_up_type<__half, 2>(most_ctas)) {
         (void)cudaGetLastError();
         return SGEMM_ERR_CUDA;
     }
@@ -529,10 +536,9 @@ int ortho_small(const OrthoCall& c, const DeviceState& st, cudaStream_t s) {
     p.c1 = c.a, p.c3 = c.b, p.c5 = c.c, p.eps = c.eps;
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
-    if (c.type == SGEMM_TYPE_F32) return w == 128 ? launch<float, 128>(c, p, s) : launch<float, 256>(c, p, s);
-    if (c.type == SGEMM_TYPE_BF16)
-        return w == 128 ? launch<__nv_bfloat16, 128>(c, p, s) : launch<__nv_bfloat16, 256>(c, p, s);
-    return w == 128 ? launch<__half, 128>(c, p, s) : launch<__half, 256>(c, p, s);
+    if (c.type == SGEMM_TYPE_F32) return launch_width<float, 2>(w, c, p, s);
+    if (c.type == SGEMM_TYPE_F16) return launch_width<__half, 2>(w, c, p, s);
+    return c.parts == 2 ? launch_width<__nv_bfloat16, 2>(w, c, p, s) : launch_width<__nv_bfloat16, 1>(w, c, p, s);
 }
 
 }  // namespace detail

@@ -116,7 +116,7 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     });
     if (st.ortho_status != SGEMM_OK) return st.ortho_status;
     if (const int rc = ortho_small(c, st, s); rc != SGEMM_ERR_UNSUPPORTED) return rc;
-    const int m = std::min(c.M, c.N), parts = c.type == SGEMM_TYPE_BF16 ? 1 : 2;
+    const int m = std::min(c.M, c.N), parts = c.parts;
     const OrthoLayout l = ortho_layout(c.E, c.M, c.N, c.steps);
     if (static_cast<long long>(c.E) * l.chunks > 0x7fffffffll) return SGEMM_ERR_INVALID_ARG;
     char* const ws = static_cast<char*>(c.workspace);
@@ -157,14 +157,14 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     prep.hi = reinterpret_cast<uint16_t*>(p.x[0].hi), prep.pitch = l.pitch, prep.plane = c.E * p.x[0].matrix;
     const int rc = ortho_prepare(prep, c.type, s);
     if (rc != SGEMM_OK) return rc;
-    // Tiles of a pair of CTAs: 256 rows by 128 columns; bf16 256 where the GPU's pairs then have two and a half each in an update.
-    // Measured, us for 256 columns / 128 / single CTAs with 128 x 128 (bf16): 512 x 512 173 / 110 / 112, 1024 x 1024
+    // Tiles of a pair of CTAs: 256 rows by 128 columns; with one plane 256 where the GPU's pairs then have two and a half each in an update.
+    // Measured, us for 256 columns / 128 / single CTAs with 128 x 128 (one plane): 512 x 512 173 / 110 / 112, 1024 x 1024
     // 213 / 135 / 136, 8 of 200 x 4000 232 / 186 / 198, 2048 x 4096 406 / 338 / 354 (128 tiles of 256 columns, 76 pairs),
-    // 2 of 3000 x 3000 (288) 768 / 897 / 942.  float32, two planes of either operand, 128 columns of a pair / single
+    // 2 of 3000 x 3000 (288) 768 / 897 / 942.  Two planes of either operand (float32), 128 columns of a pair / single
     // CTAs: 200 x 300 122 / 125, 2048 x 2048 420 / 445, 2 of 3000 x 3000 2178 / 2492.
-    // 64 columns where there are few tiles: each is done sooner, and its epilogue has registers enough. us for 64 columns / 128, float32:
+    // 64 columns where there are few tiles: each is done sooner, and its epilogue has registers enough. us for 64 columns / 128, two planes:
     // 129 x 129 75 / 105, 1024 x 1024 (64 tiles of 64 columns) 139 / 193, 2 of 1024 x 1024 (128) 177 / 199, 2 of 1025 x 1023 (160) 205 / 219,
-    // 3 of 1024 x 1024 (192) 221 / 255, 4 of them (256) 269 / 261, 2048 x 2048 (256) 467 / 402; bf16: 300 x 700 (22) 79 / 98, 1024 x 1024
+    // 3 of 1024 x 1024 (192) 221 / 255, 4 of them (256) 269 / 261, 2048 x 2048 (256) 467 / 402; one plane: 300 x 700 (22) 79 / 98, 1024 x 1024
     // 99 / 119, 1152 x 1152 (90) 128 / 124, 1500 x 1500 (144) 173 / 149.
     const long long narrow = c.E * ceil_div(c.M, 256) * ceil_div(c.N, 64);
     if (narrow <= (parts == 2 ? 8ll * st.max_pairs / 3 : st.max_pairs))

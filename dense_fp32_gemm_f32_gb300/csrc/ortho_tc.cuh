@@ -16,12 +16,14 @@
 // so that the large elements of a matrix near the identity are not rounded to 11
 // bits, and their products cost nothing.  X and A are carried in two
 // f16 planes, hi + lo (22 bits); the terms outside of the products use both, the
-// products themselves hi alone (PARTS = 1, for bf16 updates) or the three
-// products hi hi + hi lo + lo hi (PARTS = 2).  For 1024 x 2048 normal random
+// products themselves the three hi hi + hi lo + lo hi (PARTS = 2) or, for bf16
+// updates whose caller asks for it, hi alone (PARTS = 1).  For 1024 x 2048 normal random
 // matrices and five steps of the usual polynomial the error of the result's
 // norm against 64 bits is 1.8e-3 without the diagonals taken apart and 7e-4 so,
-// and with two planes only 4e-7; a matrix of rank 8 and noise 200 times smaller
-// is off by 4e-2 if X is one f16 plane, and by 6e-4 so.
+// and with products of two planes 4e-7; a matrix of rank 8 and noise 200 times smaller
+// is off by 4e-2 if X is one f16 plane, and by 6e-4 so.  The error of one plane
+// is half of bf16's rounding of the result, but grows with the steps and with what the polynomial raises:
+// it is the caller's choice.
 //
 // Scales.  X is held times 2^13, O and P times 2^12: singular values up to 2
 // (the entry refuses polynomials that go beyond) make elements up to 2^14, 2^14
@@ -55,10 +57,10 @@
 // to float32 registers every 512 of the contraction (an instruction cuts
 // sums to 24 bits).
 //
-// Measured on GB300, five steps: 8 matrices 2048 x 4096 bf16 1.74 ms (with 5 / 8 of the symmetric
-// products' flops 1.5 PFLOP/s; the GPU runs at its power limit, 1.6 GHz, at which the tensor pipe
-// would need 1.5 ms; preparation 95 us), in float32 5.2 ms; 1024 x 1024 bf16 99 us and 512 x 512 78 us, bound by
-// latency: of the 8000 to 9000 cycles of a tile of 128 columns on the way from one product to the next 1100 are the
+// Measured on GB300, five steps, of bf16 (of float32 the same but for 2 to 4 %): 8 matrices 2048 x 4096 5.2 to 5.35 ms,
+// 1.8 with products of one plane (with 5 / 8 of the symmetric products' flops 1.5 PFLOP/s in either; the GPU runs at its
+// power limit, 1.6 GHz, at which the tensor pipe would need 1.5 of the 1.8 ms; preparation 95 us); 1024 x 1024 138 us and
+// 100, 512 x 512 101 and 78, bound by latency: of the 8000 to 9000 cycles of a tile of 128 columns on the way from one product to the next 1100 are the
 // first copy's, 1000 to 2400 the products', 3300 the epilogue's and 1900 the counters'.
 //
 // Every wait is bounded by `timeout_ns`; on expiry the thread records the
@@ -354,12 +356,15 @@ __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t pat
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= 0x1p-13f;
             const long long at = t.e * p.so + r0 * p.ldo + c;
-            if (p.out_type == 0) {
-                if constexpr (S::PARTS == 2) ortho_result<S, float>(p, patch, at, v, F - r0, C - c);
-            } else if (p.out_type == 1) {
-                if constexpr (S::PARTS == 1) ortho_result<S, __nv_bfloat16>(p, patch, at, v, F - r0, C - c);
+            if constexpr (S::PARTS == 1) {
+                ortho_result<S, __nv_bfloat16>(p, patch, at, v, F - r0, C - c);
             } else {
-                if constexpr (S::PARTS == 2) ortho_result<S, __half>(p, patch, at, v, F - r0, C - c);
+                if (p.out_type == 0)
+                    ortho_result<S, float>(p, patch, at, v, F - r0, C - c);
+                else if (p.out_type == 1)
+                    ortho_result<S, __nv_bfloat16>(p, patch, at, v, F - r0, C - c);
+                else
+                    ortho_result<S, __half>(p, patch, at, v, F - r0, C - c);
             }
             return;
         }

@@ -16,6 +16,9 @@
 extern "C" {
 #endif
 
+/* Added to the type bf16, of an update: quick products (see the accuracy below). */
+enum { SGEMM_ORTHO_QUICK = 256 };
+
 /*
  * sgemm_orthogonalize -- E matrices (M x N) with their singular values brought
  * near 1 by Newton-Schulz products:
@@ -25,7 +28,7 @@ extern "C" {
  *
  * which takes each singular value s to a s + b s^3 + c s^5 and leaves the
  * singular vectors where they are.
- *   type       of G and out
+ *   type       of G and out; SGEMM_ORTHO_QUICK may be added to SGEMM_TYPE_BF16, and to no other
  *   G, ldg, stride_g       E matrices M x N, stride_g elements apart; M and N up to
  *              262144 (sums over longer rows lose more than what follows)
  *   out, ldo, stride_out   the same, overwritten
@@ -38,15 +41,20 @@ extern "C" {
  *              sgemm_orthogonalize_workspace says, 256-byte aligned, for this call alone until
  *              its work on the stream is done (NULL where it says 0)
  * Accuracy.  Each step's products take X, A and b A + c A A less their
- * diagonals as f16 operands (A's and X's rounding errors, and the diagonals,
- * are carried along outside of the products) and sum in float32.  For bf16 one
- * f16 value each (11 bits); for float32 and f16 two (22 bits), three products
- * of which stand for one in float32.  A step multiplies an error in the
- * direction of small singular values by up to a, as it does those values
- * themselves; against the result in 64 bits that comes to less than 2^-8 of its
- * norm for bf16, and for float32 and f16 to about what the same steps with
- * float32 products have (2^-18 up to rows of 65536), besides the rounding to the
- * output's type.
+ * diagonals as two f16 values each (22 bits), three products of which stand for
+ * one in float32 (A's and X's rounding errors, and the diagonals, are carried
+ * along outside of the products), and sum in float32, whatever the type.  The
+ * result is rounded to its type once.  A step multiplies an error by what
+ * it multiplies the difference of two near singular values by, up to a for small ones.
+ * Five steps of the usual polynomials (3.4445, -4.7750, 2.0315 and
+ * those that converge to 1) come to less than 2^-18 of the result's norm up to rows of 65536.
+ * Many steps of a polynomial that does not converge lose more in any arithmetic: up
+ * to 16 times what the same steps with float32 products lose (an accumulator's sum
+ * is cut to 24 bits up to 32 times).
+ *   SGEMM_ORTHO_QUICK: one f16 value each (11 bits), one product of them for one:
+ * a third of the time for large matrices.  Five steps of the polynomial above are then off by 4e-4 to 8e-4
+ * of the result's norm before it is rounded to bf16 (1.7e-3), ten by 1.6e-3, 64 by
+ * 7e-3; (3, -1, 0), which raises errors threefold a step, by 4e-3 after six and 2e-1 after ten.
  * A non-finite element makes its whole matrix NaN or infinite, and no other.
  */
 int sgemm_orthogonalize(int type, int E, int M, int N,
