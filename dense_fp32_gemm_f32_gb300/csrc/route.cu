@@ -551,8 +551,10 @@ __device__ __forceinline__ bool grid_keys(const float (&c)[NPL], uint32_t (&key)
 }
 
 // How many steps of the grid apart two scores have to be (a step more for each place's error), and two scores of groups.
+// The grid has 2^22 steps however near a token's values are to one another: where their errors are larger than all of it, so is
+// this (2^23 at most, and 2^24 for the sums of groups, which are below 2^23), and nothing is certain.
 __device__ __forceinline__ float choice_steps(const RouteParams& p, float low, float high, float sum, float scale) {
-    return fminf(choice_error(p, fmaxf(fabsf(low), fabsf(high)), sum) * scale, 0x1p20f);
+    return fminf(choice_error(p, fmaxf(fabsf(low), fabsf(high)), sum) * scale, 0x1p23f);
 }
 __device__ __forceinline__ uint32_t choice_gap(float steps) { return static_cast<uint32_t>(steps + 2.1f); }
 __device__ __forceinline__ uint32_t score_gap(const RouteParams& p, float steps) {
