@@ -68,7 +68,7 @@ bool take_quick(int* type, int* parts) {
 }
 
 bool sizes_ok(int type, int E, int M, int N, int steps) {
-    if (!type_ok(type) || E < 0 || M < 0 || N < 0 || E > kMost || M > kLongest || N > kLongest || steps < 1 || steps > 64)
+    if (!type_ok(type) || E < 0 || M < 0 || N < 0 || E > kOrthoMostMatrices || M > kLongest || N > kLongest || steps < 1 || steps > 64)
         return false;
     constexpr int64_t most = int64_t{1} << 46;  // elements
     return N == 0 || E == 0 || (M <= most / N && static_cast<int64_t>(M) * N <= most / E);

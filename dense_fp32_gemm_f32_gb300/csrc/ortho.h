@@ -49,6 +49,8 @@ struct OrthoLayout {
 };
 OrthoLayout ortho_layout(int E, int M, int N, int steps);
 int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s);
+// The most matrices of a call: the small form numbers the CTAs of their clusters, up to 16 each, in 31 bits.
+constexpr int kOrthoMostMatrices = 0x7fffffff / 16;
 // Whether every device takes the call in its small form, which needs no workspace.
 inline bool ortho_always_small(int M, int N) {
     return (M < N ? M : N) <= 128 && (M < N ? N : M) <= 8 * 256;

@@ -526,7 +526,6 @@ int ortho_small(const OrthoCall& c, const DeviceState& st, cudaStream_t s) {
     // 128 columns a CTA in clusters of up to 8; 256 where one CTA then has all, or there are more.
     const int w = n <= 128 || (n > 256 && n <= 8 * 128) ? 128 : 256;
     if (m > 128 || n > 256 * st.ortho_ctas) return SGEMM_ERR_UNSUPPORTED;
-    if (c.E > 0x7fffffff / 16) return SGEMM_ERR_UNSUPPORTED;
     OrthoSmallParams p = {};
     const int size = c.type == SGEMM_TYPE_F32 ? 4 : 2;
     p.G = c.G, p.ldg = c.ldg, p.sg = c.sg, p.out = c.out, p.ldo = c.ldo, p.so = c.so;

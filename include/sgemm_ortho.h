@@ -29,7 +29,7 @@ enum { SGEMM_ORTHO_QUICK = 256 };
  * which takes each singular value s to a s + b s^3 + c s^5 and leaves the
  * singular vectors where they are.
  *   type       of G and out; SGEMM_ORTHO_QUICK may be added to SGEMM_TYPE_BF16, and to no other
- *   G, ldg, stride_g       E matrices M x N, stride_g elements apart; M and N up to
+ *   G, ldg, stride_g       E matrices M x N, stride_g elements apart; E up to 2^27 - 1, M and N up to
  *              262144 (sums over longer rows lose more than what follows)
  *   out, ldo, stride_out   the same, overwritten
  *   steps      1 .. 64
