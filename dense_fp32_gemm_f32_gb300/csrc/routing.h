@@ -65,7 +65,8 @@ struct RowsParams {
     const int* slots;
     const float* weights;  // null: ones
     float* dweights;       // may be null
-    const int* used;       // &offsets[E]: rows from here on are zeroed
+    const int* used;       // &offsets[E]: rows of `out` from here on are zeroed (null: no `out`, or a combination's)
+    int zero;              // this launch zeroes them (set by the launch functions)
     int T, k, R, H;
     int vec;  // elements a vector, as the operands' alignment allows
 };

@@ -63,10 +63,12 @@ __device__ __forceinline__ int slot_of(const RowsParams& p, long long i) {
     return s >= 0 && s < p.R ? s : -1;
 }
 
-// Zeros to the rows from *used on, `worker` of `workers` threads.
+// The row from which on p.out is zeroed: a slot from there on names no row of it (whoever came last would decide what it holds).
+__device__ __forceinline__ int used_rows(const RowsParams& p) { return min(max(__ldg(p.used), 0), p.R); }
+
+// Zeros to the rows from `used` on, `worker` of `workers` threads.
 template <typename T, int N>
-__device__ __forceinline__ void zero_unused(const RowsParams& p, long long worker, long long workers, int nvec) {
-    const int used = min(max(__ldg(p.used), 0), p.R);
+__device__ __forceinline__ void zero_unused(const RowsParams& p, int used, long long worker, long long workers, int nvec) {
     const long long n = static_cast<long long>(p.R - used) * nvec;
     for (long long i = worker; i < n; i += workers) {
         const long long r = i / nvec;
@@ -120,6 +122,7 @@ __device__ __forceinline__ bool token_of(const RowsParams& p, uint32_t per, uint
 // A thread: U vectors of a token's row, `per` vectors apart.
 template <typename T, int N, int U>
 __global__ void __launch_bounds__(kRowsThreads) spread_kernel(const RowsParams p, uint32_t nvec, uint32_t per) {
+    const int used = used_rows(p);
     uint32_t t, v;
     if (token_of(p, per, t, v)) {
         const T* x = static_cast<const T*>(p.X) + t * p.ldx;
@@ -130,15 +133,15 @@ __global__ void __launch_bounds__(kRowsThreads) spread_kernel(const RowsParams p
         const long long first = static_cast<long long>(t) * p.k;
         for (int j = 0; j < p.k; ++j) {
             const int s = slot_of(p, first + j);
-            if (s < 0) continue;
+            if (s < 0 || s >= used) continue;
             T* y = static_cast<T*>(p.out) + s * p.ldo;
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (v + u * per < nvec) store_vec<T, N>(y + (v + u * per) * N, row[u], p.H - (v + u * per) * N);
         }
     }
-    if (p.used)
-        zero_unused<T, N>(p, blockIdx.x * static_cast<long long>(kRowsThreads) + threadIdx.x,
+    if (p.zero)
+        zero_unused<T, N>(p, used, blockIdx.x * static_cast<long long>(kRowsThreads) + threadIdx.x,
                           static_cast<long long>(gridDim.x) * kRowsThreads, nvec);
 }
 
@@ -200,6 +203,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_grad_kernel(const RowsPa
     const bool there = t < static_cast<uint32_t>(p.T);
     const T* const dx = static_cast<const T*>(p.X) + t * p.ldx;
     const long long first = static_cast<long long>(t) * p.k;
+    const int used = p.out ? used_rows(p) : 0;
     for (int j0 = 0; j0 < p.k; j0 += B) {
         int slot[B];
         float w[B], dot[B] = {};
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_grad_kernel(const RowsPa
 #pragma unroll
                         for (int i = 0; i < N; ++i) dot[b] = fmaf(x[i], z[i], dot[b]);
                     }
-                    if (p.out) {
+                    if (slot[b] < used) {
                         Vec<T, N> o;
 #pragma unroll
                         for (int i = 0; i < N; ++i) z[i] = w[b] * x[i];
@@ -273,8 +277,8 @@ __global__ void __launch_bounds__(kRowsThreads) combine_grad_kernel(const RowsPa
             }
         }
     }
-    if (p.used)
-        zero_unused<T, N>(p, blockIdx.x * static_cast<long long>(kRowsThreads) + threadIdx.x,
+    if (p.zero)
+        zero_unused<T, N>(p, used, blockIdx.x * static_cast<long long>(kRowsThreads) + threadIdx.x,
                           static_cast<long long>(gridDim.x) * kRowsThreads, nvec);
 }
 
@@ -324,7 +328,7 @@ int in_parts(const RowsParams& p, int size, long long per, L launch) {
         if (p.weights) q.weights = p.weights + row;
         if (p.dweights) q.dweights = p.dweights + row;
         if (!p.X && p.out) q.out = static_cast<char*>(p.out) + at * p.ldo * size;  // (a combination's result goes by token)
-        if (t0 > 0) q.used = nullptr;
+        q.zero = p.used && t0 == 0;
         const int rc = launch(q, q.T * per);
         if (rc != SGEMM_OK) return rc;
         t0 += q.T;
@@ -347,7 +351,7 @@ int rows_spread(const RowsParams& p, int type, int sms, cudaStream_t s) {
         const bool two = static_cast<long long>(p.T) * nvec >= 4096ll * sms;
         const uint32_t per = two ? (nvec + 1) / 2 : nvec;
         return in_parts(p, sizeof(zero), per, [&](const RowsParams& q, long long threads) {
-            const unsigned ctas = ctas_for(threads, q.used ? sms : 1);  // (the rows to zero are shared among all)
+            const unsigned ctas = ctas_for(threads, q.zero ? sms : 1);  // (the rows to zero are shared among all)
             if (two)
                 spread_kernel<decltype(zero), decltype(vec)::value, 2><<<ctas, kRowsThreads, 0, s>>>(q, nvec, per);
             else
@@ -387,7 +391,7 @@ int rows_combine_grad(const RowsParams& p, int type, int sms, cudaStream_t s) {
             while (group < kRowsThreads && (nvec > 2 * U * group || (nvec > U * group && static_cast<long long>(p.T) * group < 1024ll * sms)))
                 group *= 2;
             return in_parts(p, sizeof(T), group, [&](const RowsParams& q, long long threads) {
-                combine_grad_kernel<T, N, B, U><<<ctas_for(threads, q.used ? sms : 1), kRowsThreads, 0, s>>>(q, nvec, group);
+                combine_grad_kernel<T, N, B, U><<<ctas_for(threads, q.zero ? sms : 1), kRowsThreads, 0, s>>>(q, nvec, group);
                 return launched();
             });
         });

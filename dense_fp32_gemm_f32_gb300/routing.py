@@ -147,7 +147,8 @@ def sgemm_route_grad(logits: torch.Tensor, experts: torch.Tensor, dweights: torc
 
 def sgemm_spread(X: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None, *,
                  stream=None) -> torch.Tensor:
-    """``out[slots[t, j]] = X[t]``: every token's row to the places of its choices, zeros to the rows from ``offsets[-1]`` on.
+    """``out[slots[t, j]] = X[t]``: every token's row to the places of its choices, zeros to the rows from ``offsets[-1]`` on
+    (also to one that a slot names).
 
     ``X`` is (T, H), ``slots`` (T, k) and ``offsets`` as sgemm_route gives them; ``out`` has T * k rows by default.  Its
     gradient is sgemm_combine of the gradient, without weights.

@@ -88,8 +88,8 @@ int sgemm_route_grad(int type, int score, int T, int E, int k,
                      void* stream);
 
 /*
- * sgemm_spread -- Y[slots[t, j], :] = X[t, :], and zeros to Y's rows from
- * offsets[E] (taken within [0, R]) on.
+ * sgemm_spread -- Y[slots[t, j], :] = X[t, :] for slots below offsets[E], and zeros
+ * to Y's rows from offsets[E] (taken within [0, R]) on.
  *   X          T x H;   Y   R x H
  *   slots      T x k, different from one another where they are rows of Y
  *   E, offsets as sgemm_route gives them
@@ -115,8 +115,9 @@ int sgemm_combine(int type, int T, int k, int R, int H,
 
 /*
  * sgemm_combine_grad -- the gradients of a combination:
- *     dY[slots[t, j], :] = weights[t, j] * dout[t, :], zeros to dY's rows from
- *                          offsets[E] on (other rows as sgemm_spread), and
+ *     dY[slots[t, j], :] = weights[t, j] * dout[t, :] for slots below offsets[E],
+ *                          zeros to dY's rows from there on (other rows as
+ *                          sgemm_spread), and
  *     dweights[t, j] = sum over h of dout[t, h] * Y[slots[t, j], h], 0 where
  *                      there is no row.
  * dY NULL or dweights NULL: that gradient is not wanted (Y is read for
