@@ -1195,8 +1195,10 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
             for (int i = 0; i < NPL; ++i) most = fmaxf(most, l[i]);
             most = warp_max(most);
             float sum = 0.f;
+            uint32_t open = 0;  // (zeros to the others, also where the gradients are not finite)
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
+                open |= l[i] == -INFINITY ? 0u : 1u << i;
                 l[i] = l[i] == -INFINITY ? 0.f : fast_exp(l[i] - most);
                 sum += l[i];
             }
@@ -1204,7 +1206,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
             s = e >= 0 ? fast_exp(x - most) * inv : 0.f;
             const float less = -p.scale * inv * warp_sum(d * s);
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) v[i] = l[i] * less;
+            for (int i = 0; i < NPL; ++i) v[i] = open >> i & 1 ? l[i] * less : 0.f;
             if (e >= 0) g = p.scale * s * d;
         }
         // The chosen experts' parts, by way of a row in shared memory.
