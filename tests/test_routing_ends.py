@@ -6,7 +6,7 @@ import torch
 
 import dense_fp32_gemm_f32_gb300 as g
 from test_experts import typed
-from test_routing import HOW, TYPES, check_route, randn
+from test_routing import HOW, TYPES, check_route, randn, scores64
 
 INF, NAN = math.inf, math.nan
 
@@ -30,3 +30,29 @@ def test_gradients_that_are_not_finite_leave_experts_out_of_service_alone(E, bad
     assert torch.equal(dl[keep], want[keep])
     assert not dl[3, r.experts[3, 1].long()].isfinite()
     assert g.check_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("T,E", [(4, 32), (200, 32), (4, 256), (200, 256)])
+def test_sums_of_groups_past_the_largest_float32(T, E, best, score):
+    """Two biases whose sum float32 does not hold: groups are still ordered by it."""
+    size = E // 4
+    b = 0.1 * randn(E, seed=2)
+    b[size], b[size + 1] = 3e38, 1e38
+    b[2 * size + 1], b[2 * size + 3] = 3e38, 2e38
+    b[3 * size], b[3 * size + 1] = -3e38, -2e38
+    logits = randn(T, E, seed=3)
+    how = dict(score=score, bias=b, groups=4, top_groups=1, group_best=best)
+    r = g.sgemm_route(logits, 3, **how)
+    check_route(r, logits, 3, **how)
+    assert (r.experts[:, 0] == (size if best == 1 else 2 * size + 1)).all()
+    # Now either's sum is 3e38 + 2e38 or more, and in the second's two values that 64 bits hold equal: of one bias, they follow their logits.
+    b[size + 1], b[2 * size + 3] = 2e38, 3e38
+    r = g.sgemm_route(logits, 3, **how)
+    group = 1 if best == 1 else 2
+    c, l = (scores64(logits, score) + b.double()).cpu(), logits.cpu()
+    for t in range(T):
+        of = sorted(range(group * size, (group + 1) * size), key=lambda e: (-c[t, e].item(), -l[t, e].item(), e))
+        assert r.experts[t].tolist() == of[:3]
