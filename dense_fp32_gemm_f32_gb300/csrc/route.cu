@@ -611,12 +611,18 @@ __device__ __forceinline__ int choose_experts(const RouteParams& p, const float 
 // sigmoid(l) = e^min(l, 0) / (1 + e^-|l|): with the largest chosen logit's
 // e^min(l, 0) taken out, the renormalised ones are ratios of numbers near 1
 // however small the scores are.
+// Softmax: an expert that its bias had chosen may lie far below the largest logit, where the rounding of the difference alone, up to
+// 2^-18 from 64 on, is as large as the weight's error may be: it is added back, e^(d + r) = e^d (1 + r).
 __device__ __forceinline__ float score_over(const RouteParams& p, float x, float lead, float sum) {
     if (p.sigmoid) {
         const float low = x > 0.f ? 0.f : x;
         return __fdividef(expf(low - (p.renormalize ? fminf(lead, 0.f) : 0.f)), 1.f + expf(-fabsf(x)));
     }
-    return sum != sum ? sum : expf(x - lead);  // (a NaN or +inf that was not chosen)
+    if (sum != sum) return sum;  // (a NaN or +inf that was not chosen)
+    const float d = x - lead, e = expf(d);
+    if (!(d > -128.f)) return e;  // (0, or NaN)
+    const float less = x - d;
+    return fmaf(e, (x - (d + less)) + (less - lead), e);
 }
 
 // The weight of the lane's expert e (-1: none).

@@ -57,12 +57,12 @@ enum { SGEMM_ROUTE_MAX_EXPERTS = 1024, SGEMM_ROUTE_MAX_CHOICES = 32, SGEMM_ROUTE
  * and a token that has fewer than k experts left gets -1 with weight 0 in its
  * last places.  So a padding token is a row of -inf.
  * Ties go to the lowest expert and the lowest group.  The choice is that of
- * exact arithmetic: where values lie too near one another for float32, the
- * token is decided in 64 bits.  NaN counts as the largest value; it makes its
+ * exact arithmetic: values that lie too near one another for float32 are compared
+ * in 64 bits, or by their logits if they all have one bias (64 bits hold many sigmoids equal).  NaN counts as the largest value; it makes its
  * token's weights NaN, as +inf does with a softmax (but only its own weight
  * with sigmoid scores that are not renormalised).
  * Weights are within 2^-18 of the exact ones, relative to the token's
- * largest; renormalised ones do not depend on how small the scores are.
+ * largest, and float32's smallest number; renormalised ones do not depend on how small the scores are.
  * Limits: 1 <= k <= 32, k <= E <= 1024, groups <= 32 and a divisor of E, top_groups <= groups.
  */
 int sgemm_route(int type, int score, int T, int E, int k,

@@ -56,3 +56,21 @@ def test_sums_of_groups_past_the_largest_float32(T, E, best, score):
     for t in range(T):
         of = sorted(range(group * size, (group + 1) * size), key=lambda e: (-c[t, e].item(), -l[t, e].item(), e))
         assert r.experts[t].tolist() == of[:3]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(3000, 64, 8), (100, 64, 8), (400, 200, 8), (120, 200, 8), (400, 40, 12)])
+def test_weights_of_experts_far_below_the_largest_logit(T, E, k):
+    """Chosen by their biases: scores from e^-60 to e^-87, and from there on numbers that float32 hardly holds or does not."""
+    logits = randn(T, E, seed=5)
+    logits[:, 0] += 13
+    logits[:, 1: 1 + k] -= 2 * randn(T, k, seed=6).abs() + torch.linspace(50, 74, T, device="cuda")[:, None]
+    logits[-5:, 1: 1 + k] -= 30
+    logits[-2:, 1: 1 + k] *= 1e36
+    b = torch.zeros(E, device="cuda")
+    b[1: 1 + k] = 10.0
+    r = g.sgemm_route(logits, k, bias=b)
+    assert ((r.experts >= 1) & (r.experts <= k)).all()
+    w = torch.gather(scores64(logits, "softmax"), 1, r.experts.long())
+    assert ((r.weights.double() - w).abs() <= 2.0 ** -18 * w.amax(-1, keepdim=True) + 2.0 ** -149).all()
+    assert g.check_status() == 0
