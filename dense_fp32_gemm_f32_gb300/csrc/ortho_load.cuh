@@ -75,11 +75,12 @@ __device__ __forceinline__ double squares(const float (&v)[N][8]) {
 }
 
 // 2^13 / norm as 2^up * factor, up a power that float32 holds and the factor
-// near 1 where it can be: X's elements stay in range between.
+// near 1 where it can be: X's elements stay in range between.  A norm below 2^-160 is that of zeros and a smaller eps (the
+// smallest number that is not zero is 2^-149): they stay zeros with any factor that float32 holds.  0: NaN.
 struct OrthoScale {
     float power, factor;
     __device__ __forceinline__ explicit OrthoScale(double norm) {
-        const double inv = 1. / norm;
+        const double inv = 1. / (norm > 0. ? fmax(norm, 0x1p-160) : norm);
         const int exponent = static_cast<int>(__double_as_longlong(inv) >> 52 & 0x7ff) - 1023;
         const int up = min(max(exponent, -126), 126);
         power = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);

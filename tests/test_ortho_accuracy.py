@@ -102,3 +102,17 @@ def test_quick_products_of_other_types_are_refused(dtype):
     for out in (None, torch.empty_like(G)):
         with pytest.raises(ValueError):
             g.sgemm_orthogonalize(G, out, quick=True)
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("eps", [1e-7, 2.0 ** -140, 1e-60, 1e-100, 1e-300, 5e-324])
+@pytest.mark.parametrize("M,N", [(20, 30), (100, 300), (300, 200)])
+def test_zeros_stay_zeros_with_the_smallest_eps(M, N, eps, dtype):
+    G = update(3, M, N, dtype, seed=1)
+    G[1] = 0
+    y = g.sgemm_orthogonalize(G, eps=eps)
+    assert (y[1] == 0).all()
+    assert (beyond_rounding(y[[0, 2]], ortho64(G[[0, 2]], eps=eps)) <= 2 * 2.0 ** -18).all()
+    assert g.sgemm_orthogonalize(G, eps=0.0)[1].isnan().all()
+    assert g.check_status() == 0
