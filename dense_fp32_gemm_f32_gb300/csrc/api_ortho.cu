@@ -13,12 +13,12 @@ namespace {
 
 // The largest |b u + c u^2| and |a s + b s^3 + c s^5| for s in [0, most], u = s^2:
 // at the ends, and where the derivatives are zero.
-double largest_correction(double b, double c, double most) {
+double largest_correction(double b, double c, double most, double a = 0) {  // (a: |a + b u + c u^2|)
     const double u = most * most;
-    double top = std::fabs(b * u + c * u * u);
+    double top = std::fmax(std::fabs(a), std::fabs(a + b * u + c * u * u));
     if (c != 0) {
         const double at = -b / (2 * c);
-        if (at > 0 && at < u) top = std::fmax(top, std::fabs(b * at + c * at * at));
+        if (at > 0 && at < u) top = std::fmax(top, std::fabs(a + b * at + c * at * at));
     }
     return top;
 }
@@ -41,8 +41,8 @@ double largest_value(double a, double b, double c, double most) {
 }
 
 // Whether the polynomial keeps every singular value that can occur within 2, and
-// what is added within 15 (see the scales in ortho_tc.cuh).
-bool polynomial_ok(int steps, double a, double b, double c) {
+// what is added within 15 (see the scales in ortho_tc.cuh); `growth`: of |p(s) / s| as a power of two.
+bool polynomial_ok(int steps, double a, double b, double c, int* growth) {
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     double most = 1;
     for (int i = 0; i < steps; ++i) {
@@ -51,6 +51,8 @@ bool polynomial_ok(int steps, double a, double b, double c) {
         if (!(next <= 2)) return false;
         most = std::fmax(most, next);
     }
+    const double raises = largest_correction(b, c, most, a);  // (at most 32: of a, b + c and a + b + c two are bounded)
+    for (*growth = 0; std::ldexp(1., *growth) < raises;) ++*growth;
     return true;
 }
 
@@ -86,8 +88,8 @@ extern "C" int sgemm_orthogonalize(int type, int E, int M, int N, const void* G,
                                    float a, float b, float c, double eps, void* out, int64_t ldo, int64_t stride_out,
                                    void* workspace, int64_t workspace_bytes, void* stream) {
     const int asked = type;
-    int parts = 2;
-    if (!take_quick(&type, &parts) || !sizes_ok(type, E, M, N, steps) || !(eps >= 0) || !std::isfinite(eps) || !polynomial_ok(steps, a, b, c))
+    int parts = 2, growth = 0;
+    if (!take_quick(&type, &parts) || !sizes_ok(type, E, M, N, steps) || !(eps >= 0) || !std::isfinite(eps) || !polynomial_ok(steps, a, b, c, &growth))
         return SGEMM_ERR_INVALID_ARG;
     const int size = type_bytes(type);
     const View g{G, E, M, N, ldg, stride_g, size}, o{out, E, M, N, ldo, stride_out, size};
@@ -100,6 +102,6 @@ extern "C" int sgemm_orthogonalize(int type, int E, int M, int N, const void* G,
     DeviceState* st = nullptr;
     const int rc = experts_device(&dev, &st);
     if (rc != SGEMM_OK) return rc;
-    const OrthoCall call = {G, ldg, stride_g, out, ldo, stride_out, type, E, M, N, steps, parts, a, b, c, eps, workspace};
+    const OrthoCall call = {G, ldg, stride_g, out, ldo, stride_out, type, E, M, N, steps, parts, a, b, c, growth, eps, workspace};
     return orthogonalize(call, *st, static_cast<cudaStream_t>(stream));
 }

@@ -20,6 +20,7 @@ struct OrthoPrep {
     double* part;        // E x chunks
     int chunks, per;     // row chunks a matrix, and rows of one
     double eps;
+    int* shift;          // of each matrix: the power of two that its X is held times besides
     uint16_t* hi;        // planes of E x rows x pitch; `plane` elements apart
     long long pitch, plane;
     int* zero;           // counters to set to 0
@@ -38,6 +39,7 @@ struct OrthoCall {
     int type, E, M, N, steps;
     int parts;  // f16 values that stand for an operand in the products: 2, or 1 (bf16 alone)
     float a, b, c;
+    int growth;  // |p(s) / s| of the polynomial is at most 2^growth
     double eps;
     void* workspace;
 };
@@ -45,7 +47,7 @@ struct OrthoCall {
 struct OrthoLayout {
     int chunks, per, panels;       // of the preparation and of the counters
     long long pitch, square_pitch;  // elements a row of X's planes and of A's
-    long long part, done, d, e, a, p, x[2], bytes;
+    long long part, done, shift, d, e, a, p, x[2], bytes;
 };
 OrthoLayout ortho_layout(int E, int M, int N, int steps);
 int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s);

@@ -74,17 +74,31 @@ __device__ __forceinline__ double squares(const float (&v)[N][8]) {
     return s * __longlong_as_double(static_cast<long long>(1023 - 2 * max(up, -126)) << 52);
 }
 
-// 2^13 / norm as 2^up * factor, up a power that float32 holds and the factor
+// X of a matrix whose norm is below eps is small, and its planes would hold few of its bits.  It is held times 2^q more, such that Z = 2^q X
+// has a norm between 1/4 and 1.  A step takes Z to 2^(q' - q) (a Z + (b 4^-q + c 16^-q Z Z^T) Z Z^T Z), where q' is q less `growth`, 0 at the
+// least, and 2^growth at least |p(s) / s| of the polynomial p: so Z's singular values stay within what X's are within.
+// (2^100: there X reaches the smallest numbers of float32 itself.)
+__device__ __forceinline__ int exponent_of(double v) { return static_cast<int>(__double_as_longlong(v) >> 52 & 0x7ff) - 1023; }
+__device__ __forceinline__ int ortho_shift(double norm, double eps) {
+    const int all = exponent_of(norm + eps), own = exponent_of(norm);  // (their difference is off by less than one)
+    return all == 1024 || norm == 0. ? 0 : min(max(all - own - 1, 0), 100);
+}
+__device__ __forceinline__ float power_of_two(int n) {  // (0 below float32's normal numbers)
+    return __uint_as_float(static_cast<uint32_t>(max(n + 127, 0)) << 23);
+}
+
+// 2^13 2^shift / norm as 2^up * factor, up a power that float32 holds and the factor
 // near 1 where it can be: X's elements stay in range between.  A norm below 2^-160 is that of zeros and a smaller eps (the
 // smallest number that is not zero is 2^-149): they stay zeros with any factor that float32 holds.  0: NaN.
+// (Exponents as integers: a comparison in 64 bits by every warp of an SM costs what 16 in 32 bits do.)
 struct OrthoScale {
     float power, factor;
-    __device__ __forceinline__ explicit OrthoScale(double norm) {
-        const double inv = 1. / (norm > 0. ? fmax(norm, 0x1p-160) : norm);
-        const int exponent = static_cast<int>(__double_as_longlong(inv) >> 52 & 0x7ff) - 1023;
-        const int up = min(max(exponent, -126), 126);
-        power = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-        factor = static_cast<float>(inv * __longlong_as_double(static_cast<long long>(1023 - up) << 52)) * 8192.f;
+    __device__ __forceinline__ OrthoScale(double norm, int shift) {
+        if (__double_as_longlong(norm) != 0 && exponent_of(norm) < -160) norm = 0x1p-160;
+        const double inv = 1. / norm;
+        const int up = min(max(exponent_of(inv) + shift, -126), 126);
+        power = power_of_two(up);
+        factor = static_cast<float>(inv * __longlong_as_double(static_cast<long long>(1023 + shift - up) << 52)) * 8192.f;
     }
     __device__ __forceinline__ void split(const float (&v)[8], uint4& hi, uint4& lo) const {
         uint32_t h[4], l[4];

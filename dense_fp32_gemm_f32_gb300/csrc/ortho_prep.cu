@@ -58,7 +58,10 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_split_kernel(const OrthoPr
     grid_dependency_wait();
     static_assert(kPrepThreads >= kOrthoMostChunks, "a part a thread");
     const double mine = threadIdx.x < p.chunks ? p.part[static_cast<long long>(e) * p.chunks + threadIdx.x] : 0.;
-    const OrthoScale scale(sqrt(cta_sum(mine, scratch)) + p.eps);
+    const double norm = sqrt(cta_sum(mine, scratch));
+    const int shift = ortho_shift(norm, p.eps);
+    if (chunk == 0 && threadIdx.x == 0) p.shift[e] = shift;
+    const OrthoScale scale(norm + p.eps, shift);
     const int octs = (p.cols + 7) / 8;
     const int r0 = chunk * p.per, rows = min(p.per, p.rows - r0);
     const T* G = static_cast<const T*>(p.G) + e * p.sg;

@@ -47,6 +47,7 @@ struct OrthoSmallParams {
     int m, n, steps, width;  // width: CTAs of a cluster
     int vec, align;          // G's rows begin on 16 bytes; bytes that the result's are aligned to
     float c1, c3, c5;
+    int growth;
     double eps;
     unsigned long long timeout_ns;
     unsigned int* status;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
     const uint32_t x_hi = base, x_lo = base + S::kXBytes;
     const uint32_t a_hi = base + 2 * S::kXBytes, a_lo = a_hi + S::kABytes;  // A's, then B's; with several CTAs first A's part
     const uint32_t d_at = base + S::kPlanes, e_at = d_at + 512, sums = e_at + 512, scratch = sums + 16 * 8;
-    const uint32_t bar = scratch + 8 * (kSmallThreads / 32), tmem_slot = bar + 8;
+    const uint32_t bar = scratch + 8 * (kSmallThreads / 32), tmem_slot = bar + 8, shift_at = bar + 12;
 
     const int warp = warp_uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int rank = warp_uniform(static_cast<int>(cluster_ctarank()));
@@ -216,7 +217,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         sum = 0;
         for (int q = 0; q < p.width; ++q) sum += ld_cluster_f64(map_shared_rank(sums, q));
     }
-    const OrthoScale scale(sqrt(sum) + p.eps);
+    const double norm = sqrt(sum);
+    const int shift = ortho_shift(norm, p.eps);
+    // (in shared memory: between products registers are short)
+    if (threadIdx.x == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(shift_at), "r"(shift) : "memory");
+    auto shift_of = [&](int step) {
+        int q;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q) : "r"(shift_at) : "memory");
+        return max(0, q - step * p.growth);
+    };
+    const OrthoScale scale(norm + p.eps, shift);
 
     // ---------------------------------------------------------------- X
 #pragma unroll
@@ -374,6 +384,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         if (mine) {
             float v[32];
             sums_of(c0, v);
+            const int q = shift_of(step);
+            const float c3 = p.c3 * power_of_two(-2 * q), c5 = p.c5 * power_of_two(-4 * q);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
                 const float4 d4 = lds128(d_at + 4 * (c0 + j));
@@ -382,10 +394,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
                 for (int i = 0; i < 4; ++i) {
                     float& x = v[j + i];
                     if (c0 + j + i == row) {
-                        sts_f(e_at + 4 * row, fmaf(p.c5, fmaf(d_row, d_row, x * 0x1p-24f), p.c3 * d_row));
+                        sts_f(e_at + 4 * row, fmaf(c5, fmaf(d_row, d_row, x * 0x1p-24f), c3 * d_row));
                         x = 0.f;
                     } else {
-                        x = fmaf(p.c5, fmaf(d_row + d[i], o[j + i], x * 0x1p-12f), p.c3 * o[j + i]);
+                        x = fmaf(c5, fmaf(d_row + d[i], o[j + i], x * 0x1p-12f), c3 * o[j + i]);
                     }
                 }
             }
@@ -399,22 +411,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
             factor = p.c1 + lds_f(e_at + 4 * row);
         });
         const bool last = step + 1 == p.steps;
+        const int next = shift_of(step + 1);
+        const float down = power_of_two(next - shift_of(step));
+        factor *= down;
 #pragma unroll 1
         for (int c = c0; active && c < cols; c += 32 * kSmallShare) {
             float v[32];
             if (c != c0) load_planes(x_hi, x_lo, row, c, x);
             sums_of(c, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(factor, x[j], v[j] * 0x1p-12f);
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(factor, x[j], v[j] * (0x1p-12f * down));
             if (!last) {
                 store_planes(x_hi, x_lo, row, c, v);
             } else if (row < p.m) {
                 T* const out = static_cast<T*>(p.out) + e * p.so;
+                const float result = 0x1p-13f * power_of_two(-next);
                 if constexpr (TALL) {
                     T* o = out + (n0 + c) * p.ldo + row;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        if (c + j < cols) *o = from_f32<T>(v[j] * 0x1p-13f);
+                        if (c + j < cols) *o = from_f32<T>(v[j] * result);
                         o += p.ldo;
                     }
                 } else {
@@ -424,13 +440,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
                         for (int j = 0; j < 32; j += 16 / static_cast<int>(sizeof(T))) {
                             alignas(16) T y[16 / sizeof(T)];
 #pragma unroll
-                            for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i) y[i] = from_f32<T>(v[j + i] * 0x1p-13f);
+                            for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i) y[i] = from_f32<T>(v[j + i] * result);
                             *reinterpret_cast<uint4*>(o + j) = *reinterpret_cast<const uint4*>(y);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (c + j < cols) o[j] = from_f32<T>(v[j] * 0x1p-13f);
+                            if (c + j < cols) o[j] = from_f32<T>(v[j] * result);
                     }
                 }
             }
@@ -532,7 +548,7 @@ int ortho_small(const OrthoCall& c, const DeviceState& st, cudaStream_t s) {
     p.m = m, p.n = n, p.steps = c.steps, p.width = (n + w - 1) / w;
     p.vec = row_alignment(c.G, size, c.M > 1 ? c.ldg : 0, c.E > 1 ? c.sg : 0) == 16;
     p.align = row_alignment(c.out, size, c.M > 1 ? c.ldo : 0, c.E > 1 ? c.so : 0);
-    p.c1 = c.a, p.c3 = c.b, p.c5 = c.c, p.eps = c.eps;
+    p.c1 = c.a, p.c3 = c.b, p.c5 = c.c, p.growth = c.growth, p.eps = c.eps;
     p.timeout_ns = kDefaultTimeoutNs;
     p.status = st.status_word;
     if (c.type == SGEMM_TYPE_F32) return launch_width<float, 2>(w, c, p, s);

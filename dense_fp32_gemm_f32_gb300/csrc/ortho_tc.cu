@@ -101,6 +101,7 @@ OrthoLayout ortho_layout(int E, int M, int N, int steps) {
     };
     l.part = take(8ll * E * l.chunks);
     l.done = take(4ll * 3 * E * l.panels);
+    l.shift = take(4ll * E);
     l.d = take(4ll * E * l.square_pitch);
     l.e = take(4ll * E * l.square_pitch);
     l.a = take(2ll * 2 * E * m * l.square_pitch);
@@ -132,6 +133,8 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     prep.zero = p.done = reinterpret_cast<int*>(ws + l.done);
     prep.zeros = 3ll * c.E * l.panels;
     p.panels = l.panels;
+    prep.shift = reinterpret_cast<int*>(ws + l.shift);
+    p.shift = prep.shift, p.growth = c.growth;
     p.d = reinterpret_cast<float*>(ws + l.d);
     p.e = reinterpret_cast<float*>(ws + l.e);
     p.diag = l.square_pitch;

@@ -68,6 +68,7 @@
 #pragma once
 
 #include "experts_tc.cuh"
+#include "ortho_load.cuh"
 
 namespace gb300 {
 
@@ -90,6 +91,8 @@ struct OrthoTcParams {
     int* done;                // counters: 3 kinds (X, A, B) x E x panels, zero at the start
     int panels;
     float c1, c3, c5;         // the polynomial
+    const int* shift;         // of each matrix: X is held times this power of two besides, less `growth` a step (ortho_load.cuh)
+    int growth;
     void* out;
     long long ldo, so;
     int out_type, align;
@@ -281,6 +284,19 @@ struct OrthoState {
     }
 };
 
+// What the power of two that a matrix's X is held times (see ortho_load.cuh) makes of the polynomial in this step.
+struct OrthoPowers {
+    float c3, c5;     // of a square
+    float step, out;  // of an update: 2^(q' - q), and what X is divided by in the end
+    __device__ __forceinline__ OrthoPowers(const OrthoTcParams& p, const OrthoTile& t, int shift) {
+        const int q = max(0, shift - t.step * p.growth), next = max(0, q - p.growth);
+        c3 = p.c3 * power_of_two(-2 * q);
+        c5 = p.c5 * power_of_two(-4 * q);
+        step = power_of_two(next - q);
+        out = 0x1p-13f * power_of_two(-next);
+    }
+};
+
 // The diagonals' part of a warp's rows and columns of a tile: the lane's row, and columns 4 lane .. 4 lane + 3.
 struct OrthoDiagonal {
     float row, column[4];
@@ -321,7 +337,8 @@ __device__ __forceinline__ void ortho_result(const OrthoTcParams& p, uint32_t pa
 // A block of rows r0 .. and columns c .. of tile t, from its sums; `first`: its first column among the warp's.
 template <typename S, bool TALL, int PHASE>
 __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t patch, const OrthoTile& t, int r0, int c,
-                                            int first, const OrthoState& state, const OrthoDiagonal& d, float (&v)[32]) {
+                                            int first, const OrthoState& state, const OrthoDiagonal& d, const OrthoPowers& w,
+                                            float (&v)[32]) {
     constexpr bool SYM = PHASE != kOrthoUpdate;
     const int lane = threadIdx.x & 31, row = r0 + lane;
     const int F = SYM ? p.m : p.rows, C = SYM ? p.m : p.cols;
@@ -342,11 +359,11 @@ __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t pat
                 if (on && row < F) d_out[row] = x * 0x1p-26f;
                 x *= 0x1p-14f;
             } else if constexpr (PHASE == kOrthoSquare) {
-                if (on && row < F) d_out[row] = fmaf(p.c5, fmaf(d.row, d.row, x * 0x1p-24f), p.c3 * d.row);
+                if (on && row < F) d_out[row] = fmaf(w.c5, fmaf(d.row, d.row, x * 0x1p-24f), w.c3 * d.row);
                 const float o = state.value(j + i);
-                x = fmaf(p.c5, fmaf(d.row + dj[i], o, x * 0x1p-12f), p.c3 * o);
+                x = fmaf(w.c5, fmaf(d.row + dj[i], o, x * 0x1p-12f), w.c3 * o);
             } else {
-                x = fmaf(p.c1 + (TALL ? dj[i] : d.row), state.value(j + i), x * 0x1p-12f);
+                x = w.step * fmaf(p.c1 + (TALL ? dj[i] : d.row), state.value(j + i), x * 0x1p-12f);
             }
             if (on) x = 0.f;
         }
@@ -354,7 +371,7 @@ __device__ __forceinline__ void ortho_block(const OrthoTcParams& p, uint32_t pat
     if constexpr (PHASE == kOrthoUpdate) {
         if (t.step + 1 == p.steps) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= 0x1p-13f;
+            for (int j = 0; j < 32; ++j) v[j] *= w.out;
             const long long at = t.e * p.so + r0 * p.ldo + c;
             if constexpr (S::PARTS == 1) {
                 ortho_result<S, __nv_bfloat16>(p, patch, at, v, F - r0, C - c);
@@ -627,6 +644,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, PARTS>::kThreads, 1)
             OrthoDiagonal diagonal = {};
             const __half *hi = nullptr, *lo = nullptr;
             const bool mine = r0 + lane < F;
+            const OrthoPowers powers(p, t, __ldg(p.shift + t.e));
             if (!mbar_wait_warp<false>(there0 + 8 * (n % kOrthoSlots), (n / kOrthoSlots) & 1, 4 * tmo)) return false;
             if constexpr (PHASE != kOrthoGram) {
                 const OrthoPlanes& from = PHASE == kOrthoSquare ? p.a : p.x[t.step & 1];
@@ -643,7 +661,7 @@ __global__ void __launch_bounds__(OrthoShape<TN, PARTS>::kThreads, 1)
             }
             auto block = [&](int j, float (&v)[32]) {
                 const int c = c0 + 32 * j;
-                if (wanted(c)) ortho_block<S, TALL, PHASE>(p, patch, t, r0, c, 32 * j, next, diagonal, v);
+                if (wanted(c)) ortho_block<S, TALL, PHASE>(p, patch, t, r0, c, 32 * j, next, diagonal, powers, v);
                 if (PHASE != kOrthoGram && 32 * (j + 1) < S::kWarpCols && wanted(c + 32))
                     next.load(hi + 32 * (j + 1), lo + 32 * (j + 1), mine, mine && c + 48 < C);
             };

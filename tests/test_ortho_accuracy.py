@@ -116,3 +116,20 @@ def test_zeros_stay_zeros_with_the_smallest_eps(M, N, eps, dtype):
     assert (beyond_rounding(y[[0, 2]], ortho64(G[[0, 2]], eps=eps)) <= 2 * 2.0 ** -18).all()
     assert g.sgemm_orthogonalize(G, eps=0.0)[1].isnan().all()
     assert g.check_status() == 0
+
+
+@pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("ratio", [0.9, 1.0, 3.0, 60.0, 1e3, 1e5, 1e8, 1e14, 1e25])
+@pytest.mark.parametrize("M,N", [(60, 64), (100, 300), (300, 128), (300, 400), (700, 640)])
+def test_norms_far_below_eps(M, N, ratio, dtype):
+    """Small X, whose bits the result keeps: relative to its own norm, however small that is."""
+    G = update(3, M, N, dtype, seed=M, size=1.0)
+    G[1] *= 2.0 ** -10
+    eps = ratio * G[0].double().norm().item()
+    for steps, coefficients in ((5, QUINTIC), (1, QUINTIC), (12, (2.0, -1.5, 0.5)), (3, (1.0, 0.0, 0.0))):
+        y, exact = g.sgemm_orthogonalize(G, eps=eps, steps=steps, coefficients=coefficients), ortho64(G, steps, coefficients, eps)
+        assert (beyond_rounding(y, exact) <= 2 * 2.0 ** -18).all(), (steps, coefficients, beyond_rounding(y, exact).tolist())
+        if dtype == torch.bfloat16 and steps == 5:
+            assert (beyond_rounding(g.sgemm_orthogonalize(G, eps=eps, quick=True), exact) <= 2 * 2.0 ** -8).all()
+    assert g.check_status() == 0
