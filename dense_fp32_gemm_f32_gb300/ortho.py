@@ -35,7 +35,7 @@ def sgemm_orthogonalize(G: torch.Tensor, out: torch.Tensor | None = None, *, ste
     1/500 of the norm to between 0.7 and 1.2 in five steps; (2, -1.5, 0.5) converges to 1.  M and N are up to 262144.
 
     Products are as exact as float32's whatever the type, and the result is rounded once.  ``quick``, for bfloat16 alone: a third
-    of the work, with operands of 11 bits (off by up to 8e-4 of the norm for the default; sgemm_ortho.h says more).
+    of the work, with operands of 11 bits (4e-4 to 8e-4 of the norm off for the default, as long as G's rank is not low; sgemm_ortho.h says more).
     """
     a, b, c = coefficients
     if out is None and stream is None:

@@ -44,17 +44,20 @@ enum { SGEMM_ORTHO_QUICK = 256 };
  * diagonals as two f16 values each (22 bits), three products of which stand for
  * one in float32 (A's and X's rounding errors, and the diagonals, are carried
  * along outside of the products), and sum in float32, whatever the type.  The
- * result is rounded to its type once.  A step multiplies an error by what
- * it multiplies the difference of two near singular values by, up to a for small ones.
- * Five steps of the usual polynomials (3.4445, -4.7750, 2.0315 and
- * those that converge to 1) come to less than 2^-18 of the result's norm up to rows of 65536.
+ * result is rounded to its type once.  Before that, five steps of the usual
+ * polynomials ((3.4445, -4.7750, 2.0315) and those that converge to 1) are off by less
+ * than 2^-18 of the result's norm up to rows of 65536, if G has something in
+ * all directions.  What rounding leaves in directions where it has nothing is raised
+ * by up to a in each step, 485 times in all by the former: 1e-5 of the norm for a
+ * rank of 30, up to 2e-4 for one or two, as with float32 products.
  * Many steps of a polynomial that does not converge lose more in any arithmetic: up
  * to 16 times what the same steps with float32 products lose (an accumulator's sum
  * is cut to 24 bits up to 32 times).
  *   SGEMM_ORTHO_QUICK: one f16 value each (11 bits), one product of them for one:
- * a third of the time for large matrices.  Five steps of the polynomial above are then off by 4e-4 to 8e-4
- * of the result's norm before it is rounded to bf16 (1.7e-3), ten by 1.6e-3, 64 by
- * 7e-3; (3, -1, 0), which raises errors threefold a step, by 4e-3 after six and 2e-1 after ten.
+ * a third of the time for large matrices.  Before the rounding to bf16 (1.7e-3 of the
+ * norm) five steps of the polynomial above are then off by 4e-4 to 8e-4 (up to 5e-3
+ * for a rank of one), ten by 1.6e-3, 64 by 7e-3; nothing is promised
+ * for polynomials that raise errors: (3, -1, 0) is off by 2e-2 after six steps and by the norm itself after ten.
  * A non-finite element makes its whole matrix NaN or infinite, and no other.
  */
 int sgemm_orthogonalize(int type, int E, int M, int N,

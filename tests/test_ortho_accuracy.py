@@ -72,6 +72,24 @@ def test_many_steps_and_polynomials_that_raise_errors(coefficients, steps, M, N,
 
 
 @pytest.mark.gpu
+@typed(TYPES)
+@pytest.mark.parametrize("rank", [1, 2, 8, 30])
+@pytest.mark.parametrize("M,N", [(60, 64), (100, 300), (2000, 128), (300, 400), (512, 512), (1000, 1300)])
+def test_matrices_of_low_rank(M, N, rank, dtype):
+    """Whole numbers that every type holds: nothing but the roundings of the steps in the other directions."""
+    gen = torch.Generator(device="cuda").manual_seed(M + rank)
+    u, v = (torch.randint(-2, 3, s, generator=gen, device="cuda").float() for s in ((M, rank), (rank, N)))
+    G = (u @ v).to(dtype)[None]
+    assert torch.equal(G[0].float(), u @ v)
+    exact = ortho64(G)
+    usual = ((float32_steps(G, 5, QUINTIC).double() - exact).norm() / exact.norm()).item()
+    off = beyond_rounding(g.sgemm_orthogonalize(G), exact).item()
+    assert off <= 2 * (16 * usual + 2.0 ** -18), (off, usual)
+    assert off <= 2.0 ** -11
+    assert g.check_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rank", [0, 4])
 @pytest.mark.parametrize("E,M,N", SHAPES + [(8, 1000, 3000)])
 def test_quick_products(E, M, N, rank):
