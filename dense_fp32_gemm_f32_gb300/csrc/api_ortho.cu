@@ -65,7 +65,7 @@ constexpr int kLongest = 1 << 18;
 bool take_quick(int* type, int* parts) {
     const bool quick = (*type & SGEMM_ORTHO_QUICK) != 0;
     *type &= ~SGEMM_ORTHO_QUICK;
-    if (quick && parts) *parts = 1;
+    if (quick) *parts = 1;
     return !quick || *type == SGEMM_TYPE_BF16;
 }
 
@@ -79,9 +79,10 @@ bool sizes_ok(int type, int E, int M, int N, int steps) {
 }  // namespace
 
 extern "C" int64_t sgemm_orthogonalize_workspace(int type, int E, int M, int N, int steps) {
-    if (!take_quick(&type, nullptr) || !sizes_ok(type, E, M, N, steps)) return -1;
+    int parts = 2;
+    if (!take_quick(&type, &parts) || !sizes_ok(type, E, M, N, steps)) return -1;
     if (E == 0 || M == 0 || N == 0 || ortho_always_small(M, N)) return 0;
-    return ortho_layout(E, M, N, steps).bytes;
+    return ortho_layout(E, M, N, steps, parts).bytes;
 }
 
 extern "C" int sgemm_orthogonalize(int type, int E, int M, int N, const void* G, int64_t ldg, int64_t stride_g, int steps,

@@ -49,7 +49,7 @@ struct OrthoLayout {
     long long pitch, square_pitch;  // elements a row of X's planes and of A's
     long long part, done, shift, d, e, a, p, x[2], bytes;
 };
-OrthoLayout ortho_layout(int E, int M, int N, int steps);
+OrthoLayout ortho_layout(int E, int M, int N, int steps, int parts);
 int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s);
 // The most matrices of a call: the small form numbers the CTAs of their clusters, up to 16 each, in 31 bits.
 constexpr int kOrthoMostMatrices = 0x7fffffff / 16;

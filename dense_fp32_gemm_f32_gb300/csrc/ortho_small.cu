@@ -301,30 +301,28 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const Ort
         // ------------------------------------------------------------ gram
         product(true, false, cols, [] {});
         if (p.width == 1) {
-#pragma unroll 1
-            for (int c = 32 * share; active && c < side; c += 32 * kSmallShare) {
+            if (mine) {
                 float v[32];
-                sums_of(c, v);
+                sums_of(c0, v);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    if (c + j == row) {
+                    if (c0 + j == row) {
                         sts_f(d_at + 4 * row, v[j] * 0x1p-26f);
                         v[j] = 0.f;
                     }
                     v[j] *= 0x1p-14f;
                 }
-                store_planes(a_hi, a_lo, row, c, v);
+                store_planes(a_hi, a_lo, row, c0, v);
             }
         } else {
             // This CTA's part, in float32: rows of 512 bytes, whose 16-byte pieces trade places by the row's number.
             auto part = [&](int r, int u) { return a_hi + static_cast<uint32_t>(r * 512 + ((u ^ r) & 31) * 16); };
-#pragma unroll 1
-            for (int c = 32 * share; active && c < side; c += 32 * kSmallShare) {
+            if (mine) {
                 float v[32];
-                sums_of(c, v);
+                sums_of(c0, v);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)
-                    sts128(part(row, (c + j) / 4), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+                    sts128(part(row, (c0 + j) / 4), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
             }
             cluster_sync_all();
             // The sums of some of the rows, from all parts in their order.

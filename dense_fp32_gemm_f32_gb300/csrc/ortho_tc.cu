@@ -84,7 +84,7 @@ int launch(OrthoTcParams& p, const CUtensorMap (&maps)[4], const DeviceState& st
 
 }  // namespace
 
-OrthoLayout ortho_layout(int E, int M, int N, int steps) {
+OrthoLayout ortho_layout(int E, int M, int N, int steps, int parts) {
     const long long m = std::min(M, N);
     OrthoLayout l = {};
     l.pitch = (N + 15ll) / 16 * 16, l.square_pitch = (m + 15) / 16 * 16;  // (the epilogue's accesses of 32 bytes)
@@ -105,7 +105,7 @@ OrthoLayout ortho_layout(int E, int M, int N, int steps) {
     l.d = take(4ll * E * l.square_pitch);
     l.e = take(4ll * E * l.square_pitch);
     l.a = take(2ll * 2 * E * m * l.square_pitch);
-    l.p = take(2ll * 2 * E * m * l.square_pitch);
+    l.p = take(2ll * parts * E * m * l.square_pitch);  // (with one plane products take B's hi alone)
     l.x[0] = take(2ll * 2 * E * M * l.pitch);
     l.x[1] = steps > 1 ? take(2ll * 2 * E * M * l.pitch) : l.x[0];
     return l;
@@ -118,7 +118,7 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     if (st.ortho_status != SGEMM_OK) return st.ortho_status;
     if (const int rc = ortho_small(c, st, s); rc != SGEMM_ERR_UNSUPPORTED) return rc;
     const int m = std::min(c.M, c.N), parts = c.parts;
-    const OrthoLayout l = ortho_layout(c.E, c.M, c.N, c.steps);
+    const OrthoLayout l = ortho_layout(c.E, c.M, c.N, c.steps, parts);
     if (static_cast<long long>(c.E) * l.chunks > 0x7fffffffll) return SGEMM_ERR_INVALID_ARG;
     char* const ws = static_cast<char*>(c.workspace);
     auto planes = [&](long long at, long long ld, long long matrix) {
@@ -149,8 +149,9 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     alignas(64) CUtensorMap maps[4];
     const OrthoPlanes* const of[4] = {&p.x[0], &p.x[1], &p.a, &p.p};
     for (int i = 0; i < 4; ++i) {
-        const int rc = i < 2 ? encode_planes(&maps[i], of[i]->hi, c.N, c.M, 2ll * c.E, l.pitch)
-                             : encode_planes(&maps[i], of[i]->hi, m, m, 2ll * c.E, l.square_pitch);
+        const long long planes = (i < 3 ? 2ll : parts) * c.E;
+        const int rc = i < 2 ? encode_planes(&maps[i], of[i]->hi, c.N, c.M, planes, l.pitch)
+                             : encode_planes(&maps[i], of[i]->hi, m, m, planes, l.square_pitch);
         if (rc != SGEMM_OK) return rc;
     }
     prep.G = c.G, prep.ldg = c.ldg, prep.sg = c.sg;

@@ -76,7 +76,7 @@ enum OrthoPhase { kOrthoGram, kOrthoSquare, kOrthoUpdate };
 
 // Matrices in two f16 planes, E in each.
 struct OrthoPlanes {
-    __half *hi, *lo;       // lo null: not kept
+    __half *hi, *lo;       // (lo of B: of two planes alone)
     long long ld, matrix;  // elements a row, a matrix
 };
 

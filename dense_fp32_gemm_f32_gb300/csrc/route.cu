@@ -827,7 +827,7 @@ __device__ __forceinline__ bool choose_quad(uint32_t (&key)[N], const RouteParam
 #pragma unroll
             for (int i = 0; i < 8; ++i) merge_two(a[j], b[j], key[8 * j + i], 0u);
         }
-        // A group's first block gets what the others have.
+        // A group's first block gets what the others have: those of a lane, and of the next (a group is half of all experts at most).
 #pragma unroll
         for (int w = 1; w < B; w *= 2)
             if (blocks > w) {
@@ -835,7 +835,6 @@ __device__ __forceinline__ bool choose_quad(uint32_t (&key)[N], const RouteParam
                 for (int j = 0; j + w < B; j += 2 * w) merge_two(a[j], b[j], a[j + w], b[j + w]);
             }
         if (blocks > B) merge_two(a[0], b[0], __shfl_xor_sync(kAll, a[0], 1), __shfl_xor_sync(kAll, b[0], 1));
-        if (blocks > 2 * B) merge_two(a[0], b[0], __shfl_xor_sync(kAll, a[0], 2), __shfl_xor_sync(kAll, b[0], 2));
         // Scores with their group in them, as keys hold their expert.
         uint32_t score[B];
         bool one = false, two = false;

@@ -108,6 +108,8 @@ def test_quick_products_are_for_bf16_alone():
         t += _lib.ORTHO_QUICK
         assert lib.sgemm_orthogonalize(t, 0, 16, 32, 0, 32, 512, 5, *QUINTIC, 1e-7, 0, 32, 512, 0, 0, None) == rc
         assert (lib.sgemm_orthogonalize_workspace(t, 1, 300, 500, 5) > 0) == (rc == _lib.OK)
+    size = [lib.sgemm_orthogonalize_workspace(t, 3, 512, 1000, 5) for t in (_lib.TYPE_BF16, _lib.TYPE_BF16 + _lib.ORTHO_QUICK)]
+    assert size[0] - size[1] == 2 * 3 * 512 * 512  # (the second plane of an operand)
     small = lib.sgemm_orthogonalize_workspace(_lib.TYPE_BF16 + _lib.ORTHO_QUICK, 2, 200, 256, 5) - 256
     assert lib.sgemm_orthogonalize(_lib.TYPE_BF16 + _lib.ORTHO_QUICK, 2, 200, 256, A, 256, 51200, 5, *QUINTIC, 1e-7, B, 256, 51200, C, small,
                                    None) == _lib.ERR_INVALID_ARG
