@@ -29,10 +29,11 @@
 // a warp a token for scores, grid, sort and k rounds, 420 with four lanes a token, whose warps also wait for the
 // instructions themselves (50 KB without a loop);
 // for a few tokens by latency.  Measured on GB300 (replayed from a CUDA graph): 16384 tokens, 8 of 256
-// experts, sigmoid, bias, 4 of 8 groups 28 to 31 us (43 with a warp a token; 22 where no scores lie so near one another
-// that choose_again decides, which all wait for; with a bias of zeros, where equal bf16 logits are many, 40, and 75 if these
-// all went there), by softmax alone 17 us (22), 64 tokens of the former 6.2 us; 65536
-// tokens, 6 of 64 25 us; one token, 4 of 64 3.3 us.  What carried it:
+// experts, sigmoid, bias, 4 of 8 groups 28 to 32 us (43 with a warp a token; 22 where no scores lie so near one another
+// that choose_again decides, which all wait for; with a bias of zeros, where equal bf16 logits are many, 48, with all logits equal
+// 194, and 334 with all within 1e-6 of one another: groups by their best two are then summed in 64 bits for every token), by softmax alone 19 us
+// (22), 64 tokens of the former 6.5 us; 65536 tokens, 6 of 64 27 us; one token, 4 of 64 3.4 us.  (ptxas: 76 to 92 bytes of spills with a
+// warp a token and 128 or 256 experts, 128 to 136 in choose_again; none in the other kernels.)  What carried it:
 // keys that hold their expert (51 -> 26 us by softmax), no
 // division and no float64 but for the contested values (60 -> 47 us), clusters instead of a
 // second launch (64 tokens 16 -> 6 us), four lanes a token (43 -> 37 us), choose_again's values in registers (37 -> 28 us).
@@ -1140,7 +1141,7 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
 //   softmax:  dl_e = s_e (scale d_e - sum_j scale d_j s_j) for every expert;
 //             renormalised, a softmax over the chosen: dl = W (d - sum d W / scale)
 // A warp a token; a lane holds the NPL neighbours that it writes.  16384 x 256 bf16, 8
-// chosen: 5.1 us (3.3 TB/s of stores and reads); for every expert 6.4 us (9.4 and 12.5 with the chosen ones' parts
+// chosen: 5.4 us (3.1 TB/s of stores and reads); for every expert 6.7 us (9.4 and 12.5 with the chosen ones' parts
 // sent to their lanes by shuffles).
 constexpr int kGradWarps = 8;
 
