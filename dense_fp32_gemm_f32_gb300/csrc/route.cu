@@ -303,17 +303,16 @@ __device__ __noinline__ int choose_again(const RouteParams& p, const T* row, boo
         group_best<NPL>(key, p, a, b);
         const bool there = lane < p.groups && a;
         float score = 0.f;
-        // (half the sum: that of two finite values is finite)
-        if (there) score = 0.5f * K::value(a) + (p.group_best == 2 && b ? 0.5f * K::value(b) : 0.f);
+        // (half the sum of two: that of finite values is finite.  Not half of one: logits may be the smallest numbers)
+        if (there) score = p.group_best == 2 ? 0.5f * K::value(a) + (b ? 0.5f * K::value(b) : 0.f) : K::value(a);
         const uint32_t rank = there ? K::of(score) : 0u;
         // Surely among the best: fewer than top_groups may be better.  Surely not: as many are.
-        const float apart = p.group_best == 2 ? near : 0.5f * near;
         int may = 0, are = 0;
         for (int g = 0; g < p.groups; ++g) {
             const uint32_t other = __shfl_sync(kAll, rank, g);
             const float v = __shfl_sync(kAll, score, g);
             if (g == lane || !other) continue;
-            const bool close = apart > 0.f && fabsf(score) < INFINITY && fabsf(v) < INFINITY && fabsf(v - score) <= apart;
+            const bool close = near > 0.f && fabsf(score) < INFINITY && fabsf(v) < INFINITY && fabsf(v - score) <= near;
             const bool better = other > rank || (other == rank && g < lane);
             may += close || better;
             are += !close && better;

@@ -74,3 +74,22 @@ def test_weights_of_experts_far_below_the_largest_logit(T, E, k):
     w = torch.gather(scores64(logits, "softmax"), 1, r.experts.long())
     assert ((r.weights.double() - w).abs() <= 2.0 ** -18 * w.amax(-1, keepdim=True) + 2.0 ** -149).all()
     assert g.check_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E", [(4, 32), (300, 32), (4, 256), (300, 256), (4, 60)])
+@pytest.mark.parametrize("how", [dict(), dict(groups=4, top_groups=1), dict(groups=4, top_groups=2, bias=1)], ids=str)
+def test_logits_of_the_smallest_numbers(T, E, how):
+    """Multiples of 2^-149 in float32: in order, also from group to group.  (Scores are equal; a bias of one value moves no choice.)"""
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    units = torch.stack([torch.randperm(E, generator=gen, device="cuda") for _ in range(T)]) - E // 4
+    logits = (units.double() * 2.0 ** -149).float()
+    how = dict(how, bias=torch.full((E,), 0.5, device="cuda")) if "bias" in how else how
+    r = g.sgemm_route(logits, 3, **how)
+    by = units.clone()
+    if "groups" in how:
+        best = units.view(T, 4, -1).amax(-1)
+        kept = torch.zeros((T, 4), dtype=torch.bool, device="cuda").scatter(1, torch.sort(best, dim=-1, descending=True).indices[:, :how["top_groups"]], True)
+        by[~kept.repeat_interleave(E // 4, 1)] = -10 ** 6
+    assert torch.equal(r.experts, torch.sort(by, dim=-1, descending=True).indices[:, :3].int())
+    assert g.check_status() == 0
