@@ -69,9 +69,10 @@ int sgemm_orthogonalize(int type, int E, int M, int N,
 
 /*
  * sgemm_orthogonalize_workspace -- the bytes of workspace that a call of these
- * sizes takes (about 16 an element for several steps, 8 for one, and 16 an element
- * of the square of the shorter side; 0 for a shorter side of up to 128 and a longer
- * one of up to 2048), or -1 for sizes that it refuses.  It asks no device.
+ * sizes takes (about 8 an element for several steps, 4 for one, and 8, quick 6, an
+ * element of the square of the shorter side; 0 for a shorter side of up to 128 and a longer
+ * one of up to 2048), or -1 for sizes that it refuses.  It asks no device (some
+ * take longer ones without workspace as well).
  */
 int64_t sgemm_orthogonalize_workspace(int type, int E, int M, int N, int steps);
 

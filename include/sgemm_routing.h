@@ -94,7 +94,7 @@ int sgemm_route_grad(int type, int score, int T, int E, int k,
  *   slots      T x k, different from one another where they are rows of Y
  *   E, offsets as sgemm_route gives them
  * Rows below offsets[E] that no slot names are left as they were.
- * Its gradient is sgemm_combine without weights.
+ * Its gradient is sgemm_combine without weights (of slots below offsets[E]).
  */
 int sgemm_spread(int type, int T, int k, int R, int H,
                  const void* X, int64_t ldx,
