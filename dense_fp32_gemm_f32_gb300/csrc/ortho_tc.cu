@@ -149,9 +149,9 @@ int orthogonalize(const OrthoCall& c, DeviceState& st, cudaStream_t s) {
     alignas(64) CUtensorMap maps[4];
     const OrthoPlanes* const of[4] = {&p.x[0], &p.x[1], &p.a, &p.p};
     for (int i = 0; i < 4; ++i) {
-        const long long planes = (i < 3 ? 2ll : parts) * c.E;
-        const int rc = i < 2 ? encode_planes(&maps[i], of[i]->hi, c.N, c.M, planes, l.pitch)
-                             : encode_planes(&maps[i], of[i]->hi, m, m, planes, l.square_pitch);
+        const long long count = (i < 3 ? 2ll : parts) * c.E;
+        const int rc = i < 2 ? encode_planes(&maps[i], of[i]->hi, c.N, c.M, count, l.pitch)
+                             : encode_planes(&maps[i], of[i]->hi, m, m, count, l.square_pitch);
         if (rc != SGEMM_OK) return rc;
     }
     prep.G = c.G, prep.ldg = c.ldg, prep.sg = c.sg;
